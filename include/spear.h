@@ -250,6 +250,131 @@ spear_status spear_w4_linear_semifused(const spear_bf16 *x, int64_t M, const spe
                                        size_t ws_bytes, void *stream, void *aux_stream,
                                        void *ev_fork, void *ev_join);
 
+/* Activations of spear_epilogue and spear_experts. */
+#define SPEAR_ACT_NONE      0 /* t                                                     */
+#define SPEAR_ACT_RELU      1 /* max(t, 0)                                             */
+#define SPEAR_ACT_SILU      2 /* t / (1 + exp(-t))                                     */
+#define SPEAR_ACT_GELU      3 /* t / 2 (1 + erf(t / sqrt 2))                           */
+#define SPEAR_ACT_GELU_TANH 4 /* t / 2 (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3)))     */
+
+/* What follows the layer's output in spear_w4_linear_epilogue (device pointers). */
+typedef struct spear_epilogue {
+    const float *bias;    /* [N], added to the layer's output (W4 and EC), or NULL; 4-byte aligned */
+    const void *residual; /* [M][N], or [M][N/2] with the gated pair, of y's type, added last, or
+                             NULL; 16-byte aligned; may be y itself (each element is read before
+                             it is written)                                                      */
+    int32_t act;          /* SPEAR_ACT_*                                                           */
+    int32_t glu;          /* 1: the gated pair below (N even); 0: every channel by itself          */
+} spear_epilogue;
+
+/*
+ * spear_w4_linear_epilogue -- the layer with bias, activation and residual in
+ * its kernels' epilogue, with t the layer's output (W4 and EC, fp32):
+ *   glu == 0:  y[m][n] = act(t[m][n] + bias[n]) + residual[m][n]          (N channels)
+ *   glu == 1:  y[m][i] = act(t[m][2i] + bias[2i]) (t[m][2i+1] + bias[2i+1])
+ *                        + residual[m][i]                                 (N / 2 channels)
+ * The gated pair is a decoder's gate and up projection as one layer: row 2i of
+ * the weights (codes, scales, zero points, bias, B) is the gate's row i and row
+ * 2i + 1 the up projection's, interleaved once before spear_pack_w4.  All of
+ * the epilogue is in fp32, rounded once to y's type.  Other arguments, the
+ * workspace and the dispatch are those of spear_w4_linear_path; ep is required.
+ * An expired wait makes the outputs NaN here too (NaN passes through every
+ * activation).
+ */
+spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spear_w4 *w,
+                                      const spear_ec *ec, const spear_epilogue *ep, void *y,
+                                      int32_t out_dtype, void *workspace, size_t ws_bytes,
+                                      int32_t path, void *stream);
+
+/* Scores of spear_router. */
+#define SPEAR_SCORE_SOFTMAX 0 /* s_e = exp(z_e) / sum exp(z)  */
+#define SPEAR_SCORE_SIGMOID 1 /* s_e = 1 / (1 + exp(-z_e))    */
+/* Most experts, choices a token, and expert groups. */
+#define SPEAR_MAX_EXPERTS 512
+#define SPEAR_MAX_TOPK    32
+#define SPEAR_MAX_GROUPS  64
+
+/* Router of a mixture of experts (device pointers). */
+typedef struct spear_router {
+    const spear_bf16 *w;  /* [E][K]; 16-byte aligned                                              */
+    const float *bias;    /* [E] added to the scores for the choice alone, or NULL; 4-byte aligned */
+    int32_t E;            /* experts, 1 .. SPEAR_MAX_EXPERTS                                       */
+    int32_t topk;         /* experts a token takes, 1 .. SPEAR_MAX_TOPK                            */
+    int32_t score;        /* SPEAR_SCORE_*                                                         */
+    int32_t n_group;      /* groups of E / n_group consecutive experts, 1 .. SPEAR_MAX_GROUPS      */
+    int32_t topk_group;   /* groups kept, 1 .. n_group, holding at least topk experts              */
+    int32_t group_best;   /* a group counts the sum of its best 1 or 2 choices                     */
+    int32_t renorm;       /* 1: the chosen scores are divided by their sum                         */
+    float scale;          /* factor of the weights; must not be NaN                                */
+} spear_router;
+
+/*
+ * spear_route -- which experts each token takes, and with what weights:
+ *   z_me = sum_k x[m][k] w[e][k]    s = softmax or sigmoid of z    c = s + bias
+ *   kept groups: the topk_group largest by the sum of their group_best largest c
+ *   ids[m][0..topk): the experts of the kept groups with the largest c, in
+ *     descending order; ties (of experts and of groups) go to the lowest index
+ *   weights[m][j] = scale * s[ids[m][j]]  (/ sum_j s with renorm)
+ * Logits, scores and choices are those of exact products summed and compared
+ * in fp64, so the choice does not hang on an fp32 rounding; the weights are
+ * rounded once to fp32.  An expert whose c is NaN or -inf (a bias of -inf
+ * takes an expert out) is never chosen: a slot left without an expert gets id
+ * -1 and weight 0, and takes no part in the sum.  Scores that sum to zero
+ * give weights of zero.
+ *   x [M][K] bf16, 16-byte aligned; M >= 0 (0 does nothing); K >= 32, K % 32 == 0.
+ *   weights [M][topk] fp32, ids [M][topk] int32 outputs, 4-byte aligned.
+ *   workspace device scratch of spear_route_workspace_size bytes, 256-byte
+ *             aligned; needs no zeroing and holds nothing between calls.
+ */
+size_t spear_route_workspace_size(int64_t M, int32_t E);
+spear_status spear_route(const spear_bf16 *x, int64_t M, int64_t K, const spear_router *router,
+                         float *weights, int32_t *ids, void *workspace, size_t ws_bytes,
+                         void *stream);
+
+/*
+ * Experts of a mixture (device pointers): two 4-bit layers an expert, the
+ * expert index outermost.  The codes are spear_pack_w4's of [E * NU][K] and
+ * [E * N][I]; NU = 2 I with the gated pair (rows 2i and 2i + 1 as in
+ * spear_epilogue), else I.
+ */
+typedef struct spear_experts {
+    const uint8_t *up;         /* [E][NU][K/2]; 16-byte aligned           */
+    const float *up_scales;    /* [E][NU]                                 */
+    const uint8_t *up_zeros;   /* [E][NU], or NULL for zero point 8       */
+    const float *up_bias;      /* [E][NU], or NULL                        */
+    const uint8_t *down;       /* [E][N][I/2]; 16-byte aligned            */
+    const float *down_scales;  /* [E][N]                                  */
+    const uint8_t *down_zeros; /* [E][N], or NULL for zero point 8        */
+    const float *down_bias;    /* [E][N], or NULL                         */
+    int64_t K;                 /* input channels, >= 32, a multiple of 32 */
+    int64_t I;                 /* inner channels, >= 32, a multiple of 32 */
+    int64_t N;                 /* output channels, >= 1                   */
+    int32_t E;                 /* 1 .. SPEAR_MAX_EXPERTS                  */
+    int32_t act;               /* SPEAR_ACT_* between the two layers      */
+    int32_t glu;               /* 1: the gated pair; 0: act alone         */
+} spear_experts;
+
+/*
+ * spear_w4_experts -- the routed tokens through their experts:
+ *   h_mj   = act(up_e x_m + up_bias_e)    (or the gated pair), e = ids[m][j]
+ *   y[m]   = residual[m] + sum_j weights[m][j] (down_e h_mj + down_bias_e)
+ * with fp32 sums; h is rounded to bf16 (the layers' activation type), y once to
+ * bf16.  A slot whose id is outside [0, E) (an expert elsewhere, a padded
+ * token, a slot spear_route left empty) adds nothing, whatever its weight; an
+ * expert may occur twice in a token.
+ *   x [M][K] bf16, ids [M][topk] int32, weights [M][topk] fp32,
+ *   residual [M][N] bf16 or NULL (may be y itself), y [M][N] bf16; x, residual
+ *   and y 16-byte aligned.  y may not overlap any other input.
+ *   M >= 0 (0 does nothing), 1 <= topk <= SPEAR_MAX_TOPK, M topk < 2^31.
+ *   workspace device scratch of spear_w4_experts_workspace_size bytes, 256-byte
+ *             aligned; needs no zeroing and holds nothing between calls.
+ */
+size_t spear_w4_experts_workspace_size(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N);
+spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_experts *w,
+                              const int32_t *ids, const float *weights, int32_t topk,
+                              const spear_bf16 *residual, spear_bf16 *y, void *workspace,
+                              size_t ws_bytes, void *stream);
+
 /* Size of the library's own scratch used by spear_w4_linear_noalloc, per GPU. */
 #define SPEAR_NOALLOC_MAX_WORKSPACE ((size_t)48 << 20)
 

@@ -178,7 +178,7 @@ static std::atomic<uint32_t> g_wait_limit{0};
 static const uint32_t DEFAULT_WAIT_LIMIT = 1u << 20;
 
 // gfx950 check, cached per device.
-static spear_status check_device()
+spear_status check_device()
 {
     static std::mutex mu;
     static int known[64];   // 0 unknown, 1 ok, 2 not gfx950
@@ -491,7 +491,7 @@ static spear_status launch_path(LinearArgs &a, const spear_ec *ec, int32_t path,
     switch (path) {
     case SPEAR_PATH_DECODE:
         if (!(ec && ec->gate_h > 0 && a.rpad > 32)) {
-            e = launch_decode(a, ec ? 1 : 0, s);
+            e = a.E.on ? launch_decode_epi(a, ec ? 1 : 0, s) : launch_decode(a, ec ? 1 : 0, s);
             break;
         }
         // a vector gate over more than one 32-rank block is formed by the
@@ -504,7 +504,7 @@ static spear_status launch_path(LinearArgs &a, const spear_ec *ec, int32_t path,
                 e = launch_compact(active, M, a.idx_out, a.nact_out, s);
         }
         if (e == hipSuccess)
-            e = launch_decode(a, ec ? 2 : 0, s);
+            e = a.E.on ? launch_decode_epi(a, ec ? 2 : 0, s) : launch_decode(a, ec ? 2 : 0, s);
         break;
     default:
         if (ec && (a.g_ks > 1 || a.g_bm == 64) && cdiv(M, 16) < PRE_GROUPS) {
@@ -541,7 +541,7 @@ static spear_status launch_path(LinearArgs &a, const spear_ec *ec, int32_t path,
 // A validated layer call: dispatch and launch on `stream`.
 static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w,
                                const spear_ec *ec, void *y, int32_t out_dtype, void *workspace,
-                               int32_t path, void *stream)
+                               int32_t path, void *stream, const spear_epilogue *ep = nullptr)
 {
     const int64_t N = w->N, K = w->K;
     const WsLayout L = ws_layout(M, N, K, ec ? ec->r : 0);
@@ -558,6 +558,13 @@ static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w
 
     LinearArgs a;
     fill_args(a, x, M, w, ec, y, out_dtype, workspace, path, L);
+    if (ep) {
+        a.E.bias = ep->bias;
+        a.E.res = ep->residual;
+        a.E.act = ep->act;
+        a.E.glu = ep->glu;
+        a.E.on = 1;
+    }
     return launch_path(a, ec, path, s);
 }
 
@@ -600,6 +607,25 @@ spear_status spear_w4_linear_path(const spear_bf16 *x, int64_t M, const spear_w4
     if (st != SPEAR_OK)
         return st;
     return run_linear(x, M, w, ec, y, out_dtype, workspace, path, stream);
+}
+
+spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spear_w4 *w,
+                                      const spear_ec *ec, const spear_epilogue *ep, void *y,
+                                      int32_t out_dtype, void *workspace, size_t ws_bytes,
+                                      int32_t path, void *stream)
+{
+    if (!ep)
+        return SPEAR_E_NULL;
+    spear_status st = validate_linear(x, M, w, ec, y, out_dtype, workspace, ws_bytes, &path);
+    if (st != SPEAR_OK)
+        return st;
+    if (ep->act < SPEAR_ACT_NONE || ep->act > SPEAR_ACT_GELU_TANH || (ep->glu != 0 && ep->glu != 1))
+        return SPEAR_E_ARG;
+    if (ep->glu && w->N % 2 != 0)
+        return SPEAR_E_SHAPE;
+    if (!aligned(ep->bias, 4) || !aligned(ep->residual, 16))
+        return SPEAR_E_ALIGN;
+    return run_linear(x, M, w, ec, y, out_dtype, workspace, path, stream, ep);
 }
 
 spear_status spear_w4_linear_noalloc(const spear_bf16 *x, int64_t M, const spear_w4 *w,

@@ -54,9 +54,19 @@
 
 #include "spear_internal.hpp"
 
+// SPEAR_EPILOGUE 1 (decode_epilogue.hip, which includes this file): the same
+// kernels with bias, activation and residual in the epilogue.  A translation
+// unit of its own, so that the two sets compile side by side and the kernels
+// without an epilogue stay as they are.
+#ifndef SPEAR_EPILOGUE
+#define SPEAR_EPILOGUE 0
+#endif
+
 namespace spear {
 
 namespace {
+
+constexpr int EPI = SPEAR_EPILOGUE;
 
 // Stream waves of a workgroup: DEC_WAVES with the fused EC (its producers and
 // epilogue exchange are laid out for 4 waves); without it DEC_WAVES_PLAIN where
@@ -545,6 +555,8 @@ __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
     __shared__ DecShared<NW> sh;
     extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
     pin_dec_args(a);
+    if constexpr (EPI != 0)
+        pin_epi_args(a);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, lg = lane >> 4;
 
@@ -760,6 +772,17 @@ __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
     }
     if (EC_MODE == 1)
         __builtin_amdgcn_s_setprio(0);
+    // Bias and residual of this lane's outputs, loaded while the waves' sums
+    // meet: before the weight stream they would push the fused kernel past the
+    // 256 registers a lane that let a producer share its CU.
+    float bias_raw[4] = {0.f, 0.f, 0.f, 0.f}, res_v[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (EPI != 0) {
+        if (wave == 0) {
+            epi_load_bias(a.E.bias, a.scales, n0 + 4 * lg, N, bias_raw);
+            epi_load_res<OUT_F32>(lr < M ? a.E.res : nullptr, lr, n0 + 4 * lg, a.E.glu,
+                                  a.E.glu ? N / 2 : N, res_v);
+        }
+    }
     if ((EC_MODE == 1 || ksplit > 1) && tid == 0)
         sh.u32[0] = epoch_tag(claimed + opaque_zero64());    // both halves live until here
     __syncthreads();
@@ -941,7 +964,20 @@ __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
                     yv[i] += e[i];
             }
         }
-        if (lr < M) {
+        if constexpr (EPI != 0) {
+            if (lr < M) {
+                float o[4];
+                if (!a.E.bias)
+                    bias_raw[0] = bias_raw[1] = bias_raw[2] = bias_raw[3] = 0.f;
+                epi_apply(yv, bias_raw, a.E.act, a.E.glu, o);
+                if (a.E.res) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        o[i] += res_v[i];
+                }
+                epi_store<OUT_F32>(a.y, lr, n0 + 4 * lg, a.E.glu, a.E.glu ? N / 2 : N, o);
+            }
+        } else if (lr < M) {
             const int64_t nb = n0 + 4 * lg;
             if (OUT_F32) {
                 float *y = reinterpret_cast<float *>(a.y) + (int64_t)lr * N;
@@ -1058,7 +1094,11 @@ hipError_t launch_decode_t(const LinearArgs &a, hipStream_t s)
 
 } // namespace
 
+#if SPEAR_EPILOGUE
+hipError_t launch_decode_epi(const LinearArgs &a, int ec_mode, hipStream_t s)
+#else
 hipError_t launch_decode(const LinearArgs &a, int ec_mode, hipStream_t s)
+#endif
 {
     switch (ec_mode) {
     case 0:

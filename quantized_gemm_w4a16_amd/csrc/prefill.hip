@@ -610,9 +610,10 @@ __device__ __forceinline__ void lds_read4(const uint8_t *base, uint32_t a0, uint
 }
 
 template <int G2_WM, int G2_FM, int SPLIT, int EC, int OUT_F32, int G2_WK = 1, int G2_FN = 4, int G2_WN = 4,
-          int G2_KF = 0>
+          int G2_KF = 0, int EPI = 0>
 __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const LinearArgs a)
 {
+    // EPI: bias, activation and residual follow (EpiArgs).
     // G2_KF: K is a multiple of 128, so no DMA source ever needs clamping (its
     // per-lane selects are left out of the main loop).
     // G2_WK = 2 (64 x 64 tiles): two waves share each (token, channel) pair of
@@ -660,6 +661,8 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
 
     __shared__ uint32_t s_tagg, s_tbad;
     pin_pre_args(a);
+    if constexpr (EPI != 0)
+        pin_epi_args(a);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform: scalar branches
 
@@ -1219,6 +1222,37 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
         }
         return;
     }
+    if constexpr (EPI != 0) {
+        const int64_t NO = a.E.glu ? N / 2 : N;
+        float bv[G2_FN][4];
+#pragma unroll
+        for (int fn = 0; fn < G2_FN; fn++) {
+            epi_load_bias(a.E.bias, a.scales, n0 + (wn * G2_FN + fn) * 16 + 4 * lg, N, bv[fn]);
+            if (!a.E.bias)
+                bv[fn][0] = bv[fn][1] = bv[fn][2] = bv[fn][3] = 0.f;
+        }
+#pragma unroll
+        for (int fm = 0; fm < G2_FM; fm++) {
+            const int64_t mm = m0 + (wm * G2_FM + fm) * 16 + lr;
+            if (mm >= M)
+                continue;
+#pragma unroll
+            for (int fn = 0; fn < G2_FN; fn++) {
+                const int64_t nb = n0 + (wn * G2_FN + fn) * 16 + 4 * lg;
+                const float t[4] = {acc[fn][fm][0], acc[fn][fm][1], acc[fn][fm][2], acc[fn][fm][3]};
+                float o[4], r[4];
+                epi_apply(t, bv[fn], a.E.act, a.E.glu, o);
+                if (a.E.res) {
+                    epi_load_res<OUT_F32>(a.E.res, mm, nb, a.E.glu, NO, r);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        o[i] += r[i];
+                }
+                epi_store<OUT_F32>(a.y, mm, nb, a.E.glu, NO, o);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int fm = 0; fm < G2_FM; fm++) {
         const int64_t mm = m0 + (wm * G2_FM + fm) * 16 + lr;
@@ -1254,19 +1288,10 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     }
 }
 
-// Second launch of a K-split GEMM: y = the sum of the slices' partial tiles in
-// slice order; a thread takes 4 consecutive channels of one token.  Its few
-// values come as plain arguments (one 64-byte line; read from the layer's
-// argument block they would span five).
-template <int OUT_F32>
-__global__ __launch_bounds__(256) void splitk_reduce_kernel(void *yv, const uint8_t *partv, int64_t M,
-                                                            int64_t N, int32_t KS, int32_t bm, int32_t bn)
+// The sum over the slices for element quad (m, n .. n + 3).
+__device__ __forceinline__ f32x4 splitk_sum(const uint8_t *partv, int64_t m, int64_t n, int64_t M, int64_t N,
+                                            int32_t KS, int32_t bm, int32_t bn)
 {
-    const int64_t nq = (N + 3) / 4;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (idx >= M * nq)
-        return;
-    const int64_t m = idx / nq, n = 4 * (idx % nq);
     const int64_t tiles_n = (N + bn - 1) / bn, ntiles = tiles_n * ((M + bm - 1) / bm);
     const int64_t tile = (m / bm) * tiles_n + n / bn;
     const int64_t off = (m % bm) * bn + n % bn;
@@ -1283,6 +1308,23 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(void *yv, const uint
             if (q0 + i < KS)
                 v += p[i];
     }
+    return v;
+}
+
+// Second launch of a K-split GEMM: y = the sum of the slices' partial tiles in
+// slice order; a thread takes 4 consecutive channels of one token.  Its few
+// values come as plain arguments (one 64-byte line; read from the layer's
+// argument block they would span five).
+template <int OUT_F32>
+__global__ __launch_bounds__(256) void splitk_reduce_kernel(void *yv, const uint8_t *partv, int64_t M,
+                                                            int64_t N, int32_t KS, int32_t bm, int32_t bn)
+{
+    const int64_t nq = (N + 3) / 4;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (idx >= M * nq)
+        return;
+    const int64_t m = idx / nq, n = 4 * (idx % nq);
+    const f32x4 v = splitk_sum(partv, m, n, M, N, KS, bm, bn);
     if (OUT_F32) {
         float *y = reinterpret_cast<float *>(yv) + m * N;
         if (n + 3 < N && (N & 3) == 0) {
@@ -1307,7 +1349,33 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(void *yv, const uint
     }
 }
 
-template <int WM, int FM, int EC, int WK = 1, int FN = 4, int WN = 4, int KF = 0>
+// The same with the epilogue: its values come as one more block of arguments.
+template <int OUT_F32>
+__global__ __launch_bounds__(256) void splitk_reduce_epi_kernel(void *yv, const uint8_t *partv, int64_t M,
+                                                                int64_t N, int32_t KS, int32_t bm, int32_t bn,
+                                                                const EpiArgs E)
+{
+    const int64_t nq = (N + 3) / 4;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (idx >= M * nq)
+        return;
+    const int64_t m = idx / nq, n = 4 * (idx % nq), NO = E.glu ? N / 2 : N;
+    float b[4] = {0.f, 0.f, 0.f, 0.f}, r[4], o[4];
+    if (E.bias)
+        epi_load_bias(E.bias, E.bias, n, N, b);
+    epi_load_res<OUT_F32>(E.res, m, n, E.glu, NO, r);
+    const f32x4 v = splitk_sum(partv, m, n, M, N, KS, bm, bn);
+    const float t[4] = {v[0], v[1], v[2], v[3]};
+    epi_apply(t, b, E.act, E.glu, o);
+    if (E.res) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            o[i] += r[i];
+    }
+    epi_store<OUT_F32>(yv, m, n, E.glu, NO, o);
+}
+
+template <int EPI, int WM, int FM, int EC, int WK = 1, int FN = 4, int WN = 4, int KF = 0>
 hipError_t launch_gemm2_t(const LinearArgs &a, hipStream_t s)
 {
     const int64_t bm = 16 * FM * WM, bn = 16 * FN * WN;
@@ -1324,7 +1392,13 @@ hipError_t launch_gemm2_t(const LinearArgs &a, hipStream_t s)
             return e;
         const int64_t threads = a.M * ((a.N + 3) / 4);
         const uint8_t *part = a.ws + a.P.gpart;
-        if (a.out_f32)
+        if (EPI != 0 && a.out_f32)
+            hipLaunchKernelGGL(splitk_reduce_epi_kernel<1>, dim3((unsigned)((threads + 255) / 256)),
+                               dim3(256), 0, s, a.y, part, a.M, a.N, a.g_ks, a.g_bm, a.g_bn, a.E);
+        else if (EPI != 0)
+            hipLaunchKernelGGL(splitk_reduce_epi_kernel<0>, dim3((unsigned)((threads + 255) / 256)),
+                               dim3(256), 0, s, a.y, part, a.M, a.N, a.g_ks, a.g_bm, a.g_bn, a.E);
+        else if (a.out_f32)
             hipLaunchKernelGGL(splitk_reduce_kernel<1>, dim3((unsigned)((threads + 255) / 256)),
                                dim3(256), 0, s, a.y, part, a.M, a.N, a.g_ks, a.g_bm, a.g_bn);
         else
@@ -1333,9 +1407,9 @@ hipError_t launch_gemm2_t(const LinearArgs &a, hipStream_t s)
         return hipGetLastError();
     }
     if (a.out_f32)
-        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, EC, 1, WK, FN, WN, KF>), dim3(ka.grid), block, 0, s, ka);
+        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, EC, 1, WK, FN, WN, KF, EPI>), dim3(ka.grid), block, 0, s, ka);
     else
-        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, EC, 0, WK, FN, WN, KF>), dim3(ka.grid), block, 0, s, ka);
+        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, EC, 0, WK, FN, WN, KF, EPI>), dim3(ka.grid), block, 0, s, ka);
     return hipGetLastError();
 }
 
@@ -1433,30 +1507,40 @@ hipError_t launch_prepass(const LinearArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s)
+namespace {
+
+template <int EPI>
+hipError_t launch_gemm_e(const LinearArgs &a, int ec_on, hipStream_t s)
 {
-    (void)force_large;                                    // a.g_bm, a.g_bn, a.g_ks carry the choice
     if (a.g_bm == 64) {
         // Both tile shapes have a variant without the DMA-source clamps for K a
         // multiple of 128 (their per-lane selects cost about 8 % of the 64 x 64
         // loop).
         if (a.K % 128 == 0) {
             if (ec_on == 2)
-                return launch_gemm2_t<2, 2, 2, 2, 2, 2, 1>(a, s);
-            return ec_on ? launch_gemm2_t<2, 2, 1, 2, 2, 2, 1>(a, s) : launch_gemm2_t<2, 2, 0, 2, 2, 2, 1>(a, s);
+                return launch_gemm2_t<EPI, 2, 2, 2, 2, 2, 2, 1>(a, s);
+            return ec_on ? launch_gemm2_t<EPI, 2, 2, 1, 2, 2, 2, 1>(a, s) : launch_gemm2_t<EPI, 2, 2, 0, 2, 2, 2, 1>(a, s);
         }
         if (ec_on == 2)
-            return launch_gemm2_t<2, 2, 2, 2, 2, 2>(a, s);
-        return ec_on ? launch_gemm2_t<2, 2, 1, 2, 2, 2>(a, s) : launch_gemm2_t<2, 2, 0, 2, 2, 2>(a, s);
+            return launch_gemm2_t<EPI, 2, 2, 2, 2, 2, 2>(a, s);
+        return ec_on ? launch_gemm2_t<EPI, 2, 2, 1, 2, 2, 2>(a, s) : launch_gemm2_t<EPI, 2, 2, 0, 2, 2, 2>(a, s);
     }
     if (a.K % 128 == 0) {
         if (ec_on == 2)
-            return launch_gemm2_t<2, 4, 2, 1, 4, 4, 1>(a, s);
-        return ec_on ? launch_gemm2_t<2, 4, 1, 1, 4, 4, 1>(a, s) : launch_gemm2_t<2, 4, 0, 1, 4, 4, 1>(a, s);
+            return launch_gemm2_t<EPI, 2, 4, 2, 1, 4, 4, 1>(a, s);
+        return ec_on ? launch_gemm2_t<EPI, 2, 4, 1, 1, 4, 4, 1>(a, s) : launch_gemm2_t<EPI, 2, 4, 0, 1, 4, 4, 1>(a, s);
     }
     if (ec_on == 2)
-        return launch_gemm2_t<2, 4, 2>(a, s);
-    return ec_on ? launch_gemm2_t<2, 4, 1>(a, s) : launch_gemm2_t<2, 4, 0>(a, s);
+        return launch_gemm2_t<EPI, 2, 4, 2>(a, s);
+    return ec_on ? launch_gemm2_t<EPI, 2, 4, 1>(a, s) : launch_gemm2_t<EPI, 2, 4, 0>(a, s);
+}
+
+} // namespace
+
+hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s)
+{
+    (void)force_large;                                    // a.g_bm, a.g_bn, a.g_ks carry the choice
+    return a.E.on ? launch_gemm_e<1>(a, ec_on, s) : launch_gemm_e<0>(a, ec_on, s);
 }
 
 } // namespace spear

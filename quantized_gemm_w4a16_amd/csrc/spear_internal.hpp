@@ -150,6 +150,16 @@ struct DecOffsets {
     uint32_t hdr, epoch, splitp, pu, pz, vhi, vlo, active;
 };
 
+// The epilogue after the layer (spear_w4_linear_epilogue): one 32-byte block.
+struct EpiArgs {
+    const float *bias;      // [N] or null
+    const void *res;        // [M][N or N / 2] of the output's type, or null
+    int32_t act;            // SPEAR_ACT_*
+    int32_t glu;            // 1: channels 2i and 2i + 1 make output channel i
+    int32_t on;             // host side: the call has an epilogue
+    int32_t pad;
+};
+
 struct LinearArgs {
     // The leading block (212 bytes, four 64-byte lines) is what the decode
     // kernels load at entry.  Each further 64-byte line of arguments a kernel
@@ -193,10 +203,14 @@ struct LinearArgs {
     } P;
     // Host side only.
     WsLayout L;
+    // The kernels with an epilogue load this block too (one further line).
+    EpiArgs E;
 };
 static_assert(offsetof(LinearArgs, gw1) == 216 && offsetof(LinearArgs, D) == 180 &&
                   offsetof(LinearArgs, grid) == 212 && offsetof(LinearArgs, L) == 360,
               "the decode kernels' leading block");
+static_assert(offsetof(LinearArgs, E) / 64 == (offsetof(LinearArgs, E) + sizeof(EpiArgs) - 1) / 64,
+              "the epilogue's block in one line");
 
 // Explicit counter waits (gfx9 s_waitcnt encoding: vmcnt bits 3:0 and 15:14,
 // expcnt 6:4, lgkmcnt 11:8) and a barrier without the fence of
@@ -251,6 +265,144 @@ __device__ __forceinline__ void pin_pre_args(const LinearArgs &a)
     pin_arg(a.P.active); pin_arg(a.P.preu); pin_arg(a.P.prez); pin_arg(a.P.gpart); pin_arg(a.P.idx);
 }
 
+// The epilogue's arguments.
+__device__ __forceinline__ void pin_epi_args(const LinearArgs &a)
+{
+    pin_arg(a.E.bias); pin_arg(a.E.res); pin_arg(a.E.act); pin_arg(a.E.glu);
+}
+
+// ------------------------------------------------------------------ epilogue
+// act(t), the activation a whole launch shares (uniform branch).  expf, tanhf
+// and erff in fp32: the activation of a value near zero keeps its relative
+// accuracy (x is multiplied on, never subtracted).  silu of a large negative t
+// is t / inf = -0, as is the limit; gelu_tanh is written as t sigmoid(2 q),
+// q = sqrt(2 / pi) (t + 0.044715 t^3), which equals t / 2 (1 + tanh q) without
+// the cancellation of 1 + tanh at negative t.
+__device__ __forceinline__ float apply_act(float t, int act)
+{
+    switch (act) {
+    case SPEAR_ACT_RELU:
+        return t > 0.f ? t : (t != t ? t : 0.f);
+    case SPEAR_ACT_SILU:
+        return t == -__builtin_inff() ? 0.f : t / (1.f + expf(-t));
+    case SPEAR_ACT_GELU:
+        return t == -__builtin_inff() ? 0.f : 0.5f * t * erfcf(-0.70710678118654752f * t);
+    case SPEAR_ACT_GELU_TANH: {
+        const float q = 1.5957691216057308f * __builtin_fmaf(0.044715f * t * t, t, t);
+        return t == -__builtin_inff() ? 0.f : t / (1.f + expf(-q));
+    }
+    default:
+        return t;
+    }
+}
+
+// Four consecutive channels of one token, before and after the epilogue: t
+// holds the layer's outputs n .. n + 3, b their biases (zero without).  With
+// the gated pair o[0] and o[1] are output channels n / 2 and n / 2 + 1.
+__device__ __forceinline__ void epi_apply(const float (&t)[4], const float (&b)[4], int act, int glu,
+                                          float (&o)[4])
+{
+    if (glu) {
+        o[0] = apply_act(t[0] + b[0], act) * (t[1] + b[1]);
+        o[1] = apply_act(t[2] + b[2], act) * (t[3] + b[3]);
+        o[2] = o[3] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            o[i] = apply_act(t[i] + b[i], act);
+    }
+}
+
+// Biases of channels n .. n + 3 (clamped to N - 1), raw; read without a branch
+// from the scales when there is no bias, and then replaced by epi_bias.
+__device__ __forceinline__ void epi_load_bias(const float *bias, const float *scales, int64_t n, int64_t N,
+                                              float (&raw)[4])
+{
+    const float *p = bias ? bias : scales;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        raw[i] = p[n + i < N ? n + i : N - 1];
+}
+
+// Residual of the outputs of channels n .. n + 3 of token m, as fp32 (zero
+// where there is none or the channel is past the end).  NO = output channels.
+template <int OUT_F32>
+__device__ __forceinline__ void epi_load_res(const void *res, int64_t m, int64_t n, int glu, int64_t NO,
+                                             float (&r)[4])
+{
+    const int cnt = glu ? 2 : 4;
+    const int64_t no = glu ? n >> 1 : n;
+    r[0] = r[1] = r[2] = r[3] = 0.f;
+    if (!res || no >= NO)
+        return;
+    if (no + cnt <= NO && NO % cnt == 0) {               // a whole, aligned vector
+        if (OUT_F32) {
+            const float *p = reinterpret_cast<const float *>(res) + m * NO + no;
+            if (cnt == 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+                r[0] = v[0];
+                r[1] = v[1];
+                r[2] = v[2];
+                r[3] = v[3];
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(p);
+                r[0] = v.x;
+                r[1] = v.y;
+            }
+        } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(res) + m * NO + no;
+            uint2 v = make_uint2(0u, 0u);
+            if (cnt == 4)
+                v = *reinterpret_cast<const uint2 *>(p);
+            else
+                v.x = *reinterpret_cast<const uint32_t *>(p);
+            r[0] = __uint_as_float(v.x << 16);
+            r[1] = __uint_as_float(v.x & 0xFFFF0000u);
+            r[2] = __uint_as_float(v.y << 16);
+            r[3] = __uint_as_float(v.y & 0xFFFF0000u);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        if (i < cnt && no + i < NO)
+            r[i] = OUT_F32 ? reinterpret_cast<const float *>(res)[m * NO + no + i]
+                           : bf16f(reinterpret_cast<const uint16_t *>(res)[m * NO + no + i]);
+}
+
+// Store the outputs of channels n .. n + 3 of token m.
+template <int OUT_F32>
+__device__ __forceinline__ void epi_store(void *yv, int64_t m, int64_t n, int glu, int64_t NO,
+                                          const float (&o)[4])
+{
+    const int cnt = glu ? 2 : 4;
+    const int64_t no = glu ? n >> 1 : n;
+    const bool vec = no + cnt <= NO && NO % cnt == 0;    // a whole, aligned vector
+    if (OUT_F32) {
+        float *y = reinterpret_cast<float *>(yv) + m * NO + no;
+        if (vec && cnt == 4)
+            *reinterpret_cast<f32x4 *>(y) = f32x4{o[0], o[1], o[2], o[3]};
+        else if (vec)
+            *reinterpret_cast<float2 *>(y) = make_float2(o[0], o[1]);
+        else
+            for (int i = 0; i < cnt; i++)
+                if (no + i < NO)
+                    y[i] = o[i];
+    } else {
+        uint16_t *y = reinterpret_cast<uint16_t *>(yv) + m * NO + no;
+        const uint32_t w0 = (uint32_t)f2bf(o[0]) | ((uint32_t)f2bf(o[1]) << 16);
+        const uint32_t w1 = (uint32_t)f2bf(o[2]) | ((uint32_t)f2bf(o[3]) << 16);
+        if (vec && cnt == 4)
+            *reinterpret_cast<uint2 *>(y) = make_uint2(w0, w1);
+        else if (vec)
+            *reinterpret_cast<uint32_t *>(y) = w0;
+        else
+            for (int i = 0; i < cnt; i++)
+                if (no + i < NO)
+                    y[i] = f2bf(o[i]);
+    }
+}
+
 // ---------------------------------------------- tagged cross-workgroup exchange
 // One atomic add per workgroup.  Block b claims on counter b % EPOCH_CTRS and
 // a launch adds exactly 2^32 to every counter: the first block of each class
@@ -299,6 +451,9 @@ __device__ __forceinline__ uint64_t load_tagged(const uint64_t *p)
 }
 
 
+// Host: SPEAR_OK on a gfx950 device, cached per device (api.hip).
+spear_status check_device();
+
 hipError_t launch_pack(const void *codes, int32_t kind, int64_t N, int64_t K, uint8_t *packed,
                        int32_t *bad, hipStream_t s);
 hipError_t launch_gate(const uint16_t *x, int64_t M, int64_t K, const uint16_t *wg, float b,
@@ -309,6 +464,7 @@ hipError_t launch_compact(const int32_t *flags, int64_t M, int32_t *idx, int32_t
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
 hipError_t launch_stream_read(const void *p, size_t bytes, uint32_t *sink, hipStream_t s);
 hipError_t launch_decode(const LinearArgs &a, int ec_mode, hipStream_t s);
+hipError_t launch_decode_epi(const LinearArgs &a, int ec_mode, hipStream_t s);
 hipError_t launch_prepass(const LinearArgs &a, hipStream_t s);
 hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s);
 hipError_t launch_ec_apply(const LinearArgs &a, hipStream_t s);

@@ -30,10 +30,24 @@ PATH_PREFILL_LARGE = 4
 MAX_RANK = 256
 MAX_GATE_HIDDEN = 64
 ABI_VERSION = 2
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU = 3
+ACT_GELU_TANH = 4
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+MAX_EXPERTS = 512
+MAX_TOPK = 32
+MAX_GROUPS = 64
+E_SHAPE = -2
+E_ARG = -4
 
 EXPORTS = ("spear_pack_w4", "spear_gate", "spear_w4_linear_workspace_size",
            "spear_workspace_init", "spear_w4_linear", "spear_w4_linear_path",
-           "spear_w4_linear_noalloc", "spear_w4_linear_semifused",
+           "spear_w4_linear_noalloc", "spear_w4_linear_semifused", "spear_w4_linear_epilogue",
+           "spear_route_workspace_size", "spear_route", "spear_w4_experts_workspace_size",
+           "spear_w4_experts",
            "spear_set_wait_limit", "spear_workspace_timeouts", "spear_stream_read",
            "spear_slo_predict", "spear_slo_pick_chunk", "spear_status_string",
            "spear_abi_version")
@@ -58,6 +72,27 @@ class _EC(ctypes.Structure):
                 ("alpha", ctypes.c_float), ("gate_w1", ctypes.c_void_p),
                 ("gate_c1", ctypes.c_void_p), ("gate_w2", ctypes.c_void_p),
                 ("gate_c2", ctypes.c_void_p)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("act", ctypes.c_int32),
+                ("glu", ctypes.c_int32)]
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("E", ctypes.c_int32),
+                ("topk", ctypes.c_int32), ("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _Experts(ctypes.Structure):
+    _fields_ = [("up", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+                ("up_zeros", ctypes.c_void_p), ("up_bias", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
+                ("down_zeros", ctypes.c_void_p), ("down_bias", ctypes.c_void_p),
+                ("K", ctypes.c_int64), ("I", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("E", ctypes.c_int32), ("act", ctypes.c_int32), ("glu", ctypes.c_int32)]
 
 
 class _LUT(ctypes.Structure):
@@ -91,6 +126,16 @@ def load():
                                             i32, i32, P]
     lib.spear_w4_linear_semifused.argtypes = [P, i64, ctypes.POINTER(_W4), ctypes.POINTER(_EC), P,
                                               P, ctypes.c_size_t, P, P, P, P]
+    lib.spear_w4_linear_epilogue.argtypes = [P, i64, ctypes.POINTER(_W4), ctypes.POINTER(_EC),
+                                             ctypes.POINTER(_Epilogue), P, i32, P,
+                                             ctypes.c_size_t, i32, P]
+    lib.spear_route_workspace_size.argtypes = [i64, i32]
+    lib.spear_route_workspace_size.restype = ctypes.c_size_t
+    lib.spear_route.argtypes = [P, i64, i64, ctypes.POINTER(_Router), P, P, P, ctypes.c_size_t, P]
+    lib.spear_w4_experts_workspace_size.argtypes = [i64, i32, i32, i64, i64]
+    lib.spear_w4_experts_workspace_size.restype = ctypes.c_size_t
+    lib.spear_w4_experts.argtypes = [P, i64, ctypes.POINTER(_Experts), P, P, i32, P, P, P,
+                                     ctypes.c_size_t, P]
     lib.spear_set_wait_limit.argtypes = [ctypes.c_uint32]
     lib.spear_set_wait_limit.restype = None
     lib.spear_workspace_timeouts.argtypes = [P, ctypes.POINTER(i32), P]
@@ -103,6 +148,7 @@ def load():
     lib.spear_abi_version.restype = i32
     for name in ("spear_pack_w4", "spear_gate", "spear_workspace_init", "spear_w4_linear",
                  "spear_w4_linear_path", "spear_w4_linear_noalloc", "spear_w4_linear_semifused",
+                 "spear_w4_linear_epilogue", "spear_route", "spear_w4_experts",
                  "spear_workspace_timeouts",
                  "spear_stream_read", "spear_slo_predict", "spear_slo_pick_chunk"):
         getattr(lib, name).restype = i32
@@ -295,6 +341,234 @@ def spear_w4_linear_noalloc(x: torch.Tensor, w: W4, ec: Optional[EC] = None,
                                         ctypes.byref(ecc) if ecc is not None else None,
                                         _ptr(y), out_dtype, path, _stream(stream))
     _check("spear_w4_linear_noalloc", st)
+    return y
+
+
+def _bad(fn: str, status: int, what: str):
+    raise SpearError(fn, status, what)
+
+
+def _want(fn: str, name: str, t, dtypes, shape, device):
+    """A tensor argument: its element type, shape, device, and no gaps between
+    its elements (the library takes bare pointers and cannot see any of it)."""
+    if t.dtype not in dtypes:
+        _bad(fn, E_ARG, f"{name} has type {t.dtype}")
+    if tuple(t.shape) != shape:
+        _bad(fn, E_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        _bad(fn, E_ARG, f"{name} is not contiguous")
+    if t.device != device:
+        _bad(fn, E_ARG, f"{name} is on {t.device}, not {device}")
+
+
+def _want_workspace(fn: str, t, device):
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device:
+        _bad(fn, E_ARG, f"workspace has to be a contiguous uint8 tensor on {device}")
+
+
+_BF16 = (torch.bfloat16, torch.int16)     # raw bit tensors are taken too
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+
+
+class _On:
+    """The device and stream of one call: the arguments' device is current, and
+    what the call allocates belongs to its stream.  With the device current and
+    no stream given there is nothing to switch."""
+
+    def __init__(self, fn: str, device, stream):
+        if device.type != "cuda":
+            _bad(fn, E_ARG, f"tensors are on {device}, not on a GPU")
+        self.contexts = []
+        if device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                # the null stream has no external handle
+                stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                          else torch.cuda.default_stream(device))
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+@dataclass
+class Epilogue:
+    """What follows the layer: bias [N] fp32, act (ACT_*), glu (channels 2i and
+    2i + 1 of the weights are gate and up of output channel i), residual [M][N]
+    ([M][N/2] with glu) of the output's type, added last; it may be y itself."""
+    bias: Optional[torch.Tensor] = None
+    act: int = ACT_NONE
+    glu: bool = False
+    residual: Optional[torch.Tensor] = None
+
+    def _c(self):
+        return _Epilogue(_ptr(self.bias), _ptr(self.residual), int(self.act), int(self.glu))
+
+
+def spear_w4_linear_epilogue(x: torch.Tensor, w: W4, ep: Epilogue, ec: Optional[EC] = None,
+                             y: Optional[torch.Tensor] = None, out_dtype: int = OUT_F32,
+                             workspace: Optional[torch.Tensor] = None, path: int = PATH_AUTO,
+                             stream=None) -> torch.Tensor:
+    """The layer with bias, activation (plain or gated pair) and residual in
+    its kernels' epilogue: y [M][N], or [M][N/2] with ep.glu."""
+    fn = "spear_w4_linear_epilogue"
+    dev = x.device
+    M, NO = int(x.shape[0]), w.N // 2 if ep.glu else w.N
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    _want(fn, "x", x, _BF16, (M, w.K), dev)
+    if ep.bias is not None:
+        _want(fn, "bias", ep.bias, _F32, (w.N,), dev)
+    if ep.residual is not None:
+        _want(fn, "residual", ep.residual, (dt,), (M, NO), dev)
+    if y is not None:
+        _want(fn, "y", y, (dt,), (M, NO), dev)
+    if workspace is not None:
+        _want_workspace(fn, workspace, dev)
+    with _On(fn, dev, stream) as s:
+        if y is None:
+            y = torch.empty((M, NO), dtype=dt, device=dev)
+        if workspace is None:
+            workspace = new_workspace(M, w.N, w.K, ec.r if ec is not None else 0, dev)
+        wc, epc = w._c(), ep._c()
+        ecc = ec._c() if ec is not None else None
+        st = load().spear_w4_linear_epilogue(_ptr(x), M, ctypes.byref(wc),
+                                             ctypes.byref(ecc) if ecc is not None else None,
+                                             ctypes.byref(epc), _ptr(y), out_dtype,
+                                             _ptr(workspace), workspace.numel(), path, s)
+    _check(fn, st)
+    return y
+
+
+class Router:
+    """Router of a mixture of experts: w [E][K] bf16, bias [E] fp32 (for the
+    choice alone) or None; topk experts a token out of the topk_group best of
+    n_group groups (a group counts the sum of its group_best best choices).
+    Made once with the model; the tensors are kept, their contents may change."""
+
+    def __init__(self, w: torch.Tensor, topk: int, score: int = SCORE_SOFTMAX,
+                 bias: Optional[torch.Tensor] = None, n_group: int = 1, topk_group: int = 1,
+                 group_best: int = 2, renorm: bool = True, scale: float = 1.0):
+        E, K = (int(v) for v in w.shape)
+        _want("Router", "w", w, _BF16, (E, K), w.device)
+        if bias is not None:
+            _want("Router", "bias", bias, _F32, (E,), w.device)
+        self.w, self.bias, self.E, self.K, self.topk = w, bias, E, K, int(topk)
+        self._s = _Router(_ptr(w), _ptr(bias), E, int(topk), int(score), int(n_group),
+                          int(topk_group), int(group_best), int(bool(renorm)), float(scale))
+
+
+def spear_route_workspace_size(M: int, E: int) -> int:
+    return int(load().spear_route_workspace_size(M, E))
+
+
+def new_route_workspace(M: int, router: Router) -> torch.Tensor:
+    """A workspace for spear_route over up to M tokens (torch allocation)."""
+    return torch.empty(max(spear_route_workspace_size(M, router.E), 256), dtype=torch.uint8,
+                       device=router.w.device)
+
+
+def spear_route(x: torch.Tensor, router: Router, weights: Optional[torch.Tensor] = None,
+                ids: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None):
+    """-> (weights [M][topk] fp32, ids [M][topk] int32, best first, -1 where no
+    expert is left)."""
+    fn = "spear_route"
+    dev = x.device
+    M, shape = int(x.shape[0]), (int(x.shape[0]), router.topk)
+    _want(fn, "x", x, _BF16, (M, router.K), router.w.device)
+    if weights is not None:
+        _want(fn, "weights", weights, _F32, shape, dev)
+    if ids is not None:
+        _want(fn, "ids", ids, _I32, shape, dev)
+    if workspace is not None:
+        _want_workspace(fn, workspace, dev)
+    with _On(fn, dev, stream) as s:
+        if weights is None:
+            weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        if ids is None:
+            ids = torch.empty(shape, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = new_route_workspace(M, router)
+        st = load().spear_route(_ptr(x), M, router.K, ctypes.byref(router._s), _ptr(weights),
+                                _ptr(ids), _ptr(workspace), workspace.numel(), s)
+    _check(fn, st)
+    return weights, ids
+
+
+class Experts:
+    """The experts' two 4-bit layers, the expert index outermost: up [E][NU][K/2]
+    packed codes with scales and zeros [E][NU], down [E][N][I/2] with [E][N]
+    (zeros None: zero point 8), optional fp32 biases of the same shapes; NU = 2 I
+    with glu (rows 2i and 2i + 1 are gate and up of inner channel i), else I.
+    Made once with the model; the tensors are kept, their contents may change."""
+
+    def __init__(self, up, up_scales, up_zeros, down, down_scales, down_zeros, up_bias=None,
+                 down_bias=None, act: int = ACT_SILU, glu: bool = True):
+        fn = "Experts"
+        E, NU, K = int(up.shape[0]), int(up.shape[1]), 2 * int(up.shape[2])
+        N, I = int(down.shape[1]), 2 * int(down.shape[2])
+        dev = up.device
+        if NU != (2 * I if glu else I):
+            _bad(fn, E_SHAPE, f"up has {NU} rows for {I} inner channels (glu={bool(glu)})")
+        _want(fn, "up", up, _U8, (E, NU, K // 2), dev)
+        _want(fn, "down", down, _U8, (E, N, I // 2), dev)
+        for name, t, dt, n in (("up_scales", up_scales, _F32, NU), ("up_zeros", up_zeros, _U8, NU),
+                               ("up_bias", up_bias, _F32, NU),
+                               ("down_scales", down_scales, _F32, N),
+                               ("down_zeros", down_zeros, _U8, N),
+                               ("down_bias", down_bias, _F32, N)):
+            if t is not None:
+                _want(fn, name, t, dt, (E, n), dev)
+        self.tensors = (up, up_scales, up_zeros, up_bias, down, down_scales, down_zeros, down_bias)
+        self.E, self.K, self.I, self.N, self.device = E, K, I, N, dev
+        self._s = _Experts(*(_ptr(t) for t in self.tensors), K, I, N, E, int(act), int(bool(glu)))
+
+
+def spear_w4_experts_workspace_size(M: int, topk: int, E: int, I: int, N: int) -> int:
+    return int(load().spear_w4_experts_workspace_size(M, topk, E, I, N))
+
+
+def new_experts_workspace(M: int, topk: int, experts: Experts) -> torch.Tensor:
+    """A workspace for spear_w4_experts over up to M tokens (torch allocation)."""
+    n = spear_w4_experts_workspace_size(M, topk, experts.E, experts.I, experts.N)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=experts.device)
+
+
+def spear_w4_experts(x: torch.Tensor, experts: Experts, ids: torch.Tensor, weights: torch.Tensor,
+                     residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [M][N] bf16 = residual + the sum over a token's slots of weight times
+    expert; ids outside [0, E) add nothing."""
+    fn = "spear_w4_experts"
+    dev = x.device
+    M, topk, N = int(x.shape[0]), int(ids.shape[1]), experts.N
+    _want(fn, "x", x, _BF16, (M, experts.K), experts.device)
+    _want(fn, "ids", ids, _I32, (M, topk), dev)
+    _want(fn, "weights", weights, _F32, (M, topk), dev)
+    if residual is not None:
+        _want(fn, "residual", residual, _BF16, (M, N), dev)
+    if y is not None:
+        _want(fn, "y", y, _BF16, (M, N), dev)
+    if workspace is not None:
+        _want_workspace(fn, workspace, dev)
+    with _On(fn, dev, stream) as s:
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = new_experts_workspace(M, topk, experts)
+        st = load().spear_w4_experts(_ptr(x), M, ctypes.byref(experts._s), _ptr(ids),
+                                     _ptr(weights), topk, _ptr(residual), _ptr(y),
+                                     _ptr(workspace), workspace.numel(), s)
+    _check(fn, st)
     return y
 
 
