@@ -11,32 +11,44 @@
 //  4. join: each token's rows times their weights, in slot order, plus residual.
 // No launch waits on another workgroup, and no result depends on an order that
 // the hardware chooses: the sums of an output are taken in one fixed order.
+#include <string.h>
+
 #include "spear_internal.hpp"
 
 namespace spear {
 
 namespace {
 
-constexpr int XT = 16;                                    // rows of a tile
+constexpr int XT = 16;                                    // rows of the smallest tile
 
 struct ExpertsLayout {
-    size_t hdr, tiles, list, h, d, total;
-    int64_t slots, max_tiles;
+    size_t hdr, zeros, tiles, list, h, d, total;
+    int64_t slots;
 };
 
-// Row tiles: every expert in use has its slots cut into tiles of XT, the last
-// one ragged, so at most slots / XT + (experts in use) of them.
+// Row tiles of bm rows: every expert in use has its slots cut into tiles, the
+// last one ragged, so at most slots / bm + (experts in use) of them.
+int64_t max_tiles(int64_t slots, int32_t E, int bm) { return slots / bm + (slots < E ? slots : E); }
+
+// Rows of a tile by the slots an expert has on average.
+int tile_rows(int64_t slots, int32_t E)
+{
+    const int64_t per = slots / E;
+    return per >= 48 ? 128 : per >= 12 ? 64 : XT;
+}
+
 ExpertsLayout experts_layout(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N)
 {
     ExpertsLayout L;
     auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
     L.slots = (M < 1 ? 1 : M) * topk;
-    L.max_tiles = L.slots / XT + (L.slots < E ? L.slots : E);
     size_t off = 0;
     L.hdr = off;
     off = up(off + 64);
+    L.zeros = off;                                        // 256 zero bytes, written by the plan
+    off = up(off + 256);
     L.tiles = off;
-    off = up(off + (size_t)L.max_tiles * 16);
+    off = up(off + (size_t)max_tiles(L.slots, E, XT) * sizeof(Tile));
     L.list = off;
     off = up(off + (size_t)L.slots * 4);
     L.h = off;
@@ -47,16 +59,12 @@ ExpertsLayout experts_layout(int64_t M, int32_t topk, int32_t E, int64_t I, int6
     return L;
 }
 
-// A row tile: rows list[pos .. pos + cnt) of expert e.
-struct Tile {
-    int32_t e, pos, cnt, pad;
-};
-
 // ---------------------------------------------------------------------- plan
 // One workgroup an expert.  Every workgroup counts all slots (LDS counters; a
 // count does not depend on the order of its additions), so it knows where its
 // own rows and tiles begin, then writes its slots in ascending order by ballot.
 __global__ __launch_bounds__(1024) void plan_kernel(const int32_t *__restrict__ ids, int32_t slots, int32_t E,
+                                                    int32_t bm, uint32_t *__restrict__ zeros,
                                                     int32_t *__restrict__ ntiles, Tile *__restrict__ tiles,
                                                     int32_t *__restrict__ list)
 {
@@ -77,7 +85,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t *__restrict__ 
     if (wave == 0) {
         int pos = 0, tile = 0, all = 0;
         for (int i = lane; i < E; i += 64) {
-            const int t = (cnt[i] + XT - 1) / XT;
+            const int t = (cnt[i] + bm - 1) / bm;
             all += t;
             if (i < e) {
                 pos += cnt[i];
@@ -99,12 +107,14 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t *__restrict__ 
     __syncthreads();
     if (e == 0 && tid == 0)
         *ntiles = s_all;
+    if (e == 0 && tid < 64)
+        zeros[tid] = 0u;                                  // what the products read past K
     const int mine = cnt[e], pos0 = s_pos, tile0 = s_tile;
-    for (int t = tid; t * XT < mine; t += 1024) {
+    for (int t = tid; t * bm < mine; t += 1024) {
         Tile q;
         q.e = e;
-        q.pos = pos0 + t * XT;
-        q.cnt = mine - t * XT < XT ? mine - t * XT : XT;
+        q.pos = pos0 + t * bm;
+        q.cnt = mine - t * bm < bm ? mine - t * bm : bm;
         q.pad = 0;
         tiles[tile0 + t] = q;
     }
@@ -145,6 +155,7 @@ struct GroupArgs {
     int64_t N, K;
     int32_t div;              // a row's source is slot / div (topk for up, 1 for down)
     int32_t act, glu;
+    int32_t ncb;              // channel blocks of 64: the grid's fastest index
 };
 
 // One wave takes 16 channels of a row tile over all of K.  Lane (c, g) holds
@@ -154,13 +165,14 @@ struct GroupArgs {
 template <int UP>
 __global__ __launch_bounds__(256) void group_kernel(const GroupArgs a)
 {
-    if ((int)blockIdx.y >= *a.ntiles)
+    const int tile = (int)(blockIdx.x / (uint32_t)a.ncb), cb = (int)(blockIdx.x % (uint32_t)a.ncb);
+    if (tile >= *a.ntiles)
         return;
-    const Tile q = a.tiles[blockIdx.y];
+    const Tile q = a.tiles[tile];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane & 15, lg = lane >> 4;
     const int64_t N = a.N, K = a.K;
-    const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
+    const int64_t n0 = ((int64_t)cb * 4 + wave) * 16;
     if (n0 >= N)
         return;
     const int64_t nc = n0 + lr < N ? n0 + lr : N - 1;
@@ -280,9 +292,11 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     const ExpertsLayout L = experts_layout(M, topk, w->E, I, N);
     if (ws_bytes < L.total)
         return SPEAR_E_WORKSPACE;
-    const int64_t NU = w->glu ? 2 * I : I;
-    // grids: row tiles travel in y (at most 65535), join quads in x
-    if (L.max_tiles > 65535 || (M * ((N + 3) / 4) + 255) / 256 > 0x7FFFFFFF)
+    const int64_t NU = w->glu ? 2 * I : I, wide = NU > N ? NU : N;
+    const int bm = tile_rows(L.slots, w->E);
+    const int64_t nt = max_tiles(L.slots, w->E, bm);
+    // grids: row tiles times channel tiles of at least 64, and join quads
+    if (nt > 0x7FFFFFFF / ((wide + 63) / 64) || (M * ((N + 3) / 4) + 255) / 256 > 0x7FFFFFFF)
         return SPEAR_E_SHAPE;
     const spear_status st = check_device();
     if (st != SPEAR_OK || M == 0)
@@ -292,20 +306,58 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     int32_t *ntiles = reinterpret_cast<int32_t *>(ws + L.hdr);
     Tile *tiles = reinterpret_cast<Tile *>(ws + L.tiles);
     int32_t *list = reinterpret_cast<int32_t *>(ws + L.list);
-    hipLaunchKernelGGL(plan_kernel, dim3((unsigned)w->E), dim3(1024), 0, s, ids, (int32_t)L.slots, w->E, ntiles,
-                       tiles, list);
+    hipLaunchKernelGGL(plan_kernel, dim3((unsigned)w->E), dim3(1024), 0, s, ids, (int32_t)L.slots, w->E, bm,
+                       reinterpret_cast<uint32_t *>(ws + L.zeros), ntiles, tiles, list);
     if (hipGetLastError() != hipSuccess)
         return SPEAR_E_HIP;
-    GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, ntiles, tiles, list,
-                   NU, K, topk, w->act, w->glu};
-    hipLaunchKernelGGL(group_kernel<1>, dim3((unsigned)((NU + 63) / 64), (unsigned)L.max_tiles), dim3(256), 0, s, u);
-    if (hipGetLastError() != hipSuccess)
-        return SPEAR_E_HIP;
-    GroupArgs d = {reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
-                   w->down_bias, ws + L.d, ntiles, tiles, list, N, I, 1, SPEAR_ACT_NONE, 0};
-    hipLaunchKernelGGL(group_kernel<0>, dim3((unsigned)((N + 63) / 64), (unsigned)L.max_tiles), dim3(256), 0, s, d);
-    if (hipGetLastError() != hipSuccess)
-        return SPEAR_E_HIP;
+    if (bm == XT) {
+        GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, ntiles, tiles, list,
+                       NU, K, topk, w->act, w->glu, (int32_t)((NU + 63) / 64)};
+        hipLaunchKernelGGL(group_kernel<1>, dim3((unsigned)(nt * u.ncb)), dim3(256), 0, s, u);
+        if (hipGetLastError() != hipSuccess)
+            return SPEAR_E_HIP;
+        GroupArgs d = {reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
+                       w->down_bias, ws + L.d, ntiles, tiles, list, N, I, 1, SPEAR_ACT_NONE, 0,
+                       (int32_t)((N + 63) / 64)};
+        hipLaunchKernelGGL(group_kernel<0>, dim3((unsigned)(nt * d.ncb)), dim3(256), 0, s, d);
+        if (hipGetLastError() != hipSuccess)
+            return SPEAR_E_HIP;
+    } else {
+        LinearArgs a;
+        memset(&a, 0, sizeof a);
+        a.ws = ws;
+        a.P.zeros = L.zeros;
+        a.G.ntiles = ntiles;
+        a.G.tiles = tiles;
+        a.G.list = list;
+        a.x = x;
+        a.packed = w->up;
+        a.scales = w->up_scales;
+        a.zeros = w->up_zeros;
+        a.E.bias = w->up_bias;
+        a.E.act = w->act;
+        a.E.glu = w->glu;
+        a.y = ws + L.h;
+        a.N = NU;
+        a.K = K;
+        a.G.div = topk;
+        if (launch_gemm_grouped(a, bm, nt, s) != hipSuccess)
+            return SPEAR_E_HIP;
+        a.x = reinterpret_cast<const uint16_t *>(ws + L.h);
+        a.packed = w->down;
+        a.scales = w->down_scales;
+        a.zeros = w->down_zeros;
+        a.E.bias = w->down_bias;
+        a.E.act = SPEAR_ACT_NONE;
+        a.E.glu = 0;
+        a.y = ws + L.d;
+        a.out_f32 = 1;
+        a.N = N;
+        a.K = I;
+        a.G.div = 1;
+        if (launch_gemm_grouped(a, bm, nt, s) != hipSuccess)
+            return SPEAR_E_HIP;
+    }
     JoinArgs j = {reinterpret_cast<const float *>(ws + L.d), ids, weights, residual, y, M, N, topk, w->E};
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((M * ((N + 3) / 4) + 255) / 256)), dim3(256), 0, s, j);
     return hipGetLastError() == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;

@@ -610,10 +610,13 @@ __device__ __forceinline__ void lds_read4(const uint8_t *base, uint32_t a0, uint
 }
 
 template <int G2_WM, int G2_FM, int SPLIT, int EC, int OUT_F32, int G2_WK = 1, int G2_FN = 4, int G2_WN = 4,
-          int G2_KF = 0, int EPI = 0>
+          int G2_KF = 0, int EPI = 0, int GRP = 0>
 __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const LinearArgs a)
 {
     // EPI: bias, activation and residual follow (EpiArgs).
+    // GRP: the rows are those of a.G's row tiles, each through its expert's
+    // weights (a.N rows of them an expert), gathered and stored by slot.
+    static_assert(!GRP || (EPI && !SPLIT && !EC), "grouped: whole K, no EC, with the epilogue");
     // G2_KF: K is a multiple of 128, so no DMA source ever needs clamping (its
     // per-lane selects are left out of the main loop).
     // G2_WK = 2 (64 x 64 tiles): two waves share each (token, channel) pair of
@@ -663,6 +666,8 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     pin_pre_args(a);
     if constexpr (EPI != 0)
         pin_epi_args(a);
+    if constexpr (GRP != 0)
+        pin_grp_args(a);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform: scalar branches
 
@@ -703,8 +708,8 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     }
     const int lr = lane & 15, lg = lane >> 4;
     const int wn = wave % G2_WN, wm = (wave / G2_WN) % G2_WM, wk = wave / (G2_WN * G2_WM);
-    const int64_t M = a.M, N = a.N, K = a.K;
-    const int64_t tiles_n = (N + G2_BN - 1) / G2_BN, tiles_m = (M + G2_BM - 1) / G2_BM;
+    const int64_t N = a.N, K = a.K;
+    const int64_t tiles_n = (N + G2_BN - 1) / G2_BN, tiles_m = GRP ? *a.G.ntiles : (a.M + G2_BM - 1) / G2_BM;
     const int64_t ntiles = tiles_n * tiles_m;
     const int64_t KS = SPLIT ? a.g_ks : 1;
     const int64_t nunits = ntiles * KS;                   // unit = slice * ntiles + tile
@@ -716,8 +721,27 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     const int64_t q8 = nunits / 8, r8 = nunits % 8;
     const int64_t xcd = bid % 8, loc = bid / 8;
     const int64_t unit = xcd * q8 + (xcd < r8 ? xcd : r8) + loc;
+    // Grouped: panels of up to GPM row tiles, the row tiles of a panel fastest,
+    // so that the workgroups an XCD runs at once share weights as well as rows.
+    constexpr int64_t GPM = 4;
+    Tile gt = {0, 0, 0, 0};
+    int64_t gnt = 0;
+    if constexpr (GRP != 0) {
+        if (loc >= q8 + (xcd < r8 ? 1 : 0))
+            return;                                       // room for tiles that this call lacks
+        const int64_t panel = unit / (GPM * tiles_n), in = unit - panel * GPM * tiles_n;
+        const int64_t pm = tiles_m - panel * GPM < GPM ? tiles_m - panel * GPM : GPM;
+        gt = a.G.tiles[panel * GPM + in % pm];
+        gnt = in / pm;
+    }
     const int64_t tile = unit % ntiles, ks = unit / ntiles;
-    const int64_t n0 = (tile % tiles_n) * G2_BN, m0 = (tile / tiles_n) * G2_BM;
+    const int64_t n0 = (GRP ? gnt : tile % tiles_n) * G2_BN, m0 = GRP ? 0 : (tile / tiles_n) * G2_BM;
+    const int64_t M = GRP ? gt.cnt : a.M;                 // rows: of the tile, or all
+    const int64_t eN = GRP ? gt.e * N : 0;                // the expert's first channel
+    const int32_t *const glist = GRP ? a.G.list + gt.pos : nullptr;
+    const uint8_t *const wpk = GRP ? a.packed + eN * (K / 2) : a.packed;
+    const float *const wsc = a.scales + eN;
+    const uint8_t *const wzp = GRP && a.zeros ? a.zeros + eN : a.zeros;
     const int64_t S = (K + 127) / 128;
     const int64_t sb = ks * S / KS, se = (ks + 1) * S / KS;   // this slice's stages
     const uint8_t *zsrc = a.ws + a.P.zeros + 16 * (lane & 15);
@@ -738,7 +762,9 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     for (int j = 0; j < G2_XI; j++) {
         const int r = 4 * (G2_XI * wave + j) + (lane >> 4);
         const int c = (lane & 15) ^ (r & 15);
-        const int64_t mm = m0 + r < M ? m0 + r : M - 1;
+        int64_t mm = m0 + r < M ? m0 + r : M - 1;
+        if constexpr (GRP != 0)
+            mm = glist[mm] / a.G.div;
         xsrc[j] = reinterpret_cast<const uint8_t *>(a.x + mm * K + 8 * c);
         xlim[j] = (K - 8 * c + 127) / 128;                // stages st with 128 st + 8 c < K
     }
@@ -748,7 +774,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
         const int r = (G2_WS == 16 ? 16 : 4) * (G2_WI * wave + j) + (slot >> 2);
         const int c = (slot & 3) ^ ((r >> 1) & 3);
         const int64_t nn = n0 + r < N ? n0 + r : N - 1;
-        wsrc[j] = a.packed + nn * (K / 2) + 16 * c + (G2_WS == 16 ? 0 : 4 * (lane & 3));
+        wsrc[j] = wpk + nn * (K / 2) + 16 * c + (G2_WS == 16 ? 0 : 4 * (lane & 3));
         wlast[j] = (K - 32 * c + 127) / 128 - 1;          // last stage with 128 st + 32 c < K
     }
     auto issue_x = [&](int64_t st, uint8_t *xbase, int j) {
@@ -824,8 +850,8 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
         for (int i = 0; i < 4; i++) {
             int64_t nn = n0 + (wn * G2_FN + fn) * 16 + 4 * lg + i;
             nn = nn < N ? nn : N - 1;
-            sc_raw[fn][i] = a.scales[nn];
-            zb_raw[fn][i] = load_zero_byte(a.zeros, a.scales, nn);
+            sc_raw[fn][i] = wsc[nn];
+            zb_raw[fn][i] = load_zero_byte(wzp, wsc, nn);
         }
 
     f32x4 acc[G2_FN][G2_FM], acc1[G2_FN][G2_FM], rsq[G2_FM];
@@ -1227,15 +1253,17 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
         float bv[G2_FN][4];
 #pragma unroll
         for (int fn = 0; fn < G2_FN; fn++) {
-            epi_load_bias(a.E.bias, a.scales, n0 + (wn * G2_FN + fn) * 16 + 4 * lg, N, bv[fn]);
+            epi_load_bias(a.E.bias ? a.E.bias + eN : nullptr, wsc, n0 + (wn * G2_FN + fn) * 16 + 4 * lg, N, bv[fn]);
             if (!a.E.bias)
                 bv[fn][0] = bv[fn][1] = bv[fn][2] = bv[fn][3] = 0.f;
         }
 #pragma unroll
         for (int fm = 0; fm < G2_FM; fm++) {
-            const int64_t mm = m0 + (wm * G2_FM + fm) * 16 + lr;
+            int64_t mm = m0 + (wm * G2_FM + fm) * 16 + lr;
             if (mm >= M)
                 continue;
+            if constexpr (GRP != 0)
+                mm = glist[mm];
 #pragma unroll
             for (int fn = 0; fn < G2_FN; fn++) {
                 const int64_t nb = n0 + (wn * G2_FN + fn) * 16 + 4 * lg;
@@ -1535,7 +1563,31 @@ hipError_t launch_gemm_e(const LinearArgs &a, int ec_on, hipStream_t s)
     return ec_on ? launch_gemm2_t<EPI, 2, 4, 1>(a, s) : launch_gemm2_t<EPI, 2, 4, 0>(a, s);
 }
 
+template <int WM, int FM, int WK, int FN, int WN, int KF>
+hipError_t launch_grouped_t(const LinearArgs &a, int64_t max_tiles, hipStream_t s)
+{
+    const int64_t bn = 16 * FN * WN;
+    LinearArgs ka = a;
+    ka.grid = (uint32_t)(max_tiles * ((a.N + bn - 1) / bn));
+    if (a.out_f32)
+        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, 0, 1, WK, FN, WN, KF, 1, 1>), dim3(ka.grid),
+                           dim3(64 * WN * WM * WK), 0, s, ka);
+    else
+        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, 0, 0, WK, FN, WN, KF, 1, 1>), dim3(ka.grid),
+                           dim3(64 * WN * WM * WK), 0, s, ka);
+    return hipGetLastError();
+}
+
 } // namespace
+
+hipError_t launch_gemm_grouped(const LinearArgs &a, int bm, int64_t max_tiles, hipStream_t s)
+{
+    if (bm == 64)
+        return a.K % 128 == 0 ? launch_grouped_t<2, 2, 2, 2, 2, 1>(a, max_tiles, s)
+                              : launch_grouped_t<2, 2, 2, 2, 2, 0>(a, max_tiles, s);
+    return a.K % 128 == 0 ? launch_grouped_t<2, 4, 1, 4, 4, 1>(a, max_tiles, s)
+                          : launch_grouped_t<2, 4, 1, 4, 4, 0>(a, max_tiles, s);
+}
 
 hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s)
 {

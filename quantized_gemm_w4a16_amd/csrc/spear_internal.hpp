@@ -160,6 +160,21 @@ struct EpiArgs {
     int32_t pad;
 };
 
+// A row tile of a grouped product: rows list[pos .. pos + cnt) through expert e.
+struct Tile {
+    int32_t e, pos, cnt, pad;
+};
+
+// A grouped product (spear_w4_experts): the weights of every expert one after
+// the other, and the row tiles that a launch before wrote.
+struct GrpArgs {
+    const int32_t *ntiles;  // row tiles in use (the grid has room for the most there can be)
+    const Tile *tiles;
+    const int32_t *list;    // slots by expert
+    int32_t div;            // a row's source is slot / div
+    int32_t pad;
+};
+
 struct LinearArgs {
     // The leading block (212 bytes, four 64-byte lines) is what the decode
     // kernels load at entry.  Each further 64-byte line of arguments a kernel
@@ -205,6 +220,7 @@ struct LinearArgs {
     WsLayout L;
     // The kernels with an epilogue load this block too (one further line).
     EpiArgs E;
+    GrpArgs G;
 };
 static_assert(offsetof(LinearArgs, gw1) == 216 && offsetof(LinearArgs, D) == 180 &&
                   offsetof(LinearArgs, grid) == 212 && offsetof(LinearArgs, L) == 360,
@@ -269,6 +285,11 @@ __device__ __forceinline__ void pin_pre_args(const LinearArgs &a)
 __device__ __forceinline__ void pin_epi_args(const LinearArgs &a)
 {
     pin_arg(a.E.bias); pin_arg(a.E.res); pin_arg(a.E.act); pin_arg(a.E.glu);
+}
+
+__device__ __forceinline__ void pin_grp_args(const LinearArgs &a)
+{
+    pin_arg(a.G.ntiles); pin_arg(a.G.tiles); pin_arg(a.G.list); pin_arg(a.G.div);
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -467,6 +488,8 @@ hipError_t launch_decode(const LinearArgs &a, int ec_mode, hipStream_t s);
 hipError_t launch_decode_epi(const LinearArgs &a, int ec_mode, hipStream_t s);
 hipError_t launch_prepass(const LinearArgs &a, hipStream_t s);
 hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s);
+// Grouped: a.G's row tiles of bm rows (64 or 128), at most max_tiles of them.
+hipError_t launch_gemm_grouped(const LinearArgs &a, int bm, int64_t max_tiles, hipStream_t s);
 hipError_t launch_ec_apply(const LinearArgs &a, hipStream_t s);
 
 } // namespace spear
