@@ -315,12 +315,13 @@ typedef struct spear_router {
  *   ids[m][0..topk): the experts of the kept groups with the largest c, in
  *     descending order; ties (of experts and of groups) go to the lowest index
  *   weights[m][j] = scale * s[ids[m][j]]  (/ sum_j s with renorm)
- * Logits, scores and choices are those of exact products summed and compared
- * in fp64, so the choice does not hang on an fp32 rounding; the weights are
- * rounded once to fp32.  An expert whose c is NaN or -inf (a bias of -inf
- * takes an expert out) is never chosen: a slot left without an expert gets id
- * -1 and weight 0, and takes no part in the sum.  Scores that sum to zero
- * give weights of zero.
+ * The choice is the one of logits summed and scores compared in fp64, so it
+ * does not hang on an fp32 rounding.  The weights may come of logits summed in
+ * fp32: a logit is off by at most (36 + K / 512) 2^-23 |x_m| |w_e| (2-norms),
+ * a weight by twice that relative, then one rounding to fp32.  An expert whose
+ * c is NaN or -inf (a bias of -inf takes an expert out) is never chosen: a
+ * slot left without an expert gets id -1 and weight 0, and takes no part in
+ * the sum.  Scores that sum to zero give weights of zero.
  *   x [M][K] bf16, 16-byte aligned; M >= 0 (0 does nothing); K >= 32, K % 32 == 0.
  *   weights [M][topk] fp32, ids [M][topk] int32 outputs, 4-byte aligned.
  *   workspace device scratch of spear_route_workspace_size bytes, 256-byte
