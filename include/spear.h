@@ -317,7 +317,7 @@ typedef struct spear_router {
  *   weights[m][j] = scale * s[ids[m][j]]  (/ sum_j s with renorm)
  * The choice is the one of logits summed and scores compared in fp64, so it
  * does not hang on an fp32 rounding.  The weights may come of logits summed in
- * fp32: a logit is off by at most (36 + K / 512) 2^-23 |x_m| |w_e| (2-norms),
+ * fp32: a logit is off by at most (58 + K / 256) 2^-23 |x_m| |w_e| (2-norms),
  * a weight by twice that relative, then one rounding to fp32.  An expert whose
  * c is NaN or -inf (a bias of -inf takes an expert out) is never chosen: a
  * slot left without an expert gets id -1 and weight 0, and takes no part in

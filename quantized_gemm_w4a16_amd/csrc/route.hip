@@ -9,9 +9,9 @@
 //  * fused (few tokens): one workgroup a token sums the logits in fp64 (each
 //    bf16 x bf16 product is exact there) and its first wave chooses;
 //  * two launches: the logits by bf16 MFMA in fp32, each with a bound of its
-//    error, then one wave a token chooses.  Where the bounds leave the order of
-//    two candidates open (a few tokens in a hundred), that wave sums the
-//    logits in question again in fp64, so the choice is the same as before.
+//    error, then one wave a token chooses in fp32.  Where the bounds leave the
+//    order of two candidates open (a few tokens in a hundred), that wave sums
+//    the logits in question again in fp64, so the choice is the same as before.
 #include <math.h>
 
 #include "spear_internal.hpp"
@@ -25,30 +25,80 @@ struct RouteArgs {
     const float *bias;
     float *weights;
     int32_t *ids;
-    float *z;                                             // [M][E] logits (two launches)
-    float *xn, *wn;                                       // [M], [E]: 2-norms of the rows of x and w
+    float *z;                                             // [ks][M][E] partial logits (two launches)
+    float *xn;                                            // [ks][M]: partial squares of x's rows
+    float *wn;                                            // [ks][32]: the largest of 16 rows of w each
     int64_t M, K;
     int32_t E, topk, score, n_group, topk_group, group_best, renorm;
     float scale;
-    float zerr;                                           // error of z over xn wn
+    float zerr;                                           // error of a logit over the rows' 2-norms
+    int32_t ks, net;                                      // K slices, expert tiles
 };
 
-// ------------------------------------------------------------- fp64 reductions
+// ---------------------------------------------------------- wave reductions
+// By DPP on the vector ALU: within rows of 16 lanes by shifts of 1, 2, 4 and 8,
+// then the row totals handed on; lane 63 holds the total, read as a scalar.
+// (Through the LDS crossbar, as shuffles go, the 8192-token choice was bound by
+// it: 82 us of which two thirds were shuffles.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t ident)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)ident, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double v, double ident)
+{
+    const uint64_t a = __builtin_bit_cast(uint64_t, v), i = __builtin_bit_cast(uint64_t, ident);
+    const uint64_t r = (uint64_t)dpp<CTRL, ROWS>((uint32_t)a, (uint32_t)i) |
+                       ((uint64_t)dpp<CTRL, ROWS>((uint32_t)(a >> 32), (uint32_t)(i >> 32)) << 32);
+    return __builtin_bit_cast(double, r);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float v, float ident)
+{
+    return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(v), __float_as_uint(ident)));
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l)
+{
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, l);
+}
+__device__ __forceinline__ float lane_of(float v, int l) { return __uint_as_float(lane_of(__float_as_uint(v), l)); }
+__device__ __forceinline__ double lane_of(double v, int l)
+{
+    const uint64_t a = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)lane_of((uint32_t)a, l) |
+                                          ((uint64_t)lane_of((uint32_t)(a >> 32), l) << 32));
+}
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T v, T ident, F op)
+{
+    v = op(v, dpp<0x111, 0xF>(v, ident));                 // row_shr 1, 2, 4, 8
+    v = op(v, dpp<0x112, 0xF>(v, ident));
+    v = op(v, dpp<0x114, 0xF>(v, ident));
+    v = op(v, dpp<0x118, 0xF>(v, ident));
+    v = op(v, dpp<0x142, 0xA>(v, ident));                 // row_bcast 15 into rows 1 and 3
+    v = op(v, dpp<0x143, 0xC>(v, ident));                 // row_bcast 31 into rows 2 and 3
+    return lane_of(v, 63);
+}
 __device__ __forceinline__ double wave_sum(double v)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v += __shfl_xor(v, o);
-    return v;
+    return wave_reduce(v, 0.0, [](double p, double q) { return p + q; });
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    return wave_reduce(v, 0.f, [](float p, float q) { return p + q; });
 }
 __device__ __forceinline__ double wave_max(double v)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const double u = __shfl_xor(v, o);
-        v = u > v ? u : v;
-    }
-    return v;
+    return wave_reduce(v, -(double)INFINITY, [](double p, double q) { return q > p ? q : p; });
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    return wave_reduce(v, -INFINITY, [](float p, float q) { return q > p ? q : p; });
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    return wave_reduce(v, 0u, [](uint32_t p, uint32_t q) { return q > p ? q : p; });
 }
 
 // acc + the products of 8 bf16 of x and w: every product exact, the sum in fp64.
@@ -64,315 +114,154 @@ __device__ __forceinline__ double dot8(u32x4 x, u32x4 w, double acc)
 }
 
 // ---------------------------------------------------------------------- choice
-// One wave, one token; lane l holds experts J l .. J l + J - 1, so that index
-// order is (lane, j) order.  z: logits.  RB: each logit is known to within
-// zd[j] only; where that leaves the choice open the logits in question are
-// summed again in fp64.  A candidate that cannot be chosen is -inf.
-template <int J, int RB>
-struct Choice {
-    const RouteArgs &a;
-    const int64_t m;
-    const int lane;
-    double z[J], s[J], c[J], d[J];                        // logit, score, choice, bound of c's error
-    double mx, sum;                                       // softmax: largest logit, sum of exp(z - mx)
-
-    __device__ __forceinline__ Choice(const RouteArgs &a_, int64_t m_, int lane_) : a(a_), m(m_), lane(lane_) {}
-
-    __device__ __forceinline__ int expert(int j) const { return J * lane + j; }
-    __device__ __forceinline__ bool real(int j) const { return J * lane + j < a.E; }
-
-    // score and choice of candidate j; zd: bound of its logit's error
-    __device__ __forceinline__ void score(int j, double zd)
-    {
-        const double ninf = -INFINITY;
-        if (a.score == SPEAR_SCORE_SOFTMAX) {
-            s[j] = real(j) ? exp(z[j] - mx) / sum : 0.0;
-            d[j] = 2.5 * zd * s[j];                       // both exp(z) and the sum are off by e^zd at most
-        } else {
-            s[j] = 1.0 / (1.0 + exp(-z[j]));
-            d[j] = 0.25 * zd;
-        }
-        const double v = a.bias && real(j) ? s[j] + (double)a.bias[expert(j)] : s[j];
-        c[j] = real(j) && v == v ? v : ninf;
-        if (RB && zd != 0.0)                              // and fp64's own roundings
-            d[j] += 1e-15 + (fabs(v) < 1e300 ? 1e-15 * fabs(v) : 0.0);
-    }
-
-    __device__ __forceinline__ void softmax_sums()
-    {
-        double t = -INFINITY;
-        bool nan = false;
+// Logits of token m and n listed experts in fp64, by one wave: two experts at a
+// time, 2048 depths of loads in flight.
+__device__ __forceinline__ void exact_logits(const RouteArgs &a, int64_t m, int lane, const uint16_t *list, int n,
+                                             double *z)
+{
+    const uint16_t *xr = a.x + m * a.K;
+#pragma unroll 1
+    for (int p = 0; p < n; p += 2) {
+        const int p1 = p + 1 < n ? p + 1 : p;
+        const uint16_t *w0 = a.w + (int64_t)list[p] * a.K, *w1 = a.w + (int64_t)list[p1] * a.K;
+        double s0 = 0.0, s1 = 0.0;
+#pragma unroll 1
+        for (int64_t k0 = 0; k0 < a.K; k0 += 2048) {
+            u32x4 xv[4], v0[4], v1[4];
 #pragma unroll
-        for (int j = 0; j < J; j++)
-            if (real(j)) {
-                t = z[j] > t ? z[j] : t;
-                nan |= z[j] != z[j];
+            for (int q = 0; q < 4; q++) {
+                const int64_t k = k0 + 512 * q + 8 * lane;
+                const bool in = k < a.K;
+                xv[q] = in ? ld16(xr + k) : zero4();
+                v0[q] = in ? ld16(w0 + k) : zero4();
+                v1[q] = in ? ld16(w1 + k) : zero4();
             }
-        mx = __any(nan) ? __builtin_nan("") : wave_max(t);
-        double u = 0.0;
 #pragma unroll
-        for (int j = 0; j < J; j++)
-            u += real(j) ? exp(z[j] - mx) : 0.0;
+            for (int q = 0; q < 4; q++) {
+                s0 = dot8(xv[q], v0[q], s0);
+                s1 = dot8(xv[q], v1[q], s1);
+            }
+        }
+        s0 = wave_sum(s0);
+        s1 = wave_sum(s1);
+        if (lane == 0) {
+            z[p] = s0;
+            z[p1] = s1;
+        }
+    }
+    wait_lgkmcnt0();
+}
+
+// Appends v of the lanes where `in` holds to a list in LDS; returns its length.
+__device__ __forceinline__ int append(uint16_t *list, int n, bool in, int v, int lane)
+{
+    const uint64_t mask = __ballot(in);
+    if (in)
+        list[n + __popcll(mask & ((1ull << lane) - 1ull))] = (uint16_t)v;
+    return n + __popcll(mask);
+}
+
+__device__ __forceinline__ double score_of(const RouteArgs &a, double z, double mx, double sum)
+{
+    return a.score == SPEAR_SCORE_SOFTMAX ? exp(z - mx) / sum : 1.0 / (1.0 + exp(-z));
+}
+
+// The choice: score and bias, -inf where there is none to be made.
+__device__ __forceinline__ double choice_of(const RouteArgs &a, double s, int e)
+{
+    const double v = a.bias ? s + (double)a.bias[e] : s;
+    return v == v ? v : -(double)INFINITY;
+}
+
+// Winner t's weight and id, by lane t.
+__device__ __forceinline__ void write_choice(const RouteArgs &a, int64_t m, int lane, int id, double s)
+{
+    s = id < 0 ? 0.0 : s;
+    if (a.renorm) {
+        const double total = wave_sum(s);
+        s = total == 0.0 ? 0.0 : s / total;
+    }
+    if (lane < a.topk) {
+        a.ids[m * a.topk + lane] = id;
+        a.weights[m * a.topk + lane] = id < 0 ? 0.f : (float)(s * (double)a.scale);
+    }
+}
+
+// The whole choice of token m by one wave, from all its logits z[0..E) in fp64
+// (LDS, as is c[0..E)).  Loops are kept rolled: straight-line code that each
+// wave runs once costs more in instruction fetches than in instructions.
+__device__ __forceinline__ void choose_all(const RouteArgs &a, int64_t m, int lane, const double *z, double *c)
+{
+    const double ninf = -INFINITY;
+    const int E = a.E, G = a.n_group, gs = E / G;
+    double mx = 0.0, sum = 1.0;
+    if (a.score == SPEAR_SCORE_SOFTMAX) {
+        double t = ninf, u = 0.0;
+        bool nan = false;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64) {
+            t = z[e] > t ? z[e] : t;
+            nan |= z[e] != z[e];
+        }
+        mx = __any(nan) ? __builtin_nan("") : wave_max(t);
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            u += exp(z[e] - mx);
         sum = wave_sum(u);
     }
-
-    // The logits of the candidates in `pick` (bit j of each lane) in fp64, two
-    // experts at a time: their loads overlap.
-    __device__ void resum(uint32_t pick)
-    {
-#pragma unroll
-        for (int j = 0; j < J; j++) {
-            uint64_t todo = __ballot((pick >> j) & 1);
-            while (todo) {                                // uniform
-                const int l0 = __builtin_ctzll(todo);
-                todo &= todo - 1;
-                const int l1 = todo ? __builtin_ctzll(todo) : l0;
-                todo &= todo - 1;
-                const uint16_t *w0 = a.w + (int64_t)(J * l0 + j) * a.K, *w1 = a.w + (int64_t)(J * l1 + j) * a.K;
-                double s0 = 0.0, s1 = 0.0;
-                for (int64_t k = 8 * lane; k < a.K; k += 512) {
-                    const u32x4 xv = ld16(a.x + m * a.K + k);
-                    s0 = dot8(xv, ld16(w0 + k), s0);
-                    s1 = dot8(xv, ld16(w1 + k), s1);
-                }
-                s0 = wave_sum(s0);
-                s1 = wave_sum(s1);
-                if (lane == l0)
-                    z[j] = s0;
-                else if (lane == l1)
-                    z[j] = s1;
-            }
-        }
-    }
-
-    // All logits in fp64.
-    __device__ void resum_all()
-    {
-        uint32_t pick = 0;
-#pragma unroll
-        for (int j = 0; j < J; j++)
-            pick |= real(j) ? 1u << j : 0u;
-        resum(pick);
-        if (a.score == SPEAR_SCORE_SOFTMAX)
-            softmax_sums();
-#pragma unroll
-        for (int j = 0; j < J; j++)
-            score(j, 0.0);
-    }
-
-    // The candidates in `pick` in fp64.  Softmax with a bias compares s + bias,
-    // which the sum over all experts shifts: there all of them are summed again.
-    __device__ void settle(uint32_t pick)
-    {
-        if (a.score == SPEAR_SCORE_SOFTMAX && a.bias) {
-            resum_all();
-            return;
-        }
-        resum(pick);
-#pragma unroll
-        for (int j = 0; j < J; j++)
-            if ((pick >> j) & 1)
-                score(j, 0.0);
-    }
-
-    // ---- groups: drop the candidates of the groups that are not kept.  sc:
-    // one choice an expert, and sd: its bound, in LDS, this wave's own.
-    // Returns the kept groups as a bit mask (bit = group).
-    __device__ uint64_t groups(double *sc, double *sd, uint32_t *pick)
-    {
-        const int G = a.n_group, gs = a.E / G;
-        const double ninf = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < J; j++)
-            if (real(j)) {
-                sc[expert(j)] = c[j];
-                if (RB)
-                    sd[expert(j)] = d[j];
-            }
-        wait_lgkmcnt0();
-        double b0 = ninf, b1 = ninf, dm = 0.0, t0 = ninf, t1 = ninf;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64)
+        c[e] = choice_of(a, score_of(a, z[e], mx, sum), e);
+    wait_lgkmcnt0();
+    if (a.topk_group < G) {
+        // lane g: the sum of group g's best one or two choices
+        double b0 = ninf, b1 = ninf;
         if (lane < G)
+#pragma unroll 4
             for (int i = 0; i < gs; i++) {
-                const double v = sc[lane * gs + i];
+                const double v = c[lane * gs + i];
                 b1 = v > b0 ? b0 : (v > b1 ? v : b1);
                 b0 = v > b0 ? v : b0;
-                if (RB) {
-                    const double dv = sd[lane * gs + i], lo = v - dv;
-                    dm = dv > dm ? dv : dm;
-                    t1 = lo > t0 ? t0 : (lo > t1 ? lo : t1);
-                    t0 = lo > t0 ? lo : t0;
-                }
             }
-        const bool two = a.group_best == 2 && gs > 1;
-        double gv = lane < G ? (two ? b0 + b1 : b0) : ninf;
+        double gv = lane < G ? ((a.group_best == 2 && gs > 1) ? b0 + b1 : b0) : ninf;
         gv = gv == gv ? gv : ninf;                        // +inf and -inf biases in one group
         int rank = 0;
+#pragma unroll 1
         for (int g = 0; g < G; g++) {
-            const double o = __shfl(gv, g);
+            const double o = lane_of(gv, g);
             rank += o > gv || (o == gv && g < lane);
         }
-        const bool in = lane < G && rank < a.topk_group;
-        if (RB) {
-            // open: a kept group whose least value does not clear the largest
-            // value of the others, and the other way round
-            const double ge = two ? 2.0 * dm : dm;
-            const double least = wave_max(in ? -(gv - ge) : ninf);          // -(smallest kept)
-            const double most = wave_max(lane < G && !in ? gv + ge : ninf);
-            uint32_t want = 0;
-            if (!(-least > most)) {
-                const bool open = lane < G && (in ? !(gv - ge > most) : !(gv + ge < -least));
-                const uint64_t og = __ballot(open);
-                const double thr = two ? t1 : t0;         // what may be among the group's best
-#pragma unroll
-                for (int j = 0; j < J; j++) {
-                    const int g = real(j) ? expert(j) / gs : 0;
-                    const double tg = __shfl(thr, g);
-                    if (real(j) && ((og >> g) & 1) && d[j] != 0.0 && c[j] > ninf && !(c[j] + d[j] < tg))
-                        want |= 1u << j;
-                }
-            }
-            *pick = want;
-        }
-        return __ballot(in);
+        const uint64_t kept = __ballot(lane < G && rank < a.topk_group);
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            if (!((kept >> (e / gs)) & 1))
+                c[e] = ninf;
     }
-
-    // ---- top-k by rounds.  Winner t goes to lane t.  Returns the chosen
-    // candidates (bit j); the bounds of the choice in *ok (RB).
-    int my_id;
-    double my_s, total;
-    __device__ uint32_t top(bool *ok)
-    {
-        const double ninf = -INFINITY;
-        uint32_t left = 0, chosen = 0;
-#pragma unroll
-        for (int j = 0; j < J; j++)
-            left |= c[j] > ninf ? 1u << j : 0u;
-        my_id = -1;
-        my_s = total = 0.0;
-        double prev = INFINITY;                           // the last winner's choice, less its bound
-        bool good = true;
-        low = INFINITY;
-        for (int t = 0; t < a.topk; t++) {
-            double bv = ninf;
-            int bj = 0;
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                if (((left >> j) & 1) && c[j] > bv) {
-                    bv = c[j];
-                    bj = j;
-                }
-            const double best = wave_max(bv);
-            if (best == ninf)
-                break;                                    // no candidate is left
-            const int wl = __builtin_ctzll(__ballot(bv == best && ((left >> bj) & 1)));
-            double bs = 0.0, bd = 0.0;
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                if (bj == j) {
-                    bs = s[j];
-                    bd = d[j];
-                }
-            const int id = __shfl(J * lane + bj, wl);
-            const double ws = __shfl(bs, wl);
-            if (RB) {
-                const double wd = __shfl(bd, wl);
-                good &= prev > best + wd;
-                prev = best - wd;
-                low = prev < low ? prev : low;
+    // rounds: the best candidate left, the lowest expert of equal ones
+    int id = -1;
+#pragma unroll 1
+    for (int t = 0; t < a.topk; t++) {
+        double bv = ninf;
+        uint32_t be = 0;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            if (c[e] > bv) {
+                bv = c[e];
+                be = (uint32_t)e;
             }
-            if (lane == wl) {
-                left &= ~(1u << bj);
-                chosen |= 1u << bj;
-            }
-            total += ws;
-            if (lane == t) {
-                my_id = id;
-                my_s = ws;
-            }
-        }
-        if (RB) {
-            double u = ninf;
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                if ((left >> j) & 1)
-                    u = c[j] + d[j] > u ? c[j] + d[j] : u;
-            const double rest = wave_max(u);
-            *ok = good && (rest == ninf || rest < prev);
-        }
-        return chosen;
+        const double best = wave_max(bv);
+        if (best == ninf)
+            break;                                        // no candidate is left
+        const uint64_t who = __ballot(bv == best);
+        uint32_t e = lane_of(be, __builtin_ctzll(who));
+        if (who & (who - 1))
+            e = ~wave_max(bv == best ? ~be : 0u);
+        if ((int)(e & 63u) == lane)
+            c[e] = ninf;
+        id = lane == t ? (int)e : id;
     }
-    double low;                                           // top(): the least a winner may be
-
-    __device__ void write() const
-    {
-        if (lane < a.topk) {
-            double w = my_id < 0 ? 0.0 : my_s;
-            if (a.renorm)
-                w = total == 0.0 ? 0.0 : w / total;
-            a.ids[m * a.topk + lane] = my_id;
-            a.weights[m * a.topk + lane] = my_id < 0 ? 0.f : (float)(w * (double)a.scale);
-        }
-    }
-
-    // zd: the largest error of a logit of candidate j
-    __device__ void run(const float (&zd)[J], double *sc, double *sd)
-    {
-        bool all = false;                                 // bounds of no use: sum everything again
-        if (RB) {
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                all |= real(j) && !(zd[j] < 0.05f && z[j] == z[j]);
-            all = __any(all);
-        }
-        if (all) {
-            resum_all();
-        } else {
-            if (a.score == SPEAR_SCORE_SOFTMAX)
-                softmax_sums();
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                score(j, RB ? (double)zd[j] : 0.0);
-        }
-        if (a.topk_group < a.n_group) {
-            uint32_t pick = 0;
-            uint64_t kept = groups(sc, sd, &pick);
-            if (RB && __any(pick != 0)) {
-                settle(pick);
-                kept = groups(sc, sd, &pick);
-            }
-            const int gs = a.E / a.n_group;
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                if (real(j) && !((kept >> (expert(j) / gs)) & 1))
-                    c[j] = -INFINITY;
-        }
-        bool ok = true;
-        const uint32_t chosen = top(&ok);
-        if (RB && !ok && !all) {
-            // every candidate that may be among the best: the winners, and what
-            // reaches the least of them
-            uint32_t pick = 0;
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                if (c[j] > -INFINITY && d[j] != 0.0 && (((chosen >> j) & 1) || !(c[j] + d[j] < low)))
-                    pick |= 1u << j;
-            // settle() gives choices of dropped groups back their value: keep them out
-            uint32_t out = 0;
-#pragma unroll
-            for (int j = 0; j < J; j++)
-                out |= c[j] == -INFINITY ? 1u << j : 0u;
-            if (__any(pick != 0)) {                       // (else exact values that are equal)
-                settle(pick);
-#pragma unroll
-                for (int j = 0; j < J; j++)
-                    if ((out >> j) & 1)
-                        c[j] = -INFINITY;
-                top(&ok);
-            }
-        }
-        write();
-    }
-};
+    write_choice(a, m, lane, id, id < 0 ? 0.0 : score_of(a, z[id], mx, sum));
+}
 
 // ------------------------------------------------------------------ one launch
 // One workgroup (16 waves) a token.  Wave w sums the logits of experts w,
@@ -380,10 +269,9 @@ struct Choice {
 // first wave then chooses.
 constexpr int RF_WAVES = 16;
 
-template <int J>
 __global__ __launch_bounds__(64 * RF_WAVES) void route_fused_kernel(const RouteArgs a)
 {
-    __shared__ double s_z[SPEAR_MAX_EXPERTS];
+    __shared__ double s_z[SPEAR_MAX_EXPERTS], s_c[SPEAR_MAX_EXPERTS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m = blockIdx.x, K = a.K;
     const int E = a.E;
@@ -420,27 +308,25 @@ __global__ __launch_bounds__(64 * RF_WAVES) void route_fused_kernel(const RouteA
     __syncthreads();
     if (wave != 0)
         return;
-    Choice<J, 0> ch(a, m, lane);
-    const float zd[J] = {};
-#pragma unroll
-    for (int j = 0; j < J; j++)
-        ch.z[j] = ch.real(j) ? s_z[ch.expert(j)] : 0.0;
-    wait_lgkmcnt0();                                      // s_z is read before groups() writes it
-    ch.run(zd, s_z, nullptr);
+    choose_all(a, m, lane, s_z, s_c);
 }
 
 // ---------------------------------------------------------------- two launches
-// Logits by MFMA: a workgroup of 16 waves takes 16 FT tokens and 64 experts,
-// its waves the depth: each contracts K / 16 of it straight from global memory
-// (two or four 32-deep steps of loads in flight) and the 16 partial sums are added in
-// fp64.  A product passes through at most 32 roundings inside a matrix
-// instruction (whatever its order) and one for each further instruction of the
-// wave's chain, so the error of a logit is at most (32 + chain + 4) 2^-23
-// sum |x w|, and sum |x w| at most the product of the rows' 2-norms, which are
-// formed on the way.
-constexpr int RL_WAVES = 16;
-constexpr int RL_FE = 4;                                  // 16-expert fragments of a workgroup
-constexpr int rl_batch(int FT) { return FT == 2 ? 2 : 4; }  // steps loaded at once: 128 registers a lane
+// Logits by MFMA: a workgroup of 8 waves takes 64 WN experts and 128 tokens
+// over one of ks K slices, in stages of 64 depths that go from global memory
+// to a ring of LDS buffers by DMA (128 bytes a row, 16-byte chunks swizzled by
+// row % 8), one barrier a stage.  Wave (wn, wm) takes 64 experts x 16 FM
+// tokens.  The slices' partial sums are added by the choice.
+//
+// Error: a product passes through at most 32 roundings inside a matrix
+// instruction (whatever its order), 8 along a chain of them (the chain's sum
+// then moves to a second accumulator), one for each of a slice's chains and
+// one for each slice, of a step (2^-23) at most.  So a logit is off by at most
+// (32 + 8 + chains + ks) 2^-23 sum |x w|, and sum |x w| is at most the product
+// of the rows' 2-norms, whose squares are formed on the way.
+constexpr int RL_TM = 128;
+constexpr int RL_FRAGS = SPEAR_MAX_EXPERTS / 16;
+constexpr int RL_CHAIN = 4;                               // stages (of two instructions) a chain
 
 __device__ __forceinline__ float sq8(u32x4 v, float acc)
 {
@@ -450,141 +336,639 @@ __device__ __forceinline__ float sq8(u32x4 v, float acc)
     return acc;
 }
 
-template <int FT>
-__global__ __launch_bounds__(64 * RL_WAVES) void route_logits_kernel(const RouteArgs a, int64_t units)
+// Columns of 64 experts in a tile.
+__host__ __device__ __forceinline__ int tile_waves(int32_t E) { return E <= 64 ? 1 : E <= 128 ? 2 : 4; }
+
+template <int WN>
+__global__ __launch_bounds__(512) void route_logits_kernel(const RouteArgs a)
 {
-    __shared__ f32x4 s_z[RL_WAVES][FT * RL_FE][64];
-    __shared__ float s_n[RL_WAVES][(FT + RL_FE) * 16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int WM = 8 / WN, FM = RL_TM / (16 * WM), TE = 64 * WN;
+    constexpr int SB = (TE + RL_TM) * 128;                // bytes of a stage
+    constexpr int NI = SB / 8192;                         // DMAs a wave issues per stage
+    constexpr int RING = WN == 4 ? 3 : WN == 2 ? 4 : 6;
+    constexpr int WAIT = (RING - 2) * NI;
+    static_assert(NI * 8192 == SB && WAIT < 64, "stage split");
+    __shared__ __attribute__((aligned(16))) uint8_t s_r0[SB], s_r1[SB], s_r2[SB];
+    __shared__ __attribute__((aligned(16))) uint8_t s_r3[RING > 3 ? SB : 16], s_r4[RING > 4 ? SB : 16],
+        s_r5[RING > 5 ? SB : 16];
+    uint8_t *const ring[6] = {s_r0, s_r1, s_r2, s_r3, s_r4, s_r5};
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
+    const int wn = wave % WN, wm = wave / WN;
     const int64_t M = a.M, K = a.K;
     const int E = a.E;
-    // an XCD takes a contiguous run of units, the experts fastest, so that the
-    // workgroups of one token tile find its rows in their L2
+    // An XCD takes a contiguous run of units, the token tiles fastest, so that
+    // its L2 keeps one slice of w for all of them.
+    const int64_t ntt = (M + RL_TM - 1) / RL_TM, units = ntt * a.net * a.ks;
     const int64_t q8 = units / 8, r8 = units % 8, xcd = blockIdx.x % 8;
     const int64_t unit = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
-    const int net = (E + 16 * RL_FE - 1) / (16 * RL_FE);
-    const int64_t m0 = unit / net * (16 * FT);
-    const int e0 = (int)(unit % net) * (16 * RL_FE);
-    const int64_t T = K / 32, t0 = wave * T / RL_WAVES, t1 = (wave + 1) * T / RL_WAVES;
-    const uint16_t *xr[FT], *wr[RL_FE];
+    const int64_t m0 = unit % ntt * RL_TM;
+    const int e0 = (int)(unit / ntt % a.net) * TE, ks = (int)(unit / (ntt * a.net));
+    const int64_t S = (K + 63) / 64, sb = ks * S / a.ks, se = (ks + 1) * S / a.ks, slast = se - 1;
+
+    // DMA i of a wave fills 1 KB: rows 8 (NI wave + i) .. + 7, lane l position
+    // l % 8 of row l / 8.  A chunk past K re-reads the row's last one inside it
+    // (its step is not taken).
+    const uint16_t *src[NI];
+    int coff[NI];
 #pragma unroll
-    for (int f = 0; f < FT; f++) {
-        const int64_t m = m0 + 16 * f + lr;
-        xr[f] = a.x + (m < M ? m : M - 1) * K + 8 * lg;
+    for (int i = 0; i < NI; i++) {
+        const int r = 8 * (NI * wave + i) + (lane >> 3);
+        coff[i] = 8 * ((lane & 7) ^ (r & 7));
+        if (r < TE)
+            src[i] = a.w + (int64_t)(e0 + r < E ? e0 + r : E - 1) * K;
+        else
+            src[i] = a.x + (m0 + r - TE < M ? m0 + r - TE : M - 1) * K;
     }
+    auto issue = [&](int64_t st, uint8_t *buf) {
+        const int64_t k0 = 64 * (st < slast ? st : slast);
 #pragma unroll
-    for (int f = 0; f < RL_FE; f++) {
-        const int e = e0 + 16 * f + lr;
-        wr[f] = a.w + (int64_t)(e < E ? e : E - 1) * K + 8 * lg;
-    }
-    constexpr int RL_B = rl_batch(FT);
-    f32x4 acc[RL_FE][FT];
-    float xs[FT], ws[RL_FE];
+        for (int i = 0; i < NI; i++) {
+            const int64_t k = k0 + coff[i] < K ? k0 + coff[i] : K - 8;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(src[i] + k),
+                                             (__attribute__((address_space(3))) void *)(buf + (NI * wave + i) * 1024),
+                                             16, 0, 0);
+        }
+    };
+    f32x4 acc[4][FM], tot[4][FM];
+    float xs[FM], ws[4];
 #pragma unroll
-    for (int i = 0; i < RL_FE; i++) {
+    for (int i = 0; i < 4; i++) {
         ws[i] = 0.f;
 #pragma unroll
-        for (int f = 0; f < FT; f++)
-            acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int f = 0; f < FM; f++)
+            acc[i][f] = tot[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
-    for (int f = 0; f < FT; f++)
+    for (int f = 0; f < FM; f++)
         xs[f] = 0.f;
-    for (int64_t t = t0; t < t1; t += RL_B) {
-        u32x4 xv[RL_B][FT], wv[RL_B][RL_FE];
+    auto flush = [&]() {
 #pragma unroll
-        for (int b = 0; b < RL_B; b++) {
-            const bool live = t + b < t1;                 // uniform
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int f = 0; f < FT; f++)
-                xv[b][f] = live ? ld16(xr[f] + 32 * (t + b)) : zero4();
-#pragma unroll
-            for (int f = 0; f < RL_FE; f++)
-                wv[b][f] = live ? ld16(wr[f] + 32 * (t + b)) : zero4();
-        }
-#pragma unroll
-        for (int b = 0; b < RL_B; b++) {
-#pragma unroll
-            for (int i = 0; i < RL_FE; i++) {
-                ws[i] = sq8(wv[b][i], ws[i]);
-#pragma unroll
-                for (int f = 0; f < FT; f++)
-                    acc[i][f] = mfma16(wv[b][i], xv[b][f], acc[i][f]);
+            for (int f = 0; f < FM; f++) {
+                tot[i][f] += acc[i][f];
+                acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
+    };
+    const bool sqw = wm == 0 && m0 == 0, sqx = wn == 0 && e0 == 0;   // who forms the squares
 #pragma unroll
-            for (int f = 0; f < FT; f++)
-                xs[f] = sq8(xv[b][f], xs[f]);
+    for (int j = 0; j < RING - 1; j++)
+        issue(sb + j, ring[j]);
+    for (int64_t s0 = sb; s0 < se; s0 += RING) {
+#pragma unroll
+        for (int j = 0; j < RING; j++) {
+            const int64_t st = s0 + j;
+            wait_vmcnt<WAIT>();                           // this wave's part of stage st
+            bare_barrier();                               // every wave's part; stage st - 1 free
+            issue(st + RING - 1, ring[(j + RING - 1) % RING]);
+            if (st < se) {
+                const uint8_t *buf = ring[j];
+#pragma unroll
+                for (int dd = 0; dd < 2; dd++) {
+                    if (dd == 1 && 64 * st + 32 >= K)
+                        break;
+                    const int off = ((4 * dd + lg) ^ (lr & 7)) << 4;
+                    u32x4 wf[4], xf[FM];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        wf[i] = *reinterpret_cast<const u32x4 *>(buf + (64 * wn + 16 * i + lr) * 128 + off);
+#pragma unroll
+                    for (int f = 0; f < FM; f++)
+                        xf[f] = *reinterpret_cast<const u32x4 *>(buf + (TE + 16 * (FM * wm + f) + lr) * 128 + off);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+#pragma unroll
+                        for (int f = 0; f < FM; f++)
+                            acc[i][f] = mfma16(wf[i], xf[f], acc[i][f]);
+                    if (sqw) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            ws[i] = sq8(wf[i], ws[i]);
+                    }
+                    if (sqx) {
+#pragma unroll
+                        for (int f = 0; f < FM; f++)
+                            xs[f] = sq8(xf[f], xs[f]);
+                    }
+                }
+                if ((st - sb) % RL_CHAIN == RL_CHAIN - 1)
+                    flush();
+            }
         }
     }
+    wait_vmcnt<0>();                                      // the clamped tail DMAs
+    flush();
+    // lane (lr, lg): experts + 16 i + 4 lg + q of token + 16 f + lr
 #pragma unroll
-    for (int i = 0; i < RL_FE; i++)
+    for (int f = 0; f < FM; f++) {
+        const int64_t m = m0 + 16 * (FM * wm + f) + lr;
+        if (m >= M)
+            continue;
 #pragma unroll
-        for (int f = 0; f < FT; f++)
-            s_z[wave][i * FT + f][lane] = acc[i][f];
-#pragma unroll
-    for (int f = 0; f < FT + RL_FE; f++) {
-        float v = f < FT ? xs[f] : ws[f - FT];
-        v += __shfl_xor(v, 16);
-        v += __shfl_xor(v, 32);
-        if (lg == 0)
-            s_n[wave][16 * f + lr] = v;
-    }
-    __syncthreads();
-    // lane (token lr, lg) of fragment pair (i, f): experts e0 + 16 i + 4 lg + q
-    for (int q = tid; q < FT * RL_FE * 64; q += 64 * RL_WAVES) {
-        const int p = q >> 6, l = q & 63;
-        double s[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll
-        for (int w = 0; w < RL_WAVES; w++) {
-            const f32x4 v = s_z[w][p][l];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                s[i] += (double)v[i];
-        }
-        const int64_t m = m0 + 16 * (p % FT) + (l & 15);
-        const int e = e0 + 16 * (p / FT) + 4 * (l >> 4);
-        if (m < M) {
-            float *z = a.z + m * E + e;
+        for (int i = 0; i < 4; i++) {
+            const int e = e0 + 64 * wn + 16 * i + 4 * lg;
+            float *z = a.z + ((int64_t)ks * M + m) * E + e;
             if (e + 3 < E && E % 4 == 0)
-                *reinterpret_cast<f32x4 *>(z) = f32x4{(float)s[0], (float)s[1], (float)s[2], (float)s[3]};
+                *reinterpret_cast<f32x4 *>(z) = tot[i][f];
             else
-                for (int i = 0; i < 4; i++)
-                    if (e + i < E)
-                        z[i] = (float)s[i];
+                for (int q = 0; q < 4; q++)
+                    if (e + q < E)
+                        z[q] = tot[i][f][q];
         }
     }
-    if (tid < (FT + RL_FE) * 16) {
-        double n = 0.0;
-        for (int w = 0; w < RL_WAVES; w++)
-            n += (double)s_n[w][tid];
-        const float norm = 1.01f * (float)sqrt(n);
-        if (tid < 16 * FT) {
-            if (e0 == 0 && m0 + tid < M)
-                a.xn[m0 + tid] = norm;
-        } else if (m0 == 0 && e0 + tid - 16 * FT < E) {
-            a.wn[e0 + tid - 16 * FT] = norm;
+    if (sqx) {
+#pragma unroll
+        for (int f = 0; f < FM; f++) {
+            float v = xs[f];
+            v += __shfl_xor(v, 16);
+            v += __shfl_xor(v, 32);
+            const int64_t m = m0 + 16 * (FM * wm + f) + lr;
+            if (lg == 0 && m < M)
+                a.xn[(int64_t)ks * M + m] = v;
+        }
+    }
+    if (sqw) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float v = ws[i];
+            v += __shfl_xor(v, 16);
+            v += __shfl_xor(v, 32);
+            // rows past E repeat the last one: the largest of the 16
+            for (int o = 1; o < 16; o <<= 1) {
+                const float u = __shfl_xor(v, o);
+                v = u > v || u != u ? u : v;              // (NaN stays)
+            }
+            if (lane == 0)
+                a.wn[ks * RL_FRAGS + (e0 + 64 * wn + 16 * i) / 16] = v;
         }
     }
 }
 
-template <int J>
+// The bound of |w_e|^2 over all experts (NaN where a norm is).
+__device__ __forceinline__ float w_norm2(const RouteArgs &a, int lane)
+{
+    const int frags = 4 * tile_waves(a.E) * a.net, f = lane & (RL_FRAGS - 1);
+    float v = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < a.ks; k++) {
+        const float u = a.wn[k * RL_FRAGS + f];
+        v += f < frags ? u : 0.f;
+    }
+    return __any(v != v) ? __builtin_nanf("") : wave_max(v);
+}
+
+// Reductions over 16 lanes (a DPP row), the result in all of them: swaps within
+// quads, then of the quads and halves by mirrors, each step the same two
+// operands on both sides.
+template <typename T, typename F>
+__device__ __forceinline__ T row_reduce(T v, F op)
+{
+    v = op(v, dpp<0xB1, 0xF>(v, v));                      // quad_perm 1 0 3 2
+    v = op(v, dpp<0x4E, 0xF>(v, v));                      // quad_perm 2 3 0 1
+    v = op(v, dpp<0x141, 0xF>(v, v));                     // row_half_mirror
+    v = op(v, dpp<0x140, 0xF>(v, v));                     // row_mirror
+    return v;
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    return row_reduce(v, [](uint32_t p, uint32_t q) { return q > p ? q : p; });
+}
+__device__ __forceinline__ float row_max(float v)
+{
+    return row_reduce(v, [](float p, float q) { return q > p ? q : p; });
+}
+__device__ __forceinline__ float row_sum(float v)
+{
+    return row_reduce(v, [](float p, float q) { return p + q; });
+}
+__device__ __forceinline__ double row_sum(double v)
+{
+    return row_reduce(v, [](double p, double q) { return p + q; });
+}
+
+// A wave's LDS in the choice (an array for each type: nothing is reused as
+// another).
+template <int Q>
+struct ChooseShared {
+    uint32_t key[4][64 * Q];                              // by token and expert
+    uint32_t gval[4][SPEAR_MAX_GROUPS], gthr[4][SPEAR_MAX_GROUPS];
+    uint64_t kept[4];
+    double z[64 * Q], c[64 * Q], slot_z[SPEAR_MAX_TOPK];
+    int32_t slot_id[SPEAR_MAX_TOPK];
+    uint16_t list[64 * Q];
+};
+
+// What the wave knows of one token it has to settle.
+struct Doubt {
+    int64_t m;
+    int row;
+    uint32_t clear;                                       // choices further apart are in order
+    float mx, sum, zd;
+};
+
+// The groups of a token whose order the bounds leave open: the experts that may
+// be among the best of those groups in fp64, then the groups by them.  False:
+// all logits are needed.
+template <int Q>
+__device__ __forceinline__ bool settle_groups(const RouteArgs &a, ChooseShared<Q> &sh, const Doubt &t, int lane)
+{
+    const int E = a.E, G = a.n_group, gs = E / G;
+    if (a.score == SPEAR_SCORE_SOFTMAX && a.bias)
+        return false;
+    const bool two = a.group_best == 2 && gs > 1;
+    const uint32_t tol = (two ? 2u : 1u) * t.clear;
+    const uint32_t gv = lane < G ? sh.gval[t.row][lane] : 0u;
+    uint32_t rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < G; g++) {
+        const uint32_t o = sh.gval[t.row][g];
+        rank += o > gv || (o == gv && g < lane) ? 1u : 0u;
+    }
+    const bool in = lane < G && rank < (uint32_t)a.topk_group;
+    const uint32_t least = ~wave_max(in ? ~gv : 0u), most = wave_max(lane < G && !in ? gv : 0u);
+    const bool open = lane < G && (in ? gv <= most + tol : gv + tol >= least);
+    const uint64_t og = __ballot(open), sure = __ballot(in && !open);
+    int n = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane, g = e < E ? e / gs : 0;
+        const uint32_t k = e < E ? sh.key[t.row][e] : 0u;
+        n = append(sh.list, n, ((og >> g) & 1) && k != 0u && (k >> 9) + t.clear >= sh.gthr[t.row][g], e, lane);
+    }
+    wait_lgkmcnt0();
+    exact_logits(a, t.m, lane, sh.list, n, sh.z);
+#pragma unroll 1
+    for (int p = lane; p < n; p += 64)
+        sh.c[p] = choice_of(a, score_of(a, sh.z[p], t.mx, t.sum), sh.list[p]);
+    wait_lgkmcnt0();
+    double b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll 1
+    for (int p = 0; p < n; p++)
+        if (sh.list[p] / gs == lane) {
+            const double v = sh.c[p];
+            b1 = v > b0 ? b0 : (v > b1 ? v : b1);
+            b0 = v > b0 ? v : b0;
+        }
+    const double v = two ? b0 + b1 : b0;
+    int place = 0;
+#pragma unroll 1
+    for (int g = 0; g < G; g++) {
+        const double o = lane_of(v, g);
+        place += ((og >> g) & 1) && (o > v || (o == v && g < lane));
+    }
+    const uint64_t kept = sure | __ballot(open && place < a.topk_group - __popcll(sure));
+    if (lane == 0)
+        sh.kept[t.row] = kept;
+    wait_lgkmcnt0();
+    return true;
+}
+
+// The winners of a token whose order is open (slots `so`), and the candidates
+// behind the last one that may come before it, in fp64.  They take the open
+// slots in their exact order; the other winners are clear of them all.  id, v:
+// winner and key of slot `lane`; last: the last winner's key; rest: whether the
+// candidates left (sh.key) matter.  False: all logits are needed.
+template <int Q>
+__device__ __forceinline__ bool settle_order(const RouteArgs &a, ChooseShared<Q> &sh, const Doubt &t, int lane,
+                                             int id, uint64_t so, bool rest, uint32_t last)
+{
+    const int E = a.E;
+    int n = append(sh.list, 0, (so >> lane) & 1, id, lane);
+    if (rest)
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const uint32_t k = e0 + lane < E ? sh.key[t.row][e0 + lane] : 0u;
+            n = append(sh.list, n, k != 0u && last - (k >> 9) <= t.clear, e0 + lane, lane);
+        }
+    wait_lgkmcnt0();
+    exact_logits(a, t.m, lane, sh.list, n, sh.z);
+    const int open = __popcll(so);
+    bool decided = true;
+    const bool shift = a.score == SPEAR_SCORE_SOFTMAX && a.bias;   // s + bias: the sum's own error matters
+#pragma unroll 1
+    for (int p = lane; p < n; p += 64)
+        sh.c[p] = choice_of(a, score_of(a, sh.z[p], t.mx, t.sum), sh.list[p]);
+    wait_lgkmcnt0();
+#pragma unroll 1
+    for (int p = lane; p < n; p += 64) {
+        const double c = sh.c[p], z = sh.z[p], s = shift ? score_of(a, z, t.mx, t.sum) : 0.0;
+        const int e = sh.list[p];
+        int place = 0;
+#pragma unroll 1
+        for (int q = 0; q < n; q++) {
+            const double o = sh.c[q];
+            const int oe = sh.list[q];
+            place += o > c || (o == c && oe < e);
+            if (shift && q != p && !(fabs(o - c) > 1.25 * (double)t.zd * fabs(score_of(a, sh.z[q], t.mx, t.sum) - s)))
+                decided = false;
+        }
+        if (place < open) {
+            uint64_t m = so;                              // the place-th open slot
+#pragma unroll 1
+            for (int i = 0; i < place; i++)
+                m &= m - 1;
+            const int slot = __builtin_ctzll(m);
+            sh.slot_id[slot] = e;
+            sh.slot_z[slot] = z;
+        }
+    }
+    wait_lgkmcnt0();
+    return __all(decided);
+}
+
+// The choice, four tokens a wave: 16 lanes a token, 4 Q experts a lane
+// (64 i + 4 l + q).  A choice becomes a key of 23 bits of fixed point and 9 bits
+// of 511 - expert, so that a round is a maximum of unsigned words and its winner
+// is in the word (one wave a token, its candidates searched for each winner,
+// took 70 us of vector instructions for 8192 tokens x 256 experts).  Where
+// neighbours in the order are nearer than the bounds and the fixed point allow,
+// the whole wave settles the token with a few logits in fp64.
+template <int Q>
 __global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a)
 {
-    __shared__ double s_c[4][64 * J], s_d[4][64 * J];
+    __shared__ __attribute__((aligned(16))) ChooseShared<Q> s_w[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t m = (int64_t)blockIdx.x * 4 + wave;
-    if (m >= a.M)
+    const int lr = lane & 15, row = lane >> 4;
+    const int64_t M = a.M, m0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
+    if (m0 >= M)
         return;
-    Choice<J, 1> ch(a, m, lane);
-    float zd[J];
-    const float xe = a.zerr * a.xn[m];
+    ChooseShared<Q> &sh = s_w[wave];
+    const int64_t m = m0 + row < M ? m0 + row : M - 1;
+    const int E = a.E, G = a.n_group, gs = E / G;
+    const float wn2 = w_norm2(a, lane);
+
+    // logits: the slices' sums
+    float c[4 * Q], xn = 0.f;
 #pragma unroll
-    for (int j = 0; j < J; j++) {
-        ch.z[j] = ch.real(j) ? (double)a.z[m * a.E + ch.expert(j)] : 0.0;
-        zd[j] = ch.real(j) ? xe * a.wn[ch.expert(j)] : 0.f;
+    for (int i = 0; i < 4 * Q; i++)
+        c[i] = 0.f;
+    constexpr int U = Q <= 2 ? 4 : Q == 4 ? 2 : 1;        // slices in flight, by the registers they take
+#pragma unroll U
+    for (int k = 0; k < a.ks; k++) {
+        const float *zp = a.z + (k * M + m) * E;
+        xn += a.xn[k * M + m];
+#pragma unroll
+        for (int i = 0; i < Q; i++) {
+            const int e = 64 * i + 4 * lr;
+            if (E % 4 == 0) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(zp + (e < E ? e : E - 4));
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    c[4 * i + q] += v[q];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    c[4 * i + q] += zp[e + q < E ? e + q : E - 1];
+            }
+        }
     }
-    ch.run(zd, s_c[wave], s_d[wave]);
+    const float zd = 1.02f * a.zerr * sqrtf(xn) * sqrtf(wn2);   // 2 %: the norms' own roundings
+    auto expert = [&](int i) { return 64 * (i / 4) + 4 * lr + i % 4; };
+    auto real = [&](int i) { return expert(i) < E; };
+    bool hard = !(zd < 0.05f);                            // all logits in fp64
+#pragma unroll
+    for (int i = 0; i < 4 * Q; i++)
+        hard |= real(i) && !(fabsf(c[i]) < INFINITY);
+
+    // softmax: largest logit and sum
+    const bool soft = a.score == SPEAR_SCORE_SOFTMAX;
+    float mx = 0.f, sum = 1.f;
+    if (soft) {
+        float t = -INFINITY, u = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++)
+            t = real(i) && c[i] > t ? c[i] : t;
+        mx = row_max(t);
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++)
+            u += real(i) ? __expf(c[i] - mx) : 0.f;
+        sum = row_sum(u);
+    }
+    // Choices to [0, 1): by the logits themselves where only their order counts
+    // (softmax, no bias, no sums of groups), else by score and bias.  d bounds
+    // the error: of the logit, or its slope times that and 1e-5 for the fp32
+    // exponential (2 steps and as many as the argument's magnitude, which is
+    // below 90 where the score is not 0 or 1).
+    const bool by_z = soft && !a.bias && (a.topk_group == G || a.group_best == 1 || gs == 1);
+    float lo, unit, d;                                    // choice = lo + unit * key
+    if (by_z) {
+        lo = -64.f;                                       // further down all keys are alike: in doubt
+        unit = 64.f;
+        d = zd + 2e-5f;
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++)
+            c[i] -= mx;
+    } else {
+        float mb = 0.f;
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++) {
+            const float s = soft ? __expf(c[i] - mx) * inv : __builtin_amdgcn_rcpf(1.f + __expf(-c[i]));
+            const float b = a.bias && real(i) ? a.bias[expert(i)] : 0.f;
+            mb = fabsf(b) < INFINITY && fabsf(b) > mb ? fabsf(b) : mb;
+            hard |= b == INFINITY;
+            c[i] = s + b;
+        }
+        mb = a.bias ? row_max(mb) : 0.f;
+        lo = -mb;
+        unit = 1.f + 2.f * mb;
+        d = (soft ? 2.5f : 0.25f) * zd + 1e-5f + 5e-7f * unit;
+    }
+    // keys: 1 + 23 bits of the place in the range; 0 for what cannot be chosen
+    constexpr float TOP = 8388000.f;
+    const float up = TOP / unit;
+    uint32_t key[4 * Q];
+#pragma unroll
+    for (int i = 0; i < 4 * Q; i++) {
+        const float t = fminf(fmaxf((c[i] - lo) * up, 0.f), TOP);
+        const bool can = real(i) && c[i] > -INFINITY;     // (false for NaN)
+        key[i] = can ? (((uint32_t)t + 1u) << 9) | (uint32_t)(SPEAR_MAX_EXPERTS - 1 - expert(i)) : 0u;
+    }
+    // two choices further apart than this (in key steps) are in order
+    const float gap = 2.f * d * up + 3.f;
+    const uint32_t clear = gap < 8e6f ? (uint32_t)gap : 0x7FFFFFu;
+
+    if (a.topk_group < G) {
+        // 16 lanes a token: groups lr, lr + 16, ...
+#pragma unroll
+        for (int i = 0; i < Q; i++)
+            *reinterpret_cast<u32x4 *>(&sh.key[row][64 * i + 4 * lr]) =
+                u32x4{key[4 * i], key[4 * i + 1], key[4 * i + 2], key[4 * i + 3]};
+        wait_lgkmcnt0();
+        const bool two = a.group_best == 2 && gs > 1;
+#pragma unroll 1
+        for (int g = lr; g < G; g += 16) {
+            uint32_t b0 = 0, b1 = 0;
+#pragma unroll 8
+            for (int i = 0; i < gs; i++) {
+                const uint32_t v = sh.key[row][g * gs + i] >> 9, w = v < b0 ? v : b0;
+                b0 = v > b0 ? v : b0;
+                b1 = w > b1 ? w : b1;
+            }
+            sh.gval[row][g] = !two ? b0 : b1 ? b0 + b1 : 0u;   // (0: not enough candidates)
+            sh.gthr[row][g] = two ? b1 : b0;
+        }
+        wait_lgkmcnt0();
+        uint32_t least = 0xFFFFFFFFu, most = 0;
+        uint64_t kept = 0;
+#pragma unroll 1
+        for (int g0 = 0; g0 < G; g0 += 16) {
+            const int g = g0 + lr;
+            const uint32_t gv = g < G ? sh.gval[row][g] : 0u;
+            uint32_t rank = 0;
+#pragma unroll 4
+            for (int q = 0; q < G; q++) {
+                const uint32_t o = sh.gval[row][q];
+                rank += o > gv || (o == gv && q < g) ? 1u : 0u;
+            }
+            const bool in = g < G && rank < (uint32_t)a.topk_group;
+            least = in && gv < least ? gv : least;
+            most = g < G && !in && gv > most ? gv : most;
+            kept |= ((__ballot(in) >> (16 * row)) & 0xFFFFull) << g0;
+        }
+        least = ~row_max(~least);
+        most = row_max(most);
+        const bool open = !(least > most && least - most > (two ? 2u : 1u) * clear);
+        if (lr == 0)
+            sh.kept[row] = kept;
+        uint64_t todo = __ballot(open && !hard);
+        uint64_t fail = 0;
+        wait_lgkmcnt0();
+#pragma unroll 1
+        for (int r = 0; r < 4 && m0 + r < M; r++)
+            if ((todo >> (16 * r)) & 1) {
+                const Doubt t = {m0 + r, r, lane_of(clear, 16 * r), lane_of(mx, 16 * r), lane_of(sum, 16 * r),
+                                 lane_of(zd, 16 * r)};
+                if (!settle_groups(a, sh, t, lane))
+                    fail |= 0xFFFFull << (16 * r);
+            }
+        hard |= (fail >> lane) & 1;
+        kept = sh.kept[row];
+        const uint32_t magic = ((1u << 20) + gs - 1) / gs;    // e / gs for e < 512, gs <= 512
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++)
+            key[i] = (kept >> ((expert(i) * magic) >> 20)) & 1u ? key[i] : 0u;
+    }
+
+    // rounds: winner t to lane t % 16, slot t / 16
+    int id[2] = {-1, -1};
+    uint32_t val[2] = {0u, 0u}, prev = 0xFFFFFFFFu, behind = 0;
+    bool so[2] = {false, false};                          // slots whose order is open
+#pragma unroll 1
+    for (int t = 0; t <= a.topk; t++) {                   // one more: the best of the rest
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++)
+            best = key[i] > best ? key[i] : best;
+        best = row_max(best);
+        const uint32_t v = best >> 9;
+        if (t == a.topk) {
+            behind = v;
+            break;
+        }
+        const bool won = best != 0u, open = won && t > 0 && prev - v <= clear;
+        const int e = SPEAR_MAX_EXPERTS - 1 - (int)(best & 511u);
+        if ((t & 15) == lr) {
+            id[0] = won && t < 16 ? e : id[0];
+            id[1] = won && t >= 16 ? e : id[1];
+            val[0] = won && t < 16 ? v : val[0];
+            val[1] = won && t >= 16 ? v : val[1];
+            so[0] |= open && t < 16;
+            so[1] |= open && t >= 16;
+        }
+        if (((t - 1) & 15) == lr) {
+            so[0] |= open && t <= 16;
+            so[1] |= open && t > 16;
+        }
+        prev = won ? v : prev;
+#pragma unroll
+        for (int i = 0; i < 4 * Q; i++)
+            key[i] = key[i] == best ? 0u : key[i];
+    }
+    // candidates behind the last winner that may come before it, and the
+    // winners that they may come before
+    const bool rest = behind != 0u && prev - behind <= clear;
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+        so[h] |= rest && id[h] >= 0 && val[h] - behind <= clear;
+    const uint64_t so0 = __ballot(so[0]), so1 = __ballot(so[1]), hd = __ballot(hard), rs = __ballot(rest);
+    auto of_row = [](uint64_t b, int r) { return (b >> (16 * r)) & 0xFFFFull; };
+    const uint64_t doubt = so0 | so1 | hd;
+
+    // the weights, in fp64 from the winners' logits
+    const bool quick = of_row(doubt, row) == 0 && m0 + row < M;
+    double s[2] = {0.0, 0.0};
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+        if (quick && id[h] >= 0) {
+            float z = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < a.ks; k++)
+                z += a.z[(k * M + m) * E + id[h]];
+            s[h] = score_of(a, (double)z, (double)mx, (double)sum);
+        }
+    double f = (double)a.scale;
+    if (a.renorm) {
+        const double total = row_sum(s[0] + s[1]);
+        f = total == 0.0 ? 0.0 : f / total;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int t = 16 * h + lr;
+        if (quick && t < a.topk) {
+            a.ids[m * a.topk + t] = id[h];
+            a.weights[m * a.topk + t] = id[h] < 0 ? 0.f : (float)(s[h] * f);
+        }
+    }
+    if (doubt == 0)
+        return;
+
+    // tokens in doubt, one after the other by the whole wave
+    if (rs != 0) {
+#pragma unroll
+        for (int i = 0; i < Q; i++)
+            *reinterpret_cast<u32x4 *>(&sh.key[row][64 * i + 4 * lr]) =
+                u32x4{key[4 * i], key[4 * i + 1], key[4 * i + 2], key[4 * i + 3]};
+        wait_lgkmcnt0();
+    }
+#pragma unroll 1
+    for (int r = 0; r < 4 && m0 + r < M; r++) {
+        if (of_row(doubt, r) == 0)
+            continue;
+        const Doubt t = {m0 + r, r, lane_of(clear, 16 * r), lane_of(mx, 16 * r), lane_of(sum, 16 * r),
+                         lane_of(zd, 16 * r)};
+        bool done = false;
+        if (of_row(hd, r) == 0) {
+            const uint64_t open = of_row(so0, r) | (of_row(so1, r) << 16);
+            const int i0 = __shfl(id[0], 16 * r + (lane & 15)), i1 = __shfl(id[1], 16 * r + (lane & 15));
+            const int my = lane < 16 ? i0 : lane < 32 ? i1 : -1;
+            done = settle_order(a, sh, t, lane, my, open, of_row(rs, r) != 0, lane_of(prev, 16 * r));
+            if (done) {
+                int e = my;
+                double z = 0.0;
+                if (lane < a.topk && ((open >> lane) & 1)) {
+                    e = sh.slot_id[lane];
+                    z = sh.slot_z[lane];
+                } else if (lane < a.topk && e >= 0) {
+                    float zf = 0.f;
+                    for (int k = 0; k < a.ks; k++)
+                        zf += a.z[(k * M + t.m) * E + e];
+                    z = (double)zf;
+                }
+                write_choice(a, t.m, lane, lane < a.topk ? e : -1, score_of(a, z, (double)t.mx, (double)t.sum));
+            }
+        }
+        if (!done) {
+#pragma unroll 1
+            for (int e = lane; e < E; e += 64)
+                sh.list[e] = (uint16_t)e;
+            wait_lgkmcnt0();
+            exact_logits(a, t.m, lane, sh.list, E, sh.z);
+            choose_all(a, t.m, lane, sh.z, sh.c);
+        }
+    }
 }
 
 // One launch up to this many tokens, while the router's weights are small
@@ -594,24 +978,38 @@ constexpr int64_t RF_BYTES = 512 << 10;
 
 bool fused(int64_t M, int32_t E, int64_t K) { return M <= RF_TOKENS && 2 * K * E <= RF_BYTES; }
 
-template <int J>
+// K slices: about 256 workgroups, at most 16 slices (their sums go through
+// memory); K's own limit is applied by the launch.
+int64_t most_slices(int64_t tiles)
+{
+    const int64_t ks = 256 / tiles;
+    return ks < 1 ? 1 : ks > 16 ? 16 : ks;
+}
+
 hipError_t launch_route(const RouteArgs &a, hipStream_t s)
 {
     if (fused(a.M, a.E, a.K)) {
-        hipLaunchKernelGGL(route_fused_kernel<J>, dim3((unsigned)a.M), dim3(64 * RF_WAVES), 0, s, a);
+        hipLaunchKernelGGL(route_fused_kernel, dim3((unsigned)a.M), dim3(64 * RF_WAVES), 0, s, a);
         return hipGetLastError();
     }
-    const int64_t net = (a.E + 16 * RL_FE - 1) / (16 * RL_FE);
-    const bool two = a.M > 16;
-    const int64_t units = net * ((a.M + (two ? 31 : 15)) / (two ? 32 : 16));
-    if (two)
-        hipLaunchKernelGGL(route_logits_kernel<2>, dim3((unsigned)units), dim3(64 * RL_WAVES), 0, s, a, units);
-    else
-        hipLaunchKernelGGL(route_logits_kernel<1>, dim3((unsigned)units), dim3(64 * RL_WAVES), 0, s, a, units);
+    const unsigned grid = (unsigned)((a.M + RL_TM - 1) / RL_TM * a.net * a.ks);
+    switch (tile_waves(a.E)) {
+    case 1: hipLaunchKernelGGL(route_logits_kernel<1>, dim3(grid), dim3(512), 0, s, a); break;
+    case 2: hipLaunchKernelGGL(route_logits_kernel<2>, dim3(grid), dim3(512), 0, s, a); break;
+    default: hipLaunchKernelGGL(route_logits_kernel<4>, dim3(grid), dim3(512), 0, s, a); break;
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(route_choose_kernel<J>, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, s, a);
+    const dim3 tokens((unsigned)((a.M + 15) / 16));
+    if (a.E <= 64)
+        hipLaunchKernelGGL(route_choose_kernel<1>, tokens, dim3(256), 0, s, a);
+    else if (a.E <= 128)
+        hipLaunchKernelGGL(route_choose_kernel<2>, tokens, dim3(256), 0, s, a);
+    else if (a.E <= 256)
+        hipLaunchKernelGGL(route_choose_kernel<4>, tokens, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(route_choose_kernel<8>, tokens, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -623,11 +1021,17 @@ RouteLayout route_layout(int64_t M, int32_t E)
 {
     auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
     RouteLayout L;
-    const size_t m = (size_t)(M < 1 ? 1 : M);
+    // rows = K slices times tokens, the most that any token count up to M needs
+    const int64_t net = (E + 64 * tile_waves(E) - 1) / (64 * tile_waves(E));
+    size_t rows = (size_t)(M < 1 ? 1 : M);
+    for (int64_t t = 1; t <= 256 && RL_TM * (t - 1) < M; t++) {
+        const size_t r = (size_t)(most_slices(t * net) * (RL_TM * t < M ? RL_TM * t : M));
+        rows = r > rows ? r : rows;
+    }
     L.z = 0;
-    L.xn = up(m * (size_t)E * sizeof(float));
-    L.wn = L.xn + up(m * sizeof(float));
-    L.total = L.wn + up((size_t)E * sizeof(float));
+    L.xn = up(rows * (size_t)E * sizeof(float));
+    L.wn = L.xn + up(rows * sizeof(float));
+    L.total = L.wn + up(16 * RL_FRAGS * sizeof(float));
     return L;
 }
 
@@ -672,15 +1076,17 @@ spear_status spear_route(const spear_bf16 *x, int64_t M, int64_t K, const spear_
         return st;
     const RouteLayout L = route_layout(M, r.E);
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
-    const int64_t chain = (K / 32 + RL_WAVES - 1) / RL_WAVES;
+    const int64_t net = (r.E + 64 * tile_waves(r.E) - 1) / (64 * tile_waves(r.E));
+    const int64_t stages = (K + 63) / 64, tiles = (M + RL_TM - 1) / RL_TM * net;
+    int64_t ks = most_slices(tiles);
+    ks = ks > stages / 2 ? (stages / 2 > 1 ? stages / 2 : 1) : ks;    // two stages a slice at least
+    const int64_t chains = ((stages + ks - 1) / ks + RL_CHAIN - 1) / RL_CHAIN + 1;
     const RouteArgs a = {x, r.w, r.bias, weights, ids, reinterpret_cast<float *>(ws + L.z),
                          reinterpret_cast<float *>(ws + L.xn), reinterpret_cast<float *>(ws + L.wn), M, K, r.E,
                          r.topk, r.score, r.n_group, r.topk_group, r.group_best, r.renorm, r.scale,
-                         (float)(32 + chain + 4) * 1.1920929e-7f};
+                         (float)(32 + 2 * RL_CHAIN + chains + ks) * 1.1920929e-7f, (int32_t)ks, (int32_t)net};
     const hipStream_t s = (hipStream_t)stream;
-    const hipError_t e = r.E <= 64 ? launch_route<1>(a, s) : r.E <= 128 ? launch_route<2>(a, s)
-                         : r.E <= 256 ? launch_route<4>(a, s) : launch_route<8>(a, s);
-    return e == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
+    return launch_route(a, s) == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
 }
 
 } // extern "C"

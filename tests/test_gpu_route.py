@@ -15,13 +15,14 @@ pytestmark = pytest.mark.gpu
 
 def rtol(x64, w64):
     """Relative error of a token's weights.  The weights come of fp32 logits: a
-    product passes through at most D = 32 + K / 512 + 4 roundings of a step
-    (2^-23) each, so a logit is off by at most zd = D 2^-23 |x| |w|.  A sigmoid
+    product passes through at most D roundings of a step (2^-23) each: 32 in a
+    matrix instruction, 8 along a chain of them, one for each further chain
+    (256 depths), one for each of 16 K slices at most, so a logit is off by at most zd = D 2^-23 |x| |w|.  A sigmoid
     is then off by zd relative, an exponential by zd and the sum that it is
     divided by (softmax, renorm) by zd again, 2 zd (1 + zd) in all; then one
     rounding to fp32."""
     K = x64.shape[1]
-    zd = (32 + -(-(K // 32) // 16) + 4) * 2.0 ** -23 * np.linalg.norm(x64, axis=1) * \
+    zd = (32 + 8 + 2 + K / 256 + 16) * 2.0 ** -23 * np.linalg.norm(x64, axis=1) * \
         np.linalg.norm(w64, axis=1).max()
     return (2.0 * zd * (1.0 + zd) + 2.0 ** -24 * (1 + 1e-5))[:, None]
 
