@@ -506,19 +506,6 @@ __global__ __launch_bounds__(512) void route_logits_kernel(const RouteArgs a)
     }
 }
 
-// The bound of |w_e|^2 over all experts (NaN where a norm is).
-__device__ __forceinline__ float w_norm2(const RouteArgs &a, int lane)
-{
-    const int frags = 4 * tile_waves(a.E) * a.net, f = lane & (RL_FRAGS - 1);
-    float v = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < a.ks; k++) {
-        const float u = a.wn[k * RL_FRAGS + f];
-        v += f < frags ? u : 0.f;
-    }
-    return __any(v != v) ? __builtin_nanf("") : wave_max(v);
-}
-
 // Reductions over 16 lanes (a DPP row), the result in all of them: swaps within
 // quads, then of the quads and halves by mirrors, each step the same two
 // operands on both sides.
@@ -553,6 +540,7 @@ __device__ __forceinline__ double row_sum(double v)
 template <int Q>
 struct ChooseShared {
     uint32_t key[4][64 * Q];                              // by token and expert
+    float logit[4][64 * Q];
     uint32_t gval[4][SPEAR_MAX_GROUPS], gthr[4][SPEAR_MAX_GROUPS];
     uint64_t kept[4];
     double z[64 * Q], c[64 * Q], slot_z[SPEAR_MAX_TOPK];
@@ -686,20 +674,17 @@ __device__ __forceinline__ bool settle_order(const RouteArgs &a, ChooseShared<Q>
 // neighbours in the order are nearer than the bounds and the fixed point allow,
 // the whole wave settles the token with a few logits in fp64.
 template <int Q>
-__global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a)
+__global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
 {
-    __shared__ __attribute__((aligned(16))) ChooseShared<Q> s_w[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ __attribute__((aligned(16))) ChooseShared<Q> sh;
+    const int lane = threadIdx.x;
     const int lr = lane & 15, row = lane >> 4;
-    const int64_t M = a.M, m0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
-    if (m0 >= M)
-        return;
-    ChooseShared<Q> &sh = s_w[wave];
+    const int64_t M = a.M, m0 = (int64_t)blockIdx.x * 4;
     const int64_t m = m0 + row < M ? m0 + row : M - 1;
     const int E = a.E, G = a.n_group, gs = E / G;
-    const float wn2 = w_norm2(a, lane);
-
-    // logits: the slices' sums
+    // logits: the slices' sums; |x|^2, and the largest |w_e|^2 of 16 experts a lane
+    const int frag = lane & (RL_FRAGS - 1), frags = 4 * tile_waves(E) * a.net;
+    float wn2 = 0.f;
     float c[4 * Q], xn = 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * Q; i++)
@@ -709,6 +694,7 @@ __global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a)
     for (int k = 0; k < a.ks; k++) {
         const float *zp = a.z + (k * M + m) * E;
         xn += a.xn[k * M + m];
+        wn2 += a.wn[k * RL_FRAGS + (frag < frags ? frag : 0)];
 #pragma unroll
         for (int i = 0; i < Q; i++) {
             const int e = 64 * i + 4 * lr;
@@ -724,7 +710,12 @@ __global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a)
             }
         }
     }
+    wn2 = __any(wn2 != wn2) ? __builtin_nanf("") : wave_max(wn2);
     const float zd = 1.02f * a.zerr * sqrtf(xn) * sqrtf(wn2);   // 2 %: the norms' own roundings
+#pragma unroll
+    for (int i = 0; i < Q; i++)                           // kept for the winners' weights
+        *reinterpret_cast<f32x4 *>(&sh.logit[row][64 * i + 4 * lr]) =
+            f32x4{c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
     auto expert = [&](int i) { return 64 * (i / 4) + 4 * lr + i % 4; };
     auto real = [&](int i) { return expert(i) < E; };
     bool hard = !(zd < 0.05f);                            // all logits in fp64
@@ -902,13 +893,8 @@ __global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a)
     double s[2] = {0.0, 0.0};
 #pragma unroll
     for (int h = 0; h < 2; h++)
-        if (quick && id[h] >= 0) {
-            float z = 0.f;
-#pragma unroll 4
-            for (int k = 0; k < a.ks; k++)
-                z += a.z[(k * M + m) * E + id[h]];
-            s[h] = score_of(a, (double)z, (double)mx, (double)sum);
-        }
+        if (quick && id[h] >= 0)
+            s[h] = score_of(a, (double)sh.logit[row][id[h]], (double)mx, (double)sum);
     double f = (double)a.scale;
     if (a.renorm) {
         const double total = row_sum(s[0] + s[1]);
@@ -952,10 +938,7 @@ __global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a)
                     e = sh.slot_id[lane];
                     z = sh.slot_z[lane];
                 } else if (lane < a.topk && e >= 0) {
-                    float zf = 0.f;
-                    for (int k = 0; k < a.ks; k++)
-                        zf += a.z[(k * M + t.m) * E + e];
-                    z = (double)zf;
+                    z = (double)sh.logit[r][e];
                 }
                 write_choice(a, t.m, lane, lane < a.topk ? e : -1, score_of(a, z, (double)t.mx, (double)t.sum));
             }
@@ -978,12 +961,13 @@ constexpr int64_t RF_BYTES = 512 << 10;
 
 bool fused(int64_t M, int32_t E, int64_t K) { return M <= RF_TOKENS && 2 * K * E <= RF_BYTES; }
 
-// K slices: about 256 workgroups, at most 16 slices (their sums go through
-// memory); K's own limit is applied by the launch.
+// K slices: about 256 workgroups, at most 8 slices (their sums go through
+// memory; 777 tokens, 60 experts, logits + choice: 7.4 + 15.2 us with 16 slices,
+// 7.9 + 9.5 with 8, 9.7 + 8.6 with 4); K's own limit is applied by the launch.
 int64_t most_slices(int64_t tiles)
 {
     const int64_t ks = 256 / tiles;
-    return ks < 1 ? 1 : ks > 16 ? 16 : ks;
+    return ks < 1 ? 1 : ks > 8 ? 8 : ks;
 }
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t s)
@@ -1001,15 +985,15 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const dim3 tokens((unsigned)((a.M + 15) / 16));
+    const dim3 tokens((unsigned)((a.M + 3) / 4));
     if (a.E <= 64)
-        hipLaunchKernelGGL(route_choose_kernel<1>, tokens, dim3(256), 0, s, a);
+        hipLaunchKernelGGL(route_choose_kernel<1>, tokens, dim3(64), 0, s, a);
     else if (a.E <= 128)
-        hipLaunchKernelGGL(route_choose_kernel<2>, tokens, dim3(256), 0, s, a);
+        hipLaunchKernelGGL(route_choose_kernel<2>, tokens, dim3(64), 0, s, a);
     else if (a.E <= 256)
-        hipLaunchKernelGGL(route_choose_kernel<4>, tokens, dim3(256), 0, s, a);
+        hipLaunchKernelGGL(route_choose_kernel<4>, tokens, dim3(64), 0, s, a);
     else
-        hipLaunchKernelGGL(route_choose_kernel<8>, tokens, dim3(256), 0, s, a);
+        hipLaunchKernelGGL(route_choose_kernel<8>, tokens, dim3(64), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1031,7 +1015,7 @@ RouteLayout route_layout(int64_t M, int32_t E)
     L.z = 0;
     L.xn = up(rows * (size_t)E * sizeof(float));
     L.wn = L.xn + up(rows * sizeof(float));
-    L.total = L.wn + up(16 * RL_FRAGS * sizeof(float));
+    L.total = L.wn + up(8 * RL_FRAGS * sizeof(float));
     return L;
 }
 
