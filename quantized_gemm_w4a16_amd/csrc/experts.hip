@@ -12,6 +12,7 @@
 // No launch waits on another workgroup, and no result depends on an order that
 // the hardware chooses: the sums of an output are taken in one fixed order.
 #include <string.h>
+#include <type_traits>
 
 #include "spear_internal.hpp"
 
@@ -34,7 +35,7 @@ int64_t max_tiles(int64_t slots, int32_t E, int bm) { return slots / bm + (slots
 int tile_rows(int64_t slots, int32_t E)
 {
     const int64_t per = slots / E;
-    return per >= 48 ? 128 : per >= 12 ? 64 : XT;
+    return per >= 64 ? 128 : per >= 20 ? 64 : per >= 10 ? 32 : XT;
 }
 
 ExpertsLayout experts_layout(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N)
@@ -155,66 +156,219 @@ struct GroupArgs {
     int64_t N, K;
     int32_t div;              // a row's source is slot / div (topk for up, 1 for down)
     int32_t act, glu;
-    int32_t ncb;              // channel blocks of 64: the grid's fastest index
+    int32_t ncb;              // channel blocks: the grid's fastest index
 };
 
-// One wave takes 16 channels of a row tile over all of K.  Lane (c, g) holds
-// channel c's 32 codes k = 128 s + 32 g .. + 31 of super-step s as one 16-byte
-// load, and the same depths of row c of the tile: 64 bytes.  Rows past the
-// tile's end are zero.
-template <int UP>
-__global__ __launch_bounds__(256) void group_kernel(const GroupArgs a)
+// What depths past K read: zeros (16 bytes a lane of 16).
+__device__ __align__(256) static uint8_t g_zeros[256];
+
+// The streaming product: a workgroup of NW waves takes a row tile of up to BM
+// rows and 16 FC NW channels, wave w 16 FC of them over all of K.  Weights go
+// from memory to registers, a chunk of 512 depths (4 FC 16-byte loads a lane)
+// ahead of the one in use, and are unpacked once for all the tile's rows; the
+// rows go by DMA to two LDS buffers a chunk deep (1 KB a row, its 16-byte
+// pieces swizzled by row % 16 on the way; zeros past K), with one barrier a
+// chunk.  Lane (c, g) holds channel c's 32 codes k = 128 s + 32 g .. + 31 of
+// step s as one load, and reads the same depths of its token row as four.  The
+// rows' sums, which remove the unpacking's offset, are shared out over the
+// waves by depth and meet in LDS.  Rows past the tile's end repeat the last one
+// and are not stored: an output depends on its own row alone.
+constexpr int SC = 512;                                   // depths of a chunk
+
+template <int BM, int NW, int FC, int UP>
+__global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
 {
+    constexpr int NF = BM / 16, NI = BM / NW;
+    static_assert(BM % NW == 0 && 16 % NW == 0, "rows and depth pieces over waves");
+    __shared__ __attribute__((aligned(16))) uint8_t s_x0[BM * 1024];
+    __shared__ __attribute__((aligned(16))) uint8_t s_x1[BM * 1024];
+    __shared__ float s_rs[NW][BM];
     const int tile = (int)(blockIdx.x / (uint32_t)a.ncb), cb = (int)(blockIdx.x % (uint32_t)a.ncb);
+    const Tile q = a.tiles[tile];                         // (the table has room for every block)
     if (tile >= *a.ntiles)
         return;
-    const Tile q = a.tiles[tile];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
     const int64_t N = a.N, K = a.K;
-    const int64_t n0 = ((int64_t)cb * 4 + wave) * 16;
-    if (n0 >= N)
-        return;
-    const int64_t nc = n0 + lr < N ? n0 + lr : N - 1;
+    const int64_t n0 = ((int64_t)cb * NW + wave) * (16 * FC);
     const int64_t base = (int64_t)q.e * N;
-    const int slot = lr < q.cnt ? a.list[q.pos + lr] : -1;
-    const uint16_t *xr = a.x + (int64_t)(slot < 0 ? 0 : slot / a.div) * K;
-    const uint8_t *wr = a.packed + (base + nc) * (K / 2);
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, rs = acc;
-    const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    for (int64_t k0 = 0; k0 < K; k0 += 128) {
-        const int64_t k = k0 + 32 * lg;
-        const bool kv = k < K;
-        const u32x4 w = ld16(wr + (kv ? k : 0) / 2);
-        u32x4 xv[4];
+    const int nf = (q.cnt + 15) / 16;                     // fragments in use
+    const int64_t C = (K + SC - 1) / SC;
+    const uint8_t *wr[FC];
 #pragma unroll
-        for (int d = 0; d < 4; d++)
-            xv[d] = kv && slot >= 0 ? ld16(xr + k + 8 * d) : zero4();
+    for (int j = 0; j < FC; j++) {
+        const int64_t n = n0 + 16 * j + lr;
+        wr[j] = a.packed + (base + (n < N ? n : N - 1)) * (K / 2) + 16 * lg;
+    }
+    auto load_w = [&](int64_t c, u32x4 (&w)[FC][4]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int d = 0; d < 4; d++) {
-            acc = mfma16(unpack8(w[d]), xv[d], acc);
-            rs = mfma16(ones, xv[d], rs);
+        for (int t = 0; t < 4; t++) {
+            // past K: the row's first codes, which meet zeros
+            const bool in = SC * c + 128 * t + 32 * lg < K;
+#pragma unroll
+            for (int j = 0; j < FC; j++)
+                w[j][t] = ld16(in ? wr[j] + (SC * c + 128 * t) / 2 : wr[j] - 16 * lg);
         }
-    }
-    // lane (row lr, lg): channels n0 + 4 lg + i
-    if (slot < 0)
-        return;
-    float t[4], b[4], o[4];
-    const int64_t n = n0 + 4 * lg;
+    };
+    // rows wave, wave + NW, ... of the tile: lane l takes piece l ^ (row % 16)
+    const uint16_t *xs[NI];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t nn = base + (n + i < N ? n + i : N - 1);
-        const float zp = a.zeros ? (float)a.zeros[nn] : 8.f;
-        t[i] = a.scales[nn] * __builtin_fmaf(-(UNPACK_OFF + zp), rs[0], UNPACK_SCALE * acc[i]);
-        b[i] = a.bias ? a.bias[nn] : 0.f;
+    for (int i = 0; i < NI; i++) {
+        const int r = wave + NW * i;
+        const int rr = r < q.cnt ? r : q.cnt - 1;
+        xs[i] = a.x + (int64_t)(a.list[q.pos + rr] / a.div) * K + 8 * (lane ^ (r & 15));
     }
-    if (UP) {
-        epi_apply(t, b, a.act, a.glu, o);
-        epi_store<0>(a.out, slot, n, a.glu, a.glu ? N / 2 : N, o);
-    } else {
-        epi_apply(t, b, SPEAR_ACT_NONE, 0, o);
-        epi_store<1>(a.out, slot, n, 0, N, o);
+    auto issue_x = [&](int64_t c, uint8_t *buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            const int r = wave + NW * i;
+            const void *src = SC * c + 8 * (lane ^ (r & 15)) < K ? (const void *)(xs[i] + SC * c)
+                                                                 : (const void *)(g_zeros + 16 * lr);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                             (__attribute__((address_space(3))) void *)(buf + 1024 * r), 16, 0, 0);
+        }
+    };
+    u32x4 w0[FC][4], w1[FC][4];
+    issue_x(0, s_x0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(0, w0);
+
+    f32x4 acc[FC][NF], rs[NF];
+#pragma unroll
+    for (int f = 0; f < NF; f++) {
+        rs[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < FC; j++)
+            acc[j][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    // LDS pieces of row lr for depths 8 (16 t + 4 lg + d): 16 t + ((4 lg + d) ^ lr)
+    int xo[4];
+#pragma unroll
+    for (int d = 0; d < 4; d++)
+        xo[d] = lr * 1024 + (((4 * lg + d) ^ lr) << 4);
+    // All four steps of a chunk, past K with zero rows, and then this wave's
+    // share of the rows' sums.  No branch: it would leave weight loads pending
+    // where paths meet, and the compiler would wait for everything there; and
+    // after a matrix instruction and a taken branch this toolchain can leave out
+    // the wait states before its result is read.  FR: fragments taken.
+    auto use = [&](auto FR, const uint8_t *buf, const u32x4 (&w)[FC][4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+#pragma unroll
+            for (int d = 0; d < 4; d++) {
+                u32x4 wv[FC];
+#pragma unroll
+                for (int j = 0; j < FC; j++)
+                    wv[j] = unpack8(w[j][t][d]);
+#pragma unroll
+                for (int f = 0; f < decltype(FR)::value; f++) {
+                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(buf + xo[d] + 256 * t + 16384 * f);
+#pragma unroll
+                    for (int j = 0; j < FC; j++)
+                        acc[j][f] = mfma16(wv[j], xv, acc[j][f]);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < 16 / NW; i++) {
+            const int p = wave + NW * i;                  // piece 4 t + d
+            const int off = lr * 1024 + 256 * (p >> 2) + (((4 * lg + (p & 3)) ^ lr) << 4);
+#pragma unroll
+            for (int f = 0; f < decltype(FR)::value; f++)
+                rs[f] = mfma16(ones, *reinterpret_cast<const u32x4 *>(buf + off + 16384 * f), rs[f]);
+        }
+    };
+    auto run = [&](auto FR) __attribute__((always_inline)) {
+        int64_t c = 0;
+        for (; c + 1 < C; c += 2) {
+            // chunk c: its rows' DMAs are older than the weight loads behind them
+            wait_vmcnt<4 * FC>();
+            bare_barrier();
+            issue_x(c + 1, s_x1);
+            __builtin_amdgcn_sched_barrier(0);            // keeps that order
+            load_w(c + 1, w1);
+            use(FR, s_x0, w0);
+            wait_vmcnt<4 * FC>();
+            bare_barrier();
+            issue_x(c + 2 < C ? c + 2 : c + 1, s_x0);
+            __builtin_amdgcn_sched_barrier(0);
+            load_w(c + 2 < C ? c + 2 : c + 1, w0);
+            use(FR, s_x1, w1);
+        }
+        wait_vmcnt<0>();
+        if (c < C) {
+            bare_barrier();
+            use(FR, s_x0, w0);
+        }
+        // The epilogue's operands, without branches: one round trip.
+        float sc[FC][4], b[FC][4];
+        uint32_t zr[FC][4];
+        int32_t slot[NF];
+#pragma unroll
+        for (int j = 0; j < FC; j++) {
+            const int64_t n = n0 + 16 * j + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int64_t nn = n + i < N ? n + i : N - 1;
+                sc[j][i] = a.scales[base + nn];
+                zr[j][i] = load_zero_byte(a.zeros ? a.zeros + base : nullptr, a.scales + base, nn);
+            }
+            epi_load_bias(a.bias ? a.bias + base : nullptr, a.scales + base, n, N, b[j]);
+        }
+#pragma unroll
+        for (int f = 0; f < decltype(FR)::value; f++) {
+            slot[f] = a.list[q.pos + (16 * f + lr < q.cnt ? 16 * f + lr : 0)];
+            if (lg == 0)
+                s_rs[wave][16 * f + lr] = rs[f][0];
+        }
+        __syncthreads();
+        // lane (row lr of fragment f, lg): channels n0 + 16 j + 4 lg + i
+#pragma unroll
+        for (int f = 0; f < decltype(FR)::value; f++) {
+            const int r = 16 * f + lr;
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < NW; v++)
+                sum += s_rs[v][r];
+#pragma unroll
+            for (int j = 0; j < FC; j++) {
+                float t[4], bb[4], o[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    t[i] = sc[j][i] * __builtin_fmaf(-(UNPACK_OFF + zero_point(a.zeros, zr[j][i])), sum,
+                                                     UNPACK_SCALE * acc[j][f][i]);
+                    bb[i] = a.bias ? b[j][i] : 0.f;
+                }
+                epi_apply(t, bb, UP ? a.act : SPEAR_ACT_NONE, UP ? a.glu : 0, o);
+                if (r < q.cnt)
+                    epi_store<(UP ? 0 : 1)>(a.out, slot[f], n0 + 16 * j + 4 * lg, UP ? a.glu : 0,
+                                            UP && a.glu ? N / 2 : N, o);
+            }
+        }
+    };
+    if (NF > 1 && 2 * nf <= NF)                           // half the tile is empty
+        run(std::integral_constant<int, NF / 2 ? NF / 2 : 1>());
+    else
+        run(std::integral_constant<int, NF>());
+}
+
+template <int BM, int NW, int FC, int UP>
+hipError_t launch_stream_t(GroupArgs a, int64_t tiles, hipStream_t s)
+{
+    a.ncb = (int32_t)((a.N + 16 * FC * NW - 1) / (16 * FC * NW));
+    hipLaunchKernelGGL((stream_kernel<BM, NW, FC, UP>), dim3((unsigned)(tiles * a.ncb)), dim3(64 * NW), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int UP>
+hipError_t launch_stream(const GroupArgs &a, int bm, int64_t tiles, hipStream_t s)
+{
+    if (bm == 64)
+        return launch_stream_t<64, 8, 2, UP>(a, tiles, s);
+    if (bm == 32)
+        return launch_stream_t<32, 8, 2, UP>(a, tiles, s);
+    return launch_stream_t<16, 4, 1, UP>(a, tiles, s);
 }
 
 // ---------------------------------------------------------------------- join
@@ -310,17 +464,14 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
                        reinterpret_cast<uint32_t *>(ws + L.zeros), ntiles, tiles, list);
     if (hipGetLastError() != hipSuccess)
         return SPEAR_E_HIP;
-    if (bm == XT) {
-        GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, ntiles, tiles, list,
-                       NU, K, topk, w->act, w->glu, (int32_t)((NU + 63) / 64)};
-        hipLaunchKernelGGL(group_kernel<1>, dim3((unsigned)(nt * u.ncb)), dim3(256), 0, s, u);
-        if (hipGetLastError() != hipSuccess)
+    if (bm <= 64) {
+        const GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, ntiles, tiles, list,
+                             NU, K, topk, w->act, w->glu, 0};
+        if (launch_stream<1>(u, bm, nt, s) != hipSuccess)
             return SPEAR_E_HIP;
-        GroupArgs d = {reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
-                       w->down_bias, ws + L.d, ntiles, tiles, list, N, I, 1, SPEAR_ACT_NONE, 0,
-                       (int32_t)((N + 63) / 64)};
-        hipLaunchKernelGGL(group_kernel<0>, dim3((unsigned)(nt * d.ncb)), dim3(256), 0, s, d);
-        if (hipGetLastError() != hipSuccess)
+        const GroupArgs d = {reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
+                             w->down_bias, ws + L.d, ntiles, tiles, list, N, I, 1, SPEAR_ACT_NONE, 0, 0};
+        if (launch_stream<0>(d, bm, nt, s) != hipSuccess)
             return SPEAR_E_HIP;
     } else {
         LinearArgs a;
