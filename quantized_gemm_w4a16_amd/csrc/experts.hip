@@ -157,53 +157,129 @@ struct GroupArgs {
     int32_t div;              // a row's source is slot / div (topk for up, 1 for down)
     int32_t act, glu;
     int32_t ncb;              // channel blocks: the grid's fastest index
+    const int32_t *ids;       // few slots: the blocks' own plan
+    int32_t slots, E;
 };
+
+struct JoinArgs {
+    const float *d;           // [slots][N]
+    const int32_t *ids;
+    const float *weights;
+    const uint16_t *res;
+    uint16_t *y;
+    int64_t M, N;
+    int32_t topk, E;
+};
+
+// All of the arguments in one batch at entry (fetched where they are used, each
+// batch is a round trip before the first load).
+__device__ __forceinline__ void pin_group_args(const GroupArgs &a)
+{
+    pin_arg(a.x); pin_arg(a.packed); pin_arg(a.scales); pin_arg(a.zeros); pin_arg(a.bias);
+    pin_arg(a.out); pin_arg(a.ntiles); pin_arg(a.tiles); pin_arg(a.list); pin_arg(a.N); pin_arg(a.K);
+    pin_arg(a.div); pin_arg(a.act); pin_arg(a.glu); pin_arg(a.ncb); pin_arg(a.ids); pin_arg(a.slots);
+    pin_arg(a.E);
+}
+
+// Few slots: the most that a workgroup looks through by itself.
+constexpr int FEW_SLOTS = 64;
 
 // What depths past K read: zeros (16 bytes a lane of 16).
 __device__ __align__(256) static uint8_t g_zeros[256];
 
 // The streaming product: a workgroup of NW waves takes a row tile of up to BM
 // rows and 16 FC NW channels, wave w 16 FC of them over all of K.  Weights go
-// from memory to registers, a chunk of 512 depths (4 FC 16-byte loads a lane)
-// ahead of the one in use, and are unpacked once for all the tile's rows; the
-// rows go by DMA to two LDS buffers a chunk deep (1 KB a row, its 16-byte
+// from memory to registers, RING - 1 chunks of 512 depths (4 FC 16-byte loads a
+// lane) ahead of the one in use, and are unpacked once for all the tile's rows;
+// the rows go by DMA to RING LDS buffers a chunk deep (1 KB a row, its 16-byte
 // pieces swizzled by row % 16 on the way; zeros past K), with one barrier a
 // chunk.  Lane (c, g) holds channel c's 32 codes k = 128 s + 32 g .. + 31 of
 // step s as one load, and reads the same depths of its token row as four.  The
 // rows' sums, which remove the unpacking's offset, are shared out over the
 // waves by depth and meet in LDS.  Rows past the tile's end repeat the last one
 // and are not stored: an output depends on its own row alone.
-constexpr int SC = 512;                                   // depths of a chunk
-
-template <int BM, int NW, int FC, int UP>
+// PLAN 1 (few slots): no plan was launched.  The block's tile is (part, group):
+// the group an expert, or with fewer slots than experts a slot whose expert no
+// earlier slot has; each wave finds that expert's slots in ids by a ballot, and
+// the block takes the part-th 16 of them.
+template <int BM, int NW, int FC, int UP, int PLAN, int RING, int SC>
 __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
 {
-    constexpr int NF = BM / 16, NI = BM / NW;
-    static_assert(BM % NW == 0 && 16 % NW == 0, "rows and depth pieces over waves");
-    __shared__ __attribute__((aligned(16))) uint8_t s_x0[BM * 1024];
-    __shared__ __attribute__((aligned(16))) uint8_t s_x1[BM * 1024];
+    constexpr int NF = BM / 16, NS = SC / 128;            // fragments; steps of a chunk
+    constexpr int RB = 2 * SC, RI = 1024 / RB;            // bytes of a row's chunk; rows a DMA takes
+    constexpr int NI = BM / (RI * NW), NP = 4 * NS / NW;  // row DMAs, and depth pieces of the sums, a wave
+    static_assert(NI * RI * NW == BM && NP * NW == 4 * NS, "rows and depth pieces over waves");
+    static_assert(RING == 2 || RING == 4, "one LDS object a buffer");
+    __shared__ __attribute__((aligned(16))) uint8_t s_x0[BM * RB], s_x1[BM * RB];
+    __shared__ __attribute__((aligned(16))) uint8_t s_x2[RING > 2 ? BM * RB : 16], s_x3[RING > 2 ? BM * RB : 16];
     __shared__ float s_rs[NW][BM];
+    uint8_t *const ring[4] = {s_x0, s_x1, s_x2, s_x3};
+    pin_group_args(a);
     const int tile = (int)(blockIdx.x / (uint32_t)a.ncb), cb = (int)(blockIdx.x % (uint32_t)a.ncb);
-    const Tile q = a.tiles[tile];                         // (the table has room for every block)
-    if (tile >= *a.ntiles)
-        return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
+    Tile q;
+    uint64_t mine = 0;                                    // PLAN: the expert's slots from the tile's first on
+    if constexpr (PLAN != 0) {
+        const int groups = a.slots < a.E ? a.slots : a.E;
+        const int part = tile / groups, g = tile - part * groups;
+        const int id = lane < a.slots ? a.ids[lane] : -1;
+        const int e = a.slots < a.E ? __builtin_amdgcn_readlane(id, g) : g;
+        mine = __ballot(id == e && lane < a.slots);
+        const int cnt = __popcll(mine) - 16 * part;
+        if (e < 0 || e >= a.E || cnt <= 0 || (a.slots < a.E && __builtin_ctzll(mine) != g))
+            return;
+        for (int i = 0; i < 16 * part; i++)
+            mine &= mine - 1;
+        q = {e, 0, cnt < 16 ? cnt : 16, 0};
+    } else {
+        q = a.tiles[tile];                                // (the table has room for every block)
+        if (tile >= *a.ntiles)
+            return;
+    }
+    auto slot_of = [&](int r) __attribute__((always_inline)) {
+        if constexpr (PLAN != 0) {
+            uint64_t m = mine;                            // the r-th set bit
+            for (int i = 0; i < r; i++)
+                m &= m - 1;
+            return (int)__builtin_ctzll(m);
+        } else {
+            return a.list[q.pos + r];
+        }
+    };
     const int64_t N = a.N, K = a.K;
     const int64_t n0 = ((int64_t)cb * NW + wave) * (16 * FC);
     const int64_t base = (int64_t)q.e * N;
-    const int nf = (q.cnt + 15) / 16;                     // fragments in use
     const int64_t C = (K + SC - 1) / SC;
+    // The epilogue's operands, without branches.  Their lines are cold, a round
+    // trip of 2 to 3 us: with registers to spare (16-row tiles) they are loaded
+    // ahead of the stream, else in one go behind it.
+    constexpr bool EARLY = BM == 16;
+    float sc[FC][4], b[FC][4];
+    uint32_t zr[FC][4];
+    auto operands = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < FC; j++) {
+            const int64_t n = n0 + 16 * j + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int64_t nn = n + i < N ? n + i : N - 1;
+                sc[j][i] = a.scales[base + nn];
+                zr[j][i] = load_zero_byte(a.zeros ? a.zeros + base : nullptr, a.scales + base, nn);
+            }
+            epi_load_bias(a.bias ? a.bias + base : nullptr, a.scales + base, n, N, b[j]);
+        }
+    };
     const uint8_t *wr[FC];
 #pragma unroll
     for (int j = 0; j < FC; j++) {
         const int64_t n = n0 + 16 * j + lr;
         wr[j] = a.packed + (base + (n < N ? n : N - 1)) * (K / 2) + 16 * lg;
     }
-    auto load_w = [&](int64_t c, u32x4 (&w)[FC][4]) __attribute__((always_inline)) {
+    auto load_w = [&](int64_t c, u32x4 (&w)[FC][NS]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 4; t++) {
+        for (int t = 0; t < NS; t++) {
             // past K: the row's first codes, which meet zeros
             const bool in = SC * c + 128 * t + 32 * lg < K;
 #pragma unroll
@@ -211,28 +287,35 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
                 w[j][t] = ld16(in ? wr[j] + (SC * c + 128 * t) / 2 : wr[j] - 16 * lg);
         }
     };
-    // rows wave, wave + NW, ... of the tile: lane l takes piece l ^ (row % 16)
+    u32x4 w[RING][FC][NS];
+#pragma unroll
+    for (int j = 0; j < RING; j++)
+        load_w(j < C ? j : C - 1, w[j]);
+    if constexpr (EARLY)
+        operands();
+    // DMA i of a wave fills 1 KB: RI rows from RI (wave + NW i) on, lane l the
+    // piece p ^ (row % 16) of row l / (64 / RI), p = l % (64 / RI)
     const uint16_t *xs[NI];
+    int xk[NI];
 #pragma unroll
     for (int i = 0; i < NI; i++) {
-        const int r = wave + NW * i;
+        const int r = RI * (wave + NW * i) + (RI > 1 ? lane / (64 / RI) : 0);
         const int rr = r < q.cnt ? r : q.cnt - 1;
-        xs[i] = a.x + (int64_t)(a.list[q.pos + rr] / a.div) * K + 8 * (lane ^ (r & 15));
+        xk[i] = 8 * ((lane % (64 / RI)) ^ (r & 15));
+        xs[i] = a.x + (int64_t)(slot_of(rr) / a.div) * K + xk[i];
     }
     auto issue_x = [&](int64_t c, uint8_t *buf) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            const int r = wave + NW * i;
-            const void *src = SC * c + 8 * (lane ^ (r & 15)) < K ? (const void *)(xs[i] + SC * c)
-                                                                 : (const void *)(g_zeros + 16 * lr);
+            const void *src = SC * c + xk[i] < K ? (const void *)(xs[i] + SC * c) : (const void *)(g_zeros + 16 * lr);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                             (__attribute__((address_space(3))) void *)(buf + 1024 * r), 16, 0, 0);
+                                             (__attribute__((address_space(3))) void *)(buf + 1024 * (wave + NW * i)),
+                                             16, 0, 0);
         }
     };
-    u32x4 w0[FC][4], w1[FC][4];
-    issue_x(0, s_x0);
-    __builtin_amdgcn_sched_barrier(0);
-    load_w(0, w0);
+#pragma unroll
+    for (int j = 0; j < RING; j++)
+        issue_x(j < C ? j : C - 1, ring[j]);
 
     f32x4 acc[FC][NF], rs[NF];
 #pragma unroll
@@ -247,15 +330,15 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
     int xo[4];
 #pragma unroll
     for (int d = 0; d < 4; d++)
-        xo[d] = lr * 1024 + (((4 * lg + d) ^ lr) << 4);
-    // All four steps of a chunk, past K with zero rows, and then this wave's
-    // share of the rows' sums.  No branch: it would leave weight loads pending
-    // where paths meet, and the compiler would wait for everything there; and
-    // after a matrix instruction and a taken branch this toolchain can leave out
-    // the wait states before its result is read.  FR: fragments taken.
-    auto use = [&](auto FR, const uint8_t *buf, const u32x4 (&w)[FC][4]) __attribute__((always_inline)) {
+        xo[d] = lr * RB + (((4 * lg + d) ^ lr) << 4);
+    // All steps of a chunk, past K with zero rows, and then this wave's share of
+    // the rows' sums.  No branch: it would leave weight loads pending where
+    // paths meet, and the compiler would wait for everything there; and after a
+    // matrix instruction and a taken branch this toolchain can leave out the
+    // wait states before its result is read.  FR: fragments taken.
+    auto use = [&](auto FR, const uint8_t *buf, const u32x4 (&w)[FC][NS]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 4; t++)
+        for (int t = 0; t < NS; t++)
 #pragma unroll
             for (int d = 0; d < 4; d++) {
                 u32x4 wv[FC];
@@ -264,61 +347,66 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
                     wv[j] = unpack8(w[j][t][d]);
 #pragma unroll
                 for (int f = 0; f < decltype(FR)::value; f++) {
-                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(buf + xo[d] + 256 * t + 16384 * f);
+                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(buf + xo[d] + 256 * t + 16 * RB * f);
 #pragma unroll
                     for (int j = 0; j < FC; j++)
                         acc[j][f] = mfma16(wv[j], xv, acc[j][f]);
                 }
             }
 #pragma unroll
-        for (int i = 0; i < 16 / NW; i++) {
+        for (int i = 0; i < NP; i++) {
             const int p = wave + NW * i;                  // piece 4 t + d
-            const int off = lr * 1024 + 256 * (p >> 2) + (((4 * lg + (p & 3)) ^ lr) << 4);
+            const int off = lr * RB + 256 * (p >> 2) + (((4 * lg + (p & 3)) ^ lr) << 4);
 #pragma unroll
             for (int f = 0; f < decltype(FR)::value; f++)
-                rs[f] = mfma16(ones, *reinterpret_cast<const u32x4 *>(buf + off + 16384 * f), rs[f]);
+                rs[f] = mfma16(ones, *reinterpret_cast<const u32x4 *>(buf + off + 16 * RB * f), rs[f]);
         }
     };
     auto run = [&](auto FR) __attribute__((always_inline)) {
-        int64_t c = 0;
-        for (; c + 1 < C; c += 2) {
-            // chunk c: its rows' DMAs are older than the weight loads behind them
-            wait_vmcnt<4 * FC>();
-            bare_barrier();
-            issue_x(c + 1, s_x1);
-            __builtin_amdgcn_sched_barrier(0);            // keeps that order
-            load_w(c + 1, w1);
-            use(FR, s_x0, w0);
-            wait_vmcnt<4 * FC>();
-            bare_barrier();
-            issue_x(c + 2 < C ? c + 2 : c + 1, s_x0);
-            __builtin_amdgcn_sched_barrier(0);
-            load_w(c + 2 < C ? c + 2 : c + 1, w0);
-            use(FR, s_x1, w1);
-        }
+        // Younger than the rows of the next chunk: its weights, and the further chunks.
+        constexpr int WAIT = NS * FC + (RING - 2) * (NI + NS * FC);
+        static_assert(WAIT < 64, "vmcnt");
         wait_vmcnt<0>();
-        if (c < C) {
-            bare_barrier();
-            use(FR, s_x0, w0);
+        bare_barrier();
+        int64_t c = 0;
+        for (; c + 2 * RING <= C; c += RING) {
+#pragma unroll
+            for (int j = 0; j < RING; j++) {
+                use(FR, ring[j], w[j]);
+                wait_vmcnt<WAIT>();                       // this wave's rows of the next chunk
+                bare_barrier();                           // every wave's; chunk c + j free
+                issue_x(c + j + RING, ring[j]);
+                __builtin_amdgcn_sched_barrier(0);        // keeps the order the wait counts on
+                load_w(c + j + RING, w[j]);
+            }
         }
-        // The epilogue's operands, without branches: one round trip.
-        float sc[FC][4], b[FC][4];
-        uint32_t zr[FC][4];
+        // the last RING .. 2 RING - 1 chunks (fewer where K is short)
+        wait_vmcnt<0>();
+        bare_barrier();
+#pragma unroll
+        for (int j = 0; j < RING; j++)
+            if (c + j < C) {
+                use(FR, ring[j], w[j]);
+                if (j < RING - 1 && c + j + RING < C) {
+                    bare_barrier();
+                    issue_x(c + j + RING, ring[j]);
+                    load_w(c + j + RING, w[j]);
+                }
+            }
+        if (c + RING < C) {
+            wait_vmcnt<0>();
+            bare_barrier();
+#pragma unroll
+            for (int j = 0; j < RING - 1; j++)
+                if (c + RING + j < C)
+                    use(FR, ring[j], w[j]);
+        }
+        if constexpr (!EARLY)
+            operands();
         int32_t slot[NF];
 #pragma unroll
-        for (int j = 0; j < FC; j++) {
-            const int64_t n = n0 + 16 * j + 4 * lg;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int64_t nn = n + i < N ? n + i : N - 1;
-                sc[j][i] = a.scales[base + nn];
-                zr[j][i] = load_zero_byte(a.zeros ? a.zeros + base : nullptr, a.scales + base, nn);
-            }
-            epi_load_bias(a.bias ? a.bias + base : nullptr, a.scales + base, n, N, b[j]);
-        }
-#pragma unroll
         for (int f = 0; f < decltype(FR)::value; f++) {
-            slot[f] = a.list[q.pos + (16 * f + lr < q.cnt ? 16 * f + lr : 0)];
+            slot[f] = slot_of(16 * f + lr < q.cnt ? 16 * f + lr : 0);
             if (lg == 0)
                 s_rs[wave][16 * f + lr] = rs[f][0];
         }
@@ -347,17 +435,22 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
             }
         }
     };
-    if (NF > 1 && 2 * nf <= NF)                           // half the tile is empty
-        run(std::integral_constant<int, NF / 2 ? NF / 2 : 1>());
+    const int nf = (q.cnt + 15) / 16;                     // fragments in use
+    if (NF >= 4 && nf == 3)
+        run(std::integral_constant<int, NF >= 4 ? 3 : 1>());
+    else if (NF >= 4 && nf == 2)
+        run(std::integral_constant<int, NF >= 4 ? 2 : 1>());
+    else if (NF > 1 && nf == 1)
+        run(std::integral_constant<int, 1>());
     else
         run(std::integral_constant<int, NF>());
 }
 
-template <int BM, int NW, int FC, int UP>
+template <int BM, int NW, int FC, int UP, int PLAN, int RING, int SC>
 hipError_t launch_stream_t(GroupArgs a, int64_t tiles, hipStream_t s)
 {
     a.ncb = (int32_t)((a.N + 16 * FC * NW - 1) / (16 * FC * NW));
-    hipLaunchKernelGGL((stream_kernel<BM, NW, FC, UP>), dim3((unsigned)(tiles * a.ncb)), dim3(64 * NW), 0, s, a);
+    hipLaunchKernelGGL((stream_kernel<BM, NW, FC, UP, PLAN, RING, SC>), dim3((unsigned)(tiles * a.ncb)), dim3(64 * NW), 0, s, a);
     return hipGetLastError();
 }
 
@@ -365,23 +458,130 @@ template <int UP>
 hipError_t launch_stream(const GroupArgs &a, int bm, int64_t tiles, hipStream_t s)
 {
     if (bm == 64)
-        return launch_stream_t<64, 8, 2, UP>(a, tiles, s);
+        return launch_stream_t<64, 8, 2, UP, 0, 2, 512>(a, tiles, s);
     if (bm == 32)
-        return launch_stream_t<32, 8, 2, UP>(a, tiles, s);
-    return launch_stream_t<16, 4, 1, UP>(a, tiles, s);
+        return launch_stream_t<32, 8, 2, UP, 0, 2, 512>(a, tiles, s);
+    return launch_stream_t<16, 4, 1, UP, 0, 2, 512>(a, tiles, s);
+}
+
+// ------------------------------------------------- few slots: down and join
+// One launch for the second layer and the join: a workgroup takes 16 output
+// channels, its 8 waves the experts in use (a wave an expert at a time, its 16
+// channels of weights straight to registers, the rows of h from L2), each
+// slot's sums go to LDS, and after one barrier a thread takes one channel of a
+// token over its slots in order, as the join does.  With at most four experts
+// in use two waves share one by depth.
+struct FewArgs {
+    GroupArgs g;              // the second layer: x is h by slot
+    JoinArgs j;
+};
+constexpr int FW_WAVES = 8;
+constexpr int FW_B = 8;                                   // 128-deep steps loaded at once
+
+__global__ __launch_bounds__(64 * FW_WAVES) void few_down_kernel(const FewArgs a)
+{
+    __shared__ float s_d[2][FEW_SLOTS][17];
+    pin_group_args(a.g);
+    pin_arg(a.j.weights); pin_arg(a.j.res); pin_arg(a.j.y); pin_arg(a.j.M); pin_arg(a.j.topk);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int64_t N = a.g.N, K = a.g.K, n0 = (int64_t)blockIdx.x * 16;
+    const int slots = a.g.slots, E = a.g.E;
+    int id = lane < slots ? a.g.ids[lane] : -1;           // lane: a slot's expert
+    id = id >= 0 && id < E ? id : -1;
+    const float wt = lane < slots ? a.j.weights[lane] : 0.f;
+    int jobs = 0;                                         // experts in use
+    for (int s = 0; s < slots; s++) {
+        const int e = __builtin_amdgcn_readlane(id, s);
+        jobs += e >= 0 && __builtin_ctzll(__ballot(id == e)) == s;
+    }
+    const int topk = a.j.topk, M = (int)a.j.M;
+    const int64_t rn = n0 + (tid & 15);                   // the join's first residual, ahead of the stream
+    const float res0 = a.j.res && (tid >> 4) < M && rn < N ? bf16f(a.j.res[(int64_t)(tid >> 4) * N + rn]) : 0.f;
+    const int parts = 2 * jobs <= FW_WAVES ? 2 : 1, part = wave % parts;
+    const int64_t S = (K + 127) / 128, t0 = part * S / parts, t1 = (part + 1) * S / parts;
+    const int64_t nc = n0 + lr < N ? n0 + lr : N - 1;
+    const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    for (int s = 0, job = 0; s < slots; s++) {
+        const int e = __builtin_amdgcn_readlane(id, s);
+        uint64_t rows = __ballot(id == e);                // the expert's slots
+        if (e < 0 || __builtin_ctzll(rows) != s)
+            continue;
+        if (job++ % (FW_WAVES / parts) != wave / parts)
+            continue;
+        const int64_t base = (int64_t)e * N;
+        const uint8_t *wr = a.g.packed + (base + nc) * (K / 2) + 16 * lg;
+        float sc[4], b[4];
+        uint32_t zr[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int64_t nn = n0 + 4 * lg + i < N ? n0 + 4 * lg + i : N - 1;
+            sc[i] = a.g.scales[base + nn];
+            zr[i] = load_zero_byte(a.g.zeros ? a.g.zeros + base : nullptr, a.g.scales + base, nn);
+        }
+        epi_load_bias(a.g.bias ? a.g.bias + base : nullptr, a.g.scales + base, n0 + 4 * lg, N, b);
+        const float bf = a.g.bias && part == 0 ? 1.f : 0.f;
+        while (rows) {                                    // 16 slots at a time
+            int slot = -1;                                // lane row lr: the lr-th of them
+            for (int i = 0; i < 16; i++) {
+                if (lr == i && rows)
+                    slot = __builtin_ctzll(rows);
+                rows &= rows ? rows - 1 : 0;
+            }
+            const uint16_t *hr = a.g.x + (int64_t)(slot < 0 ? 0 : slot) * K + 32 * lg;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, rs = acc;
+            for (int64_t t = t0; t < t1; t += FW_B) {
+                u32x4 w[FW_B], xv[FW_B][4];
+#pragma unroll
+                for (int i = 0; i < FW_B; i++) {
+                    const int64_t k = 128 * (t + i);
+                    const bool kv = t + i < t1 && k + 32 * lg < K;
+                    w[i] = ld16(kv ? wr + k / 2 : wr - 16 * lg);
+#pragma unroll
+                    for (int d = 0; d < 4; d++)
+                        xv[i][d] = kv && slot >= 0 ? ld16(hr + k + 8 * d) : zero4();
+                }
+#pragma unroll
+                for (int i = 0; i < FW_B; i++)
+#pragma unroll
+                    for (int d = 0; d < 4; d++) {
+                        acc = mfma16(unpack8(w[i][d]), xv[i][d], acc);
+                        rs = mfma16(ones, xv[i][d], rs);
+                    }
+            }
+            if (slot >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    s_d[part][slot][4 * lg + i] =
+                        sc[i] * __builtin_fmaf(-(UNPACK_OFF + zero_point(a.g.zeros, zr[i])), rs[0],
+                                               UNPACK_SCALE * acc[i]) + (bf != 0.f ? b[i] : 0.f);
+            }
+        }
+    }
+    __syncthreads();
+    for (int i0 = 0; i0 < 16 * M; i0 += 64 * FW_WAVES) {  // uniform: every lane shuffles
+        const int i = i0 + tid, m = i >> 4;
+        const int64_t n = n0 + (i & 15);
+        const bool in = m < M && n < N;
+        float o = i0 == 0 ? res0 : in && a.j.res ? bf16f(a.j.res[m * N + n]) : 0.f;
+        for (int j = 0; j < topk; j++) {
+            const int slot = m < M ? m * topk + j : 0;
+            const int e = __shfl(id, slot);
+            const float ws = __shfl(wt, slot);
+            if (in && e >= 0) {
+                const float d = parts == 2 ? s_d[0][slot][i & 15] + s_d[1][slot][i & 15] : s_d[0][slot][i & 15];
+                o = __builtin_fmaf(ws, d, o);
+            }
+        }
+        if (in)
+            a.j.y[m * N + n] = f2bf(o);
+    }
 }
 
 // ---------------------------------------------------------------------- join
 // A thread takes four channels of one token.
-struct JoinArgs {
-    const float *d;           // [slots][N]
-    const int32_t *ids;
-    const float *weights;
-    const uint16_t *res;
-    uint16_t *y;
-    int64_t M, N;
-    int32_t topk, E;
-};
+constexpr int JB = 8;
 
 __global__ __launch_bounds__(256) void join_kernel(const JoinArgs a)
 {
@@ -392,20 +592,31 @@ __global__ __launch_bounds__(256) void join_kernel(const JoinArgs a)
     const int64_t m = idx / nq, n = 4 * (idx % nq), N = a.N;
     float o[4];
     epi_load_res<0>(a.res, m, n, 0, N, o);
-    for (int j = 0; j < a.topk; j++) {
-        const int64_t slot = m * a.topk + j;
-        const int e = a.ids[slot];
-        if (e < 0 || e >= a.E)
-            continue;
-        const float w = a.weights[slot];
-        float v[4];
-        epi_load_res<1>(a.d, slot, n, 0, N, v);
+    // JB slots' loads in flight at once; a slot without an expert has an unwritten
+    // row, whose values are dropped
+    for (int j0 = 0; j0 < a.topk; j0 += JB) {
+        float v[JB][4], w[JB];
+        int e[JB];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            o[i] = __builtin_fmaf(w, v[i], o[i]);
+        for (int j = 0; j < JB; j++) {
+            const int64_t slot = m * a.topk + (j0 + j < a.topk ? j0 + j : a.topk - 1);
+            e[j] = j0 + j < a.topk ? a.ids[slot] : -1;
+            w[j] = a.weights[slot];
+            epi_load_res<1>(a.d, slot, n, 0, N, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < JB; j++)
+            if (e[j] >= 0 && e[j] < a.E) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    o[i] = __builtin_fmaf(w[j], v[j][i], o[i]);
+            }
     }
     epi_store<0>(a.y, m, n, 0, N, o);
 }
+
+// Two launches: few slots, and few of them an expert.
+bool few(int64_t slots, int32_t E) { return slots <= FEW_SLOTS && tile_rows(slots, E) == XT; }
 
 bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 
@@ -460,17 +671,30 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     int32_t *ntiles = reinterpret_cast<int32_t *>(ws + L.hdr);
     Tile *tiles = reinterpret_cast<Tile *>(ws + L.tiles);
     int32_t *list = reinterpret_cast<int32_t *>(ws + L.list);
+    if (few(L.slots, w->E)) {
+        GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, nullptr, nullptr, nullptr,
+                       NU, K, topk, w->act, w->glu, 0, ids, (int32_t)L.slots, w->E};
+        const int64_t blocks = (L.slots < w->E ? L.slots : w->E) * ((L.slots + 15) / 16);
+        if (launch_stream_t<16, 4, 1, 1, 1, 4, 512>(u, blocks, s) != hipSuccess)
+            return SPEAR_E_HIP;
+        const FewArgs f = {{reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
+                            w->down_bias, nullptr, nullptr, nullptr, nullptr, N, I, 1, SPEAR_ACT_NONE, 0, 0, ids,
+                            (int32_t)L.slots, w->E},
+                           {nullptr, ids, weights, residual, y, M, N, topk, w->E}};
+        hipLaunchKernelGGL(few_down_kernel, dim3((unsigned)((N + 15) / 16)), dim3(64 * FW_WAVES), 0, s, f);
+        return hipGetLastError() == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
+    }
     hipLaunchKernelGGL(plan_kernel, dim3((unsigned)w->E), dim3(1024), 0, s, ids, (int32_t)L.slots, w->E, bm,
                        reinterpret_cast<uint32_t *>(ws + L.zeros), ntiles, tiles, list);
     if (hipGetLastError() != hipSuccess)
         return SPEAR_E_HIP;
     if (bm <= 64) {
         const GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, ntiles, tiles, list,
-                             NU, K, topk, w->act, w->glu, 0};
+                             NU, K, topk, w->act, w->glu, 0, ids, 0, w->E};
         if (launch_stream<1>(u, bm, nt, s) != hipSuccess)
             return SPEAR_E_HIP;
         const GroupArgs d = {reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
-                             w->down_bias, ws + L.d, ntiles, tiles, list, N, I, 1, SPEAR_ACT_NONE, 0, 0};
+                             w->down_bias, ws + L.d, ntiles, tiles, list, N, I, 1, SPEAR_ACT_NONE, 0, 0, ids, 0, w->E};
         if (launch_stream<0>(d, bm, nt, s) != hipSuccess)
             return SPEAR_E_HIP;
     } else {
