@@ -203,7 +203,7 @@ __device__ __align__(256) static uint8_t g_zeros[256];
 // earlier slot has; each wave finds that expert's slots in ids by a ballot, and
 // the block takes the part-th 16 of them.
 template <int BM, int NW, int FC, int UP, int PLAN, int RING, int SC>
-__global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) void stream_kernel(const GroupArgs a)
 {
     constexpr int NF = BM / 16, NS = SC / 128;            // fragments; steps of a chunk
     constexpr int RB = 2 * SC, RI = 1024 / RB;            // bytes of a row's chunk; rows a DMA takes
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
     for (int i = 0; i < NI; i++) {
         const int r = RI * (wave + NW * i) + (RI > 1 ? lane / (64 / RI) : 0);
         const int rr = r < q.cnt ? r : q.cnt - 1;
-        xk[i] = 8 * ((lane % (64 / RI)) ^ (r & 15));
+        xk[i] = 8 * ((lane % (64 / RI)) ^ row_turn(r & 15));
         xs[i] = a.x + (int64_t)(slot_of(rr) / a.div) * K + xk[i];
     }
     auto issue_x = [&](int64_t c, uint8_t *buf) __attribute__((always_inline)) {
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
     int xo[4];
 #pragma unroll
     for (int d = 0; d < 4; d++)
-        xo[d] = lr * RB + (((4 * lg + d) ^ lr) << 4);
+        xo[d] = lr * RB + (((4 * lg + d) ^ row_turn(lr)) << 4);
     // All steps of a chunk, past K with zero rows, and then this wave's share of
     // the rows' sums.  No branch: it would leave weight loads pending where
     // paths meet, and the compiler would wait for everything there; and after a
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(const GroupArgs a)
 #pragma unroll
         for (int i = 0; i < NP; i++) {
             const int p = wave + NW * i;                  // piece 4 t + d
-            const int off = lr * RB + 256 * (p >> 2) + (((4 * lg + (p & 3)) ^ lr) << 4);
+            const int off = lr * RB + 256 * (p >> 2) + (((4 * lg + (p & 3)) ^ row_turn(lr)) << 4);
 #pragma unroll
             for (int f = 0; f < decltype(FR)::value; f++)
                 rs[f] = mfma16(ones, *reinterpret_cast<const u32x4 *>(buf + off + 16 * RB * f), rs[f]);
@@ -458,7 +458,7 @@ template <int UP>
 hipError_t launch_stream(const GroupArgs &a, int bm, int64_t tiles, hipStream_t s)
 {
     if (bm == 64)
-        return launch_stream_t<64, 8, 2, UP, 0, 2, 512>(a, tiles, s);
+        return launch_stream_t<64, 8, 1, UP, 0, 2, 256>(a, tiles, s);
     if (bm == 32)
         return launch_stream_t<32, 8, 2, UP, 0, 2, 512>(a, tiles, s);
     return launch_stream_t<16, 4, 1, UP, 0, 2, 512>(a, tiles, s);

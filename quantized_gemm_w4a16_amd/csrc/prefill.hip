@@ -578,7 +578,7 @@ __global__ __launch_bounds__(512) void prepass2_kernel(const LinearArgs a)
 // depend on the DMAs into the others and does not wait for them.
 // Layouts are XOR-swizzled on the global side so the rows one MFMA operand
 // reads fall in distinct banks: activation rows (256 bytes of bf16) swap their
-// 16-byte chunks by row % 16, weight rows (64 bytes of nibbles) by
+// 16-byte chunks by row_turn(row % 16), weight rows (64 bytes of nibbles) by
 // (row / 2) % 4.  Weights are unpacked as they leave LDS (the packed word
 // order makes the unpacked pairs line up with the activations' own pairs).
 // Chunks past K are DMA'd from a zero block of the workspace.  The per-token
@@ -596,7 +596,7 @@ constexpr int G2_STAGES = 3;
 constexpr int G2_WBA = 256 * 64;                          // bytes of a 256-channel weight stage
 
 // LDS byte offsets: chunk c (0..15) of activation row r, chunk c (0..3) of weight row r.
-__device__ __forceinline__ uint32_t g2_xoff(int r, int c) { return r * 256 + ((c ^ (r & 15)) << 4); }
+__device__ __forceinline__ uint32_t g2_xoff(int r, int c) { return r * 256 + ((c ^ row_turn(r & 15)) << 4); }
 __device__ __forceinline__ uint32_t g2_woff(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
 
 // Four 16-byte LDS reads.
@@ -748,7 +748,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
 
     // DMA of one stage.  Activations: instruction j of wave w fills rows
     // 4 (G2_XI w + j) .. +3, lane i the slot i of that 1 KB (chunk (i % 16) ^
-    // (row % 16) of its row); rows past M repeat row M - 1 (never stored).
+    // row_turn(row % 16) of its row); rows past M repeat row M - 1 (never stored).
     // Weights: instruction j fills rows 16 (G2_WI w + j) .. +15, lane i the slot
     // i of that 1 KB (chunk (i % 4) ^ ((row / 2) % 4)); with 4-byte DMAs rows
     // 4 (G2_WI w + j) .. +3, lane i word i % 4 of slot i / 4.  Rows past N repeat
@@ -761,7 +761,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
 #pragma unroll
     for (int j = 0; j < G2_XI; j++) {
         const int r = 4 * (G2_XI * wave + j) + (lane >> 4);
-        const int c = (lane & 15) ^ (r & 15);
+        const int c = (lane & 15) ^ row_turn(r & 15);
         int64_t mm = m0 + r < M ? m0 + r : M - 1;
         if constexpr (GRP != 0)
             mm = glist[mm] / a.G.div;
