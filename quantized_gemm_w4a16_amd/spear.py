@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -126,16 +127,14 @@ def load():
                                             i32, i32, P]
     lib.spear_w4_linear_semifused.argtypes = [P, i64, ctypes.POINTER(_W4), ctypes.POINTER(_EC), P,
                                               P, ctypes.c_size_t, P, P, P, P]
-    lib.spear_w4_linear_epilogue.argtypes = [P, i64, ctypes.POINTER(_W4), ctypes.POINTER(_EC),
-                                             ctypes.POINTER(_Epilogue), P, i32, P,
-                                             ctypes.c_size_t, i32, P]
+    # (structs as pointers to their bytes)
+    lib.spear_w4_linear_epilogue.argtypes = [P, i64, P, P, P, P, i32, P, ctypes.c_size_t, i32, P]
     lib.spear_route_workspace_size.argtypes = [i64, i32]
     lib.spear_route_workspace_size.restype = ctypes.c_size_t
-    lib.spear_route.argtypes = [P, i64, i64, ctypes.POINTER(_Router), P, P, P, ctypes.c_size_t, P]
+    lib.spear_route.argtypes = [P, i64, i64, P, P, P, P, ctypes.c_size_t, P]
     lib.spear_w4_experts_workspace_size.argtypes = [i64, i32, i32, i64, i64]
     lib.spear_w4_experts_workspace_size.restype = ctypes.c_size_t
-    lib.spear_w4_experts.argtypes = [P, i64, ctypes.POINTER(_Experts), P, P, i32, P, P, P,
-                                     ctypes.c_size_t, P]
+    lib.spear_w4_experts.argtypes = [P, i64, P, P, P, i32, P, P, P, ctypes.c_size_t, P]
     lib.spear_set_wait_limit.argtypes = [ctypes.c_uint32]
     lib.spear_set_wait_limit.restype = None
     lib.spear_workspace_timeouts.argtypes = [P, ctypes.POINTER(i32), P]
@@ -214,6 +213,12 @@ class EC:
     @property
     def gate_h(self) -> int:
         return 0 if self.gate_w1 is None else int(self.gate_w1.shape[0])
+
+    def _packed(self) -> bytes:
+        return _PACK_EC(_at(self.A), _at(self.B), _at(self.w_gate), self.b, self.tau, self.hard,
+                        self.r, _at(self.g_out), _at(self.idx_out), _at(self.n_active_out),
+                        self.gate_h, self.alpha, _at(self.gate_w1), _at(self.gate_c1),
+                        _at(self.gate_w2), _at(self.gate_c2))
 
     def _c(self):
         return _EC(_ptr(self.A), _ptr(self.B), _ptr(self.w_gate), float(self.b), float(self.tau),
@@ -351,18 +356,19 @@ def _bad(fn: str, status: int, what: str):
 def _want(fn: str, name: str, t, dtypes, shape, device):
     """A tensor argument: its element type, shape, device, and no gaps between
     its elements (the library takes bare pointers and cannot see any of it)."""
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype not in dtypes:
         _bad(fn, E_ARG, f"{name} has type {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         _bad(fn, E_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if not t.is_contiguous():
-        _bad(fn, E_ARG, f"{name} is not contiguous")
     if t.device != device:
         _bad(fn, E_ARG, f"{name} is on {t.device}, not {device}")
+    _bad(fn, E_ARG, f"{name} is not contiguous")
 
 
 def _want_workspace(fn: str, t, device):
-    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device:
+    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
         _bad(fn, E_ARG, f"workspace has to be a contiguous uint8 tensor on {device}")
 
 
@@ -374,15 +380,10 @@ _U8 = (torch.uint8,)
 
 class _On:
     """The device and stream of one call: the arguments' device is current, and
-    what the call allocates belongs to its stream.  With the device current and
-    no stream given there is nothing to switch."""
+    what the call allocates belongs to its stream."""
 
-    def __init__(self, fn: str, device, stream):
-        if device.type != "cuda":
-            _bad(fn, E_ARG, f"tensors are on {device}, not on a GPU")
-        self.contexts = []
-        if device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
+    def __init__(self, device, stream):
+        self.contexts = [torch.cuda.device(device)]
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 # the null stream has no external handle
@@ -393,11 +394,39 @@ class _On:
     def __enter__(self):
         for c in self.contexts:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
+
+
+def _on(fn: str, device, stream, call):
+    """call(stream handle) with the device and stream current.  Small layers take
+    10 us on the GPU, so nothing is switched that already is as it should be."""
+    if device.type != "cuda":
+        _bad(fn, E_ARG, f"tensors are on {device}, not on a GPU")
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(_current_stream(device.index))
+    with _On(device, stream):
+        return call(_current_stream(device.index))
+
+
+def _public_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own raw query, where it has one (0.1 us for 1.2)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+
+# The C structs as packed bytes, a fifth of the time of filling ctypes
+# structures field by field.
+_PACK_W4 = struct.Struct("@PPPqq").pack
+_PACK_EC = struct.Struct("@PPPffiiPPPifPPPP").pack
+_PACK_EPILOGUE = struct.Struct("@PPii").pack
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 @dataclass
@@ -410,9 +439,6 @@ class Epilogue:
     glu: bool = False
     residual: Optional[torch.Tensor] = None
 
-    def _c(self):
-        return _Epilogue(_ptr(self.bias), _ptr(self.residual), int(self.act), int(self.glu))
-
 
 def spear_w4_linear_epilogue(x: torch.Tensor, w: W4, ep: Epilogue, ec: Optional[EC] = None,
                              y: Optional[torch.Tensor] = None, out_dtype: int = OUT_F32,
@@ -422,7 +448,7 @@ def spear_w4_linear_epilogue(x: torch.Tensor, w: W4, ep: Epilogue, ec: Optional[
     its kernels' epilogue: y [M][N], or [M][N/2] with ep.glu."""
     fn = "spear_w4_linear_epilogue"
     dev = x.device
-    M, NO = int(x.shape[0]), w.N // 2 if ep.glu else w.N
+    M, NO = x.shape[0], w.N // 2 if ep.glu else w.N
     dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
     _want(fn, "x", x, _BF16, (M, w.K), dev)
     if ep.bias is not None:
@@ -433,18 +459,22 @@ def spear_w4_linear_epilogue(x: torch.Tensor, w: W4, ep: Epilogue, ec: Optional[
         _want(fn, "y", y, (dt,), (M, NO), dev)
     if workspace is not None:
         _want_workspace(fn, workspace, dev)
-    with _On(fn, dev, stream) as s:
+
+    def call(s):
+        nonlocal y, workspace
         if y is None:
             y = torch.empty((M, NO), dtype=dt, device=dev)
         if workspace is None:
             workspace = new_workspace(M, w.N, w.K, ec.r if ec is not None else 0, dev)
-        wc, epc = w._c(), ep._c()
-        ecc = ec._c() if ec is not None else None
-        st = load().spear_w4_linear_epilogue(_ptr(x), M, ctypes.byref(wc),
-                                             ctypes.byref(ecc) if ecc is not None else None,
-                                             ctypes.byref(epc), _ptr(y), out_dtype,
-                                             _ptr(workspace), workspace.numel(), path, s)
-    _check(fn, st)
+        return load().spear_w4_linear_epilogue(
+            x.data_ptr(), M, _PACK_W4(_at(w.packed), _at(w.scales), _at(w.zeros), w.N, w.K),
+            None if ec is None else ec._packed(),
+            _PACK_EPILOGUE(_at(ep.bias), _at(ep.residual), ep.act, ep.glu),
+            y.data_ptr(), out_dtype, workspace.data_ptr(), workspace.numel(), path, s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
     return y
 
 
@@ -462,8 +492,8 @@ class Router:
         if bias is not None:
             _want("Router", "bias", bias, _F32, (E,), w.device)
         self.w, self.bias, self.E, self.K, self.topk = w, bias, E, K, int(topk)
-        self._s = _Router(_ptr(w), _ptr(bias), E, int(topk), int(score), int(n_group),
-                          int(topk_group), int(group_best), int(bool(renorm)), float(scale))
+        self._s = bytes(_Router(_ptr(w), _ptr(bias), E, int(topk), int(score), int(n_group),
+                                int(topk_group), int(group_best), int(bool(renorm)), float(scale)))
 
 
 def spear_route_workspace_size(M: int, E: int) -> int:
@@ -483,7 +513,8 @@ def spear_route(x: torch.Tensor, router: Router, weights: Optional[torch.Tensor]
     expert is left)."""
     fn = "spear_route"
     dev = x.device
-    M, shape = int(x.shape[0]), (int(x.shape[0]), router.topk)
+    M = x.shape[0]
+    shape = (M, router.topk)
     _want(fn, "x", x, _BF16, (M, router.K), router.w.device)
     if weights is not None:
         _want(fn, "weights", weights, _F32, shape, dev)
@@ -491,16 +522,21 @@ def spear_route(x: torch.Tensor, router: Router, weights: Optional[torch.Tensor]
         _want(fn, "ids", ids, _I32, shape, dev)
     if workspace is not None:
         _want_workspace(fn, workspace, dev)
-    with _On(fn, dev, stream) as s:
+
+    def call(s):
+        nonlocal weights, ids, workspace
         if weights is None:
             weights = torch.empty(shape, dtype=torch.float32, device=dev)
         if ids is None:
             ids = torch.empty(shape, dtype=torch.int32, device=dev)
         if workspace is None:
             workspace = new_route_workspace(M, router)
-        st = load().spear_route(_ptr(x), M, router.K, ctypes.byref(router._s), _ptr(weights),
-                                _ptr(ids), _ptr(workspace), workspace.numel(), s)
-    _check(fn, st)
+        return load().spear_route(x.data_ptr(), M, router.K, router._s, weights.data_ptr(),
+                                  ids.data_ptr(), workspace.data_ptr(), workspace.numel(), s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
     return weights, ids
 
 
@@ -530,7 +566,8 @@ class Experts:
                 _want(fn, name, t, dt, (E, n), dev)
         self.tensors = (up, up_scales, up_zeros, up_bias, down, down_scales, down_zeros, down_bias)
         self.E, self.K, self.I, self.N, self.device = E, K, I, N, dev
-        self._s = _Experts(*(_ptr(t) for t in self.tensors), K, I, N, E, int(act), int(bool(glu)))
+        self._s = bytes(_Experts(*(_ptr(t) for t in self.tensors), K, I, N, E, int(act),
+                                 int(bool(glu))))
 
 
 def spear_w4_experts_workspace_size(M: int, topk: int, E: int, I: int, N: int) -> int:
@@ -550,7 +587,7 @@ def spear_w4_experts(x: torch.Tensor, experts: Experts, ids: torch.Tensor, weigh
     expert; ids outside [0, E) add nothing."""
     fn = "spear_w4_experts"
     dev = x.device
-    M, topk, N = int(x.shape[0]), int(ids.shape[1]), experts.N
+    M, topk, N = x.shape[0], ids.shape[1], experts.N
     _want(fn, "x", x, _BF16, (M, experts.K), experts.device)
     _want(fn, "ids", ids, _I32, (M, topk), dev)
     _want(fn, "weights", weights, _F32, (M, topk), dev)
@@ -560,15 +597,20 @@ def spear_w4_experts(x: torch.Tensor, experts: Experts, ids: torch.Tensor, weigh
         _want(fn, "y", y, _BF16, (M, N), dev)
     if workspace is not None:
         _want_workspace(fn, workspace, dev)
-    with _On(fn, dev, stream) as s:
+
+    def call(s):
+        nonlocal y, workspace
         if y is None:
             y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         if workspace is None:
             workspace = new_experts_workspace(M, topk, experts)
-        st = load().spear_w4_experts(_ptr(x), M, ctypes.byref(experts._s), _ptr(ids),
-                                     _ptr(weights), topk, _ptr(residual), _ptr(y),
-                                     _ptr(workspace), workspace.numel(), s)
-    _check(fn, st)
+        return load().spear_w4_experts(x.data_ptr(), M, experts._s, ids.data_ptr(),
+                                       weights.data_ptr(), topk, _at(residual), y.data_ptr(),
+                                       workspace.data_ptr(), workspace.numel(), s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
     return y
 
 

@@ -155,3 +155,15 @@ def test_binding_checks_its_tensors():
     refused(E_SHAPE, sp.spear_w4_linear_epilogue, x, layer, sp.Epilogue(bias=torch.zeros(32)))
     refused(E_ARG, sp.spear_w4_linear_epilogue, x, layer, sp.Epilogue(residual=torch.zeros(4, 64, dtype=bf)))
     refused(E_SHAPE, sp.spear_w4_linear_epilogue, x, layer, sp.Epilogue(glu=True), y=torch.zeros(4, 64))
+
+
+def test_packed_structs_are_the_ctypes_ones():
+    """The byte strings that the binding passes have the C structs' layout."""
+    t = [torch.zeros(8, 32) for _ in range(10)]
+    w = sp.W4(t[0], t[1], None, 8, 32)
+    assert sp._PACK_W4(t[0].data_ptr(), t[1].data_ptr(), 0, 8, 32) == bytes(w._c())
+    e = sp.EC(t[0], t[1], t[2], 0.5, 0.25, 1, t[3], t[4], t[5], t[6], t[7], t[8], t[9], 0.75)
+    assert e._packed() == bytes(e._c())
+    e = sp.EC(t[0], t[1], t[2])
+    assert e._packed() == bytes(e._c())
+    assert sp._PACK_EPILOGUE(5, 7, 2, True) == bytes(sp._Epilogue(5, 7, 2, 1))
