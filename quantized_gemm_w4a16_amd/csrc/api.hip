@@ -170,6 +170,10 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t r)
     L.gpart = off;
     off = align256(off + gemm_part_bytes(M, N, K));
     L.total = off;
+    L.few = off;
+    if (r > 0 && L.rpad <= FEW_RANK)
+        off = align256(off + (size_t)FEW_SLICES * 16 * (L.rpad * sizeof(float) + sizeof(double)));
+    L.total_epi = off;
     return L;
 }
 
@@ -295,7 +299,7 @@ size_t spear_w4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r
 {
     if (M < 0 || N < 1 || K < 32 || r < 0)
         return 0;
-    return ws_layout(M, N, K, r).total;
+    return ws_layout(M, N, K, r).total_epi;
 }
 
 spear_status spear_workspace_init(void *ws, size_t bytes, void *stream)
@@ -342,7 +346,8 @@ namespace spear {
 // from SPEAR_PATH_AUTO.
 static spear_status validate_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w,
                                     const spear_ec *ec, const void *y, int32_t out_dtype,
-                                    const void *workspace, size_t ws_bytes, int32_t *path_io)
+                                    const void *workspace, size_t ws_bytes, int32_t *path_io,
+                                    bool epi = false)
 {
     int32_t path = *path_io;
     if (!w || !workspace || !w->packed || !w->scales)
@@ -386,7 +391,7 @@ static spear_status validate_linear(const spear_bf16 *x, int64_t M, const spear_
         return SPEAR_E_ALIGN;
     const int32_t r = ec ? ec->r : 0;
     const WsLayout L = ws_layout(M, N, K, r);
-    if (ws_bytes < L.total)
+    if (ws_bytes < (epi ? L.total_epi : L.total))
         return SPEAR_E_WORKSPACE;
     if (L.ncg * L.ksplit > GRID_MAX || cdiv(N, 64) * cdiv(M, 64) > GRID_MAX)
         return SPEAR_E_SHAPE;
@@ -538,10 +543,18 @@ static spear_status launch_path(LinearArgs &a, const spear_ec *ec, int32_t path,
     return hip_status(e);
 }
 
+// Decode with an epilogue, no path asked for: the EC's pre-pass in a launch of
+// its own before the decode kernel, rather than exchanged inside it.
+static bool few_ec_prepass(const spear_ec *ec)
+{
+    return ec && ec->gate_h == 0 && cdiv(ec->r, 32) * 32 <= FEW_RANK;
+}
+
 // A validated layer call: dispatch and launch on `stream`.
 static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w,
                                const spear_ec *ec, void *y, int32_t out_dtype, void *workspace,
-                               int32_t path, void *stream, const spear_epilogue *ep = nullptr)
+                               int32_t path, void *stream, const spear_epilogue *ep = nullptr,
+                               bool few_ec = false)
 {
     const int64_t N = w->N, K = w->K;
     const WsLayout L = ws_layout(M, N, K, ec ? ec->r : 0);
@@ -564,6 +577,14 @@ static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w
         a.E.act = ep->act;
         a.E.glu = ep->glu;
         a.E.on = 1;
+        if (few_ec) {
+            // about 1024 depths a slice
+            const int64_t p = cdiv(K, 1024);
+            a.E.few = (int32_t)(p < FEW_SLICES ? p : FEW_SLICES);
+            a.E.fu = reinterpret_cast<const float *>(a.ws + L.few);
+            a.E.fz = reinterpret_cast<const double *>(a.ws + L.few + (size_t)FEW_SLICES * 16 * L.rpad * sizeof(float));
+            return hip_status(launch_decode_epi(a, 3, s));
+        }
     }
     return launch_path(a, ec, path, s);
 }
@@ -616,7 +637,8 @@ spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spea
 {
     if (!ep)
         return SPEAR_E_NULL;
-    spear_status st = validate_linear(x, M, w, ec, y, out_dtype, workspace, ws_bytes, &path);
+    const bool any = path == SPEAR_PATH_AUTO;
+    spear_status st = validate_linear(x, M, w, ec, y, out_dtype, workspace, ws_bytes, &path, true);
     if (st != SPEAR_OK)
         return st;
     if (ep->act < SPEAR_ACT_NONE || ep->act > SPEAR_ACT_GELU_TANH || (ep->glu != 0 && ep->glu != 1))
@@ -625,7 +647,8 @@ spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spea
         return SPEAR_E_SHAPE;
     if (!aligned(ep->bias, 4) || !aligned(ep->residual, 16))
         return SPEAR_E_ALIGN;
-    return run_linear(x, M, w, ec, y, out_dtype, workspace, path, stream, ep);
+    return run_linear(x, M, w, ec, y, out_dtype, workspace, path, stream, ep,
+                      any && path == SPEAR_PATH_DECODE && few_ec_prepass(ec));
 }
 
 spear_status spear_w4_linear_noalloc(const spear_bf16 *x, int64_t M, const spear_w4 *w,

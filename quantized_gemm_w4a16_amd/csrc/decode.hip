@@ -84,6 +84,9 @@ struct DecShared {
     float xs[NW];        // one token: the activation sum of each wave's chunks
     double zl[NW];       // one token, hard gate: each wave's gate-logit partial
     uint32_t u32[4];
+#if SPEAR_EPILOGUE
+    float gate[16];      // pre-pass of its own: each token's gate, 0 where it takes no EC
+#endif
 };
 
 
@@ -548,6 +551,115 @@ __device__ f32x4 ec_consume(const LinearArgs &a, const u32x4 *bpre, int64_t cg, 
     return e * gs;
 }
 
+#if SPEAR_EPILOGUE
+// EC pre-pass of up to 16 tokens in a launch of its own: workgroup p takes one
+// of a.E.few K slices, its 8 waves eighths of it, and stores the slice's part
+// of A x (MFMA, fp32) and of the gate logit (fp64) as plain words.  The decode
+// kernel behind it adds the slices as it starts its epilogue: nothing is
+// exchanged inside a launch, so no workgroup waits for another and the decode
+// kernel needs no registers for polling.
+constexpr int FP_WAVES = 8;
+
+__global__ __launch_bounds__(64 * FP_WAVES) void few_prepass_kernel(const LinearArgs a)
+{
+    __shared__ f32x4 s_u[FP_WAVES][4][64];
+    __shared__ double s_z[FP_WAVES][64];
+    pin_arg(a.x); pin_arg(a.A); pin_arg(a.wg); pin_arg(a.M); pin_arg(a.K); pin_arg(a.r); pin_arg(a.rpad);
+    pin_epi_args(a);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int lr = lane & 15, lg = lane >> 4;
+    const int64_t K = a.K, M = a.M, T = K / 32, p = blockIdx.x, P = a.E.few;
+    const int64_t s0 = p * T / P, s1 = (p + 1) * T / P;
+    const int64_t t0 = s0 + wave * (s1 - s0) / FP_WAVES, t1 = s0 + (wave + 1) * (s1 - s0) / FP_WAVES;
+    const int r = a.r, ntile = a.rpad / 16;               // 2 or 4 tiles of 16 ranks
+    f32x4 acc[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    double zp = 0.0;
+    for (int64_t t = t0; t < t1; t += 4) {
+        u32x4 xv[4], wv[4], av[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int64_t k = 32 * (t + i) + 8 * lg;
+            const bool in = t + i < t1;
+            xv[i] = in && lr < M ? ld16(a.x + (int64_t)lr * K + k) : zero4();
+            wv[i] = in ? ld16(a.wg + k) : zero4();
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                av[i][q] = in && q < ntile && 16 * q + lr < r ? ld16(a.A + (int64_t)(16 * q + lr) * K + k) : zero4();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            zp = dot8_f64(xv[i], wv[i], zp);
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                acc[q] = mfma16(av[i][q], xv[i], acc[q]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        s_u[wave][q][lane] = acc[q];
+    s_z[wave][lane] = zp;
+    __syncthreads();
+    // tile q, lane (token lr, lg): ranks 16 q + 4 lg + i
+    if (wave < ntile && lr < M) {
+        f32x4 u = {0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < FP_WAVES; w++)
+            u += s_u[w][wave][lane];
+        *reinterpret_cast<f32x4 *>(const_cast<float *>(a.E.fu) + (p * 16 + lr) * a.rpad + 16 * wave + 4 * lg) = u;
+    }
+    if (wave == FP_WAVES - 1 && lane < M) {
+        double z = 0.0;
+        for (int w = 0; w < FP_WAVES; w++)
+            for (int q = 0; q < 4; q++)
+                z += s_z[w][lane + 16 * q];
+        const_cast<double *>(a.E.fz)[p * 16 + lane] = z;
+    }
+}
+
+// The decode kernel's side: the slices' partials of this thread's elements
+// (token, rank).  One token: a word a slice, loaded ahead of the weight stream;
+// more tokens: loaded as the contraction ends, when the registers are free.
+template <int NT, int GV>
+struct FewEc {
+    static constexpr int EL = GV ? 1 : 16 * FEW_RANK / NT;
+    float v[FEW_SLICES][EL], u[EL];
+    double zv[FEW_SLICES], z;
+
+    __device__ __forceinline__ void load(const LinearArgs &a, int tid)
+    {
+        const int n = (int)a.M * a.rpad, P = a.E.few;
+#pragma unroll
+        for (int p = 0; p < FEW_SLICES; p++) {
+            const int pp = p < P ? p : P - 1;
+#pragma unroll
+            for (int i = 0; i < EL; i++) {
+                const int e = tid + i * NT;
+                v[p][i] = a.E.fu[(int64_t)pp * 16 * a.rpad + (e < n ? e : n - 1)];
+            }
+            zv[p] = a.E.fz[pp * 16 + (tid < a.M ? tid : 0)];
+        }
+    }
+    __device__ __forceinline__ void add(const LinearArgs &a)
+    {
+        const int P = a.E.few;
+        z = (double)a.b;
+#pragma unroll
+        for (int i = 0; i < EL; i++)
+            u[i] = 0.f;
+#pragma unroll
+        for (int p = 0; p < FEW_SLICES; p++)
+            if (p < P) {
+                z += zv[p];
+#pragma unroll
+                for (int i = 0; i < EL; i++)
+                    u[i] += v[p][i];
+            }
+    }
+};
+#endif
+
 template <int EC_MODE, int OUT_F32, int SW, int GV, int NW>
 __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
 {
@@ -612,6 +724,12 @@ __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
             }
         }
     }
+
+#if SPEAR_EPILOGUE
+    FewEc<64 * NW, GV> few;
+    if (EC_MODE == 3 && GV)
+        few.load(a, tid);
+#endif
 
     // 3. Activations -> LDS directly (global_load_lds, 16 bytes a lane, 64
     //    consecutive chunks of one token row per wave instruction).  Each wave
@@ -783,9 +901,43 @@ __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
                                   a.E.glu ? N / 2 : N, res_v);
         }
     }
+#if SPEAR_EPILOGUE
+    if (EC_MODE == 3 && ks == ksplit - 1) {
+        if (!GV)
+            few.load(a, tid);
+        few.add(a);
+    }
+#endif
     if ((EC_MODE == 1 || ksplit > 1) && tid == 0)
         sh.u32[0] = epoch_tag(claimed + opaque_zero64());    // both halves live until here
     __syncthreads();
+#if SPEAR_EPILOGUE
+    // u and the tokens' gates to LDS (the activations there are done with)
+    float *const s_fu = reinterpret_cast<float *>(s_x);
+    if (EC_MODE == 3 && ks == ksplit - 1) {
+        const int n = (int)M * a.rpad;
+#pragma unroll
+        for (int i = 0; i < FewEc<64 * NW, GV>::EL; i++)
+            if (tid + i * 64 * NW < n)
+                s_fu[tid + i * 64 * NW] = few.u[i];
+        if (wave == 0) {
+            const float g = (float)(1.0 / (1.0 + exp(-few.z)));
+            const int act = lane < M && (a.hard ? few.z > a.thr : 1);
+            if (lane < 16)
+                sh.gate[lane] = act ? g : 0.f;
+            if (cg == 0) {
+                const uint64_t mask = __ballot(act);
+                if (lane < M && a.g_out)
+                    a.g_out[lane] = g;
+                if (act && a.idx_out)
+                    a.idx_out[__popcll(mask & ((1ull << lane) - 1ull))] = lane;
+                if (lane == 0 && a.nact_out)
+                    *a.nact_out = __popcll(mask);
+            }
+        }
+        __syncthreads();
+    }
+#endif
 
     // 7. Reduce the stream waves (fixed order).  Afterwards lane (t, g) of
     //    wave 0 holds channels n0 + 4 g + i of token t, and token t's sum of x.
@@ -938,6 +1090,32 @@ __global__ __launch_bounds__(64 * NW) void decode_kernel(const LinearArgs a)
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 yv[i] += ec_e[i];
+        } else if (EC_MODE == 3) {
+#if SPEAR_EPILOGUE
+            // v = g u, token lr, ranks 32 t + 8 lg + q, as bf16 hi + lo
+            const float g = sh.gate[lr];
+            if (__ballot(g != 0.f) != 0ull) {
+                f32x4 e = {0.f, 0.f, 0.f, 0.f};
+                const int rpad = a.rpad;
+                for (int t = 0; t < rpad / 32; t++) {
+                    const float *u = s_fu + (lr < M ? lr : 0) * rpad + 32 * t + 8 * lg;
+                    u32x4 vh, vl;
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const float v0 = g != 0.f ? g * u[2 * q] : 0.f, v1 = g != 0.f ? g * u[2 * q + 1] : 0.f;
+                        const uint16_t h0 = f2bf(v0), h1 = f2bf(v1);
+                        vh[q] = (uint32_t)h0 | ((uint32_t)h1 << 16);
+                        vl[q] = (uint32_t)f2bf(v0 - bf16f(h0)) | ((uint32_t)f2bf(v1 - bf16f(h1)) << 16);
+                    }
+                    const u32x4 bf = bpre[t == 0 ? 0 : 1];
+                    e = mfma16(bf, vh, e);
+                    e = mfma16(bf, vl, e);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    yv[i] += e[i];
+            }
+#endif
         } else if (EC_MODE == 2) {
             // v precomputed by the pre-pass (bf16 hi + lo, zero for skipped tokens)
             const int32_t *active = reinterpret_cast<const int32_t *>(a.ws + a.D.active);
@@ -1105,6 +1283,13 @@ hipError_t launch_decode(const LinearArgs &a, int ec_mode, hipStream_t s)
         return launch_decode_t<0>(a, s);
     case 1:
         return launch_decode_t<1>(a, s);
+#if SPEAR_EPILOGUE
+    case 3: {
+        hipLaunchKernelGGL(few_prepass_kernel, dim3((unsigned)a.E.few), dim3(64 * FP_WAVES), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        return e != hipSuccess ? e : launch_decode_t<3>(a, s);
+    }
+#endif
     default:
         return launch_decode_t<2>(a, s);
     }

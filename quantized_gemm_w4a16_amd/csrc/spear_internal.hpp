@@ -132,11 +132,14 @@ constexpr int PROD_WORDS = 4096;  // above 8 tokens: partial words an epilogue l
 constexpr int PROD_CHUNK = 4;     // producer partials a consumer wave loads per batch
 constexpr int PRE_SLOTS = 512;    // EC pre-pass: (token group, K slice) partial slots, at most
                                   // (fewer than PRE_GROUPS groups, about 256 workgroups)
+constexpr int FEW_SLICES = 8;     // decode's own EC pre-pass: K slices, at most
+constexpr int FEW_RANK = 64;      // ... and padded rank, at most
 constexpr int PRE_GROUPS = 128;   // EC pre-pass: token groups below which K is split
 
 struct WsLayout {
     size_t hdr, epoch, zeros, splitp, pu, pz, vhi, vlo, vtag, active, preu, prez, gpart, total;
     size_t idx;         // semi-fused prefill: the active-token list [mpad], then its count
+    size_t few, total_epi;   // epilogue calls: partials of the decode's own pre-pass; all of it
     int64_t ncg, ksplit, spw, nprod, prod_k, rpad, mpad;
 };
 
@@ -150,14 +153,16 @@ struct DecOffsets {
     uint32_t hdr, epoch, splitp, pu, pz, vhi, vlo, active;
 };
 
-// The epilogue after the layer (spear_w4_linear_epilogue): one 32-byte block.
+// The epilogue after the layer (spear_w4_linear_epilogue): one 64-byte line.
 struct EpiArgs {
     const float *bias;      // [N] or null
     const void *res;        // [M][N or N / 2] of the output's type, or null
     int32_t act;            // SPEAR_ACT_*
     int32_t glu;            // 1: channels 2i and 2i + 1 make output channel i
     int32_t on;             // host side: the call has an epilogue
-    int32_t pad;
+    int32_t few;            // decode with the EC's pre-pass before it: K slices of the partials
+    const float *fu;        // [few][16][rpad] partials of A x
+    const double *fz;       // [few][16] partials of the gate logit
 };
 
 // A row tile of a grouped product: rows list[pos .. pos + cnt) through expert e.
@@ -216,17 +221,15 @@ struct LinearArgs {
     struct {
         size_t hdr, zeros, vhi, vlo, vtag, active, preu, prez, gpart, idx;
     } P;
+    // The kernels with an epilogue load this line too, the grouped ones the next.
+    alignas(64) EpiArgs E;
+    GrpArgs G;
     // Host side only.
     WsLayout L;
-    // The kernels with an epilogue load this block too (one further line).
-    EpiArgs E;
-    GrpArgs G;
 };
 static_assert(offsetof(LinearArgs, gw1) == 216 && offsetof(LinearArgs, D) == 180 &&
-                  offsetof(LinearArgs, grid) == 212 && offsetof(LinearArgs, L) == 360,
+                  offsetof(LinearArgs, grid) == 212 && offsetof(LinearArgs, E) == 384,
               "the decode kernels' leading block");
-static_assert(offsetof(LinearArgs, E) / 64 == (offsetof(LinearArgs, E) + sizeof(EpiArgs) - 1) / 64,
-              "the epilogue's block in one line");
 
 // Swizzle of rows staged in LDS for MFMA operands: the 16-byte pieces of row r
 // swap places by piece ^ row_turn(r % 16).  A 16-byte LDS read serves its lanes
@@ -297,7 +300,8 @@ __device__ __forceinline__ void pin_pre_args(const LinearArgs &a)
 // The epilogue's arguments.
 __device__ __forceinline__ void pin_epi_args(const LinearArgs &a)
 {
-    pin_arg(a.E.bias); pin_arg(a.E.res); pin_arg(a.E.act); pin_arg(a.E.glu);
+    pin_arg(a.E.bias); pin_arg(a.E.res); pin_arg(a.E.act); pin_arg(a.E.glu); pin_arg(a.E.few);
+    pin_arg(a.E.fu); pin_arg(a.E.fz);
 }
 
 __device__ __forceinline__ void pin_grp_args(const LinearArgs &a)

@@ -109,13 +109,39 @@ def test_activations(M, kind):
 
 @pytest.mark.parametrize("M", [1, 6, 100])
 def test_no_epilogue_is_the_layer_bit_for_bit(M):
-    """No bias, no activation, no residual: the plain entry point's bits."""
+    """No bias, no activation, no residual: the plain entry point's bits, on
+    every path and, without an error compensator, where the path is chosen."""
     c = Case(M, 274, 1024, 32, 1, M, False, False, False, sp.OUT_F32)
     for out in (sp.OUT_F32, sp.OUT_BF16):
         for path in (DECODE if M <= 16 else PREFILL):
-            a = sp.spear_w4_linear(c.x, c.w, c.ec, out_dtype=out, path=path)
-            b = sp.spear_w4_linear_epilogue(c.x, c.w, sp.Epilogue(), c.ec, out_dtype=out, path=path)
-            assert torch.equal(a, b), (M, out, path)
+            for ec in ([c.ec, None] if path != sp.PATH_AUTO else [None]):
+                a = sp.spear_w4_linear(c.x, c.w, ec, out_dtype=out, path=path)
+                b = sp.spear_w4_linear_epilogue(c.x, c.w, sp.Epilogue(), ec, out_dtype=out, path=path)
+                assert torch.equal(a, b), (M, out, path)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 32, 8), (1, 2048, 2048, 32), (2, 100, 96, 64), (5, 48, 9000 // 32 * 32, 40),
+                                     (16, 300, 1056, 64), (16, 64, 12288, 32), (11, 4112, 512, 16)])
+@pytest.mark.parametrize("hard", [0, 1])
+def test_chosen_path_with_the_compensator(M, N, K, r, hard):
+    """The path that the call chooses: the gates and the selected tokens are the
+    gate entry point's, and the outputs hold on a workspace that other calls of
+    the layer have used."""
+    c = Case(M, N, K, r, hard, M + N + K, False, True, False, sp.OUT_F32)
+    ref, tol = c.reference(ref64.SILU)
+    ws = sp.new_workspace(M, N, K, r)
+    g, idx, n = sp.spear_gate(c.x, c.ec.w_gate, c.ec.b, c.ec.tau, hard)
+    for i in range(3):
+        c.ec.g_out = torch.full((M,), -1.0, device="cuda")
+        c.ec.idx_out = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+        c.ec.n_active_out = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+        y = sp.spear_w4_linear_epilogue(c.x, c.w, c.epilogue(sp.ACT_SILU), c.ec, workspace=ws)
+        check(y, ref, tol, f"chosen M={M} N={N} K={K} r={r} hard={hard} call {i}")
+        k = int(n.item())
+        assert int(c.ec.n_active_out.item()) == k and torch.equal(c.ec.idx_out[:k], idx[:k])
+        np.testing.assert_allclose(host(c.ec.g_out), host(g), rtol=2e-7)
+        sp.spear_w4_linear(c.x, c.w, c.ec, workspace=ws, path=[sp.PATH_DECODE, sp.PATH_PREFILL, sp.PATH_AUTO][i])
+    assert sp.spear_workspace_timeouts(ws) == 0
 
 
 @pytest.mark.parametrize("M", [1, 9, 65, 200])
