@@ -14,6 +14,8 @@
 //    the logits in question again in fp64, so the choice is the same as before.
 #include <math.h>
 
+#include <type_traits>
+
 #include "spear_internal.hpp"
 
 namespace spear {
@@ -99,6 +101,25 @@ __device__ __forceinline__ float wave_max(float v)
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
     return wave_reduce(v, 0u, [](uint32_t p, uint32_t q) { return q > p ? q : p; });
+}
+
+// Four sums over the wave at once, z[l % 4] in lane l: the first two steps halve
+// what is left to add.
+__device__ __forceinline__ double wave_sum4(const double (&z)[4], int lane)
+{
+    const bool b0 = lane & 1, b1 = lane & 2;
+    double p = b0 ? z[1] : z[0], q = b0 ? z[3] : z[2], o = b0 ? z[0] : z[1];
+    p += dpp<0xB1, 0xF>(o, o);                            // quad_perm 1 0 3 2
+    o = b0 ? z[2] : z[3];
+    q += dpp<0xB1, 0xF>(o, o);
+    o = b1 ? p : q;
+    p = b1 ? q : p;
+    p += dpp<0x4E, 0xF>(o, o);                            // quad_perm 2 3 0 1
+    p += dpp<0x124, 0xF>(p, p);                           // row_ror 4, 8
+    p += dpp<0x128, 0xF>(p, p);
+    p += __shfl_xor(p, 16);
+    p += __shfl_xor(p, 32);
+    return p;
 }
 
 // acc + the products of 8 bf16 of x and w: every product exact, the sum in fp64.
@@ -548,54 +569,202 @@ struct ChooseShared {
     uint16_t list[64 * Q];
 };
 
-// What the wave knows of one token it has to settle.
+// Waves of a workgroup of the choice, four tokens each.  Tokens in doubt are the
+// whole workgroup's: it sums their logits together, then each wave settles the
+// next one (settled by its own wave alone, a token took 10 to 20 thousand
+// cycles and the last wave of 8192 tokens had four of them).  Two waves for more
+// than 256 experts, so that LDS holds the same tokens a CU.
+template <int Q>
+constexpr int RC_WAVES = Q == 8 ? 2 : 4;
+constexpr int RC_JOINT = 16;                              // logits a token that are summed together
+
+// A token that has to be settled.
 struct Doubt {
     int64_t m;
-    int row;
-    uint32_t clear;                                       // choices further apart are in order
     float mx, sum, zd;
+    uint32_t clear;                                       // choices further apart are in order
+    uint32_t slots, last;                                 // winners whose order is open; the last one's key
+    int32_t n, hard, rest;                                // experts in the list (up to RC_JOINT of them)
+    int32_t id[SPEAR_MAX_TOPK];                           // winners
+    alignas(8) uint16_t list[RC_JOINT];
 };
 
-// The groups of a token whose order the bounds leave open: the experts that may
-// be among the best of those groups in fp64, then the groups by them.  False:
-// all logits are needed.
 template <int Q>
-__device__ __forceinline__ bool settle_groups(const RouteArgs &a, ChooseShared<Q> &sh, const Doubt &t, int lane)
+struct Joint {
+    static constexpr int NW = RC_WAVES<Q>;
+    Doubt t[4 * NW];
+    double part[4 * NW][RC_JOINT][NW];                    // logits by K range
+    uint32_t open[2][NW];                                 // a wave's tokens in doubt, a bit each: groups, order
+};
+
+// Logits of the listed experts of all tokens in `todo` over this wave's share of
+// K, in units of four experts and 1024 depths, two with their loads in flight.
+// Lists and rows are read as scalars: every load then is a base and a lane's
+// offset (addresses by lane made a unit 3200 cycles; 2500 so).
+template <int Q>
+__device__ __forceinline__ void joint_logits(const RouteArgs &a, Joint<Q> &jt, uint32_t todo, int wave, int lane)
 {
-    const int E = a.E, G = a.n_group, gs = E / G;
-    if (a.score == SPEAR_SCORE_SOFTMAX && a.bias)
-        return false;
-    const bool two = a.group_best == 2 && gs > 1;
-    const uint32_t tol = (two ? 2u : 1u) * t.clear;
-    const uint32_t gv = lane < G ? sh.gval[t.row][lane] : 0u;
+    constexpr int NW = RC_WAVES<Q>, UNITS = 2;
+    const int64_t kb = a.K / 8 * wave / NW * 8, ke = a.K / 8 * (wave + 1) / NW * 8;
+    int u = 0, n = 0, p = 0;
+    int64_t k = ke;
+    const uint16_t *xr = a.x, *wr[4] = {a.w, a.w, a.w, a.w};
+    bool more = true;
+    auto next = [&]() __attribute__((always_inline)) {    // (an empty share of K has one unit, of zeros)
+        k += 1024;
+        if (k < ke)
+            return;
+        k = kb;
+        p += 4;
+        while (more && p >= n) {
+            p = n = 0;
+            more = todo != 0;
+            if (more) {
+                u = __builtin_ctz(todo);
+                todo &= todo - 1;
+                const Doubt &t = jt.t[u];
+                n = __builtin_amdgcn_readfirstlane(t.n);
+                n = n > RC_JOINT ? 0 : n;
+                const uint64_t m = (uint64_t)t.m;
+                xr = a.x + (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(m >> 32)) << 32) |
+                                     (uint32_t)__builtin_amdgcn_readfirstlane((int)m)) * a.K;
+            }
+        }
+        if (more) {
+            const uint32_t *list = reinterpret_cast<const uint32_t *>(&jt.t[u].list[p]);
+            const uint32_t l0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)list[0]),
+                           l1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)list[1]);
+            wr[0] = a.w + (int64_t)(l0 & 0xFFFF) * a.K;
+            wr[1] = p + 1 < n ? a.w + (int64_t)(l0 >> 16) * a.K : wr[0];
+            wr[2] = p + 2 < n ? a.w + (int64_t)(l1 & 0xFFFF) * a.K : wr[0];
+            wr[3] = p + 3 < n ? a.w + (int64_t)(l1 >> 16) * a.K : wr[0];
+        }
+    };
+    next();
+#pragma unroll 1
+    while (more) {
+        u32x4 xv[UNITS][2], wv[UNITS][4][2];
+        int uu[UNITS], pp[UNITS], nn[UNITS];
+        bool begin[UNITS], inside[UNITS][2];
+#pragma unroll
+        for (int i = 0; i < UNITS; i++) {
+            uu[i] = u;
+            pp[i] = p;
+            nn[i] = more ? n : 0;
+            begin[i] = k == kb;
+            if (more) {
+                const int64_t kc = k < a.K - 8 ? k : a.K - 8;
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    // (a chunk past the share reads its first one, times zero)
+                    const uint32_t l = 512 * q + 8 * lane;
+                    const bool in = (int64_t)l < ke - k;
+                    const uint32_t off = in ? l : 0;
+                    xv[i][q] = ld16(xr + kc + off);
+                    inside[i][q] = in;
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        wv[i][r][q] = ld16(wr[r] + kc + off);
+                }
+                next();
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < UNITS; i++)
+            if (nn[i] != 0) {
+                double z[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+                    xv[i][q] = inside[i][q] ? xv[i][q] : zero4();
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    if (pp[i] + r < nn[i])
+                        z[r] = dot8(xv[i][1], wv[i][r][1], dot8(xv[i][0], wv[i][r][0], 0.0));
+                const double t = wave_sum4(z, lane);
+                if (lane < 4 && pp[i] + lane < nn[i]) {
+                    double &d = jt.part[uu[i]][pp[i] + lane][wave];
+                    d = begin[i] ? t : d + t;
+                }
+            }
+    }
+}
+
+// The list of token u and its logits to the wave's own LDS, after joint_logits.
+template <int Q>
+__device__ __forceinline__ void take_joint(ChooseShared<Q> &sh, const Joint<Q> &jt, int u, int n, int lane)
+{
+    if (lane < n) {
+        double z = 0.0;
+#pragma unroll
+        for (int w = 0; w < RC_WAVES<Q>; w++)
+            z += jt.part[u][lane][w];
+        sh.z[lane] = z;
+        sh.list[lane] = jt.t[u].list[lane];
+    }
+    wait_lgkmcnt0();
+}
+
+// Groups of the token in row `row` whose order the bounds leave open (lane g for
+// group g): og those, sure the ones kept whatever their order.
+template <int Q>
+__device__ __forceinline__ void open_groups(const RouteArgs &a, const ChooseShared<Q> &sh, int row, uint32_t clear,
+                                            int lane, uint64_t &og, uint64_t &sure)
+{
+    const int G = a.n_group;
+    const uint32_t tol = (a.group_best == 2 && a.E / G > 1 ? 2u : 1u) * clear;
+    const uint32_t gv = lane < G ? sh.gval[row][lane] : 0u;
     uint32_t rank = 0;
 #pragma unroll 1
     for (int g = 0; g < G; g++) {
-        const uint32_t o = sh.gval[t.row][g];
+        const uint32_t o = sh.gval[row][g];
         rank += o > gv || (o == gv && g < lane) ? 1u : 0u;
     }
     const bool in = lane < G && rank < (uint32_t)a.topk_group;
     const uint32_t least = ~wave_max(in ? ~gv : 0u), most = wave_max(lane < G && !in ? gv : 0u);
     const bool open = lane < G && (in ? gv <= most + tol : gv + tol >= least);
-    const uint64_t og = __ballot(open), sure = __ballot(in && !open);
+    og = __ballot(open);
+    sure = __ballot(in && !open);
+}
+
+// The experts that may be among the best of those groups in fp64, to sh.list of
+// the wave `to`; returns their number.
+template <int Q>
+__device__ __forceinline__ int list_groups(const RouteArgs &a, const ChooseShared<Q> &sh, ChooseShared<Q> &to, int row,
+                                           uint32_t clear, int lane)
+{
+    const int E = a.E, gs = E / a.n_group;
+    uint64_t og, sure;
+    open_groups(a, sh, row, clear, lane, og, sure);
     int n = 0;
 #pragma unroll 1
     for (int e0 = 0; e0 < E; e0 += 64) {
         const int e = e0 + lane, g = e < E ? e / gs : 0;
-        const uint32_t k = e < E ? sh.key[t.row][e] : 0u;
-        n = append(sh.list, n, ((og >> g) & 1) && k != 0u && (k >> 9) + t.clear >= sh.gthr[t.row][g], e, lane);
+        const uint32_t k = e < E ? sh.key[row][e] : 0u;
+        n = append(to.list, n, e < E && ((og >> g) & 1) && k != 0u && (k >> 9) + clear >= sh.gthr[row][g], e, lane);
     }
     wait_lgkmcnt0();
-    exact_logits(a, t.m, lane, sh.list, n, sh.z);
+    return n;
+}
+
+// The groups to keep, by the n listed logits in my.z; own: the LDS of the token's
+// own wave.
+template <int Q>
+__device__ __forceinline__ void settle_groups(const RouteArgs &a, ChooseShared<Q> &my, ChooseShared<Q> &own, int row,
+                                              const Doubt &t, int n, int lane)
+{
+    const int G = a.n_group, gs = a.E / G;
+    const bool two = a.group_best == 2 && gs > 1;
+    uint64_t og, sure;
+    open_groups(a, own, row, t.clear, lane, og, sure);
 #pragma unroll 1
     for (int p = lane; p < n; p += 64)
-        sh.c[p] = choice_of(a, score_of(a, sh.z[p], t.mx, t.sum), sh.list[p]);
+        my.c[p] = choice_of(a, score_of(a, my.z[p], t.mx, t.sum), my.list[p]);
     wait_lgkmcnt0();
     double b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll 1
     for (int p = 0; p < n; p++)
-        if (sh.list[p] / gs == lane) {
-            const double v = sh.c[p];
+        if (my.list[p] / gs == lane) {
+            const double v = my.c[p];
             b1 = v > b0 ? b0 : (v > b1 ? v : b1);
             b0 = v > b0 ? v : b0;
         }
@@ -606,64 +775,92 @@ __device__ __forceinline__ bool settle_groups(const RouteArgs &a, ChooseShared<Q
         const double o = lane_of(v, g);
         place += ((og >> g) & 1) && (o > v || (o == v && g < lane));
     }
-    const uint64_t kept = sure | __ballot(open && place < a.topk_group - __popcll(sure));
+    const uint64_t kept = sure | __ballot(((og >> lane) & 1) && place < a.topk_group - __popcll(sure));
     if (lane == 0)
-        sh.kept[t.row] = kept;
-    wait_lgkmcnt0();
-    return true;
+        own.kept[row] = kept;
 }
 
-// The winners of a token whose order is open (slots `so`), and the candidates
-// behind the last one that may come before it, in fp64.  They take the open
-// slots in their exact order; the other winners are clear of them all.  id, v:
-// winner and key of slot `lane`; last: the last winner's key; rest: whether the
-// candidates left (sh.key) matter.  False: all logits are needed.
+// The winners whose order is open, and (rest) the candidates behind the last one
+// that may come before it, to to.list; returns their number.
 template <int Q>
-__device__ __forceinline__ bool settle_order(const RouteArgs &a, ChooseShared<Q> &sh, const Doubt &t, int lane,
-                                             int id, uint64_t so, bool rest, uint32_t last)
+__device__ __forceinline__ int list_order(const RouteArgs &a, const ChooseShared<Q> &own, ChooseShared<Q> &to, int row,
+                                          int id, uint32_t slots, bool rest, uint32_t last, uint32_t clear, int lane)
 {
-    const int E = a.E;
-    int n = append(sh.list, 0, (so >> lane) & 1, id, lane);
+    int n = append(to.list, 0, lane < SPEAR_MAX_TOPK && ((slots >> (lane & 31)) & 1), id, lane);
     if (rest)
 #pragma unroll 1
-        for (int e0 = 0; e0 < E; e0 += 64) {
-            const uint32_t k = e0 + lane < E ? sh.key[t.row][e0 + lane] : 0u;
-            n = append(sh.list, n, k != 0u && last - (k >> 9) <= t.clear, e0 + lane, lane);
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            const uint32_t k = e0 + lane < a.E ? own.key[row][e0 + lane] : 0u;
+            n = append(to.list, n, k != 0u && last - (k >> 9) <= clear, e0 + lane, lane);
         }
     wait_lgkmcnt0();
-    exact_logits(a, t.m, lane, sh.list, n, sh.z);
-    const int open = __popcll(so);
+    return n;
+}
+
+// The n listed experts take the token's open slots in the order of their logits
+// in my.z (to my.slot_id, my.slot_z); the other winners are clear of them all.
+// False: all logits are needed.
+template <int Q>
+__device__ __forceinline__ bool settle_order(const RouteArgs &a, ChooseShared<Q> &my, const Doubt &t, int n, int lane)
+{
+    const int open = __popc(t.slots);
     bool decided = true;
     const bool shift = a.score == SPEAR_SCORE_SOFTMAX && a.bias;   // s + bias: the sum's own error matters
 #pragma unroll 1
     for (int p = lane; p < n; p += 64)
-        sh.c[p] = choice_of(a, score_of(a, sh.z[p], t.mx, t.sum), sh.list[p]);
+        my.c[p] = choice_of(a, score_of(a, my.z[p], t.mx, t.sum), my.list[p]);
     wait_lgkmcnt0();
 #pragma unroll 1
     for (int p = lane; p < n; p += 64) {
-        const double c = sh.c[p], z = sh.z[p], s = shift ? score_of(a, z, t.mx, t.sum) : 0.0;
-        const int e = sh.list[p];
+        const double c = my.c[p], z = my.z[p], s = shift ? score_of(a, z, t.mx, t.sum) : 0.0;
+        const int e = my.list[p];
         int place = 0;
 #pragma unroll 1
         for (int q = 0; q < n; q++) {
-            const double o = sh.c[q];
-            const int oe = sh.list[q];
+            const double o = my.c[q];
+            const int oe = my.list[q];
             place += o > c || (o == c && oe < e);
-            if (shift && q != p && !(fabs(o - c) > 1.25 * (double)t.zd * fabs(score_of(a, sh.z[q], t.mx, t.sum) - s)))
+            if (shift && q != p && !(fabs(o - c) > 1.25 * (double)t.zd * fabs(score_of(a, my.z[q], t.mx, t.sum) - s)))
                 decided = false;
         }
         if (place < open) {
-            uint64_t m = so;                              // the place-th open slot
+            uint32_t m = t.slots;                         // the place-th open slot
 #pragma unroll 1
             for (int i = 0; i < place; i++)
                 m &= m - 1;
-            const int slot = __builtin_ctzll(m);
-            sh.slot_id[slot] = e;
-            sh.slot_z[slot] = z;
+            const int slot = __builtin_ctz(m);
+            my.slot_id[slot] = e;
+            my.slot_z[slot] = z;
         }
     }
     wait_lgkmcnt0();
     return __all(decided);
+}
+
+// All logits of token t in fp64 to my.z.  A row of x that is all zero has zeros
+// (zd == 0: then w has no infinity or NaN either), without reading w.
+template <int Q>
+__device__ __forceinline__ void all_logits(const RouteArgs &a, ChooseShared<Q> &my, const Doubt &t, int lane)
+{
+    bool zero = t.zd == 0.f;
+    if (zero) {
+        uint32_t any = 0;
+        const uint16_t *xr = a.x + t.m * a.K;
+#pragma unroll 1
+        for (int64_t k = 8 * lane; k < a.K; k += 512) {
+            const u32x4 v = ld16(xr + k);
+            any |= (v[0] | v[1] | v[2] | v[3]) & 0x7FFF7FFFu;
+        }
+        zero = !__any(any != 0);
+    }
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+        my.list[e] = (uint16_t)e;
+        my.z[e] = 0.0;
+    }
+    wait_lgkmcnt0();
+    if (!zero)
+        exact_logits(a, t.m, lane, my.list, a.E, my.z);
 }
 
 // The choice, four tokens a wave: 16 lanes a token, 4 Q experts a lane
@@ -674,12 +871,16 @@ __device__ __forceinline__ bool settle_order(const RouteArgs &a, ChooseShared<Q>
 // neighbours in the order are nearer than the bounds and the fixed point allow,
 // the whole wave settles the token with a few logits in fp64.
 template <int Q>
-__global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
+__global__ __launch_bounds__(64 * RC_WAVES<Q>, 2) void route_choose_kernel(const RouteArgs a)
 {
-    __shared__ __attribute__((aligned(16))) ChooseShared<Q> sh;
-    const int lane = threadIdx.x;
+    constexpr int NW = RC_WAVES<Q>;
+    __shared__ __attribute__((aligned(16))) ChooseShared<Q> s_sh[NW];
+    __shared__ Joint<Q> jt;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    ChooseShared<Q> &sh = s_sh[wave];
     const int lr = lane & 15, row = lane >> 4;
-    const int64_t M = a.M, m0 = (int64_t)blockIdx.x * 4;
+    const int64_t M = a.M, first = (int64_t)blockIdx.x * (4 * NW), m0 = first + 4 * wave;
     const int64_t m = m0 + row < M ? m0 + row : M - 1;
     const int E = a.E, G = a.n_group, gs = E / G;
     // logits: the slices' sums; |x|^2, and the largest |w_e|^2 of 16 experts a lane
@@ -689,7 +890,13 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
 #pragma unroll
     for (int i = 0; i < 4 * Q; i++)
         c[i] = 0.f;
-    constexpr int U = Q <= 2 ? 4 : Q == 4 ? 2 : 1;        // slices in flight, by the registers they take
+    float bias[4 * Q];
+#pragma unroll
+    for (int i = 0; i < 4 * Q; i++) {
+        const int e = 64 * (i / 4) + 4 * lr + i % 4;
+        bias[i] = a.bias && e < E ? a.bias[e] : 0.f;
+    }
+    constexpr int U = Q <= 4 ? 4 : 2;        // slices in flight, by the registers they take
 #pragma unroll U
     for (int k = 0; k < a.ks; k++) {
         const float *zp = a.z + (k * M + m) * E;
@@ -718,13 +925,14 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
             f32x4{c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
     auto expert = [&](int i) { return 64 * (i / 4) + 4 * lr + i % 4; };
     auto real = [&](int i) { return expert(i) < E; };
+    const bool soft = a.score == SPEAR_SCORE_SOFTMAX;
+    const bool by_z = soft && !a.bias && (a.topk_group == G || a.group_best == 1 || gs == 1);
     bool hard = !(zd < 0.05f);                            // all logits in fp64
 #pragma unroll
     for (int i = 0; i < 4 * Q; i++)
         hard |= real(i) && !(fabsf(c[i]) < INFINITY);
 
     // softmax: largest logit and sum
-    const bool soft = a.score == SPEAR_SCORE_SOFTMAX;
     float mx = 0.f, sum = 1.f;
     if (soft) {
         float t = -INFINITY, u = 0.f;
@@ -742,7 +950,6 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
     // the error: of the logit, or its slope times that and 1e-5 for the fp32
     // exponential (2 steps and as many as the argument's magnitude, which is
     // below 90 where the score is not 0 or 1).
-    const bool by_z = soft && !a.bias && (a.topk_group == G || a.group_best == 1 || gs == 1);
     float lo, unit, d;                                    // choice = lo + unit * key
     if (by_z) {
         lo = -64.f;                                       // further down all keys are alike: in doubt
@@ -757,7 +964,7 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
 #pragma unroll
         for (int i = 0; i < 4 * Q; i++) {
             const float s = soft ? __expf(c[i] - mx) * inv : __builtin_amdgcn_rcpf(1.f + __expf(-c[i]));
-            const float b = a.bias && real(i) ? a.bias[expert(i)] : 0.f;
+            const float b = bias[i];
             mb = fabsf(b) < INFINITY && fabsf(b) > mb ? fabsf(b) : mb;
             hard |= b == INFINITY;
             c[i] = s + b;
@@ -791,10 +998,14 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
         const bool two = a.group_best == 2 && gs > 1;
 #pragma unroll 1
         for (int g = lr; g < G; g += 16) {
+            // (each lane from another place: all lanes in step through one
+            // bank took 7700 cycles for 8 groups of 32, 3600 so)
             uint32_t b0 = 0, b1 = 0;
+            int j = lane % gs;
 #pragma unroll 8
             for (int i = 0; i < gs; i++) {
-                const uint32_t v = sh.key[row][g * gs + i] >> 9, w = v < b0 ? v : b0;
+                const uint32_t v = sh.key[row][g * gs + j] >> 9, w = v < b0 ? v : b0;
+                j = j + 1 == gs ? 0 : j + 1;
                 b0 = v > b0 ? v : b0;
                 b1 = w > b1 ? w : b1;
             }
@@ -824,18 +1035,57 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
         const bool open = !(least > most && least - most > (two ? 2u : 1u) * clear);
         if (lr == 0)
             sh.kept[row] = kept;
-        uint64_t todo = __ballot(open && !hard);
-        uint64_t fail = 0;
+        const bool all = soft && a.bias;                  // its sum's error: all logits are needed
+        const uint64_t todo = __ballot(open && !hard && !all && m0 + row < M);
+        hard |= open && all;
         wait_lgkmcnt0();
+        uint32_t fail = 0;
+        if (todo != 0) {
 #pragma unroll 1
-        for (int r = 0; r < 4 && m0 + r < M; r++)
-            if ((todo >> (16 * r)) & 1) {
-                const Doubt t = {m0 + r, r, lane_of(clear, 16 * r), lane_of(mx, 16 * r), lane_of(sum, 16 * r),
-                                 lane_of(zd, 16 * r)};
-                if (!settle_groups(a, sh, t, lane))
-                    fail |= 0xFFFFull << (16 * r);
+            for (int r = 0; r < 4; r++) {
+                if (((todo >> (16 * r)) & 1) == 0)
+                    continue;
+                Doubt &t = jt.t[4 * wave + r];
+                const uint32_t cl = lane_of(clear, 16 * r);
+                const int n = list_groups(a, sh, sh, r, cl, lane);
+                if (n > RC_JOINT) {
+                    fail |= 1u << r;
+                } else if (lane < n) {
+                    t.list[lane] = sh.list[lane];
+                }
+                if (lane == 16 * r) {
+                    t.m = m;
+                    t.mx = mx;
+                    t.sum = sum;
+                    t.zd = zd;
+                    t.clear = cl;
+                    t.n = n;
+                }
             }
-        hard |= (fail >> lane) & 1;
+        }
+        hard |= (fail >> row) & 1;
+        if (lane == 0)
+            jt.open[0][wave] = ((todo & 1) | ((todo >> 15) & 2) | ((todo >> 30) & 4) | ((todo >> 45) & 8)) & ~fail;
+        __syncthreads();
+        uint32_t open_all = 0;
+#pragma unroll
+        for (int w = 0; w < NW; w++)
+            open_all |= __builtin_amdgcn_readfirstlane(jt.open[0][w]) << (4 * w);
+        if (open_all != 0) {                              // (the same for all waves)
+            joint_logits(a, jt, open_all, wave, lane);
+            __syncthreads();
+            int turn = 0;
+#pragma unroll 1
+            for (uint32_t o = open_all; o; o &= o - 1) {
+                if (turn++ % NW != wave)
+                    continue;
+                const int u = __builtin_ctz(o);
+                const int n = __builtin_amdgcn_readfirstlane(jt.t[u].n);
+                take_joint(sh, jt, u, n, lane);
+                settle_groups(a, sh, s_sh[u / 4], u % 4, jt.t[u], n, lane);
+            }
+            __syncthreads();
+        }
         kept = sh.kept[row];
         const uint32_t magic = ((1u << 20) + gs - 1) / gs;    // e / gs for e < 512, gs <= 512
 #pragma unroll
@@ -908,47 +1158,93 @@ __global__ __launch_bounds__(64) void route_choose_kernel(const RouteArgs a)
             a.weights[m * a.topk + t] = id[h] < 0 ? 0.f : (float)(s[h] * f);
         }
     }
-    if (doubt == 0)
-        return;
-
-    // tokens in doubt, one after the other by the whole wave
+    // tokens in doubt: their lists
     if (rs != 0) {
 #pragma unroll
         for (int i = 0; i < Q; i++)
             *reinterpret_cast<u32x4 *>(&sh.key[row][64 * i + 4 * lr]) =
                 u32x4{key[4 * i], key[4 * i + 1], key[4 * i + 2], key[4 * i + 3]};
-        wait_lgkmcnt0();
     }
+    const bool mine = of_row(doubt, row) != 0 && m0 + row < M;
+    if (mine) {
+        Doubt &t = jt.t[4 * wave + row];
+        t.id[lr] = id[0];
+        t.id[16 + lr] = id[1];
+        if (lr == 0) {
+            t.m = m;
+            t.mx = mx;
+            t.sum = sum;
+            t.zd = zd;
+            t.clear = clear;
+            t.slots = (uint32_t)(of_row(so0, row) | (of_row(so1, row) << 16));
+            t.last = prev;
+            t.n = 0;
+            t.hard = of_row(hd, row) != 0;
+            t.rest = rest;
+        }
+    }
+    const uint64_t todo = __ballot(mine);
+    wait_lgkmcnt0();
+    if (todo != 0) {
 #pragma unroll 1
-    for (int r = 0; r < 4 && m0 + r < M; r++) {
-        if (of_row(doubt, r) == 0)
+        for (int r = 0; r < 4; r++) {
+            Doubt &t = jt.t[4 * wave + r];
+            if (((todo >> (16 * r)) & 1) == 0 || t.hard)
+                continue;
+            const int n = list_order(a, sh, sh, r, lane < SPEAR_MAX_TOPK ? t.id[lane] : -1, t.slots,
+                                     t.rest != 0, t.last, t.clear, lane);
+            if (lane < n && n <= RC_JOINT)
+                t.list[lane] = sh.list[lane];
+            if (lane == 0) {
+                t.n = n;
+                t.hard = n > 64;                          // so many: rounds over all of them are quicker
+            }
+        }
+    }
+    if (lane == 0)
+        jt.open[1][wave] = (todo & 1) | ((todo >> 15) & 2) | ((todo >> 30) & 4) | ((todo >> 45) & 8);
+    __syncthreads();
+    uint32_t open_all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; w++)
+        open_all |= __builtin_amdgcn_readfirstlane(jt.open[1][w]) << (4 * w);
+    if (open_all == 0)                                    // (the same for all waves)
+        return;
+    joint_logits(a, jt, open_all, wave, lane);
+    __syncthreads();
+    int turn = 0;
+#pragma unroll 1
+    for (uint32_t o = open_all; o; o &= o - 1) {
+        if (turn++ % NW != wave)
             continue;
-        const Doubt t = {m0 + r, r, lane_of(clear, 16 * r), lane_of(mx, 16 * r), lane_of(sum, 16 * r),
-                         lane_of(zd, 16 * r)};
+        const int u = __builtin_ctz(o), r = u % 4;
+        const Doubt &t = jt.t[u];
+        const ChooseShared<Q> &own = s_sh[u / 4];
         bool done = false;
-        if (of_row(hd, r) == 0) {
-            const uint64_t open = of_row(so0, r) | (of_row(so1, r) << 16);
-            const int i0 = __shfl(id[0], 16 * r + (lane & 15)), i1 = __shfl(id[1], 16 * r + (lane & 15));
-            const int my = lane < 16 ? i0 : lane < 32 ? i1 : -1;
-            done = settle_order(a, sh, t, lane, my, open, of_row(rs, r) != 0, lane_of(prev, 16 * r));
+        if (!t.hard) {
+            const int my = lane < SPEAR_MAX_TOPK ? t.id[lane] : -1;
+            const int n = __builtin_amdgcn_readfirstlane(t.n);
+            if (n <= RC_JOINT) {
+                take_joint(sh, jt, u, n, lane);
+            } else {
+                list_order(a, own, sh, r, my, t.slots, t.rest != 0, t.last, t.clear, lane);
+                exact_logits(a, t.m, lane, sh.list, n, sh.z);
+            }
+            done = settle_order(a, sh, t, n, lane);
             if (done) {
                 int e = my;
                 double z = 0.0;
-                if (lane < a.topk && ((open >> lane) & 1)) {
+                if (lane < a.topk && ((t.slots >> lane) & 1)) {
                     e = sh.slot_id[lane];
                     z = sh.slot_z[lane];
                 } else if (lane < a.topk && e >= 0) {
-                    z = (double)sh.logit[r][e];
+                    z = (double)own.logit[r][e];
                 }
                 write_choice(a, t.m, lane, lane < a.topk ? e : -1, score_of(a, z, (double)t.mx, (double)t.sum));
             }
         }
         if (!done) {
-#pragma unroll 1
-            for (int e = lane; e < E; e += 64)
-                sh.list[e] = (uint16_t)e;
-            wait_lgkmcnt0();
-            exact_logits(a, t.m, lane, sh.list, E, sh.z);
+            all_logits(a, sh, t, lane);
             choose_all(a, t.m, lane, sh.z, sh.c);
         }
     }
@@ -985,15 +1281,19 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const dim3 tokens((unsigned)((a.M + 3) / 4));
+    auto choose = [&](auto q) {
+        constexpr int NW = RC_WAVES<decltype(q)::value>;
+        hipLaunchKernelGGL(route_choose_kernel<decltype(q)::value>, dim3((unsigned)((a.M + 4 * NW - 1) / (4 * NW))),
+                           dim3(64 * NW), 0, s, a);
+    };
     if (a.E <= 64)
-        hipLaunchKernelGGL(route_choose_kernel<1>, tokens, dim3(64), 0, s, a);
+        choose(std::integral_constant<int, 1>{});
     else if (a.E <= 128)
-        hipLaunchKernelGGL(route_choose_kernel<2>, tokens, dim3(64), 0, s, a);
+        choose(std::integral_constant<int, 2>{});
     else if (a.E <= 256)
-        hipLaunchKernelGGL(route_choose_kernel<4>, tokens, dim3(64), 0, s, a);
+        choose(std::integral_constant<int, 4>{});
     else
-        hipLaunchKernelGGL(route_choose_kernel<8>, tokens, dim3(64), 0, s, a);
+        choose(std::integral_constant<int, 8>{});
     return hipGetLastError();
 }
 

@@ -143,3 +143,24 @@ def test_no_tokens_and_rows_behind():
     sp.spear_route(x, sp.Router(w, topk=2), weights=bw[:3], ids=bi[:3])
     assert bool((bw[3:] == 7).all()) and bool((bi[3:] == 7).all())
     assert np.array_equal(host(bi[:3]), ref64.route(x64, w64, 2, False)[1])
+
+
+@pytest.mark.parametrize("E,G,kept,topk,copies", [(64, 1, 1, 8, 5), (128, 1, 1, 32, 24), (256, 8, 4, 8, 20),
+                                                  (256, 1, 1, 8, 100), (512, 16, 3, 32, 40), (60, 6, 2, 4, 60)])
+@pytest.mark.parametrize("score", [sp.SCORE_SOFTMAX, sp.SCORE_SIGMOID])
+def test_many_ties_in_a_long_batch(E, G, kept, topk, copies, score):
+    """Whole groups of equal experts, rows of zeros among the tokens, a batch that
+    ends inside four tokens.  Small integers over 16: every sum is exact whatever
+    its order, so ties are ties, and go to the lowest index."""
+    rng = np.random.default_rng(E + copies)
+    M, K = 203, 2112
+    x = rng.integers(-3, 4, (M, K)) * (rng.random((M, K)) < 0.02)
+    x[rng.random(M) < 0.2] = 0
+    w = rng.integers(-3, 4, (E, K)) / 16.0
+    w[rng.choice(E, copies, replace=False)] = w[0]
+    xt, x64 = bf16(x.astype(np.float64))
+    wt, w64 = bf16(w)
+    assert np.array_equal(x64, x) and np.array_equal(w64, w)
+    compare(xt, x64, wt, w64, None, topk, score, n_group=G, topk_group=kept)
+    bias = (rng.integers(-1, 2, E) / 8.0).astype(np.float32)
+    compare(xt, x64, wt, w64, bias, topk, score, n_group=G, topk_group=kept, renorm=False)
