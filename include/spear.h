@@ -277,7 +277,10 @@ typedef struct spear_epilogue {
  * the weights (codes, scales, zero points, bias, B) is the gate's row i and row
  * 2i + 1 the up projection's, interleaved once before spear_pack_w4.  All of
  * the epilogue is in fp32, rounded once to y's type.  Other arguments, the
- * workspace and the dispatch are those of spear_w4_linear_path; ep is required.
+ * workspace and the paths are those of spear_w4_linear_path; ep is required.
+ * SPEAR_PATH_AUTO with M <= 16, a compensator of rank 64 at most and no gate
+ * vector of its own takes the compensator's first half as a launch of its own
+ * (t may differ from spear_w4_linear's in the order of its sums).
  * An expired wait makes the outputs NaN here too (NaN passes through every
  * activation).
  */
@@ -322,7 +325,8 @@ typedef struct spear_router {
  * c is NaN or -inf (a bias of -inf takes an expert out) is never chosen: a
  * slot left without an expert gets id -1 and weight 0, and takes no part in
  * the sum.  Scores that sum to zero give weights of zero.
- *   x [M][K] bf16, 16-byte aligned; M >= 0 (0 does nothing); K >= 32, K % 32 == 0.
+ *   x [M][K] bf16, 16-byte aligned; 0 <= M <= 2^27 (0 does nothing); K >= 32,
+ *     K % 32 == 0.
  *   weights [M][topk] fp32, ids [M][topk] int32 outputs, 4-byte aligned.
  *   workspace device scratch of spear_route_workspace_size bytes, 256-byte
  *             aligned; needs no zeroing and holds nothing between calls.
@@ -366,7 +370,7 @@ typedef struct spear_experts {
  *   x [M][K] bf16, ids [M][topk] int32, weights [M][topk] fp32,
  *   residual [M][N] bf16 or NULL (may be y itself), y [M][N] bf16; x, residual
  *   and y 16-byte aligned.  y may not overlap any other input.
- *   M >= 0 (0 does nothing), 1 <= topk <= SPEAR_MAX_TOPK, M topk < 2^31.
+ *   M >= 0 (0 does nothing), 1 <= topk <= SPEAR_MAX_TOPK, M topk <= 2^30.
  *   workspace device scratch of spear_w4_experts_workspace_size bytes, 256-byte
  *             aligned; needs no zeroing and holds nothing between calls.
  */

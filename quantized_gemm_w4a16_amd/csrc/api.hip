@@ -169,11 +169,10 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t r)
     }
     L.gpart = off;
     off = align256(off + gemm_part_bytes(M, N, K));
-    L.total = off;
     L.few = off;
     if (r > 0 && L.rpad <= FEW_RANK)
         off = align256(off + (size_t)FEW_SLICES * 16 * (L.rpad * sizeof(float) + sizeof(double)));
-    L.total_epi = off;
+    L.total = off;
     return L;
 }
 
@@ -299,7 +298,7 @@ size_t spear_w4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r
 {
     if (M < 0 || N < 1 || K < 32 || r < 0)
         return 0;
-    return ws_layout(M, N, K, r).total_epi;
+    return ws_layout(M, N, K, r).total;
 }
 
 spear_status spear_workspace_init(void *ws, size_t bytes, void *stream)
@@ -346,8 +345,7 @@ namespace spear {
 // from SPEAR_PATH_AUTO.
 static spear_status validate_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w,
                                     const spear_ec *ec, const void *y, int32_t out_dtype,
-                                    const void *workspace, size_t ws_bytes, int32_t *path_io,
-                                    bool epi = false)
+                                    const void *workspace, size_t ws_bytes, int32_t *path_io)
 {
     int32_t path = *path_io;
     if (!w || !workspace || !w->packed || !w->scales)
@@ -391,7 +389,7 @@ static spear_status validate_linear(const spear_bf16 *x, int64_t M, const spear_
         return SPEAR_E_ALIGN;
     const int32_t r = ec ? ec->r : 0;
     const WsLayout L = ws_layout(M, N, K, r);
-    if (ws_bytes < (epi ? L.total_epi : L.total))
+    if (ws_bytes < L.total)
         return SPEAR_E_WORKSPACE;
     if (L.ncg * L.ksplit > GRID_MAX || cdiv(N, 64) * cdiv(M, 64) > GRID_MAX)
         return SPEAR_E_SHAPE;
@@ -544,7 +542,10 @@ static spear_status launch_path(LinearArgs &a, const spear_ec *ec, int32_t path,
 }
 
 // Decode with an epilogue, no path asked for: the EC's pre-pass in a launch of
-// its own before the decode kernel, rather than exchanged inside it.
+// its own before the decode kernel, rather than exchanged inside it (2048 -> 16384
+// pair, one token: 13.4 us, 16.4 exchanged; 8192 -> 2048, 16 tokens: 15.0, 17.1).
+// Above rank 64 the partials no longer fit what a decode workgroup loads ahead;
+// a gate vector needs all of them before its own layers.
 static bool few_ec_prepass(const spear_ec *ec)
 {
     return ec && ec->gate_h == 0 && cdiv(ec->r, 32) * 32 <= FEW_RANK;
@@ -638,7 +639,7 @@ spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spea
     if (!ep)
         return SPEAR_E_NULL;
     const bool any = path == SPEAR_PATH_AUTO;
-    spear_status st = validate_linear(x, M, w, ec, y, out_dtype, workspace, ws_bytes, &path, true);
+    spear_status st = validate_linear(x, M, w, ec, y, out_dtype, workspace, ws_bytes, &path);
     if (st != SPEAR_OK)
         return st;
     if (ep->act < SPEAR_ACT_NONE || ep->act > SPEAR_ACT_GELU_TANH || (ep->glu != 0 && ep->glu != 1))

@@ -21,6 +21,7 @@ namespace spear {
 namespace {
 
 constexpr int XT = 16;                                    // rows of the smallest tile
+constexpr int64_t MAX_SLOTS = 1 << 30;
 
 struct ExpertsLayout {
     size_t hdr, zeros, tiles, list, h, d, total;
@@ -31,11 +32,18 @@ struct ExpertsLayout {
 // last one ragged, so at most slots / bm + (experts in use) of them.
 int64_t max_tiles(int64_t slots, int32_t E, int bm) { return slots / bm + (slots < E ? slots : E); }
 
-// Rows of a tile by the slots an expert has on average.
-int tile_rows(int64_t slots, int32_t E)
+// Rows of a tile by the slots an expert has on average.  Whole calls, us with 16
+// / 64 rows (32 rows are behind one of them everywhere):
+//   32 experts 2048 -> 2 x 1408 -> 2048:  12 slots 59 / 62, 16: 63 / 65, 20: 74 / 68
+//    8 experts 4096 -> 2 x 4096 -> 4096:  12 slots 70 / 72, 16: 83 / 75, 20: 92 / 76
+// and with 64 / 128 rows, where 128 need long enough rows to fill their pipeline:
+//   the first:                            256 slots 280 / 332, 768: 729 / 761, 1024: 959 / 999
+//   the second:                           128 slots 195 / 216, 320: 372 / 368, 1024: 1058 / 1002
+//    8 experts 4096 -> 2 x 8192 -> 4096:  256 slots 611 / 632, 320: 699 / 671, 1024: 2081 / 1781
+int tile_rows(int64_t slots, int32_t E, int64_t K, int64_t I)
 {
-    const int64_t per = slots / E;
-    return per >= 64 ? 128 : per >= 20 ? 64 : per >= 10 ? 32 : XT;
+    const int64_t per = slots / E, depth = K < I ? K : I;
+    return per < 16 ? XT : per * depth < 320 * 4096 ? 64 : 128;
 }
 
 ExpertsLayout experts_layout(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N)
@@ -181,28 +189,31 @@ __device__ __forceinline__ void pin_group_args(const GroupArgs &a)
     pin_arg(a.E);
 }
 
-// Few slots: the most that a workgroup looks through by itself.
-constexpr int FEW_SLOTS = 64;
+// Up to this many slots, two launches: the products make their own plan, the
+// second joins.  us with two / four launches, 2048 -> 2 x 1024 -> 2048: 8 slots of
+// 64 experts 18.8 / 21.8, 12: 24.7 / 25.4, 16: 27.3 / 25.4, 24: 35.7 / 30.4; of 16
+// experts 12: 24.9 / 25.5, 16: 24.3 / 24.8, 24: 26.8 / 25.1; of 8 experts 16: 19.7 /
+// 22.1, 32: 22.1 / 21.8.
+constexpr int FEW_SLOTS = 16;
 
 // What depths past K read: zeros (16 bytes a lane of 16).
 __device__ __align__(256) static uint8_t g_zeros[256];
 
 // The streaming product: a workgroup of NW waves takes a row tile of up to BM
-// rows and 16 FC NW channels, wave w 16 FC of them over all of K.  Weights go
-// from memory to registers, RING - 1 chunks of 512 depths (4 FC 16-byte loads a
+// rows and 16 NW channels, wave w 16 of them over all of K.  Weights go from
+// memory to registers, RING - 1 chunks of SC depths (SC / 128 16-byte loads a
 // lane) ahead of the one in use, and are unpacked once for all the tile's rows;
-// the rows go by DMA to RING LDS buffers a chunk deep (1 KB a row, its 16-byte
-// pieces swizzled by row % 16 on the way; zeros past K), with one barrier a
-// chunk.  Lane (c, g) holds channel c's 32 codes k = 128 s + 32 g .. + 31 of
+// the rows go by DMA to RING LDS buffers a chunk deep (2 SC bytes a row, its
+// 16-byte pieces swizzled by row % 16 on the way; zeros past K), with one
+// barrier a chunk.  Lane (c, g) holds channel c's 32 codes k = 128 s + 32 g .. + 31 of
 // step s as one load, and reads the same depths of its token row as four.  The
 // rows' sums, which remove the unpacking's offset, are shared out over the
 // waves by depth and meet in LDS.  Rows past the tile's end repeat the last one
 // and are not stored: an output depends on its own row alone.
-// PLAN 1 (few slots): no plan was launched.  The block's tile is (part, group):
-// the group an expert, or with fewer slots than experts a slot whose expert no
-// earlier slot has; each wave finds that expert's slots in ids by a ballot, and
-// the block takes the part-th 16 of them.
-template <int BM, int NW, int FC, int UP, int PLAN, int RING, int SC>
+// PLAN 1 (few slots): no plan was launched.  The block's tile is an expert, or
+// with fewer slots than experts a slot whose expert no earlier slot has; each
+// wave finds that expert's slots in ids by a ballot.
+template <int BM, int NW, int UP, int PLAN, int RING, int SC>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) void stream_kernel(const GroupArgs a)
 {
     constexpr int NF = BM / 16, NS = SC / 128;            // fragments; steps of a chunk
@@ -220,19 +231,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
     Tile q;
-    uint64_t mine = 0;                                    // PLAN: the expert's slots from the tile's first on
+    uint64_t mine = 0;                                    // PLAN: the expert's slots
     if constexpr (PLAN != 0) {
-        const int groups = a.slots < a.E ? a.slots : a.E;
-        const int part = tile / groups, g = tile - part * groups;
+        static_assert(FEW_SLOTS <= BM, "an expert's slots are one tile");
         const int id = lane < a.slots ? a.ids[lane] : -1;
-        const int e = a.slots < a.E ? __builtin_amdgcn_readlane(id, g) : g;
+        const int e = a.slots < a.E ? __builtin_amdgcn_readlane(id, tile) : tile;
         mine = __ballot(id == e && lane < a.slots);
-        const int cnt = __popcll(mine) - 16 * part;
-        if (e < 0 || e >= a.E || cnt <= 0 || (a.slots < a.E && __builtin_ctzll(mine) != g))
+        if (e < 0 || e >= a.E || mine == 0 || (a.slots < a.E && __builtin_ctzll(mine) != tile))
             return;
-        for (int i = 0; i < 16 * part; i++)
-            mine &= mine - 1;
-        q = {e, 0, cnt < 16 ? cnt : 16, 0};
+        q = {e, 0, (int)__popcll(mine), 0};
     } else {
         q = a.tiles[tile];                                // (the table has room for every block)
         if (tile >= *a.ntiles)
@@ -249,45 +256,35 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
         }
     };
     const int64_t N = a.N, K = a.K;
-    const int64_t n0 = ((int64_t)cb * NW + wave) * (16 * FC);
+    const int64_t n0 = ((int64_t)cb * NW + wave) * 16;
     const int64_t base = (int64_t)q.e * N;
     const int64_t C = (K + SC - 1) / SC;
     // The epilogue's operands, without branches.  Their lines are cold, a round
     // trip of 2 to 3 us: with registers to spare (16-row tiles) they are loaded
     // ahead of the stream, else in one go behind it.
     constexpr bool EARLY = BM == 16;
-    float sc[FC][4], b[FC][4];
-    uint32_t zr[FC][4];
+    float sc[4], b[4];
+    uint32_t zr[4];
     auto operands = [&]() __attribute__((always_inline)) {
+        const int64_t n = n0 + 4 * lg;
 #pragma unroll
-        for (int j = 0; j < FC; j++) {
-            const int64_t n = n0 + 16 * j + 4 * lg;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int64_t nn = n + i < N ? n + i : N - 1;
-                sc[j][i] = a.scales[base + nn];
-                zr[j][i] = load_zero_byte(a.zeros ? a.zeros + base : nullptr, a.scales + base, nn);
-            }
-            epi_load_bias(a.bias ? a.bias + base : nullptr, a.scales + base, n, N, b[j]);
+        for (int i = 0; i < 4; i++) {
+            const int64_t nn = n + i < N ? n + i : N - 1;
+            sc[i] = a.scales[base + nn];
+            zr[i] = load_zero_byte(a.zeros ? a.zeros + base : nullptr, a.scales + base, nn);
         }
+        epi_load_bias(a.bias ? a.bias + base : nullptr, a.scales + base, n, N, b);
     };
-    const uint8_t *wr[FC];
-#pragma unroll
-    for (int j = 0; j < FC; j++) {
-        const int64_t n = n0 + 16 * j + lr;
-        wr[j] = a.packed + (base + (n < N ? n : N - 1)) * (K / 2) + 16 * lg;
-    }
-    auto load_w = [&](int64_t c, u32x4 (&w)[FC][NS]) __attribute__((always_inline)) {
+    const uint8_t *const wr = a.packed + (base + (n0 + lr < N ? n0 + lr : N - 1)) * (K / 2) + 16 * lg;
+    auto load_w = [&](int64_t c, u32x4 (&w)[NS]) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NS; t++) {
             // past K: the row's first codes, which meet zeros
             const bool in = SC * c + 128 * t + 32 * lg < K;
-#pragma unroll
-            for (int j = 0; j < FC; j++)
-                w[j][t] = ld16(in ? wr[j] + (SC * c + 128 * t) / 2 : wr[j] - 16 * lg);
+            w[t] = ld16(in ? wr + (SC * c + 128 * t) / 2 : wr - 16 * lg);
         }
     };
-    u32x4 w[RING][FC][NS];
+    u32x4 w[RING][NS];
 #pragma unroll
     for (int j = 0; j < RING; j++)
         load_w(j < C ? j : C - 1, w[j]);
@@ -317,14 +314,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
     for (int j = 0; j < RING; j++)
         issue_x(j < C ? j : C - 1, ring[j]);
 
-    f32x4 acc[FC][NF], rs[NF];
+    f32x4 acc[NF], rs[NF];
 #pragma unroll
-    for (int f = 0; f < NF; f++) {
-        rs[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < FC; j++)
-            acc[j][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int f = 0; f < NF; f++)
+        acc[f] = rs[f] = f32x4{0.f, 0.f, 0.f, 0.f};
     const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     // LDS pieces of row lr for depths 8 (16 t + 4 lg + d): 16 t + ((4 lg + d) ^ lr)
     int xo[4];
@@ -336,22 +329,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
     // paths meet, and the compiler would wait for everything there; and after a
     // matrix instruction and a taken branch this toolchain can leave out the
     // wait states before its result is read.  FR: fragments taken.
-    auto use = [&](auto FR, const uint8_t *buf, const u32x4 (&w)[FC][NS]) __attribute__((always_inline)) {
+    auto use = [&](auto FR, const uint8_t *buf, const u32x4 (&w)[NS]) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NS; t++)
 #pragma unroll
             for (int d = 0; d < 4; d++) {
-                u32x4 wv[FC];
+                const u32x4 wv = unpack8(w[t][d]);
 #pragma unroll
-                for (int j = 0; j < FC; j++)
-                    wv[j] = unpack8(w[j][t][d]);
-#pragma unroll
-                for (int f = 0; f < decltype(FR)::value; f++) {
-                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(buf + xo[d] + 256 * t + 16 * RB * f);
-#pragma unroll
-                    for (int j = 0; j < FC; j++)
-                        acc[j][f] = mfma16(wv[j], xv, acc[j][f]);
-                }
+                for (int f = 0; f < decltype(FR)::value; f++)
+                    acc[f] = mfma16(wv, *reinterpret_cast<const u32x4 *>(buf + xo[d] + 256 * t + 16 * RB * f), acc[f]);
             }
 #pragma unroll
         for (int i = 0; i < NP; i++) {
@@ -364,7 +350,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
     };
     auto run = [&](auto FR) __attribute__((always_inline)) {
         // Younger than the rows of the next chunk: its weights, and the further chunks.
-        constexpr int WAIT = NS * FC + (RING - 2) * (NI + NS * FC);
+        constexpr int WAIT = NS + (RING - 2) * (NI + NS);
         static_assert(WAIT < 64, "vmcnt");
         wait_vmcnt<0>();
         bare_barrier();
@@ -411,7 +397,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
                 s_rs[wave][16 * f + lr] = rs[f][0];
         }
         __syncthreads();
-        // lane (row lr of fragment f, lg): channels n0 + 16 j + 4 lg + i
+        // lane (row lr of fragment f, lg): channels n0 + 4 lg + i
 #pragma unroll
         for (int f = 0; f < decltype(FR)::value; f++) {
             const int r = 16 * f + lr;
@@ -419,49 +405,53 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
 #pragma unroll
             for (int v = 0; v < NW; v++)
                 sum += s_rs[v][r];
+            float t[4], bb[4], o[4];
 #pragma unroll
-            for (int j = 0; j < FC; j++) {
-                float t[4], bb[4], o[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    t[i] = sc[j][i] * __builtin_fmaf(-(UNPACK_OFF + zero_point(a.zeros, zr[j][i])), sum,
-                                                     UNPACK_SCALE * acc[j][f][i]);
-                    bb[i] = a.bias ? b[j][i] : 0.f;
-                }
-                epi_apply(t, bb, UP ? a.act : SPEAR_ACT_NONE, UP ? a.glu : 0, o);
-                if (r < q.cnt)
-                    epi_store<(UP ? 0 : 1)>(a.out, slot[f], n0 + 16 * j + 4 * lg, UP ? a.glu : 0,
-                                            UP && a.glu ? N / 2 : N, o);
+            for (int i = 0; i < 4; i++) {
+                t[i] = sc[i] * __builtin_fmaf(-(UNPACK_OFF + zero_point(a.zeros, zr[i])), sum,
+                                              UNPACK_SCALE * acc[f][i]);
+                bb[i] = a.bias ? b[i] : 0.f;
             }
+            epi_apply(t, bb, UP ? a.act : SPEAR_ACT_NONE, UP ? a.glu : 0, o);
+            if (r < q.cnt)
+                epi_store<(UP ? 0 : 1)>(a.out, slot[f], n0 + 4 * lg, UP ? a.glu : 0, UP && a.glu ? N / 2 : N, o);
         }
     };
     const int nf = (q.cnt + 15) / 16;                     // fragments in use
-    if (NF >= 4 && nf == 3)
-        run(std::integral_constant<int, NF >= 4 ? 3 : 1>());
-    else if (NF >= 4 && nf == 2)
-        run(std::integral_constant<int, NF >= 4 ? 2 : 1>());
-    else if (NF > 1 && nf == 1)
+    if constexpr (NF == 4) {
+        if (nf == 3)
+            run(std::integral_constant<int, 3>());
+        else if (nf == 2)
+            run(std::integral_constant<int, 2>());
+        else if (nf == 1)
+            run(std::integral_constant<int, 1>());
+        else
+            run(std::integral_constant<int, 4>());
+    } else {
+        static_assert(NF == 1, "fragments of a tile");
         run(std::integral_constant<int, 1>());
-    else
-        run(std::integral_constant<int, NF>());
+    }
 }
 
-template <int BM, int NW, int FC, int UP, int PLAN, int RING, int SC>
+template <int BM, int NW, int UP, int PLAN, int RING, int SC>
 hipError_t launch_stream_t(GroupArgs a, int64_t tiles, hipStream_t s)
 {
-    a.ncb = (int32_t)((a.N + 16 * FC * NW - 1) / (16 * FC * NW));
-    hipLaunchKernelGGL((stream_kernel<BM, NW, FC, UP, PLAN, RING, SC>), dim3((unsigned)(tiles * a.ncb)), dim3(64 * NW), 0, s, a);
+    a.ncb = (int32_t)((a.N + 16 * NW - 1) / (16 * NW));
+    hipLaunchKernelGGL((stream_kernel<BM, NW, UP, PLAN, RING, SC>), dim3((unsigned)(tiles * a.ncb)), dim3(64 * NW), 0,
+                       s, a);
     return hipGetLastError();
 }
 
+// 64 rows: 8 waves of 16 channels and 256 depths a chunk (300 tokens, 32 experts,
+// first product: 48 us; 512 depths 57, 32 channels a wave 58, 16 waves 61).  16
+// rows: two buffers of 512 depths with a plan (16 tokens, 64 experts: 31 us, four
+// buffers 43, whose registers leave half the workgroups a CU), four without one
+// (a few workgroups a CU at most, where depth in flight is all there is).
 template <int UP>
 hipError_t launch_stream(const GroupArgs &a, int bm, int64_t tiles, hipStream_t s)
 {
-    if (bm == 64)
-        return launch_stream_t<64, 8, 1, UP, 0, 2, 256>(a, tiles, s);
-    if (bm == 32)
-        return launch_stream_t<32, 8, 2, UP, 0, 2, 512>(a, tiles, s);
-    return launch_stream_t<16, 4, 1, UP, 0, 2, 512>(a, tiles, s);
+    return bm == 64 ? launch_stream_t<64, 8, UP, 0, 2, 256>(a, tiles, s)
+                    : launch_stream_t<16, 4, UP, 0, 2, 512>(a, tiles, s);
 }
 
 // ------------------------------------------------- few slots: down and join
@@ -522,61 +512,58 @@ __global__ __launch_bounds__(64 * FW_WAVES) void few_down_kernel(const FewArgs a
         }
         epi_load_bias(a.g.bias ? a.g.bias + base : nullptr, a.g.scales + base, n0 + 4 * lg, N, b);
         const float bf = a.g.bias && part == 0 ? 1.f : 0.f;
-        while (rows) {                                    // 16 slots at a time
-            int slot = -1;                                // lane row lr: the lr-th of them
-            for (int i = 0; i < 16; i++) {
-                if (lr == i && rows)
-                    slot = __builtin_ctzll(rows);
-                rows &= rows ? rows - 1 : 0;
+        int slot = -1;                                // lane row lr: the lr-th of them
+        for (int i = 0; i < FEW_SLOTS && rows; i++) {
+            if (lr == i)
+                slot = __builtin_ctzll(rows);
+            rows &= rows - 1;
+        }
+        const uint16_t *hr = a.g.x + (int64_t)(slot < 0 ? 0 : slot) * K + 32 * lg;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, rs = acc;
+        for (int64_t t = t0; t < t1; t += FW_B) {
+            u32x4 w[FW_B], xv[FW_B][4];
+#pragma unroll
+            for (int i = 0; i < FW_B; i++) {
+                const int64_t k = 128 * (t + i);
+                const bool kv = t + i < t1 && k + 32 * lg < K;
+                w[i] = ld16(kv ? wr + k / 2 : wr - 16 * lg);
+#pragma unroll
+                for (int d = 0; d < 4; d++)
+                    xv[i][d] = kv && slot >= 0 ? ld16(hr + k + 8 * d) : zero4();
             }
-            const uint16_t *hr = a.g.x + (int64_t)(slot < 0 ? 0 : slot) * K + 32 * lg;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, rs = acc;
-            for (int64_t t = t0; t < t1; t += FW_B) {
-                u32x4 w[FW_B], xv[FW_B][4];
 #pragma unroll
-                for (int i = 0; i < FW_B; i++) {
-                    const int64_t k = 128 * (t + i);
-                    const bool kv = t + i < t1 && k + 32 * lg < K;
-                    w[i] = ld16(kv ? wr + k / 2 : wr - 16 * lg);
+            for (int i = 0; i < FW_B; i++)
 #pragma unroll
-                    for (int d = 0; d < 4; d++)
-                        xv[i][d] = kv && slot >= 0 ? ld16(hr + k + 8 * d) : zero4();
+                for (int d = 0; d < 4; d++) {
+                    acc = mfma16(unpack8(w[i][d]), xv[i][d], acc);
+                    rs = mfma16(ones, xv[i][d], rs);
                 }
+        }
+        if (slot >= 0) {
 #pragma unroll
-                for (int i = 0; i < FW_B; i++)
-#pragma unroll
-                    for (int d = 0; d < 4; d++) {
-                        acc = mfma16(unpack8(w[i][d]), xv[i][d], acc);
-                        rs = mfma16(ones, xv[i][d], rs);
-                    }
-            }
-            if (slot >= 0) {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    s_d[part][slot][4 * lg + i] =
-                        sc[i] * __builtin_fmaf(-(UNPACK_OFF + zero_point(a.g.zeros, zr[i])), rs[0],
-                                               UNPACK_SCALE * acc[i]) + (bf != 0.f ? b[i] : 0.f);
-            }
+            for (int i = 0; i < 4; i++)
+                s_d[part][slot][4 * lg + i] =
+                    sc[i] * __builtin_fmaf(-(UNPACK_OFF + zero_point(a.g.zeros, zr[i])), rs[0],
+                                           UNPACK_SCALE * acc[i]) + (bf != 0.f ? b[i] : 0.f);
         }
     }
     __syncthreads();
-    for (int i0 = 0; i0 < 16 * M; i0 += 64 * FW_WAVES) {  // uniform: every lane shuffles
-        const int i = i0 + tid, m = i >> 4;
-        const int64_t n = n0 + (i & 15);
-        const bool in = m < M && n < N;
-        float o = i0 == 0 ? res0 : in && a.j.res ? bf16f(a.j.res[m * N + n]) : 0.f;
-        for (int j = 0; j < topk; j++) {
-            const int slot = m < M ? m * topk + j : 0;
-            const int e = __shfl(id, slot);
-            const float ws = __shfl(wt, slot);
-            if (in && e >= 0) {
-                const float d = parts == 2 ? s_d[0][slot][i & 15] + s_d[1][slot][i & 15] : s_d[0][slot][i & 15];
-                o = __builtin_fmaf(ws, d, o);
-            }
+    // thread: channel tid % 16 of token tid / 16 (every lane shuffles)
+    static_assert(16 * FEW_SLOTS <= 64 * FW_WAVES, "a thread an output");
+    const int m = tid >> 4;
+    const bool in = m < M && rn < N;
+    float o = res0;
+    for (int j = 0; j < topk; j++) {
+        const int slot = m < M ? m * topk + j : 0;
+        const int e = __shfl(id, slot);
+        const float ws = __shfl(wt, slot);
+        if (in && e >= 0) {
+            const float d = parts == 2 ? s_d[0][slot][tid & 15] + s_d[1][slot][tid & 15] : s_d[0][slot][tid & 15];
+            o = __builtin_fmaf(ws, d, o);
         }
-        if (in)
-            a.j.y[m * N + n] = f2bf(o);
     }
+    if (in)
+        a.j.y[m * N + rn] = f2bf(o);
 }
 
 // ---------------------------------------------------------------------- join
@@ -585,38 +572,35 @@ constexpr int JB = 8;
 
 __global__ __launch_bounds__(256) void join_kernel(const JoinArgs a)
 {
-    const int64_t nq = (a.N + 3) / 4;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (idx >= a.M * nq)
-        return;
-    const int64_t m = idx / nq, n = 4 * (idx % nq), N = a.N;
-    float o[4];
-    epi_load_res<0>(a.res, m, n, 0, N, o);
-    // JB slots' loads in flight at once; a slot without an expert has an unwritten
-    // row, whose values are dropped
-    for (int j0 = 0; j0 < a.topk; j0 += JB) {
-        float v[JB][4], w[JB];
-        int e[JB];
+    const int64_t nq = (a.N + 3) / 4, N = a.N, step = (int64_t)gridDim.x * 256;
+    for (int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x; idx < a.M * nq; idx += step) {
+        const int64_t m = idx / nq, n = 4 * (idx % nq);
+        float o[4];
+        epi_load_res<0>(a.res, m, n, 0, N, o);
+        // JB slots' loads in flight at once; a slot without an expert has an
+        // unwritten row, whose values are dropped
+        for (int j0 = 0; j0 < a.topk; j0 += JB) {
+            float v[JB][4], w[JB];
+            int e[JB];
 #pragma unroll
-        for (int j = 0; j < JB; j++) {
-            const int64_t slot = m * a.topk + (j0 + j < a.topk ? j0 + j : a.topk - 1);
-            e[j] = j0 + j < a.topk ? a.ids[slot] : -1;
-            w[j] = a.weights[slot];
-            epi_load_res<1>(a.d, slot, n, 0, N, v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < JB; j++)
-            if (e[j] >= 0 && e[j] < a.E) {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    o[i] = __builtin_fmaf(w[j], v[j][i], o[i]);
+            for (int j = 0; j < JB; j++) {
+                const int64_t slot = m * a.topk + (j0 + j < a.topk ? j0 + j : a.topk - 1);
+                e[j] = j0 + j < a.topk ? a.ids[slot] : -1;
+                w[j] = a.weights[slot];
+                epi_load_res<1>(a.d, slot, n, 0, N, v[j]);
             }
+#pragma unroll
+            for (int j = 0; j < JB; j++)
+                if (e[j] >= 0 && e[j] < a.E) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        o[i] = __builtin_fmaf(w[j], v[j][i], o[i]);
+                }
+        }
+        epi_store<0>(a.y, m, n, 0, N, o);
     }
-    epi_store<0>(a.y, m, n, 0, N, o);
 }
-
-// Two launches: few slots, and few of them an expert.
-bool few(int64_t slots, int32_t E) { return slots <= FEW_SLOTS && tile_rows(slots, E) == XT; }
+constexpr int64_t JOIN_BLOCKS = 1 << 22;                  // most of a launch (2^32 threads are too many)
 
 bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 
@@ -630,7 +614,7 @@ extern "C" {
 size_t spear_w4_experts_workspace_size(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N)
 {
     if (M < 0 || topk < 1 || topk > SPEAR_MAX_TOPK || E < 1 || E > SPEAR_MAX_EXPERTS || I < 32 || N < 1 ||
-        M > 0x7FFFFFFF / topk || I > ((int64_t)1 << 31) || N > ((int64_t)1 << 31))
+        M > MAX_SLOTS / topk || I > ((int64_t)1 << 31) || N > ((int64_t)1 << 31))
         return 0;
     return experts_layout(M, topk, E, I, N).total;
 }
@@ -646,7 +630,7 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     const int64_t K = w->K, I = w->I, N = w->N;
     const int64_t lim = (int64_t)1 << 31;
     if (M < 0 || topk < 1 || topk > SPEAR_MAX_TOPK || w->E < 1 || w->E > SPEAR_MAX_EXPERTS || K < 32 ||
-        K % 32 != 0 || I < 32 || I % 32 != 0 || N < 1 || M > 0x7FFFFFFF / topk || K > lim || I > lim || N > lim)
+        K % 32 != 0 || I < 32 || I % 32 != 0 || N < 1 || M > MAX_SLOTS / topk || K > lim || I > lim || N > lim)
         return SPEAR_E_SHAPE;
     if (w->act < SPEAR_ACT_NONE || w->act > SPEAR_ACT_GELU_TANH || (w->glu != 0 && w->glu != 1))
         return SPEAR_E_ARG;
@@ -658,10 +642,11 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     if (ws_bytes < L.total)
         return SPEAR_E_WORKSPACE;
     const int64_t NU = w->glu ? 2 * I : I, wide = NU > N ? NU : N;
-    const int bm = tile_rows(L.slots, w->E);
+    const int bm = tile_rows(L.slots, w->E, K, I);
     const int64_t nt = max_tiles(L.slots, w->E, bm);
-    // grids: row tiles times channel tiles of at least 64, and join quads
-    if (nt > 0x7FFFFFFF / ((wide + 63) / 64) || (M * ((N + 3) / 4) + 255) / 256 > 0x7FFFFFFF)
+    // a launch's threads: below 2^32, by the narrowest channel block of 64 and 512
+    // threads (few slots: as many tiles at most, and 16 channels a workgroup)
+    if ((nt > FEW_SLOTS ? nt : FEW_SLOTS) > ((int64_t)1 << 23) / ((wide + 63) / 64 + 1))
         return SPEAR_E_SHAPE;
     const spear_status st = check_device();
     if (st != SPEAR_OK || M == 0)
@@ -671,11 +656,11 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     int32_t *ntiles = reinterpret_cast<int32_t *>(ws + L.hdr);
     Tile *tiles = reinterpret_cast<Tile *>(ws + L.tiles);
     int32_t *list = reinterpret_cast<int32_t *>(ws + L.list);
-    if (few(L.slots, w->E)) {
+    if (L.slots <= FEW_SLOTS) {
         GroupArgs u = {x, w->up, w->up_scales, w->up_zeros, w->up_bias, ws + L.h, nullptr, nullptr, nullptr,
                        NU, K, topk, w->act, w->glu, 0, ids, (int32_t)L.slots, w->E};
-        const int64_t blocks = (L.slots < w->E ? L.slots : w->E) * ((L.slots + 15) / 16);
-        if (launch_stream_t<16, 4, 1, 1, 1, 4, 512>(u, blocks, s) != hipSuccess)
+        const int64_t blocks = L.slots < w->E ? L.slots : w->E;
+        if (launch_stream_t<16, 4, 1, 1, 4, 512>(u, blocks, s) != hipSuccess)
             return SPEAR_E_HIP;
         const FewArgs f = {{reinterpret_cast<const uint16_t *>(ws + L.h), w->down, w->down_scales, w->down_zeros,
                             w->down_bias, nullptr, nullptr, nullptr, nullptr, N, I, 1, SPEAR_ACT_NONE, 0, 0, ids,
@@ -716,7 +701,7 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
         a.N = NU;
         a.K = K;
         a.G.div = topk;
-        if (launch_gemm_grouped(a, bm, nt, s) != hipSuccess)
+        if (launch_gemm_grouped(a, nt, s) != hipSuccess)
             return SPEAR_E_HIP;
         a.x = reinterpret_cast<const uint16_t *>(ws + L.h);
         a.packed = w->down;
@@ -730,11 +715,12 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
         a.N = N;
         a.K = I;
         a.G.div = 1;
-        if (launch_gemm_grouped(a, bm, nt, s) != hipSuccess)
+        if (launch_gemm_grouped(a, nt, s) != hipSuccess)
             return SPEAR_E_HIP;
     }
     JoinArgs j = {reinterpret_cast<const float *>(ws + L.d), ids, weights, residual, y, M, N, topk, w->E};
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((M * ((N + 3) / 4) + 255) / 256)), dim3(256), 0, s, j);
+    const int64_t jb = (M * ((N + 3) / 4) + 255) / 256;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(jb < JOIN_BLOCKS ? jb : JOIN_BLOCKS)), dim3(256), 0, s, j);
     return hipGetLastError() == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
 }
 

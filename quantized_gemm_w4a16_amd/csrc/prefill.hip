@@ -1580,11 +1580,8 @@ hipError_t launch_grouped_t(const LinearArgs &a, int64_t max_tiles, hipStream_t 
 
 } // namespace
 
-hipError_t launch_gemm_grouped(const LinearArgs &a, int bm, int64_t max_tiles, hipStream_t s)
+hipError_t launch_gemm_grouped(const LinearArgs &a, int64_t max_tiles, hipStream_t s)
 {
-    if (bm == 64)
-        return a.K % 128 == 0 ? launch_grouped_t<2, 2, 1, 4, 4, 1>(a, max_tiles, s)
-                              : launch_grouped_t<2, 2, 1, 4, 4, 0>(a, max_tiles, s);
     return a.K % 128 == 0 ? launch_grouped_t<2, 4, 1, 4, 4, 1>(a, max_tiles, s)
                           : launch_grouped_t<2, 4, 1, 4, 4, 0>(a, max_tiles, s);
 }

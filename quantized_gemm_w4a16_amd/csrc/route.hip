@@ -22,6 +22,8 @@ namespace spear {
 
 namespace {
 
+constexpr int64_t MAX_TOKENS = 1 << 27;                   // a launch stays below 2^32 threads
+
 struct RouteArgs {
     const uint16_t *x, *w;
     const float *bias;
@@ -342,7 +344,10 @@ __global__ __launch_bounds__(64 * RF_WAVES) void route_fused_kernel(const RouteA
 // Error: a product passes through at most 32 roundings inside a matrix
 // instruction (whatever its order), 8 along a chain of them (the chain's sum
 // then moves to a second accumulator), one for each of a slice's chains and
-// one for each slice, of a step (2^-23) at most.  So a logit is off by at most
+// one for each slice, of a step (2^-23) at most (the hardware rounds to nearest
+// and fewer times: with sums of one sign, with a first product 3000 times the
+// others, and with exponents spread over 12 bits, K of 256 to 8192, the largest
+// error of a logit was 5.8 such units where this allows 52).  So a logit is off by at most
 // (32 + 8 + chains + ks) 2^-23 sum |x w|, and sum |x w| is at most the product
 // of the rows' 2-norms, whose squares are formed on the way.
 constexpr int RL_TM = 128;
@@ -1250,9 +1255,11 @@ __global__ __launch_bounds__(64 * RC_WAVES<Q>, 2) void route_choose_kernel(const
     }
 }
 
-// One launch up to this many tokens, while the router's weights are small
-// enough for one CU to read them in the time that a second launch would cost.
-constexpr int64_t RF_TOKENS = 64;
+// One launch while every token has a CU of its own and the router's weights are
+// small enough for one CU to read.  us in graphs, one / two launches: 64 experts x
+// 2048 1 token 10.7 / 14.2, 256: 11.7 / 20.1, 384: 21.0 / 20.2; 128 x 2048 (512 KiB)
+// 1: 15.9 / 17.4, 256: 17.6 / 24.0; 128 x 4096 (1 MiB) 1: 24.4 / 20.4, 64: 25.6 / 24.7.
+constexpr int64_t RF_TOKENS = 256;
 constexpr int64_t RF_BYTES = 512 << 10;
 
 bool fused(int64_t M, int32_t E, int64_t K) { return M <= RF_TOKENS && 2 * K * E <= RF_BYTES; }
@@ -1330,7 +1337,7 @@ extern "C" {
 
 size_t spear_route_workspace_size(int64_t M, int32_t E)
 {
-    if (M < 0 || E < 1 || E > SPEAR_MAX_EXPERTS || M > ((int64_t)1 << 40))
+    if (M < 0 || E < 1 || E > SPEAR_MAX_EXPERTS || M > MAX_TOKENS)
         return 0;
     return route_layout(M, E).total;
 }
@@ -1342,7 +1349,7 @@ spear_status spear_route(const spear_bf16 *x, int64_t M, int64_t K, const spear_
     if (!router || !router->w || !workspace || (M > 0 && (!x || !weights || !ids)))
         return SPEAR_E_NULL;
     const spear_router &r = *router;
-    if (M < 0 || M > 0x7FFFFFFF || K < 32 || K % 32 != 0 || r.E < 1 || r.E > SPEAR_MAX_EXPERTS ||
+    if (M < 0 || M > MAX_TOKENS || K < 32 || K % 32 != 0 || r.E < 1 || r.E > SPEAR_MAX_EXPERTS ||
         r.topk < 1 || r.topk > SPEAR_MAX_TOPK || r.n_group < 1 || r.n_group > SPEAR_MAX_GROUPS ||
         r.E % r.n_group != 0 || r.topk_group < 1 || r.topk_group > r.n_group ||
         (int64_t)r.topk > (int64_t)r.topk_group * (r.E / r.n_group))

@@ -139,7 +139,7 @@ constexpr int PRE_GROUPS = 128;   // EC pre-pass: token groups below which K is 
 struct WsLayout {
     size_t hdr, epoch, zeros, splitp, pu, pz, vhi, vlo, vtag, active, preu, prez, gpart, total;
     size_t idx;         // semi-fused prefill: the active-token list [mpad], then its count
-    size_t few, total_epi;   // epilogue calls: partials of the decode's own pre-pass; all of it
+    size_t few;   // epilogue calls: partials of the decode's own pre-pass; all of it
     int64_t ncg, ksplit, spw, nprod, prod_k, rpad, mpad;
 };
 
@@ -506,7 +506,7 @@ hipError_t launch_decode_epi(const LinearArgs &a, int ec_mode, hipStream_t s);
 hipError_t launch_prepass(const LinearArgs &a, hipStream_t s);
 hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s);
 // Grouped: a.G's row tiles of bm rows (64 or 128), at most max_tiles of them.
-hipError_t launch_gemm_grouped(const LinearArgs &a, int bm, int64_t max_tiles, hipStream_t s);
+hipError_t launch_gemm_grouped(const LinearArgs &a, int64_t max_tiles, hipStream_t s);
 hipError_t launch_ec_apply(const LinearArgs &a, hipStream_t s);
 
 } // namespace spear

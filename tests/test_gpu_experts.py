@@ -167,3 +167,23 @@ def test_a_row_does_not_depend_on_its_neighbours():
     p = c.rng.permutation(150)
     z = sp.spear_w4_experts(c.x[torch.from_numpy(p).cuda()].contiguous(), c.experts, dev(c.ids[p]), dev(c.weights[p]))
     assert torch.equal(z, y[torch.from_numpy(p).cuda()])
+
+
+@pytest.mark.parametrize("M,E,topk", [(16, 9, 1), (17, 9, 1), (2, 64, 8), (3, 40, 6), (4, 1, 4), (33, 2, 1),
+                                      (31, 2, 1), (32, 2, 1)])
+def test_where_the_launches_change(M, E, topk):
+    """Slots on both sides of the two-launch form and of the 64-row tiles."""
+    c = Case(M, E, topk, 160, 96, 72, bias=True, residual=True, seed=M + E,
+             ids=None if E >= topk else np.zeros((M, topk)))
+    c.check(c.run(), f"M={M} E={E} topk={topk}")
+
+
+@pytest.mark.parametrize("K,I", [(2048, 2048), (2080, 2112)])
+def test_tiles_of_128_rows(K, I):
+    """Many slots an expert at depths long enough for the largest tiles; the last
+    tile of an expert ragged, one expert empty, some slots elsewhere."""
+    rng = np.random.default_rng(K)
+    E, M, N = 3, 2200, 136
+    ids = rng.choice([0, 2, 2, 2, -1], (M, 1))
+    c = Case(M, E, 1, K, I, N, bias=True, residual=True, seed=K, ids=ids)
+    c.check(c.run(), f"128 rows K={K} I={I}")

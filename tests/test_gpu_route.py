@@ -164,3 +164,9 @@ def test_many_ties_in_a_long_batch(E, G, kept, topk, copies, score):
     compare(xt, x64, wt, w64, None, topk, score, n_group=G, topk_group=kept)
     bias = (rng.integers(-1, 2, E) / 8.0).astype(np.float32)
     compare(xt, x64, wt, w64, bias, topk, score, n_group=G, topk_group=kept, renorm=False)
+
+
+@pytest.mark.parametrize("M", [255, 256, 257])
+def test_where_the_launches_change(M):
+    x, x64, w, w64, rng = draw(M, 48, 288, M)
+    compare(x, x64, w, w64, rng.normal(0, 0.1, 48).astype(np.float32), 6, sp.SCORE_SIGMOID, n_group=4, topk_group=2)
