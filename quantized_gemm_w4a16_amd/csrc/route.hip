@@ -5,13 +5,14 @@
 //   z_me = sum_k x[m][k] w[e][k], s = softmax(z) or sigmoid(z), c = s + bias;
 //   the topk largest c of the kept groups, weights from s.
 //
-// The choice is that of logits summed in fp64.  Two forms reach it:
-//  * fused (few tokens): one workgroup a token sums the logits in fp64 (each
-//    bf16 x bf16 product is exact there) and its first wave chooses;
-//  * two launches: the logits by bf16 MFMA in fp32, each with a bound of its
-//    error, then one wave a token chooses in fp32.  Where the bounds leave the
-//    order of two candidates open (a few tokens in a hundred), that wave sums
-//    the logits in question again in fp64, so the choice is the same as before.
+// The choice is that of logits summed in fp64.  Three forms reach it:
+//  * few tokens, two launches: the logits in fp64 by the whole chip (each bf16 x
+//    bf16 product is exact there), then one wave a token chooses;
+//  * some tokens and a small router, one launch: a workgroup a token does both;
+//  * many tokens, two launches: the logits by bf16 MFMA in fp32, each with a
+//    bound of its error, then 16 lanes a token choose in fp32.  Where the bounds
+//    leave the order of two candidates open (a few tokens in a hundred), the
+//    logits in question are summed again in fp64, so the choice is the same.
 #include <math.h>
 
 #include <type_traits>
@@ -334,7 +335,63 @@ __global__ __launch_bounds__(64 * RF_WAVES) void route_fused_kernel(const RouteA
     choose_all(a, m, lane, s_z, s_c);
 }
 
-// ---------------------------------------------------------------- two launches
+// ------------------------------------------------------- two launches, few tokens
+// A wave sums the logits of one token and two experts in fp64 (to the
+// workspace); in the second launch one wave a token chooses.  One token is bound
+// by the two round trips to memory and the launches (8.7 us in a graph), more of
+// them by fp64 conversions (64 tokens, 256 experts x 4096: 21.7 us).
+constexpr int RX_WAVES = 4;
+
+__global__ __launch_bounds__(64 * RX_WAVES) void route_exact_kernel(const RouteArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t m = blockIdx.y, K = a.K;
+    const int E = a.E, e0 = 2 * ((int)blockIdx.x * RX_WAVES + wave);
+    if (e0 >= E)
+        return;
+    const uint16_t *xr = a.x + m * K, *w0 = a.w + (int64_t)e0 * K, *w1 = e0 + 1 < E ? w0 + K : w0;
+    double s0 = 0.0, s1 = 0.0;
+#pragma unroll 1
+    for (int64_t k0 = 0; k0 < K; k0 += 4096) {
+        u32x4 xv[8], v0[8], v1[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            const int64_t k = k0 + 512 * q + 8 * lane;
+            const int64_t kk = k < K ? k : 8 * lane % K;  // (past K: zeros times the row's first ones)
+            xv[q] = k < K ? ld16(xr + k) : zero4();
+            v0[q] = ld16(w0 + kk);
+            v1[q] = ld16(w1 + kk);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            s0 = dot8(xv[q], v0[q], s0);
+            s1 = dot8(xv[q], v1[q], s1);
+        }
+    }
+    s0 = wave_sum(s0);
+    s1 = wave_sum(s1);
+    double *z = reinterpret_cast<double *>(a.z) + m * E + e0;
+    if (lane == 0) {
+        z[0] = s0;
+        if (e0 + 1 < E)
+            z[1] = s1;
+    }
+}
+
+__global__ __launch_bounds__(64) void route_pick_kernel(const RouteArgs a)
+{
+    __shared__ double s_z[SPEAR_MAX_EXPERTS], s_c[SPEAR_MAX_EXPERTS];
+    const int lane = threadIdx.x;
+    const int64_t m = blockIdx.x;
+    const double *z = reinterpret_cast<const double *>(a.z) + m * a.E;
+    for (int e = lane; e < a.E; e += 64)
+        s_z[e] = z[e];
+    wait_lgkmcnt0();
+    choose_all(a, m, lane, s_z, s_c);
+}
+
+// ------------------------------------------------------ two launches, many tokens
 // Logits by MFMA: a workgroup of 8 waves takes 64 WN experts and 128 tokens
 // over one of ks K slices, in stages of 64 depths that go from global memory
 // to a ring of LDS buffers by DMA (128 bytes a row, 16-byte chunks swizzled by
@@ -1255,14 +1312,21 @@ __global__ __launch_bounds__(64 * RC_WAVES<Q>, 2) void route_choose_kernel(const
     }
 }
 
-// One launch while every token has a CU of its own and the router's weights are
-// small enough for one CU to read.  us in graphs, one / two launches: 64 experts x
-// 2048 1 token 10.7 / 14.2, 256: 11.7 / 20.1, 384: 21.0 / 20.2; 128 x 2048 (512 KiB)
-// 1: 15.9 / 17.4, 256: 17.6 / 24.0; 128 x 4096 (1 MiB) 1: 24.4 / 20.4, 64: 25.6 / 24.7.
+// The three forms, us in graphs (two launches in fp64 / one launch / MFMA logits):
+//   64 experts x 2048 (256 KiB)   1 token 8.7 / 10.6 / 14.3, 64: 10.4 / 10.9 / 18.8, 128: 13.1 / 11.1 / 19.2,
+//                                 256: - / 11.7 / 20.1, 384: - / 21.0 / 20.2
+//   128 x 2048 (512 KiB)          1: 9.6 / 15.9 / 17.4, 64: 14.2 / 16.5 / 22.1, 128: 19.7 / 16.9 / 22.7
+//   128 x 4096 (1 MiB)            1: 9.6 / 24.3 / 19.3, 64: 14.4 / 25.6 / 23.9, 128: 20.0 / 26.2 / 25.6
+//   256 x 4096 (2 MiB)            1: 11.4 / 43.3 / 29.7, 64: 21.7 / 44.3 / 36.6, 128: 31.8 / 45.7 / 37.6
+//   512 x 4096 (4 MiB)            1: 15.2 / 80.1 / 42.2, 64: 36.4 / 81.8 / 52.4, 128: 54.6 / 83.3 / 54.6
+// So: fp64 by the whole chip for few tokens, one launch while every token has a CU
+// of its own and the router's weights are small enough for a CU to read, else MFMA.
+constexpr int64_t RX_TOKENS = 64, RX_MOST = 128;
 constexpr int64_t RF_TOKENS = 256;
 constexpr int64_t RF_BYTES = 512 << 10;
 
-bool fused(int64_t M, int32_t E, int64_t K) { return M <= RF_TOKENS && 2 * K * E <= RF_BYTES; }
+bool fused(int64_t M, int32_t E, int64_t K) { return M > RX_TOKENS && M <= RF_TOKENS && 2 * K * E <= RF_BYTES; }
+bool spread(int64_t M, int32_t E, int64_t K) { return M <= RX_TOKENS || (M <= RX_MOST && 2 * K * E > RF_BYTES); }
 
 // K slices: about 256 workgroups, at most 8 slices (their sums go through
 // memory; 777 tokens, 60 experts, logits + choice: 7.4 + 15.2 us with 16 slices,
@@ -1277,6 +1341,13 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s)
 {
     if (fused(a.M, a.E, a.K)) {
         hipLaunchKernelGGL(route_fused_kernel, dim3((unsigned)a.M), dim3(64 * RF_WAVES), 0, s, a);
+        return hipGetLastError();
+    }
+    if (spread(a.M, a.E, a.K)) {
+        const int per = 2 * RX_WAVES;
+        hipLaunchKernelGGL(route_exact_kernel, dim3((unsigned)((a.E + per - 1) / per), (unsigned)a.M),
+                           dim3(64 * RX_WAVES), 0, s, a);
+        hipLaunchKernelGGL(route_pick_kernel, dim3((unsigned)a.M), dim3(64), 0, s, a);
         return hipGetLastError();
     }
     const unsigned grid = (unsigned)((a.M + RL_TM - 1) / RL_TM * a.net * a.ks);

@@ -63,7 +63,7 @@ def test_route_parity(M, E, K, topk, score):
 @pytest.mark.parametrize("E,G,kept,best,topk", [(64, 8, 4, 2, 8), (64, 8, 1, 1, 8), (256, 8, 4, 2, 8),
                                                 (60, 4, 3, 2, 5), (64, 64, 6, 2, 6), (512, 64, 9, 1, 32),
                                                 (24, 3, 2, 2, 16), (7, 7, 7, 2, 7)])
-@pytest.mark.parametrize("M", [1, 5, 70])
+@pytest.mark.parametrize("M", [1, 5, 70, 290])
 def test_groups(E, G, kept, best, topk, M):
     for score in (sp.SCORE_SOFTMAX, sp.SCORE_SIGMOID):
         x, x64, w, w64, rng = draw(M, E, 256, E + G + M)
@@ -71,7 +71,7 @@ def test_groups(E, G, kept, best, topk, M):
         compare(x, x64, w, w64, bias, topk, score, n_group=G, topk_group=kept, group_best=best)
 
 
-@pytest.mark.parametrize("M", [1, 37, 200])
+@pytest.mark.parametrize("M", [1, 37, 200, 300])
 def test_near_ties_are_decided_in_fp64(M):
     """Experts whose logits differ in the 8th digit and beyond: the small
     components decide behind large ones that cancel nothing, and copies of an
@@ -101,7 +101,7 @@ def test_exact_ties_go_to_the_lowest_index():
     assert np.array_equal(ids, np.tile(np.arange(6), (5, 1)))
 
 
-@pytest.mark.parametrize("M", [4, 150])
+@pytest.mark.parametrize("M", [4, 150, 310])
 def test_left_out_experts_empty_slots_and_nan(M):
     """A bias of -inf takes experts out; slots left over are -1 with weight 0;
     a token with NaN in it has no experts; scores of zero sum to zero weights."""
@@ -126,7 +126,7 @@ def test_left_out_experts_empty_slots_and_nan(M):
     assert np.all(got_w == 0) and np.array_equal(got_i, np.tile(np.arange(4), (M, 1)))
 
 
-@pytest.mark.parametrize("M", [2, 64])
+@pytest.mark.parametrize("M", [2, 64, 260])
 def test_large_logits(M):
     """Softmax of logits far apart neither overflows nor loses its choice."""
     x, x64, w, w64, _ = draw(M, 48, 1024, 9, gain=1000.0)
@@ -153,7 +153,7 @@ def test_many_ties_in_a_long_batch(E, G, kept, topk, copies, score):
     ends inside four tokens.  Small integers over 16: every sum is exact whatever
     its order, so ties are ties, and go to the lowest index."""
     rng = np.random.default_rng(E + copies)
-    M, K = 203, 2112
+    M, K = 303, 2112
     x = rng.integers(-3, 4, (M, K)) * (rng.random((M, K)) < 0.02)
     x[rng.random(M) < 0.2] = 0
     w = rng.integers(-3, 4, (E, K)) / 16.0
@@ -166,7 +166,11 @@ def test_many_ties_in_a_long_batch(E, G, kept, topk, copies, score):
     compare(xt, x64, wt, w64, bias, topk, score, n_group=G, topk_group=kept, renorm=False)
 
 
-@pytest.mark.parametrize("M", [255, 256, 257])
-def test_where_the_launches_change(M):
-    x, x64, w, w64, rng = draw(M, 48, 288, M)
-    compare(x, x64, w, w64, rng.normal(0, 0.1, 48).astype(np.float32), 6, sp.SCORE_SIGMOID, n_group=4, topk_group=2)
+@pytest.mark.parametrize("M,E,K", [(64, 48, 288), (65, 48, 288), (256, 48, 288), (257, 48, 288), (64, 300, 992),
+                                   (65, 300, 992), (128, 300, 992), (129, 300, 992), (3, 511, 4128), (1, 12, 8224)])
+def test_where_the_launches_change(M, E, K):
+    x, x64, w, w64, rng = draw(M, E, K, M + E)
+    bias = rng.normal(0, 0.1, E).astype(np.float32)
+    G = 4 if E % 4 == 0 else 7
+    compare(x, x64, w, w64, bias, 6, sp.SCORE_SIGMOID, n_group=G, topk_group=2)
+    compare(x, x64, w, w64, None, 6, sp.SCORE_SOFTMAX)
