@@ -209,3 +209,30 @@ def test_expired_wait_gives_nan_through_the_activation():
     assert np.all((np.abs(got - ref) <= tol) | bad)
     y = sp.spear_w4_linear_epilogue(c.x, c.w, ep, c.ec, workspace=ws, path=sp.PATH_DECODE)
     check(y, ref, tol, "after an expired wait")
+
+
+@pytest.mark.parametrize("M", [1, 7, 16, 90])
+@pytest.mark.parametrize("r,h", [(32, 12), (72, 0), (256, 0)])
+def test_compensators_that_keep_the_layers_own_launch(M, r, h):
+    """A gate vector, ranks above 64: the plain entry point's bits where the path
+    is chosen, and its gates."""
+    c = Case(M, 140, 1056, r, 0, M + r + h, False, False, False, sp.OUT_F32)
+    if h:
+        rng = np.random.default_rng(r)
+        for name, shape in (("gate_w1", (h, r)), ("gate_c1", (h,)), ("gate_w2", (r, h)), ("gate_c2", (r,))):
+            setattr(c.ec, name, dev(rng.normal(0, 0.4, shape).astype(np.float32)))
+        c.ec.alpha = 0.7
+    a = sp.spear_w4_linear(c.x, c.w, c.ec)
+    assert torch.equal(a, sp.spear_w4_linear_epilogue(c.x, c.w, sp.Epilogue(), c.ec))
+
+
+def test_outputs_past_32_bit_offsets():
+    """An output of more than 2^32 bytes: its last rows against the reference."""
+    M, N, K = 40000, 32768, 64
+    c = Case(8, N, K, 0, 0, 5, False, True, False, sp.OUT_F32)
+    ref, tol = c.reference(ref64.SILU)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-8:] = c.x
+    y = sp.spear_w4_linear_epilogue(x, c.w, c.epilogue(sp.ACT_SILU), None)
+    assert y.numel() * 4 > 1 << 32
+    check(y[-8:], ref, tol, "last rows")

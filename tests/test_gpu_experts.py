@@ -187,3 +187,24 @@ def test_tiles_of_128_rows(K, I):
     ids = rng.choice([0, 2, 2, 2, -1], (M, 1))
     c = Case(M, E, 1, K, I, N, bias=True, residual=True, seed=K, ids=ids)
     c.check(c.run(), f"128 rows K={K} I={I}")
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_weights_past_32_bit_offsets(M):
+    """More than 2^32 bytes of weights: the last expert's rows are those of an
+    experts' handle that has it alone."""
+    E, K, I, N = 512, 8192, 1056, 64
+    packed = torch.randint(0, 256, (E, 2 * I, K // 2), dtype=torch.uint8, device="cuda")
+    assert packed.numel() > 1 << 32
+    us = torch.full((E, 2 * I), 0.002, device="cuda")
+    down = torch.randint(0, 256, (E, N, I // 2), dtype=torch.uint8, device="cuda")
+    ds = torch.full((E, N), 0.01, device="cuda")
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    weights = torch.rand(M, 1, device="cuda")
+    ids = torch.full((M, 1), E - 1, dtype=torch.int32, device="cuda")
+    y = sp.spear_w4_experts(x, sp.Experts(packed, us, None, down, ds, None), ids, weights)
+    # (8 copies, of which the fourth is asked for)
+    alone = sp.Experts(packed[-1:].expand(8, -1, -1).contiguous(), us[:8], None,
+                       down[-1:].expand(8, -1, -1).contiguous(), ds[:8], None)
+    z = sp.spear_w4_experts(x, alone, torch.full_like(ids, 3), weights)
+    assert torch.equal(y, z) and bool(torch.isfinite(y.float()).all())

@@ -174,3 +174,18 @@ def test_where_the_launches_change(M, E, K):
     G = 4 if E % 4 == 0 else 7
     compare(x, x64, w, w64, bias, 6, sp.SCORE_SIGMOID, n_group=G, topk_group=2)
     compare(x, x64, w, w64, None, 6, sp.SCORE_SOFTMAX)
+
+
+def test_rows_past_32_bit_offsets():
+    """A batch of more than 2^32 bytes: its last tokens against the reference."""
+    M, E, K = 1100003, 16, 2048
+    _, _, w, w64, _ = draw(1, E, K, 3)
+    tail, t64 = bf16(np.random.default_rng(4).normal(0, 1, (40, K)))
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-40:] = tail
+    assert x.numel() * 2 > 1 << 32
+    weights, ids = sp.spear_route(x, sp.Router(w, topk=3))
+    ref_w, ref_i = ref64.route(t64, w64, 3, False)
+    assert np.array_equal(host(ids[-40:]), ref_i)
+    assert np.all(np.abs(host(weights[-40:]) - ref_w) <= rtol(t64, w64) * ref_w)
+    assert bool((ids[:-40] == torch.arange(3, dtype=torch.int32, device="cuda")).all())
