@@ -72,6 +72,8 @@ ExpertsLayout experts_layout(int64_t M, int32_t topk, int32_t E, int64_t I, int6
 // One workgroup an expert.  Every workgroup counts all slots (LDS counters; a
 // count does not depend on the order of its additions), so it knows where its
 // own rows and tiles begin, then writes its slots in ascending order by ballot.
+// Bound by the round trips of its two passes over the ids: 4 to 5 us up to 1200
+// slots, 11.6 us for 8192 of 8 experts.
 __global__ __launch_bounds__(1024) void plan_kernel(const int32_t *__restrict__ ids, int32_t slots, int32_t E,
                                                     int32_t bm, uint32_t *__restrict__ zeros,
                                                     int32_t *__restrict__ ntiles, Tile *__restrict__ tiles,
@@ -567,7 +569,10 @@ __global__ __launch_bounds__(64 * FW_WAVES) void few_down_kernel(const FewArgs a
 }
 
 // ---------------------------------------------------------------------- join
-// A thread takes four channels of one token.
+// A thread takes four channels of one token.  4096 tokens x 4096 channels, two
+// slots each, residual: 40 us for 201 MB, 5.0 TB/s, what a copy reaches.  Few tokens
+// are bound by round trips, so JB slots' rows are in flight at once (16 tokens x 8
+// slots: 4 us).
 constexpr int JB = 8;
 
 __global__ __launch_bounds__(256) void join_kernel(const JoinArgs a)

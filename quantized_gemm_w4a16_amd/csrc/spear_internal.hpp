@@ -132,14 +132,16 @@ constexpr int PROD_WORDS = 4096;  // above 8 tokens: partial words an epilogue l
 constexpr int PROD_CHUNK = 4;     // producer partials a consumer wave loads per batch
 constexpr int PRE_SLOTS = 512;    // EC pre-pass: (token group, K slice) partial slots, at most
                                   // (fewer than PRE_GROUPS groups, about 256 workgroups)
-constexpr int FEW_SLICES = 8;     // decode's own EC pre-pass: K slices, at most
+// Decode's own EC pre-pass: K slices, at most (2048 -> 16384 pair at one token and
+// 8192 -> 2048 at 16, us: 4 slices 13.0 and 17.4, 8: 13.4 and 15.0, 16: 16.0 and 15.6).
+constexpr int FEW_SLICES = 8;
 constexpr int FEW_RANK = 64;      // ... and padded rank, at most
 constexpr int PRE_GROUPS = 128;   // EC pre-pass: token groups below which K is split
 
 struct WsLayout {
     size_t hdr, epoch, zeros, splitp, pu, pz, vhi, vlo, vtag, active, preu, prez, gpart, total;
     size_t idx;         // semi-fused prefill: the active-token list [mpad], then its count
-    size_t few;   // epilogue calls: partials of the decode's own pre-pass; all of it
+    size_t few;   // epilogue calls: partials of the decode's own pre-pass
     int64_t ncg, ksplit, spw, nprod, prod_k, rpad, mpad;
 };
 
@@ -505,7 +507,7 @@ hipError_t launch_decode(const LinearArgs &a, int ec_mode, hipStream_t s);
 hipError_t launch_decode_epi(const LinearArgs &a, int ec_mode, hipStream_t s);
 hipError_t launch_prepass(const LinearArgs &a, hipStream_t s);
 hipError_t launch_gemm(const LinearArgs &a, int ec_on, int force_large, hipStream_t s);
-// Grouped: a.G's row tiles of bm rows (64 or 128), at most max_tiles of them.
+// Grouped: a.G's row tiles of 128 rows, at most max_tiles of them.
 hipError_t launch_gemm_grouped(const LinearArgs &a, int64_t max_tiles, hipStream_t s);
 hipError_t launch_ec_apply(const LinearArgs &a, hipStream_t s);
 
