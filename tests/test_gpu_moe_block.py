@@ -70,7 +70,7 @@ def tokens(M, seed):
     return bf16(np.random.default_rng(seed).normal(0, 1, (M, D)))
 
 
-@pytest.mark.parametrize("M", [1, 4, 16, 47, 200])
+@pytest.mark.parametrize("M", [1, 4, 16, 47, 200, 420])
 def test_block_parity(M):
     b = Block(M)
     x, x64 = tokens(M, M)
@@ -80,7 +80,7 @@ def test_block_parity(M):
     assert worst <= 1.0
 
 
-@pytest.mark.parametrize("M", [1, 8, 90])
+@pytest.mark.parametrize("M", [1, 8, 90, 420])
 def test_block_in_a_graph(M):
     """Captured once, replayed on new tokens with eager work of its own buffers
     in between, each replay the eager result bit for bit."""
