@@ -359,14 +359,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
         constexpr int WAIT = NS + (RING - 2) * (NI + NS);
         static_assert(WAIT < 64, "vmcnt");
         wait_vmcnt<0>();
-        bare_barrier();
+        read_barrier();
         int64_t c = 0;
         for (; c + 2 * RING <= C; c += RING) {
 #pragma unroll
             for (int j = 0; j < RING; j++) {
                 use(FR, ring[j], w[j]);
                 wait_vmcnt<WAIT>();                       // this wave's rows of the next chunk
-                bare_barrier();                           // every wave's; chunk c + j free
+                read_barrier();                           // every wave's; chunk c + j free
                 issue_x(c + j + RING, ring[j]);
                 __builtin_amdgcn_sched_barrier(0);        // keeps the order the wait counts on
                 load_w(c + j + RING, w[j]);
@@ -374,20 +374,20 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
         }
         // the last RING .. 2 RING - 1 chunks (fewer where K is short)
         wait_vmcnt<0>();
-        bare_barrier();
+        read_barrier();
 #pragma unroll
         for (int j = 0; j < RING; j++)
             if (c + j < C) {
                 use(FR, ring[j], w[j]);
                 if (j < RING - 1 && c + j + RING < C) {
-                    bare_barrier();
+                    read_barrier();
                     issue_x(c + j + RING, ring[j]);
                     load_w(c + j + RING, w[j]);
                 }
             }
         if (c + RING < C) {
             wait_vmcnt<0>();
-            bare_barrier();
+            read_barrier();
 #pragma unroll
             for (int j = 0; j < RING - 1; j++)
                 if (c + RING + j < C)

@@ -257,6 +257,15 @@ __device__ __forceinline__ void wait_vmcnt()
 }
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 __device__ __forceinline__ void bare_barrier() { __builtin_amdgcn_s_barrier(); }
+// A barrier behind which an LDS buffer that the waves have read is written again:
+// this wave's reads have returned before it (bare_barrier alone waits for none,
+// and a read still in flight could return what another wave writes).  No memory
+// operation moves past the wait.
+__device__ __forceinline__ void read_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    bare_barrier();
+}
 
 // Load the arguments a kernel uses at entry, in one batch.  The compiler
 // otherwise fetches fields of a large argument struct lazily, in several
