@@ -511,7 +511,7 @@ __global__ __launch_bounds__(512) void prepass2_kernel(const LinearArgs a)
         for (int j = 0; j < RING; j++) {
             const int64_t ci = c0 + j;
             wait_vmcnt<WAIT>();                           // this wave's DMAs of chunk ci and its w_g
-            bare_barrier();                               // every wave's part; chunk ci - 1 free
+            read_barrier();                               // every wave's part; chunk ci - 1 free
             issue_wg(ci + RING - 2, wgr[(j + RING - 2) % RING]);
             issue(ci + RING - 1, ring[(j + RING - 1) % RING]);
             if (ci < nch) {
@@ -941,7 +941,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
             for (int p = 0; p < 3; p++) {
                 const int64_t s = s0 + 2 * p;
                 wait_vmcnt<G2_WAIT2>();                       // this wave's part of stages s, s + 1
-                bare_barrier();                               // every wave's part; pair p - 1 free
+                read_barrier();                               // every wave's part; pair p - 1 free
                 const int64_t sn0 = (s + 4 < slast) ? s + 4 : slast, sn1 = (s + 5 < slast) ? s + 5 : slast;
                 uint8_t *const nx0 = s_xb[(2 * p + 4) % 6], *const nw0 = s_wb[(2 * p + 4) % 6];
                 uint8_t *const nx1 = s_xb[(2 * p + 5) % 6], *const nw1 = s_wb[(2 * p + 5) % 6];
@@ -984,7 +984,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
             for (int j = 0; j < G2_ST; j++) {
                 const int64_t s = s0 + j;
                 wait_vmcnt<G2_WAIT>();                        // this wave's part of stage s
-                bare_barrier();                               // every wave's part; stage s - 1 free
+                read_barrier();                               // every wave's part; stage s - 1 free
                 const int64_t sn = (s + G2_ST - 1 < slast) ? s + G2_ST - 1 : slast;
                 uint8_t *const nxb = s_xb[(j + G2_ST - 1) % G2_ST];
                 uint8_t *const nwb = s_wb[(j + G2_ST - 1) % G2_ST];

@@ -507,7 +507,7 @@ __global__ __launch_bounds__(512) void route_logits_kernel(const RouteArgs a)
         for (int j = 0; j < RING; j++) {
             const int64_t st = s0 + j;
             wait_vmcnt<WAIT>();                           // this wave's part of stage st
-            bare_barrier();                               // every wave's part; stage st - 1 free
+            read_barrier();                               // every wave's part; stage st - 1 free
             issue(st + RING - 1, ring[(j + RING - 1) % RING]);
             if (st < se) {
                 const uint8_t *buf = ring[j];

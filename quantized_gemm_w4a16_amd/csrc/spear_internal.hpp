@@ -256,15 +256,13 @@ __device__ __forceinline__ void wait_vmcnt()
     __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | 0x70 | 0xF00);
 }
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
-__device__ __forceinline__ void bare_barrier() { __builtin_amdgcn_s_barrier(); }
-// A barrier behind which an LDS buffer that the waves have read is written again:
-// this wave's reads have returned before it (bare_barrier alone waits for none,
-// and a read still in flight could return what another wave writes).  No memory
-// operation moves past the wait.
+// The barrier waits for this wave's LDS reads: a buffer that the waves have read
+// is written again behind it, and a read still in flight could return what
+// another wave writes.  No memory operation moves past that wait.
 __device__ __forceinline__ void read_barrier()
 {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    bare_barrier();
+    __builtin_amdgcn_s_barrier();
 }
 
 // Load the arguments a kernel uses at entry, in one batch.  The compiler

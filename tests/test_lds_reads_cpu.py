@@ -80,7 +80,7 @@ def test_the_walk_itself():
     assert pending_at_barriers(*found)
 
 
-@pytest.mark.parametrize("source", ["experts.hip", "route.hip"])
+@pytest.mark.parametrize("source", ["experts.hip", "route.hip", "prefill.hip"])
 def test_no_lds_read_in_flight_at_a_barrier(source, tmp_path):
     hipcc = build._hipcc()
     if shutil.which(hipcc) is None:
