@@ -212,10 +212,15 @@ __device__ __align__(256) static uint8_t g_zeros[256];
 // step s as one load, and reads the same depths of its token row as four.  The
 // rows' sums, which remove the unpacking's offset, are shared out over the
 // waves by depth and meet in LDS.  16-row tiles are bound by the weights' way in
-// (16 tokens, 8 of 64 experts, 2048 -> 2 x 1024: 33 us for 119 MB, 3.6 TB/s), 64-row
-// tiles by the LDS reads of the rows, every wave all of them (300 tokens, 4 of 32,
-// 2048 -> 2 x 1408: 48 us for 94 MB).  Rows past the tile's end repeat the last one
-// and are not stored: an output depends on its own row alone.
+// (16 tokens, 8 of 64 experts, 2048 -> 2 x 1024: 33 us for 119 MB, 3.6 TB/s).  In
+// 64-row tiles the weights' loads become FLAT ones (their row variants share the
+// pointers by reference), which count as LDS reads too, so each chunk waits for
+// all that is in flight; that round trip and the LDS reads, every wave all the
+// rows and one at a time, bound them (300 tokens, 4 of 32, 2048 -> 2 x 1408: 48 us
+// for 94 MB).  With global loads in their place the waits hold as counted, but it
+// measured slower: 61 us, and 58 with the LDS reads four at a time (84 registers
+// instead of 64).  Rows past the tile's end repeat the last one and are
+// not stored: an output depends on its own row alone.
 // PLAN 1 (few slots): no plan was launched.  The block's tile is an expert, or
 // with fewer slots than experts a slot whose expert no earlier slot has; each
 // wave finds that expert's slots in ids by a ballot.
