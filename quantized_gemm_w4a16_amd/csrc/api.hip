@@ -123,6 +123,7 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t r)
     // smaller M, and the decode path after the prefill path.
     int64_t pk1 = 0;
     const int64_t nprod_max = r > 0 ? ec_producers(1, K, L.rpad, L.ncg, &pk1) : 0;
+    L.nslot = nprod_max;
 
     size_t off = 0;
     L.hdr = off;
@@ -169,9 +170,6 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t r)
     }
     L.gpart = off;
     off = align256(off + gemm_part_bytes(M, N, K));
-    L.few = off;
-    if (r > 0 && L.rpad <= FEW_RANK)
-        off = align256(off + (size_t)FEW_SLICES * 16 * (L.rpad * sizeof(float) + sizeof(double)));
     L.total = off;
     return L;
 }
@@ -579,11 +577,12 @@ static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w
         a.E.glu = ep->glu;
         a.E.on = 1;
         if (few_ec) {
-            // about 1024 depths a slice
-            const int64_t p = cdiv(K, 1024);
-            a.E.few = (int32_t)(p < FEW_SLICES ? p : FEW_SLICES);
-            a.E.fu = reinterpret_cast<const float *>(a.ws + L.few);
-            a.E.fz = reinterpret_cast<const double *>(a.ws + L.few + (size_t)FEW_SLICES * 16 * L.rpad * sizeof(float));
+            // about 1024 depths a slice, in the place of the fused form's words
+            int64_t p = cdiv(K, 1024);
+            p = p < FEW_SLICES ? p : FEW_SLICES;
+            a.E.few = (int32_t)(p < L.nslot ? p : L.nslot);
+            a.E.fu = reinterpret_cast<uint32_t *>(a.ws + L.pu);
+            a.E.fz = reinterpret_cast<uint32_t *>(a.ws + L.pz);
             return hip_status(launch_decode_epi(a, 3, s));
         }
     }

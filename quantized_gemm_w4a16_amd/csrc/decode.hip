@@ -554,7 +554,7 @@ __device__ f32x4 ec_consume(const LinearArgs &a, const u32x4 *bpre, int64_t cg, 
 #if SPEAR_EPILOGUE
 // EC pre-pass of up to 16 tokens in a launch of its own: workgroup p takes one
 // of a.E.few K slices, its 8 waves eighths of it, and stores the slice's part
-// of A x (MFMA, fp32) and of the gate logit (fp64) as plain words.  The decode
+// of A x (MFMA, fp32) and of the gate logit (fp64) as words without a tag.  The decode
 // kernel behind it adds the slices as it starts its epilogue: nothing is
 // exchanged inside a launch, so no workgroup waits for another and the decode
 // kernel needs no registers for polling.  Bound by its round trip to memory and
@@ -608,14 +608,17 @@ __global__ __launch_bounds__(64 * FP_WAVES) void few_prepass_kernel(const Linear
         f32x4 u = {0.f, 0.f, 0.f, 0.f};
         for (int w = 0; w < FP_WAVES; w++)
             u += s_u[w][wave][lane];
-        *reinterpret_cast<f32x4 *>(const_cast<float *>(a.E.fu) + (p * 16 + lr) * a.rpad + 16 * wave + 4 * lg) = u;
+        u32x4 *const d = reinterpret_cast<u32x4 *>(a.E.fu + 2 * ((p * 16 + lr) * a.rpad + 16 * wave + 4 * lg));
+        d[0] = u32x4{__float_as_uint(u[0]), 0u, __float_as_uint(u[1]), 0u};
+        d[1] = u32x4{__float_as_uint(u[2]), 0u, __float_as_uint(u[3]), 0u};
     }
     if (wave == FP_WAVES - 1 && lane < M) {
         double z = 0.0;
         for (int w = 0; w < FP_WAVES; w++)
             for (int q = 0; q < 4; q++)
                 z += s_z[w][lane + 16 * q];
-        const_cast<double *>(a.E.fz)[p * 16 + lane] = z;
+        const uint64_t zb = __builtin_bit_cast(uint64_t, z);
+        *reinterpret_cast<u32x4 *>(a.E.fz + 4 * (p * 16 + lane)) = u32x4{(uint32_t)zb, 0u, (uint32_t)(zb >> 32), 0u};
     }
 }
 
@@ -626,7 +629,8 @@ template <int NT, int GV>
 struct FewEc {
     static constexpr int EL = GV ? 1 : 16 * FEW_RANK / NT;
     float v[FEW_SLICES][EL], u[EL];
-    double zv[FEW_SLICES], z;
+    uint32_t zl[FEW_SLICES], zh[FEW_SLICES];
+    double z;
 
     __device__ __forceinline__ void load(const LinearArgs &a, int tid)
     {
@@ -637,9 +641,11 @@ struct FewEc {
 #pragma unroll
             for (int i = 0; i < EL; i++) {
                 const int e = tid + i * NT;
-                v[p][i] = a.E.fu[(int64_t)pp * 16 * a.rpad + (e < n ? e : n - 1)];
+                v[p][i] = __uint_as_float(a.E.fu[2 * ((int64_t)pp * 16 * a.rpad + (e < n ? e : n - 1))]);
             }
-            zv[p] = a.E.fz[pp * 16 + (tid < a.M ? tid : 0)];
+            const uint32_t *zw = a.E.fz + 4 * (pp * 16 + (tid < a.M ? tid : 0));
+            zl[p] = zw[0];
+            zh[p] = zw[2];
         }
     }
     __device__ __forceinline__ void add(const LinearArgs &a)
@@ -652,7 +658,7 @@ struct FewEc {
 #pragma unroll
         for (int p = 0; p < FEW_SLICES; p++)
             if (p < P) {
-                z += zv[p];
+                z += __builtin_bit_cast(double, (uint64_t)zl[p] | ((uint64_t)zh[p] << 32));
 #pragma unroll
                 for (int i = 0; i < EL; i++)
                     u[i] += v[p][i];

@@ -141,7 +141,7 @@ constexpr int PRE_GROUPS = 128;   // EC pre-pass: token groups below which K is 
 struct WsLayout {
     size_t hdr, epoch, zeros, splitp, pu, pz, vhi, vlo, vtag, active, preu, prez, gpart, total;
     size_t idx;         // semi-fused prefill: the active-token list [mpad], then its count
-    size_t few;   // epilogue calls: partials of the decode's own pre-pass
+    int64_t nslot;      // producers that pu and pz have room for
     int64_t ncg, ksplit, spw, nprod, prod_k, rpad, mpad;
 };
 
@@ -163,8 +163,11 @@ struct EpiArgs {
     int32_t glu;            // 1: channels 2i and 2i + 1 make output channel i
     int32_t on;             // host side: the call has an epilogue
     int32_t few;            // decode with the EC's pre-pass before it: K slices of the partials
-    const float *fu;        // [few][16][rpad] partials of A x
-    const double *fz;       // [few][16] partials of the gate logit
+    // Partials of A x [few][16][rpad] and of the gate logit [few][16][2 halves],
+    // 64-bit words as in the fused exchange, whose place they take.  Their upper
+    // half is zero, the tag of no launch: whatever layout another call's token
+    // count gives the workspace, none takes them for its own.
+    uint32_t *fu, *fz;
 };
 
 // A row tile of a grouped product: rows list[pos .. pos + cnt) through expert e.
