@@ -359,11 +359,16 @@ __global__ __launch_bounds__(64 * RX_WAVES) void route_exact_kernel(const RouteA
 #pragma unroll
         for (int q = 0; q < 8; q++) {
             const int64_t k = k0 + 512 * q + 8 * lane;
-            const int64_t kk = k < K ? k : 8 * lane % K;  // (past K: zeros times the row's first ones)
-            xv[q] = k < K ? ld16(xr + k) : zero4();
+            const int64_t kk = k < K ? k : 8 * lane % K;  // (past K: the rows' first ones, made zeros)
+            xv[q] = ld16(xr + kk);
             v0[q] = ld16(w0 + kk);
             v1[q] = ld16(w1 + kk);
         }
+        // both operands: zero times an infinite weight is no zero
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            if (k0 + 512 * q + 8 * lane >= K)
+                xv[q] = v0[q] = v1[q] = zero4();
 #pragma unroll
         for (int q = 0; q < 8; q++) {
             s0 = dot8(xv[q], v0[q], s0);
