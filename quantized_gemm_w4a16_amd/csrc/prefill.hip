@@ -756,8 +756,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     // 4 (G2_WI w + j) .. +3, lane i word i % 4 of slot i / 4.  Rows past N repeat
     // the last row.  Each lane's stage-0 source and the number of stages its chunk
     // stays inside K are computed once.  Activation chunks past K come from the
-    // zero block; weight chunks past K re-read the lane's last chunk inside K
-    // (finite values that meet zero activations).
+    // zero block; weight chunks past K re-read one inside it (w_offset).
     const uint8_t *xsrc[G2_XI], *wsrc[G2_WI];
     int64_t xlim[G2_XI], wlast[G2_WI];
 #pragma unroll
@@ -776,8 +775,8 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
         const int r = (G2_WS == 16 ? 16 : 4) * (G2_WI * wave + j) + (slot >> 2);
         const int c = (slot & 3) ^ ((r >> 1) & 3);
         const int64_t nn = n0 + r < N ? n0 + r : N - 1;
-        wsrc[j] = wpk + nn * (K / 2) + 16 * c + (G2_WS == 16 ? 0 : 4 * (lane & 3));
-        wlast[j] = (K - 32 * c + 127) / 128 - 1;          // last stage with 128 st + 32 c < K
+        wsrc[j] = wpk + nn * (K / 2) + w_offset(K, c, 0) + (G2_WS == 16 ? 0 : 4 * (lane & 3));
+        wlast[j] = w_last_stage(K, c);
     }
     auto issue_x = [&](int64_t st, uint8_t *xbase, int j) {
         const void *src = (G2_KF || st < xlim[j]) ? (const void *)(xsrc[j] + 256 * st) : (const void *)zsrc;
@@ -787,7 +786,7 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     };
     auto issue_w = [&](int64_t st, uint8_t *wbase, int j) {
         const int64_t sw = (G2_KF || st < wlast[j]) ? st : wlast[j];
-        const auto *src = (const __attribute__((address_space(1))) void *)(wsrc[j] + 64 * sw);
+        const auto *src = (const __attribute__((address_space(1))) void *)(wsrc[j] + 64 * sw);   // w_offset(K, c, st)
         auto *dst = (__attribute__((address_space(3))) void *)(wbase + 64 * G2_WS * (G2_WI * wave + j));
         if constexpr (G2_BN == 64)
             __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);

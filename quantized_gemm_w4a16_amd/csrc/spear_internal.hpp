@@ -249,6 +249,21 @@ __host__ __device__ __forceinline__ int row_turn(int r)
     return (r & 3) | ((q == 0 ? 0 : q == 3 ? 1 : q + 1) << 2);
 }
 
+// Byte offset in a row of packed weights (K / 2 bytes) of what the GEMM stages
+// for its 32-deep piece c (0..3) of the 128-deep stage st.  Past K the piece's
+// last one inside K, or the row's first where none is (K < 128): finite values
+// that meet zero activations, and always inside the row.
+__host__ __device__ __forceinline__ int64_t w_piece(int64_t K, int c) { return 32 * c < K ? c : 0; }
+__host__ __device__ __forceinline__ int64_t w_last_stage(int64_t K, int c)
+{
+    return (K - 32 * w_piece(K, c) + 127) / 128 - 1;
+}
+__host__ __device__ __forceinline__ int64_t w_offset(int64_t K, int c, int64_t st)
+{
+    const int64_t last = w_last_stage(K, c);
+    return 16 * w_piece(K, c) + 64 * (st < last ? st : last);
+}
+
 // Explicit counter waits (gfx9 s_waitcnt encoding: vmcnt bits 3:0 and 15:14,
 // expcnt 6:4, lgkmcnt 11:8) and a barrier without the fence of
 // __syncthreads, for code that orders its memory operations itself.
