@@ -351,9 +351,9 @@ typedef struct spear_experts {
     const float *down_scales;  /* [E][N]                                  */
     const uint8_t *down_zeros; /* [E][N], or NULL for zero point 8        */
     const float *down_bias;    /* [E][N], or NULL                         */
-    int64_t K;                 /* input channels, >= 32, a multiple of 32 */
-    int64_t I;                 /* inner channels, >= 32, a multiple of 32 */
-    int64_t N;                 /* output channels, >= 1                   */
+    int64_t K;                 /* input channels, 32 .. 2^31, a multiple of 32 */
+    int64_t I;                 /* inner channels, 32 .. 2^25, a multiple of 32 */
+    int64_t N;                 /* output channels, 1 .. 2^25              */
     int32_t E;                 /* 1 .. SPEAR_MAX_EXPERTS                  */
     int32_t act;               /* SPEAR_ACT_* between the two layers      */
     int32_t glu;               /* 1: the gated pair; 0: act alone         */
@@ -371,8 +371,9 @@ typedef struct spear_experts {
  *   residual [M][N] bf16 or NULL (may be y itself), y [M][N] bf16; x, residual
  *   and y 16-byte aligned.  y may not overlap any other input.
  *   M >= 0 (0 does nothing), 1 <= topk <= SPEAR_MAX_TOPK, M topk <= 2^30.
- *   workspace device scratch of spear_w4_experts_workspace_size bytes, 256-byte
- *             aligned; needs no zeroing and holds nothing between calls.
+ *   workspace device scratch of spear_w4_experts_workspace_size bytes (0 for
+ *             sizes out of range), 256-byte aligned; needs no zeroing and holds
+ *             nothing between calls.
  */
 size_t spear_w4_experts_workspace_size(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N);
 spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_experts *w,

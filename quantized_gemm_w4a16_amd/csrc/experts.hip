@@ -23,6 +23,7 @@ namespace {
 
 constexpr int XT = 16;                                    // rows of the smallest tile
 constexpr int64_t MAX_SLOTS = 1 << 30;
+constexpr int64_t MAX_CHANNELS = 1 << 25;                 // I and N: a row tile's blocks fit one launch
 
 struct ExpertsLayout {
     size_t hdr, zeros, tiles, list, h, d, total;
@@ -170,6 +171,7 @@ struct GroupArgs {
     int32_t ncb;              // channel blocks: the grid's fastest index
     const int32_t *ids;       // few slots: the blocks' own plan
     int32_t slots, E;
+    int32_t tile0;            // the launch's first row tile
 };
 
 struct JoinArgs {
@@ -189,7 +191,7 @@ __device__ __forceinline__ void pin_group_args(const GroupArgs &a)
     pin_arg(a.x); pin_arg(a.packed); pin_arg(a.scales); pin_arg(a.zeros); pin_arg(a.bias);
     pin_arg(a.out); pin_arg(a.ntiles); pin_arg(a.tiles); pin_arg(a.list); pin_arg(a.N); pin_arg(a.K);
     pin_arg(a.div); pin_arg(a.act); pin_arg(a.glu); pin_arg(a.ncb); pin_arg(a.ids); pin_arg(a.slots);
-    pin_arg(a.E);
+    pin_arg(a.E); pin_arg(a.tile0);
 }
 
 // Up to this many slots, two launches: the products make their own plan, the
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1))) vo
     __shared__ float s_rs[NW][BM];
     uint8_t *const ring[4] = {s_x0, s_x1, s_x2, s_x3};
     pin_group_args(a);
-    const int tile = (int)(blockIdx.x / (uint32_t)a.ncb), cb = (int)(blockIdx.x % (uint32_t)a.ncb);
+    const int tile = a.tile0 + (int)(blockIdx.x / (uint32_t)a.ncb), cb = (int)(blockIdx.x % (uint32_t)a.ncb);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
@@ -448,9 +450,17 @@ template <int BM, int NW, int UP, int PLAN, int RING, int SC>
 hipError_t launch_stream_t(GroupArgs a, int64_t tiles, hipStream_t s)
 {
     a.ncb = (int32_t)((a.N + 16 * NW - 1) / (16 * NW));
-    hipLaunchKernelGGL((stream_kernel<BM, NW, UP, PLAN, RING, SC>), dim3((unsigned)(tiles * a.ncb)), dim3(64 * NW), 0,
-                       s, a);
-    return hipGetLastError();
+    const int64_t most = MAX_BLOCKS > a.ncb ? MAX_BLOCKS / a.ncb : 1;    // tiles a launch
+    for (int64_t t = 0; t < tiles; t += most) {
+        a.tile0 = (int32_t)t;
+        const int64_t n = tiles - t < most ? tiles - t : most;
+        hipLaunchKernelGGL((stream_kernel<BM, NW, UP, PLAN, RING, SC>), dim3((unsigned)(n * a.ncb)), dim3(64 * NW), 0,
+                           s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 // 64 rows: 8 waves of 16 channels and 256 depths a chunk (300 tokens, 32 experts,
@@ -628,8 +638,8 @@ extern "C" {
 
 size_t spear_w4_experts_workspace_size(int64_t M, int32_t topk, int32_t E, int64_t I, int64_t N)
 {
-    if (M < 0 || topk < 1 || topk > SPEAR_MAX_TOPK || E < 1 || E > SPEAR_MAX_EXPERTS || I < 32 || N < 1 ||
-        M > MAX_SLOTS / topk || I > ((int64_t)1 << 31) || N > ((int64_t)1 << 31))
+    if (M < 0 || topk < 1 || topk > SPEAR_MAX_TOPK || E < 1 || E > SPEAR_MAX_EXPERTS || I < 32 || I % 32 != 0 || N < 1 ||
+        M > MAX_SLOTS / topk || I > MAX_CHANNELS || N > MAX_CHANNELS)
         return 0;
     return experts_layout(M, topk, E, I, N).total;
 }
@@ -643,9 +653,9 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
         (M > 0 && (!x || !ids || !weights || !y)))
         return SPEAR_E_NULL;
     const int64_t K = w->K, I = w->I, N = w->N;
-    const int64_t lim = (int64_t)1 << 31;
     if (M < 0 || topk < 1 || topk > SPEAR_MAX_TOPK || w->E < 1 || w->E > SPEAR_MAX_EXPERTS || K < 32 ||
-        K % 32 != 0 || I < 32 || I % 32 != 0 || N < 1 || M > MAX_SLOTS / topk || K > lim || I > lim || N > lim)
+        K % 32 != 0 || I < 32 || I % 32 != 0 || N < 1 || M > MAX_SLOTS / topk || K > ((int64_t)1 << 31) ||
+        I > MAX_CHANNELS || N > MAX_CHANNELS)
         return SPEAR_E_SHAPE;
     if (w->act < SPEAR_ACT_NONE || w->act > SPEAR_ACT_GELU_TANH || (w->glu != 0 && w->glu != 1))
         return SPEAR_E_ARG;
@@ -656,13 +666,9 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
     const ExpertsLayout L = experts_layout(M, topk, w->E, I, N);
     if (ws_bytes < L.total)
         return SPEAR_E_WORKSPACE;
-    const int64_t NU = w->glu ? 2 * I : I, wide = NU > N ? NU : N;
+    const int64_t NU = w->glu ? 2 * I : I;
     const int bm = tile_rows(L.slots, w->E, K, I);
     const int64_t nt = max_tiles(L.slots, w->E, bm);
-    // a launch's threads: below 2^32, by the narrowest channel block of 64 and 512
-    // threads (few slots: as many tiles at most, and 16 channels a workgroup)
-    if ((nt > FEW_SLOTS ? nt : FEW_SLOTS) > ((int64_t)1 << 23) / ((wide + 63) / 64 + 1))
-        return SPEAR_E_SHAPE;
     const spear_status st = check_device();
     if (st != SPEAR_OK || M == 0)
         return st;

@@ -719,7 +719,8 @@ __global__ __launch_bounds__(64 * G2_WN * G2_WM * G2_WK) void gemm2_kernel(const
     // Blocks are dealt round-robin to the 8 XCDs; give each XCD a contiguous run
     // of units (channels fastest, then tokens, then K slices) so its L2 shares
     // activation rows.
-    const int64_t bid = (int64_t)blockIdx.x - (EC == 2 ? a.npre : 0);   // npre % 8 == 0
+    const int64_t bid = (int64_t)blockIdx.x - (EC == 2 ? a.npre : 0)    // npre % 8 == 0
+                        + (GRP ? 8 * (int64_t)a.G.base8 : 0);
     const int64_t q8 = nunits / 8, r8 = nunits % 8;
     const int64_t xcd = bid % 8, loc = bid / 8;
     const int64_t unit = xcd * q8 + (xcd < r8 ? xcd : r8) + loc;
@@ -1568,16 +1569,22 @@ hipError_t launch_gemm_e(const LinearArgs &a, int ec_on, hipStream_t s)
 template <int WM, int FM, int WK, int FN, int WN, int KF>
 hipError_t launch_grouped_t(const LinearArgs &a, int64_t max_tiles, hipStream_t s)
 {
-    const int64_t bn = 16 * FN * WN;
+    const int64_t bn = 16 * FN * WN, blocks = max_tiles * ((a.N + bn - 1) / bn);
     LinearArgs ka = a;
-    ka.grid = (uint32_t)(max_tiles * ((a.N + bn - 1) / bn));
-    if (a.out_f32)
-        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, 0, 1, WK, FN, WN, KF, 1, 1>), dim3(ka.grid),
-                           dim3(64 * WN * WM * WK), 0, s, ka);
-    else
-        hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, 0, 0, WK, FN, WN, KF, 1, 1>), dim3(ka.grid),
-                           dim3(64 * WN * WM * WK), 0, s, ka);
-    return hipGetLastError();
+    for (int64_t b = 0; b < blocks; b += MAX_BLOCKS) {
+        ka.G.base8 = (uint32_t)(b / 8);
+        ka.grid = (uint32_t)(blocks - b < MAX_BLOCKS ? blocks - b : MAX_BLOCKS);
+        if (a.out_f32)
+            hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, 0, 1, WK, FN, WN, KF, 1, 1>), dim3(ka.grid),
+                               dim3(64 * WN * WM * WK), 0, s, ka);
+        else
+            hipLaunchKernelGGL((gemm2_kernel<WM, FM, 0, 0, 0, WK, FN, WN, KF, 1, 1>), dim3(ka.grid),
+                               dim3(64 * WN * WM * WK), 0, s, ka);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace

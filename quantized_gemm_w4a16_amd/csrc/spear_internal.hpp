@@ -182,8 +182,12 @@ struct GrpArgs {
     const Tile *tiles;
     const int32_t *list;    // slots by expert
     int32_t div;            // a row's source is slot / div
-    int32_t pad;
+    uint32_t base8;         // the launch's first block, in eights (an XCD each)
 };
+
+// Blocks of one launch of a product over row tiles, at most: more take several
+// launches (a launch holds less than 2^32 threads).
+constexpr int64_t MAX_BLOCKS = 1 << 20;
 
 struct LinearArgs {
     // The leading block (212 bytes, four 64-byte lines) is what the decode
@@ -333,7 +337,7 @@ __device__ __forceinline__ void pin_epi_args(const LinearArgs &a)
 
 __device__ __forceinline__ void pin_grp_args(const LinearArgs &a)
 {
-    pin_arg(a.G.ntiles); pin_arg(a.G.tiles); pin_arg(a.G.list); pin_arg(a.G.div);
+    pin_arg(a.G.ntiles); pin_arg(a.G.tiles); pin_arg(a.G.list); pin_arg(a.G.div); pin_arg(a.G.base8);
 }
 
 // ------------------------------------------------------------------ epilogue
