@@ -41,6 +41,7 @@ SCORE_SIGMOID = 1
 MAX_EXPERTS = 512
 MAX_TOPK = 32
 MAX_GROUPS = 64
+E_NULL = -1
 E_SHAPE = -2
 E_ARG = -4
 
@@ -372,6 +373,42 @@ def _want_workspace(fn: str, t, device):
         _bad(fn, E_ARG, f"workspace has to be a contiguous uint8 tensor on {device}")
 
 
+def _want_flat(fn: str, name: str, t, dtypes, n: int, device):
+    """The same for a tensor that is taken by its number of elements."""
+    if t.dtype in dtypes and t.numel() == n and t.device == device and t.is_contiguous():
+        return
+    if t.numel() != n:
+        _bad(fn, E_SHAPE, f"{name} has {t.numel()} elements, not {n}")
+    _want(fn, name, t, dtypes, t.shape, device)
+
+
+def _want_layer(fn: str, w: W4, ec: Optional[EC], M: int, device):
+    """The weights and the compensator of a layer call."""
+    N, K = w.N, w.K
+    _want_flat(fn, "packed", w.packed, _U8, N * K // 2, device)
+    _want_flat(fn, "scales", w.scales, _F32, N, device)
+    if w.zeros is not None:
+        _want_flat(fn, "zeros", w.zeros, _U8, N, device)
+    if ec is None:
+        return
+    r = ec.r
+    _want_flat(fn, "A", ec.A, _BF16, r * K, device)
+    _want_flat(fn, "B", ec.B, _BF16, N * r, device)
+    _want_flat(fn, "w_gate", ec.w_gate, _BF16, K, device)
+    for name, dtypes, n in (("g_out", _F32, M), ("idx_out", _I32, M), ("n_active_out", _I32, 1)):
+        t = getattr(ec, name)
+        if t is not None and not (t.dtype in dtypes and t.numel() >= n and t.device == device and
+                                  t.is_contiguous()):
+            _want_flat(fn, name, t, dtypes, n, device)
+    if ec.gate_w1 is not None:
+        h = ec.gate_h
+        for name, n in (("gate_w1", h * r), ("gate_c1", h), ("gate_w2", r * h), ("gate_c2", r)):
+            t = getattr(ec, name)
+            if t is None:
+                _bad(fn, E_NULL, f"{name} is missing")
+            _want_flat(fn, name, t, _F32, n, device)
+
+
 _BF16 = (torch.bfloat16, torch.int16)     # raw bit tensors are taken too
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
@@ -459,6 +496,7 @@ def spear_w4_linear_epilogue(x: torch.Tensor, w: W4, ep: Epilogue, ec: Optional[
         _want(fn, "y", y, (dt,), (M, NO), dev)
     if workspace is not None:
         _want_workspace(fn, workspace, dev)
+    _want_layer(fn, w, ec, M, dev)
 
     def call(s):
         nonlocal y, workspace
