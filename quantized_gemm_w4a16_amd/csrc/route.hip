@@ -89,10 +89,6 @@ __device__ __forceinline__ double wave_sum(double v)
 {
     return wave_reduce(v, 0.0, [](double p, double q) { return p + q; });
 }
-__device__ __forceinline__ float wave_sum(float v)
-{
-    return wave_reduce(v, 0.f, [](float p, float q) { return p + q; });
-}
 __device__ __forceinline__ double wave_max(double v)
 {
     return wave_reduce(v, -(double)INFINITY, [](double p, double q) { return q > p ? q : p; });

@@ -342,9 +342,9 @@ __device__ __forceinline__ void pin_grp_args(const LinearArgs &a)
 }
 
 // ------------------------------------------------------------------ epilogue
-// act(t), the activation a whole launch shares (uniform branch).  expf, tanhf
-// and erff in fp32: the activation of a value near zero keeps its relative
-// accuracy (x is multiplied on, never subtracted).  silu of a large negative t
+// act(t), the activation a whole launch shares (uniform branch).  expf and
+// erfcf in fp32: the activation of a value near zero keeps its relative
+// accuracy (t is multiplied on, never subtracted).  silu of a large negative t
 // is t / inf = -0, as is the limit; gelu_tanh is written as t sigmoid(2 q),
 // q = sqrt(2 / pi) (t + 0.044715 t^3), which equals t / 2 (1 + tanh q) without
 // the cancellation of 1 + tanh at negative t.
@@ -384,7 +384,7 @@ __device__ __forceinline__ void epi_apply(const float (&t)[4], const float (&b)[
 }
 
 // Biases of channels n .. n + 3 (clamped to N - 1), raw; read without a branch
-// from the scales when there is no bias, and then replaced by epi_bias.
+// from the scales when there is no bias, and then replaced by zeros by the caller.
 __device__ __forceinline__ void epi_load_bias(const float *bias, const float *scales, int64_t n, int64_t N,
                                               float (&raw)[4])
 {
