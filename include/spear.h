@@ -280,7 +280,8 @@ typedef struct spear_epilogue {
  * workspace and the paths are those of spear_w4_linear_path; ep is required.
  * SPEAR_PATH_AUTO with M <= 16, a compensator of rank 64 at most and no gate
  * vector of its own takes the compensator's first half as a launch of its own
- * (t may differ from spear_w4_linear's in the order of its sums).
+ * where the layer is wide (t may then differ from spear_w4_linear's in the order
+ * of its sums).
  * An expired wait makes the outputs NaN here too (NaN passes through every
  * activation).
  */

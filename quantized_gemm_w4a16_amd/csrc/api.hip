@@ -539,21 +539,42 @@ static spear_status launch_path(LinearArgs &a, const spear_ec *ec, int32_t path,
     return hip_status(e);
 }
 
-// Decode with an epilogue, no path asked for: the EC's pre-pass in a launch of
-// its own before the decode kernel, rather than exchanged inside it (2048 -> 16384
-// pair, one token: 13.4 us, 16.4 exchanged; 8192 -> 2048, 16 tokens: 15.0, 17.1).
+// Decode with an epilogue, no path asked for: is the EC's pre-pass a launch of its
+// own before the decode kernel, rather than exchanged inside it?  That costs a
+// launch and its round trip (4.7 us) and pays where the exchange is slow: where
+// more stream workgroups than the chip takes at once wait behind the producers,
+// and with many tokens where every epilogue loads many partials.  us a call in
+// graphs, pre-pass / exchange, rank 32 (ranks 16 and 64 change sides at the same
+// sizes), "w" the workgroups (channel groups times K ranges):
+//     N x K               w     1 token       4             8             16
+//      2048 x  2048      128   10.5 /  7.8   11.4 /  7.6   11.7 /  8.0   12.8 /  9.1
+//      8192 x  2048      512   12.8 / 12.0   13.6 / 13.0   14.1 / 13.7   15.4 / 14.5
+//      6144 x  4096      384   14.2 / 10.7   15.7 / 12.0   16.8 / 14.6   22.0 / 22.8 (w 768)
+//     10240 x  1024      640   12.6 / 14.0   13.4 / 14.4   14.3 / 15.5   16.9 / 19.3
+//     16384 x   256     1024   10.5 / 15.3   11.0 / 16.1   11.7 / 17.5   13.3 / 19.6
+//     16384 x  2048     1024   15.0 / 19.2   16.5 / 20.3   20.4 / 22.0   22.1 / 24.0
+//      8192 x  8192     1024   20.1 / 23.7   25.4 / 26.4   28.0 / 30.3   40.4 / 56.5
+//     28672 x  4096     1792   25.5 / 35.7   32.6 / 42.5   42.0 / 50.4   60.2 / 75.0
+// and layers of no more channel groups than CUs, at 16 tokens: 2048 x 4096 14.5 /
+// 11.7 (w 256), 4096 x 4096 16.1 / 16.4 (w 512), 2048 x 8192 16.3 / 19.1 (w 512),
+// 4096 x 8192 24.4 / 28.4 (w 1024), 4096 x 14336 35.3 / 31.9 (w 1792), 1024 x 22016
+// 40.8 / 36.2 (w 640); with fewer the exchange (4096 x 8192 15.3 / 13.7 at one
+// token and 24.7 / 20.7 at 12, 4096 x 11008 19.4 / 17.3 at one).  A token that the hard gate skips takes 14.7 / 14.4 at
+// 16384 x 2048 and 10.1 / 5.7 at 2048 x 2048.
 // Above rank 64 the partials no longer fit what a decode workgroup loads ahead;
 // a gate vector needs all of them before its own layers.
-static bool few_ec_prepass(const spear_ec *ec)
+static bool few_ec_prepass(const spear_ec *ec, const WsLayout &L, int64_t M, int64_t K)
 {
-    return ec && ec->gate_h == 0 && cdiv(ec->r, 32) * 32 <= FEW_RANK;
+    const int64_t w = L.ncg * L.ksplit;
+    return ec && ec->gate_h == 0 && L.rpad <= FEW_RANK &&
+           ((L.ncg > EC_WIDE_GROUPS && w >= 640) || (M >= 14 && w >= 512 && K >= 4096 && K <= 8192));
 }
 
 // A validated layer call: dispatch and launch on `stream`.
 static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w,
                                const spear_ec *ec, void *y, int32_t out_dtype, void *workspace,
                                int32_t path, void *stream, const spear_epilogue *ep = nullptr,
-                               bool few_ec = false)
+                               bool chosen = false)
 {
     const int64_t N = w->N, K = w->K;
     const WsLayout L = ws_layout(M, N, K, ec ? ec->r : 0);
@@ -576,7 +597,7 @@ static spear_status run_linear(const spear_bf16 *x, int64_t M, const spear_w4 *w
         a.E.act = ep->act;
         a.E.glu = ep->glu;
         a.E.on = 1;
-        if (few_ec) {
+        if (chosen && path == SPEAR_PATH_DECODE && few_ec_prepass(ec, L, M, K)) {
             // about 1024 depths a slice, in the place of the fused form's words
             int64_t p = cdiv(K, 1024);
             p = p < FEW_SLICES ? p : FEW_SLICES;
@@ -637,7 +658,7 @@ spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spea
 {
     if (!ep)
         return SPEAR_E_NULL;
-    const bool any = path == SPEAR_PATH_AUTO;
+    const bool chosen = path == SPEAR_PATH_AUTO;
     spear_status st = validate_linear(x, M, w, ec, y, out_dtype, workspace, ws_bytes, &path);
     if (st != SPEAR_OK)
         return st;
@@ -647,8 +668,7 @@ spear_status spear_w4_linear_epilogue(const spear_bf16 *x, int64_t M, const spea
         return SPEAR_E_SHAPE;
     if (!aligned(ep->bias, 4) || !aligned(ep->residual, 16))
         return SPEAR_E_ALIGN;
-    return run_linear(x, M, w, ec, y, out_dtype, workspace, path, stream, ep,
-                      any && path == SPEAR_PATH_DECODE && few_ec_prepass(ec));
+    return run_linear(x, M, w, ec, y, out_dtype, workspace, path, stream, ep, chosen);
 }
 
 spear_status spear_w4_linear_noalloc(const spear_bf16 *x, int64_t M, const spear_w4 *w,
