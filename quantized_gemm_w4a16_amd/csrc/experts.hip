@@ -10,6 +10,10 @@
 //  2. up:   each row tile's tokens through its expert's first layer, h by slot;
 //  3. down: h through the second layer, fp32 rows by slot;
 //  4. join: each token's rows times their weights, in slot order, plus residual.
+// h is held in bf16, what the second layer's matrix instructions take (as fp32 it
+// would be two words there, twice the instructions and twice the rows' LDS); its
+// rounding, 2^-8 at most, is why outputs differ from fp32 throughout by more than
+// their own.
 // No launch waits on another workgroup, and no result depends on an order that
 // the hardware chooses: the sums of an output are taken in one fixed order.
 #include <string.h>
@@ -34,7 +38,9 @@ struct ExpertsLayout {
 // last one ragged, so at most slots / bm + (experts in use) of them.
 int64_t max_tiles(int64_t slots, int32_t E, int bm) { return slots / bm + (slots < E ? slots : E); }
 
-// Rows of a tile by the slots an expert has on average.  Whole calls, us with 16
+// Rows of a tile by the slots an expert has on average; slots without an expert
+// here count too, the ids being on the device, so a device that holds an eighth of
+// the experts takes the tiles of eight times its load.  Whole calls, us with 16
 // / 64 rows (32 rows are behind one of them everywhere):
 //   32 experts 2048 -> 2 x 1408 -> 2048:  12 slots 59 / 62, 16: 63 / 65, 20: 74 / 68
 //    8 experts 4096 -> 2 x 4096 -> 4096:  12 slots 70 / 72, 16: 83 / 75, 20: 92 / 76
@@ -75,7 +81,7 @@ ExpertsLayout experts_layout(int64_t M, int32_t topk, int32_t E, int64_t I, int6
 // count does not depend on the order of its additions), so it knows where its
 // own rows and tiles begin, then writes its slots in ascending order by ballot.
 // Bound by the round trips of its two passes over the ids: 4 to 5 us up to 1200
-// slots, 11.6 us for 8192 of 8 experts.
+// slots, 11.6 us for 8192 of 8 experts, and in proportion from there.
 __global__ __launch_bounds__(1024) void plan_kernel(const int32_t *__restrict__ ids, int32_t slots, int32_t E,
                                                     int32_t bm, uint32_t *__restrict__ zeros,
                                                     int32_t *__restrict__ ntiles, Tile *__restrict__ tiles,
