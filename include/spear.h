@@ -382,6 +382,185 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
                               const spear_bf16 *residual, spear_bf16 *y, void *workspace,
                               size_t ws_bytes, void *stream);
 
+/*
+ * Attention over a cache held in 4 bits: the plan of a serving step, rotary
+ * positions, the write into the cache, and the attention that reads it.
+ *
+ * The cache holds a channel as e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign) and
+ * one power of two for every block of 32 channels of a token's head.  With a
+ * the largest |x| of a block and f = floor(log2 a):
+ *   e = f - 2, or f - 1 where a / 2^f >= 1.75 (a rounded to two significant bits
+ *       has the next exponent), held within [-125, 125]; a = 0 gives -125
+ *   code = x / 2^e rounded to the nearest level, ties to the even code, at most 6
+ *   scale byte = e + 127;  a block with a NaN or an infinity: 255, and reads NaN
+ * so that a value that is read back is exact in bf16.  Pages of P tokens, a
+ * head's tokens side by side (device pointers, each 16-byte aligned):
+ */
+typedef struct spear_kv4 {
+    uint8_t *k_codes;   /* [pages][heads][P][D/2], the lower channel in the low nibble */
+    uint8_t *k_scales;  /* [pages][heads][D/32][P]                                      */
+    uint8_t *v_codes;   /* as k_codes                                                   */
+    uint8_t *v_scales;  /* as k_scales                                                  */
+    int64_t pages;      /* 1 .. 2^31 - 1                                                */
+    int32_t heads;      /* key heads, 1 .. SPEAR_MAX_HEADS                              */
+    int32_t D;          /* channels of a head: 64, 96, 128, 192 or 256                  */
+    int32_t P;          /* tokens of a page: 16, 32, 64, 128, 256, 512 or 1024          */
+} spear_kv4;
+
+#define SPEAR_MAX_HEADS    1024 /* query or key heads                     */
+#define SPEAR_MAX_REQUESTS 4096 /* requests of a step                     */
+#define SPEAR_MAX_ROWS     ((int64_t)1 << 23) /* token rows of a step     */
+#define SPEAR_MAX_CONTEXT  ((int64_t)1 << 30) /* tokens that a table's row can hold */
+
+/*
+ * What spear_kv4_plan makes of a step's lengths (device pointers).
+ */
+typedef struct spear_kv4_step {
+    int32_t *q_start;   /* [B + 1] first row of each request                          */
+    int32_t *kv_len;    /* [B] tokens in the cache after the step                     */
+    int32_t *positions; /* [T] position of each row in its request                    */
+    int64_t *slots;     /* [T] page * P + place in the page; 8-byte aligned           */
+    int32_t *n_left;    /* [1] pages left in the free list                            */
+    int32_t *status;    /* [2] pages that the free list lacked; pages that the rows of
+                           the table have no room for                                  */
+} spear_kv4_step;
+
+/*
+ * spear_kv4_plan -- block table and slot map of a serving step, from the
+ * requests' lengths alone (nothing is read back by the host).
+ *   cached [B]  tokens that each request has in the cache (negative: 0)
+ *   fresh  [B]  tokens that the step adds to each (negative: 0); 0 is a request
+ *               that pauses
+ *   table  [B][width]  each request's pages in order, updated in place: the first
+ *               ceil(cached / P) entries of a row are read, new pages are written
+ *               behind them, the rest of the row is left as it is
+ *   free_pages [n_pages]  page ids, a stack of which the first *n_free are free
+ *               (clamped to [0, n_pages]); pages are taken from its end, in the
+ *               requests' order.  n_free is read, what is left goes to n_left
+ *   T           rows of the step (a captured step keeps the largest)
+ * The requests' fresh tokens lie in the rows one behind the other.  Fresh tokens
+ * past T rows are dropped: q_start, kv_len and the pages count the others.  Rows
+ * behind the last token get position 0 and slot -1 (no place in the cache), as
+ * do tokens of a page that the free list lacked (its table entry is -1 too) or
+ * that the table has no room for; the latter two keep their positions.
+ *   0 <= B <= SPEAR_MAX_REQUESTS, 0 <= T <= SPEAR_MAX_ROWS, width >= 1,
+ *   width * P <= SPEAR_MAX_CONTEXT; a request's tokens are less than 2^31.
+ *   The outputs overlap neither each other nor an input: two steps alternate
+ *   between two sets of them.
+ */
+spear_status spear_kv4_plan(const int32_t *cached, const int32_t *fresh, int32_t B, int32_t *table,
+                            int64_t width, const int32_t *free_pages, int64_t n_pages,
+                            const int32_t *n_free, int64_t T, int32_t P,
+                            const spear_kv4_step *step, void *stream);
+
+/* Which channels of a head a rotation pairs. */
+#define SPEAR_ROPE_HALF  0 /* channel i with channel i + rot / 2 */
+#define SPEAR_ROPE_PAIRS 1 /* channel 2i with channel 2i + 1     */
+
+/* Rotary positions: the first rot channels of every head, the others as they are. */
+typedef struct spear_rotation {
+    const double *freqs; /* device [rot / 2]: angle of one position, radians; 8-byte aligned */
+    double scale;        /* factor of the rotated channels (1: none); finite                  */
+    int32_t rot;         /* even, 2 .. D                                                       */
+    int32_t layout;      /* SPEAR_ROPE_HALF or SPEAR_ROPE_PAIRS                               */
+} spear_rotation;
+
+/* How spear_rope_frequencies stretches the positions. */
+#define SPEAR_ROPE_PLAIN  0 /* f_i = base^(-2i / rot)                                       */
+#define SPEAR_ROPE_LINEAR 1 /* f_i / factor                                                 */
+#define SPEAR_ROPE_BASE   2 /* base factor^(rot / (rot - 2)) in place of base: the slowest
+                               pair turns factor times slower, the fastest as before        */
+#define SPEAR_ROPE_PARTS  3 /* by the turns t = original f_i / 2 pi that a pair makes over the
+                               original context: f_i from high turns on, f_i / factor up to
+                               low, and g f_i + (1 - g) f_i / factor between them with
+                               g = (t - low) / (high - low)                                  */
+
+/*
+ * spear_rope_frequencies -- host only, no HIP call: the rot / 2 frequencies of
+ * a rotation into freqs (HOST pointer), all in fp64.
+ *   rot even, 2 .. 256 (4 at least for SPEAR_ROPE_BASE); base > 1; factor > 0;
+ *   original > 0 and low < high for SPEAR_ROPE_PARTS (else unused).
+ */
+spear_status spear_rope_frequencies(int32_t rot, double base, int32_t kind, double factor,
+                                    double original, double low, double high, double *freqs);
+
+/*
+ * spear_rope -- y = x with every head rotated to its row's position:
+ *   y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t),
+ *   t = position * freqs[i], (a, b) the i-th pair, m = scale
+ * computed in fp64 and rounded once to bf16, so that far positions lose nothing.
+ *   x [T][H][D] bf16, x_stride elements from a row to the next (a multiple of 8,
+ *     at least H D); y likewise with y_stride; x and y 16-byte aligned.  y may be
+ *     x itself (then with its stride); it overlaps no other input.
+ *   positions [T], any int32.
+ *   0 <= T <= SPEAR_MAX_ROWS, 1 <= H <= SPEAR_MAX_HEADS, D a multiple of 8 in
+ *   [8, 256].
+ */
+spear_status spear_rope(const spear_bf16 *x, int64_t x_stride, int64_t T, int32_t H, int32_t D,
+                        const int32_t *positions, const spear_rotation *rope, spear_bf16 *y,
+                        int64_t y_stride, void *stream);
+
+/*
+ * spear_rope_kv4_write -- what follows the q/k/v projection, in one launch:
+ * q rotated into q_out; k rotated and v as it is, each held in 4 bits in its
+ * slot of the cache (k is rounded once, from the fp64 rotation).  rope == NULL
+ * rotates nothing (positions is then unused).
+ *   q [T][Hq][D], k and v [T][heads][D] bf16, each with a stride from row to row
+ *     (a multiple of 8, at least its row); 16-byte aligned.  They may be parts of
+ *     one row, and q_out may be q itself (with its stride).
+ *   slots [T]: page * P + place; a row whose slot lies outside the cache is
+ *     not written to it (its q is rotated all the same).  No slot may occur twice.
+ */
+spear_status spear_rope_kv4_write(const spear_bf16 *q, int64_t q_stride, const spear_bf16 *k,
+                                  int64_t k_stride, const spear_bf16 *v, int64_t v_stride,
+                                  int64_t T, int32_t Hq, const int32_t *positions,
+                                  const int64_t *slots, const spear_rotation *rope,
+                                  const spear_kv4 *kv, spear_bf16 *q_out, int64_t q_out_stride,
+                                  void *stream);
+
+/*
+ * spear_kv4_read -- rows of the cache as bf16 (exact): k and v [T][heads][D],
+ * either of them NULL if it is not wanted; a row whose slot lies outside the
+ * cache is zeros.  k and v 16-byte aligned, slots 8-byte aligned.
+ */
+spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T, spear_bf16 *k,
+                            spear_bf16 *v, void *stream);
+
+/*
+ * spear_kv4_attention -- attention of the step's rows over the cache, after
+ * their own k and v have been written to it:
+ *   row t of request b (q_start[b] <= t < q_start[b + 1]) stands at position
+ *     p = kv_len[b] - (q_start[b + 1] - t)
+ *   and sees the positions j <= p of its request, with window > 0 those above
+ *     p - window only
+ *   y[t][h] = sum_j softmax_j(scale q[t][h] . k[j][h / G]) v[j][h / G],  G = Hq / heads
+ *   lse[t][h] = log sum_j exp(scale q . k)       (natural; optional)
+ * Sums and softmax are in fp32, y is rounded once to bf16.  Requests of one
+ * token, of a few and of long chunks may stand side by side.  A row that sees
+ * nothing gets zeros and lse -inf; rows behind the last request are left as they
+ * were.  A table entry outside [0, pages) (a page that was let go) is as if its
+ * tokens were masked; what masked places hold, NaN and infinities among it, does
+ * not count.  kv_len is held within [0, width P] and q_start within [0, T].
+ *   q [T][Hq][D] bf16 with q_stride elements from row to row (a multiple of 8);
+ *     y [T][Hq][D] bf16 without gaps; both 16-byte aligned; y may be q itself if
+ *     q has no gaps.  Hq a multiple of heads, G <= 64, T Hq <= 2^27.
+ *   table [B][width], q_start [B + 1], kv_len [B] as spear_kv4_plan leaves them.
+ *   max_fresh: no request has more rows than that (an upper bound that the host
+ *     knows; it chooses kernels and their tiles, the result is right without it).
+ *   scale > 0, finite; window 0 (none) .. 2^30.
+ *   workspace device scratch of spear_kv4_attention_workspace_size bytes (0 for
+ *     sizes out of range), 256-byte aligned; needs no zeroing and holds nothing
+ *     between calls.  The size grows with T and B and hangs on neither max_fresh
+ *     nor width, so one for the largest step serves the others.
+ */
+size_t spear_kv4_attention_workspace_size(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
+                                          int32_t heads, int32_t D, int64_t width, int32_t P);
+spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t T, int32_t Hq,
+                                 const spear_kv4 *kv, const int32_t *table, int64_t width,
+                                 const int32_t *q_start, const int32_t *kv_len, int32_t B,
+                                 int64_t max_fresh, float scale, int32_t window, spear_bf16 *y,
+                                 float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 /* Size of the library's own scratch used by spear_w4_linear_noalloc, per GPU. */
 #define SPEAR_NOALLOC_MAX_WORKSPACE ((size_t)48 << 20)
 

@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspear.so")
 SOURCES = ["api.hip", "pack_gate.hip", "decode.hip", "decode_epilogue.hip", "prefill.hip", "route.hip",
-           "experts.hip", "slo.cpp"]
+           "experts.hip", "kv_step.hip", "kv_attention.hip", "slo.cpp"]
 ARCH = "gfx950"
 # Packed fp32 arithmetic is left to nothing: it is disabled for all device code.
 # The atomic optimizer turns a one-lane atomic with a uniform address into a

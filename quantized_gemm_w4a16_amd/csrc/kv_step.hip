@@ -1,0 +1,532 @@
+// kv_step.hip -- the plan of a serving step, rotary positions, and the cache of
+// 4 bits written and read (spear_kv4_plan, spear_rope, spear_rope_kv4_write,
+// spear_kv4_read, spear_rope_frequencies) for gfx950.
+#include <math.h>
+
+#include "kv4.hpp"
+
+namespace spear {
+namespace {
+
+bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
+
+// ----------------------------------------------------------------------- plan
+// Every workgroup forms the same prefix sums over the requests (eight at most a
+// thread) and takes its share of the new pages and of the rows; the first writes
+// what there is one of.  Nothing that a workgroup reads is written by another:
+// a row whose page is new computes the page from the free list.
+constexpr int PL_THREADS = 512;
+constexpr int PL_MOST = SPEAR_MAX_REQUESTS / PL_THREADS;
+
+struct PlanArgs {
+    const int32_t *cached, *fresh;
+    int32_t *table;
+    const int32_t *free_pages, *n_free;
+    spear_kv4_step out;
+    int64_t width, n_pages, T;
+    int32_t B, log_p;
+};
+
+// Sum of v over the lower threads of the workgroup, and over all of them.
+__device__ int64_t before_me(int64_t v, int64_t *total, int64_t *s_wave)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t incl = v;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t o = __shfl_up(incl, d);
+        incl += lane >= d ? o : 0;
+    }
+    if (lane == 63)
+        s_wave[wave] = incl;
+    __syncthreads();
+    int64_t base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < PL_THREADS / 64; w++) {
+        base += w < wave ? s_wave[w] : 0;
+        all += s_wave[w];
+    }
+    __syncthreads();
+    *total = all;
+    return base + incl - v;
+}
+
+// The last index of a[0 .. n), ascending, whose value is at most v (a[0] <= v).
+__device__ int last_at_most(const int32_t *a, int n, int32_t v)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__global__ __launch_bounds__(PL_THREADS) void plan_step_kernel(const PlanArgs a)
+{
+    __shared__ int64_t s_wave[PL_THREADS / 64];
+    __shared__ int32_t s_start[SPEAR_MAX_REQUESTS], s_taken[SPEAR_MAX_REQUESTS], s_cached[SPEAR_MAX_REQUESTS];
+    const int tid = threadIdx.x, B = a.B, lp = a.log_p;
+    const int per = (B + PL_THREADS - 1) / PL_THREADS, first = tid * per;
+    const int64_t P1 = (1 << lp) - 1, width = a.width;
+    const bool writer = blockIdx.x == 0;
+
+    int32_t fresh[PL_MOST], cached[PL_MOST];
+    int64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < PL_MOST; j++) {
+        const int i = first + j;
+        const bool in = j < per && i < B;
+        const int32_t f = in ? a.fresh[i] : 0, c = in ? a.cached[i] : 0;
+        fresh[j] = f < 0 ? 0 : (f > a.T ? (int32_t)a.T : f);
+        cached[j] = c < 0 ? 0 : c;
+        sum += fresh[j];
+    }
+    int64_t nf = a.n_free[0];
+    nf = nf < 0 ? 0 : (nf > a.n_pages ? a.n_pages : nf);
+    int64_t all;
+    int64_t start = before_me(sum, &all, s_wave);
+    const int32_t rows = (int32_t)(all < a.T ? all : a.T);
+
+    int64_t takes = 0, beyond = 0;
+#pragma unroll
+    for (int j = 0; j < PL_MOST; j++) {
+        const int i = first + j;
+        const int64_t s0 = start < a.T ? start : a.T;
+        start += fresh[j];
+        const int64_t s1 = start < a.T ? start : a.T;
+        if (j < per && i < B) {
+            const int64_t kv = (int64_t)cached[j] + (s1 - s0);
+            const int64_t held = ((int64_t)cached[j] + P1) >> lp, full = (kv + P1) >> lp;
+            s_start[i] = (int32_t)s0;
+            s_cached[i] = cached[j];
+            fresh[j] = (int32_t)((full < width ? full : width) - (held < width ? held : width));   // pages taken
+            takes += fresh[j];
+            beyond += full > (held > width ? held : width) ? full - (held > width ? held : width) : 0;
+            if (writer) {
+                a.out.q_start[i] = (int32_t)s0;
+                a.out.kv_len[i] = (int32_t)(kv < 0x7FFFFFFF ? kv : 0x7FFFFFFF);
+            }
+        } else
+            fresh[j] = 0;
+    }
+    int64_t wanted, over;
+    int64_t taken = before_me(takes, &wanted, s_wave);
+    before_me(beyond, &over, s_wave);
+#pragma unroll
+    for (int j = 0; j < PL_MOST; j++)
+        if (j < per && first + j < B) {
+            s_taken[first + j] = (int32_t)taken;
+            taken += fresh[j];
+        }
+    if (writer && tid == 0) {
+        a.out.q_start[B] = rows;
+        a.out.n_left[0] = (int32_t)(nf > wanted ? nf - wanted : 0);
+        a.out.status[0] = (int32_t)(wanted > nf ? wanted - nf : 0);
+        a.out.status[1] = (int32_t)over;
+    }
+    __syncthreads();
+
+    const int64_t me = (int64_t)blockIdx.x * PL_THREADS + tid, step = (int64_t)gridDim.x * PL_THREADS;
+    for (int64_t k = me; k < wanted; k += step) {
+        const int i = last_at_most(s_taken, B, (int32_t)k);
+        const int64_t held = ((int64_t)s_cached[i] + P1) >> lp;
+        a.table[i * width + held + (k - s_taken[i])] = k < nf ? a.free_pages[nf - 1 - k] : -1;
+    }
+    for (int64_t t = me; t < a.T; t += step) {
+        int32_t pos = 0;
+        int64_t slot = -1;
+        if (t < rows) {
+            const int i = last_at_most(s_start, B, (int32_t)t);
+            const int64_t p = (int64_t)s_cached[i] + (t - s_start[i]), j = p >> lp;
+            const int64_t held = ((int64_t)s_cached[i] + P1) >> lp;
+            pos = (int32_t)p;
+            if (j < width) {
+                int32_t page;
+                if (j >= held) {
+                    const int64_t k = s_taken[i] + (j - held);
+                    page = k < nf ? a.free_pages[nf - 1 - k] : -1;
+                } else
+                    page = a.table[i * width + j];
+                slot = page < 0 ? -1 : ((int64_t)page << lp) + (p & P1);
+            }
+        }
+        a.out.positions[t] = pos;
+        a.out.slots[t] = slot;
+    }
+}
+
+// ----------------------------------------------------------- rotation and write
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *y;
+    int64_t qs, ks, vs, ys;          // elements from row to row
+    const int32_t *pos;
+    const int64_t *slots;
+    const double *freqs;             // NULL: nothing is rotated
+    double scale;
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t places;                  // pages * P
+    int32_t Hq, Hkv, D, rot, layout, log_p;
+};
+
+// The fp32 that rounds on to fewer bits as x does: the bits that fp32 has no room
+// for go into its last one (a tie stays a tie only if it is one).
+__device__ __forceinline__ float keep_odd(double x)
+{
+    const uint64_t b = __double_as_longlong(x);
+    const uint32_t lo = (uint32_t)b;
+    const uint32_t kept = (lo & 0xE0000000u) | ((lo & 0x1FFFFFFFu) ? 0x20000000u : 0u);
+    return (float)__longlong_as_double((b & 0xFFFFFFFF00000000ull) | kept);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+// Eight channels of a block of 32 whose other channels the lane's quad holds ->
+// the eight codes; *byte the block's scale.
+__device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+        top = b > top ? b : top;
+    }
+    uint32_t o = quad<0xB1>(top);                        // lanes 1 0 3 2 of the quad
+    top = o > top ? o : top;
+    o = quad<0x4E>(top);                                 // lanes 2 3 0 1
+    top = o > top ? o : top;
+    // a mantissa of 1.75 or more carries into the exponent
+    int e = (int)((top + 0x200000u) >> 23) - 2;
+    e = e < 2 ? 2 : (e > 252 ? 252 : e);
+    const float s = kv4_scale((uint32_t)e);
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[0], f[1], s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[2], f[3], s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[4], f[5], s, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[6], f[7], s, 3);
+    *byte = top >= 0x7F800000u ? 255u : (uint32_t)e;     // a NaN or an infinity
+    return r;
+}
+
+// A workgroup takes one row and up to N * (256 / (D / 8)) of its heads, a thread
+// eight channels (16 bytes) of up to N heads, always the same channels, so that
+// their cosines stay in registers.  The row is staged in LDS, where a channel
+// finds its partner whatever rot is; all reads of a head come before its writes
+// (a row may be rotated in place).  Angles, rotation and rounding are in fp64: at
+// position 2^20 an fp32 angle is off by 2^-5, and a value next to a border of
+// e2m1 would fall on the other side.
+template <int N, bool KV>
+__global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
+{
+    __shared__ u32x4 s_x[N][256];
+    __shared__ double2 s_cs[128];
+    const int tid = threadIdx.x, D = a.D, cph = D / 8, hpi = 256 / cph;
+    const int hl = tid / cph, c = tid - hl * cph;
+    const int heads = a.Hq + (KV ? 2 * a.Hkv : 0), h0 = blockIdx.y * (hpi * N) + hl;
+    const int64_t t = blockIdx.x;
+    const int n = a.rot / 2;
+    u32x4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int h = h0 + i * hpi;
+        x[i] = zero4();
+        if (hl < hpi && h < heads) {
+            const uint16_t *p = h < a.Hq ? a.q + t * a.qs + (int64_t)h * D
+                                : h < a.Hq + a.Hkv ? a.k + t * a.ks + (int64_t)(h - a.Hq) * D
+                                                   : a.v + t * a.vs + (int64_t)(h - a.Hq - a.Hkv) * D;
+            x[i] = ld16(p + 8 * c);
+        }
+    }
+    int64_t slot = -1;
+    if (KV)
+        slot = a.slots[t];
+    if (a.freqs && tid < n) {
+        double s, co;
+        sincos((double)a.pos[t] * a.freqs[tid], &s, &co);
+        s_cs[tid] = make_double2(co * a.scale, s * a.scale);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        s_x[i][tid] = x[i];
+    __syncthreads();
+    if (hl >= hpi)
+        return;
+
+    // y_j = x_j co_j + x_partner si_j for the channels below rot
+    const bool turn = a.freqs && 8 * c < a.rot;
+    double co[8], si[8];
+    int at[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const int e = 8 * c + j;
+        co[j] = 1.0;
+        si[j] = 0.0;
+        at[j] = e;
+        if (a.freqs && e < a.rot) {
+            const bool second = a.layout == SPEAR_ROPE_PAIRS ? (e & 1) : e >= n;
+            const int i = a.layout == SPEAR_ROPE_PAIRS ? e >> 1 : (second ? e - n : e);
+            const double2 cs = s_cs[i];
+            co[j] = cs.x;
+            si[j] = second ? cs.y : -cs.y;
+            at[j] = a.layout == SPEAR_ROPE_PAIRS ? e ^ 1 : (second ? e - n : e + n);
+        }
+    }
+    const bool there = KV && slot >= 0 && slot < a.places;
+    const int64_t page = slot >> a.log_p, off = slot & ((1 << a.log_p) - 1);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int h = h0 + i * hpi;
+        if (h >= heads)
+            continue;
+        const bool is_q = h < a.Hq, is_v = KV && h >= a.Hq + a.Hkv;
+        float f[8];
+        if (turn && !is_v) {
+            const uint16_t *row = reinterpret_cast<const uint16_t *>(&s_x[i][hl * cph]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float own = bf16f((uint16_t)(x[i][j >> 1] >> (16 * (j & 1))));
+                const double r = (double)own * co[j] + (double)bf16f(row[at[j]]) * si[j];
+                f[j] = 8 * c + j < a.rot ? keep_odd(r) : own;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                f[j] = bf16f((uint16_t)(x[i][j >> 1] >> (16 * (j & 1))));
+        }
+        if (is_q) {
+            u32x4 o;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                o[j] = (uint32_t)f2bf(f[2 * j]) | ((uint32_t)f2bf(f[2 * j + 1]) << 16);
+            *reinterpret_cast<u32x4 *>(a.y + t * a.ys + (int64_t)h * D + 8 * c) = o;
+        } else if (KV && there) {
+            uint32_t byte;
+            const uint32_t codes = hold8(f, &byte);
+            const int64_t ph = page * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0));
+            uint8_t *cp = is_v ? a.v_codes : a.k_codes, *sp = is_v ? a.v_scales : a.k_scales;
+            *reinterpret_cast<uint32_t *>(cp + (((ph << a.log_p) + off) * (D / 2) + 4 * c)) = codes;
+            if ((c & 3) == 0)
+                sp[((ph * (D / 32) + (c >> 2)) << a.log_p) + off] = (uint8_t)byte;
+        }
+    }
+}
+
+template <bool KV>
+hipError_t launch_rope(const RopeArgs &a, int64_t T, hipStream_t s)
+{
+    const int heads = a.Hq + (KV ? 2 * a.Hkv : 0), hpi = 256 / (a.D / 8);
+    // few rows: more workgroups, a head a thread
+    if (T * heads <= (int64_t)hpi * 2048)
+        hipLaunchKernelGGL((rope_kernel<1, KV>), dim3((unsigned)T, (unsigned)((heads + hpi - 1) / hpi)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((rope_kernel<4, KV>), dim3((unsigned)T, (unsigned)((heads + 4 * hpi - 1) / (4 * hpi))), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// A thread takes eight channels of a row: 4 bytes of codes to 16 of bf16.
+__global__ __launch_bounds__(256) void read_kernel(const spear_kv4 kv, const int64_t *slots, int64_t n, int log_p,
+                                                   uint16_t *k, uint16_t *v)
+{
+    uint16_t *out = blockIdx.y ? v : k;
+    const uint8_t *codes = blockIdx.y ? kv.v_codes : kv.k_codes, *scales = blockIdx.y ? kv.v_scales : kv.k_scales;
+    if (!out)
+        return;
+    const int cph = kv.D / 8;
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const int64_t th = i / cph, t = th / kv.heads;
+        const int c = (int)(i - th * cph), h = (int)(th - t * kv.heads);
+        const int64_t slot = slots[t];
+        u32x4 o = zero4();
+        if (slot >= 0 && slot < kv.pages * kv.P) {
+            const int64_t ph = (slot >> log_p) * kv.heads + h, off = slot & (kv.P - 1);
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + (((ph << log_p) + off) * (kv.D / 2) + 4 * c));
+            o = kv4_bf16(w, kv4_scale(scales[((ph * (kv.D / 32) + (c >> 2)) << log_p) + off]));
+        }
+        *reinterpret_cast<u32x4 *>(out + 8 * i) = o;
+    }
+}
+
+spear_status check_rotation(const spear_rotation *r, int32_t D)
+{
+    if (!r->freqs)
+        return SPEAR_E_NULL;
+    if (r->rot < 2 || r->rot > D || r->rot % 2 != 0)
+        return SPEAR_E_SHAPE;
+    if ((r->layout != SPEAR_ROPE_HALF && r->layout != SPEAR_ROPE_PAIRS) || !isfinite(r->scale))
+        return SPEAR_E_ARG;
+    return al(r->freqs, 8) ? SPEAR_OK : SPEAR_E_ALIGN;
+}
+
+bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8 != 0 || stride > ((int64_t)1 << 36); }
+
+} // namespace
+
+spear_status check_kv4(const spear_kv4 *kv)
+{
+    if (!kv || !kv->k_codes || !kv->k_scales || !kv->v_codes || !kv->v_scales)
+        return SPEAR_E_NULL;
+    if (kv->pages < 1 || kv->pages > 0x7FFFFFFF || kv->heads < 1 || kv->heads > SPEAR_MAX_HEADS ||
+        (kv->D != 64 && kv->D != 96 && kv->D != 128 && kv->D != 192 && kv->D != 256) || kv->P < 16 || kv->P > 1024 ||
+        (kv->P & (kv->P - 1)) != 0)
+        return SPEAR_E_SHAPE;
+    return al(kv->k_codes, 16) && al(kv->k_scales, 16) && al(kv->v_codes, 16) && al(kv->v_scales, 16) ? SPEAR_OK
+                                                                                                     : SPEAR_E_ALIGN;
+}
+
+} // namespace spear
+
+using namespace spear;
+
+extern "C" {
+
+spear_status spear_kv4_plan(const int32_t *cached, const int32_t *fresh, int32_t B, int32_t *table,
+                            int64_t width, const int32_t *free_pages, int64_t n_pages,
+                            const int32_t *n_free, int64_t T, int32_t P,
+                            const spear_kv4_step *step, void *stream)
+{
+    if (!step || !step->q_start || !step->n_left || !step->status || !n_free ||
+        (B > 0 && (!cached || !fresh || !table || !step->kv_len)) || (n_pages > 0 && !free_pages) ||
+        (T > 0 && (!step->positions || !step->slots)))
+        return SPEAR_E_NULL;
+    if (B < 0 || B > SPEAR_MAX_REQUESTS || T < 0 || T > SPEAR_MAX_ROWS || P < 16 || P > 1024 || (P & (P - 1)) != 0 ||
+        width < 1 || width > SPEAR_MAX_CONTEXT / P || n_pages < 0 || n_pages > 0x7FFFFFFF)
+        return SPEAR_E_SHAPE;
+    if (!al(cached, 4) || !al(fresh, 4) || !al(table, 4) || !al(free_pages, 4) || !al(n_free, 4) ||
+        !al(step->q_start, 4) || !al(step->kv_len, 4) || !al(step->positions, 4) || !al(step->slots, 8) ||
+        !al(step->n_left, 4) || !al(step->status, 4))
+        return SPEAR_E_ALIGN;
+    if (step->n_left == n_free || (B > 0 && (step->kv_len == cached || step->kv_len == fresh)))
+        return SPEAR_E_ARG;
+    const spear_status st = check_device();
+    if (st != SPEAR_OK)
+        return st;
+    const PlanArgs a = {cached, fresh, table, free_pages, n_free, *step, width, n_pages, T, B, __builtin_ctz(P)};
+    const int64_t want = (T + PL_THREADS - 1) / PL_THREADS;
+    hipLaunchKernelGGL(plan_step_kernel, dim3((unsigned)(want < 1 ? 1 : (want > 256 ? 256 : want))), dim3(PL_THREADS), 0,
+                       (hipStream_t)stream, a);
+    return hipGetLastError() == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
+}
+
+spear_status spear_rope_frequencies(int32_t rot, double base, int32_t kind, double factor,
+                                    double original, double low, double high, double *freqs)
+{
+    if (!freqs)
+        return SPEAR_E_NULL;
+    if (rot < 2 || rot > 256 || rot % 2 != 0 || (kind == SPEAR_ROPE_BASE && rot < 4))
+        return SPEAR_E_SHAPE;
+    if (kind < SPEAR_ROPE_PLAIN || kind > SPEAR_ROPE_PARTS || !(base > 1.0) || !isfinite(base) || !(factor > 0.0) ||
+        !isfinite(factor) ||
+        (kind == SPEAR_ROPE_PARTS && (!(original > 0.0) || !isfinite(original) || !(low < high) || !isfinite(low) ||
+                                      !isfinite(high))))
+        return SPEAR_E_ARG;
+    const double b = kind == SPEAR_ROPE_BASE ? base * pow(factor, (double)rot / (rot - 2)) : base;
+    for (int i = 0; i < rot / 2; i++) {
+        double f = pow(b, -2.0 * i / rot);
+        if (kind == SPEAR_ROPE_LINEAR)
+            f /= factor;
+        if (kind == SPEAR_ROPE_PARTS) {
+            double g = (original * f / (2.0 * M_PI) - low) / (high - low);
+            g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
+            f = (1.0 - g) * f / factor + g * f;
+        }
+        freqs[i] = f;
+    }
+    return SPEAR_OK;
+}
+
+spear_status spear_rope(const spear_bf16 *x, int64_t x_stride, int64_t T, int32_t H, int32_t D,
+                        const int32_t *positions, const spear_rotation *rope, spear_bf16 *y,
+                        int64_t y_stride, void *stream)
+{
+    if (!rope || (T > 0 && (!x || !positions || !y)))
+        return SPEAR_E_NULL;
+    if (T < 0 || T > SPEAR_MAX_ROWS || H < 1 || H > SPEAR_MAX_HEADS || D < 8 || D > 256 || D % 8 != 0 ||
+        bad_stride(x_stride, (int64_t)H * D) || bad_stride(y_stride, (int64_t)H * D) || (x == y && x_stride != y_stride))
+        return SPEAR_E_SHAPE;
+    spear_status st = check_rotation(rope, D);
+    if (st != SPEAR_OK)
+        return st;
+    if (!al(x, 16) || !al(y, 16) || !al(positions, 4))
+        return SPEAR_E_ALIGN;
+    st = check_device();
+    if (st != SPEAR_OK || T == 0)
+        return st;
+    RopeArgs a = {};
+    a.q = x;
+    a.qs = x_stride;
+    a.y = y;
+    a.ys = y_stride;
+    a.pos = positions;
+    a.freqs = rope->freqs;
+    a.scale = rope->scale;
+    a.rot = rope->rot;
+    a.layout = rope->layout;
+    a.Hq = H;
+    a.D = D;
+    return launch_rope<false>(a, T, (hipStream_t)stream) == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
+}
+
+spear_status spear_rope_kv4_write(const spear_bf16 *q, int64_t q_stride, const spear_bf16 *k,
+                                  int64_t k_stride, const spear_bf16 *v, int64_t v_stride,
+                                  int64_t T, int32_t Hq, const int32_t *positions,
+                                  const int64_t *slots, const spear_rotation *rope,
+                                  const spear_kv4 *kv, spear_bf16 *q_out, int64_t q_out_stride,
+                                  void *stream)
+{
+    if (T > 0 && (!q || !k || !v || !slots || !q_out || (rope && !positions)))
+        return SPEAR_E_NULL;
+    spear_status st = check_kv4(kv);
+    if (st != SPEAR_OK)
+        return st;
+    const int64_t kvr = (int64_t)kv->heads * kv->D;
+    if (T < 0 || T > SPEAR_MAX_ROWS || Hq < 1 || Hq > SPEAR_MAX_HEADS || bad_stride(q_stride, (int64_t)Hq * kv->D) ||
+        bad_stride(q_out_stride, (int64_t)Hq * kv->D) || bad_stride(k_stride, kvr) || bad_stride(v_stride, kvr) ||
+        (q == q_out && q_stride != q_out_stride))
+        return SPEAR_E_SHAPE;
+    if (rope) {
+        st = check_rotation(rope, kv->D);
+        if (st != SPEAR_OK)
+            return st;
+    }
+    if (!al(q, 16) || !al(k, 16) || !al(v, 16) || !al(q_out, 16) || !al(positions, 4) || !al(slots, 8))
+        return SPEAR_E_ALIGN;
+    st = check_device();
+    if (st != SPEAR_OK || T == 0)
+        return st;
+    RopeArgs a = {q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, positions, slots, rope ? rope->freqs : nullptr,
+                  rope ? rope->scale : 1.0, kv->k_codes, kv->k_scales, kv->v_codes, kv->v_scales, kv->pages * kv->P, Hq,
+                  kv->heads, kv->D, rope ? rope->rot : 0, rope ? rope->layout : 0, __builtin_ctz(kv->P)};
+    return launch_rope<true>(a, T, (hipStream_t)stream) == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
+}
+
+spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T, spear_bf16 *k,
+                            spear_bf16 *v, void *stream)
+{
+    if (T > 0 && !slots)
+        return SPEAR_E_NULL;
+    spear_status st = check_kv4(kv);
+    if (st != SPEAR_OK)
+        return st;
+    if (T < 0 || T > SPEAR_MAX_ROWS)
+        return SPEAR_E_SHAPE;
+    if (!al(slots, 8) || !al(k, 16) || !al(v, 16))
+        return SPEAR_E_ALIGN;
+    st = check_device();
+    if (st != SPEAR_OK || T == 0 || (!k && !v))
+        return st;
+    const int64_t n = T * kv->heads * (kv->D / 8), blocks = (n + 255) / 256;
+    hipLaunchKernelGGL(read_kernel, dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), 2), dim3(256), 0,
+                       (hipStream_t)stream, *kv, slots, n, __builtin_ctz(kv->P), k, v);
+    return hipGetLastError() == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
+}
+
+} // extern "C"

@@ -41,6 +41,12 @@ SCORE_SIGMOID = 1
 MAX_EXPERTS = 512
 MAX_TOPK = 32
 MAX_GROUPS = 64
+ROPE_HALF = 0
+ROPE_PAIRS = 1
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_PARTS = 3
 E_NULL = -1
 E_SHAPE = -2
 E_ARG = -4
@@ -49,7 +55,9 @@ EXPORTS = ("spear_pack_w4", "spear_gate", "spear_w4_linear_workspace_size",
            "spear_workspace_init", "spear_w4_linear", "spear_w4_linear_path",
            "spear_w4_linear_noalloc", "spear_w4_linear_semifused", "spear_w4_linear_epilogue",
            "spear_route_workspace_size", "spear_route", "spear_w4_experts_workspace_size",
-           "spear_w4_experts",
+           "spear_w4_experts", "spear_kv4_plan", "spear_rope_frequencies", "spear_rope",
+           "spear_rope_kv4_write", "spear_kv4_read", "spear_kv4_attention_workspace_size",
+           "spear_kv4_attention",
            "spear_set_wait_limit", "spear_workspace_timeouts", "spear_stream_read",
            "spear_slo_predict", "spear_slo_pick_chunk", "spear_status_string",
            "spear_abi_version")
@@ -97,6 +105,24 @@ class _Experts(ctypes.Structure):
                 ("E", ctypes.c_int32), ("act", ctypes.c_int32), ("glu", ctypes.c_int32)]
 
 
+class _KV4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("P", ctypes.c_int32)]
+
+
+class _Step(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("n_left", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("scale", ctypes.c_double), ("rot", ctypes.c_int32),
+                ("layout", ctypes.c_int32)]
+
+
 class _LUT(ctypes.Structure):
     _fields_ = [("npoints", ctypes.c_int32), ("tokens", ctypes.c_void_p),
                 ("nkinds", ctypes.c_int32), ("us", ctypes.c_void_p), ("count", ctypes.c_void_p),
@@ -136,6 +162,16 @@ def load():
     lib.spear_w4_experts_workspace_size.argtypes = [i64, i32, i32, i64, i64]
     lib.spear_w4_experts_workspace_size.restype = ctypes.c_size_t
     lib.spear_w4_experts.argtypes = [P, i64, P, P, P, i32, P, P, P, ctypes.c_size_t, P]
+    f64 = ctypes.c_double
+    lib.spear_kv4_plan.argtypes = [P, P, i32, P, i64, P, i64, P, i64, i32, P, P]
+    lib.spear_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
+    lib.spear_rope.argtypes = [P, i64, i64, i32, i32, P, P, P, i64, P]
+    lib.spear_rope_kv4_write.argtypes = [P, i64, P, i64, P, i64, i64, i32, P, P, P, P, P, i64, P]
+    lib.spear_kv4_read.argtypes = [P, P, i64, P, P, P]
+    lib.spear_kv4_attention_workspace_size.argtypes = [i64, i32, i64, i32, i32, i32, i64, i32]
+    lib.spear_kv4_attention_workspace_size.restype = ctypes.c_size_t
+    lib.spear_kv4_attention.argtypes = [P, i64, i64, i32, P, P, i64, P, P, i32, i64, ctypes.c_float,
+                                        i32, P, P, P, ctypes.c_size_t, P]
     lib.spear_set_wait_limit.argtypes = [ctypes.c_uint32]
     lib.spear_set_wait_limit.restype = None
     lib.spear_workspace_timeouts.argtypes = [P, ctypes.POINTER(i32), P]
@@ -149,7 +185,8 @@ def load():
     for name in ("spear_pack_w4", "spear_gate", "spear_workspace_init", "spear_w4_linear",
                  "spear_w4_linear_path", "spear_w4_linear_noalloc", "spear_w4_linear_semifused",
                  "spear_w4_linear_epilogue", "spear_route", "spear_w4_experts",
-                 "spear_workspace_timeouts",
+                 "spear_kv4_plan", "spear_rope_frequencies", "spear_rope", "spear_rope_kv4_write",
+                 "spear_kv4_read", "spear_kv4_attention", "spear_workspace_timeouts",
                  "spear_stream_read", "spear_slo_predict", "spear_slo_pick_chunk"):
         getattr(lib, name).restype = i32
     _lib = lib
@@ -412,6 +449,7 @@ def _want_layer(fn: str, w: W4, ec: Optional[EC], M: int, device):
 _BF16 = (torch.bfloat16, torch.int16)     # raw bit tensors are taken too
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
 _U8 = (torch.uint8,)
 
 
@@ -645,6 +683,280 @@ def spear_w4_experts(x: torch.Tensor, experts: Experts, ids: torch.Tensor, weigh
         return load().spear_w4_experts(x.data_ptr(), M, experts._s, ids.data_ptr(),
                                        weights.data_ptr(), topk, _at(residual), y.data_ptr(),
                                        workspace.data_ptr(), workspace.numel(), s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
+    return y
+
+
+class KV4:
+    """A cache of keys and values in 4 bits: codes [pages][heads][P][D/2] and scales
+    [pages][heads][D/32][P], uint8, for k and v (the layout is spear.h's).  Made
+    once; the tensors are kept, spear_rope_kv4_write fills them."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        fn = "KV4"
+        if k_codes.dim() != 4:
+            _bad(fn, E_SHAPE, f"k_codes has {k_codes.dim()} dimensions, not 4")
+        pages, heads, P, half = (int(v) for v in k_codes.shape)
+        dev, D = k_codes.device, 2 * half
+        for name, t, shape in (("k_codes", k_codes, (pages, heads, P, half)),
+                               ("v_codes", v_codes, (pages, heads, P, half)),
+                               ("k_scales", k_scales, (pages, heads, D // 32, P)),
+                               ("v_scales", v_scales, (pages, heads, D // 32, P))):
+            _want(fn, name, t, _U8, shape, dev)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.pages, self.heads, self.D, self.P, self.device = pages, heads, D, P, dev
+        self._s = bytes(_KV4(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages,
+                             heads, D, P))
+
+
+def new_kv4(pages: int, heads: int, D: int, P: int, device="cuda") -> KV4:
+    """An empty cache (torch allocation; its contents are undefined)."""
+    def u8(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+    return KV4(u8(pages, heads, P, D // 2), u8(pages, heads, D // 32, P),
+               u8(pages, heads, P, D // 2), u8(pages, heads, D // 32, P))
+
+
+class KV4Plan:
+    """What spear_kv4_plan fills: q_start [B + 1], kv_len [B], positions [T] int32,
+    slots [T] int64, n_left [1], status [2] int32."""
+
+    def __init__(self, q_start, kv_len, positions, slots, n_left, status):
+        fn = "KV4Plan"
+        B, T, dev = kv_len.numel(), positions.numel(), kv_len.device
+        for name, t, dtypes, n in (("q_start", q_start, _I32, B + 1), ("kv_len", kv_len, _I32, B),
+                                   ("positions", positions, _I32, T), ("slots", slots, _I64, T),
+                                   ("n_left", n_left, _I32, 1), ("status", status, _I32, 2)):
+            _want(fn, name, t, dtypes, (n,), dev)
+        self.q_start, self.kv_len, self.positions, self.slots = q_start, kv_len, positions, slots
+        self.n_left, self.status, self.B, self.T, self.device = n_left, status, B, T, dev
+        self._s = bytes(_Step(*(_ptr(t) for t in (q_start, kv_len, positions, slots, n_left, status))))
+
+
+def new_kv4_plan(B: int, T: int, device="cuda") -> KV4Plan:
+    """The tensors of a plan for B requests and T rows (torch allocation)."""
+    def i32(n):
+        return torch.empty(n, dtype=torch.int32, device=device)
+    return KV4Plan(i32(B + 1), i32(B), i32(T), torch.empty(T, dtype=torch.int64, device=device),
+                   i32(1), i32(2))
+
+
+def spear_kv4_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
+                   free_pages: torch.Tensor, n_free: torch.Tensor, T: int, P: int,
+                   plan: Optional[KV4Plan] = None, stream=None) -> KV4Plan:
+    """Block table (updated in place) and slot map of a step whose requests have
+    cached [B] tokens in the cache and bring fresh [B] ones, in T rows."""
+    fn = "spear_kv4_plan"
+    dev, B = cached.device, cached.numel()
+    if table.dim() != 2:
+        _bad(fn, E_SHAPE, f"table has {table.dim()} dimensions, not 2")
+    width = int(table.shape[1])
+    _want(fn, "cached", cached, _I32, (B,), dev)
+    _want(fn, "fresh", fresh, _I32, (B,), dev)
+    _want(fn, "table", table, _I32, (B, width), dev)
+    _want(fn, "free_pages", free_pages, _I32, (free_pages.numel(),), dev)
+    _want(fn, "n_free", n_free, _I32, (1,), dev)
+    if plan is not None and (plan.B != B or plan.T != T):
+        _bad(fn, E_SHAPE, f"the plan is one for {plan.B} requests and {plan.T} rows, not {B} and {T}")
+    if plan is not None and plan.device != dev:
+        _bad(fn, E_ARG, f"the plan is on {plan.device}, not {dev}")
+
+    def call(s):
+        nonlocal plan
+        if plan is None:
+            plan = new_kv4_plan(B, T, dev)
+        return load().spear_kv4_plan(cached.data_ptr(), fresh.data_ptr(), B, table.data_ptr(), width,
+                                     free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), T,
+                                     P, plan._s, s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
+    return plan
+
+
+def spear_rope_frequencies(rot: int, base: float = 10000.0, kind: int = ROPE_PLAIN,
+                           factor: float = 1.0, original: float = 1.0, low: float = 1.0,
+                           high: float = 32.0) -> torch.Tensor:
+    """The rot / 2 frequencies of a rotation, fp64 on the host; kind (ROPE_PLAIN,
+    _LINEAR, _BASE, _PARTS) says how positions are stretched by factor."""
+    f = torch.empty(max(rot // 2, 1), dtype=torch.float64)
+    _check("spear_rope_frequencies",
+           load().spear_rope_frequencies(rot, base, kind, factor, original, low, high, _ptr(f)))
+    return f
+
+
+class Rope:
+    """Rotary positions: freqs [rot/2] fp64 on the device (the angle of one
+    position), layout ROPE_HALF or ROPE_PAIRS, scale the factor of the rotated
+    channels (for frequencies by parts, usually 0.1 ln(factor) + 1)."""
+
+    def __init__(self, freqs: torch.Tensor, layout: int = ROPE_HALF, scale: float = 1.0):
+        _want("Rope", "freqs", freqs, (torch.float64,), (freqs.numel(),), freqs.device)
+        self.freqs, self.layout, self.scale, self.rot = freqs, int(layout), float(scale), 2 * freqs.numel()
+        self._s = bytes(_Rotation(_ptr(freqs), self.scale, self.rot, self.layout))
+
+
+def _want_rows(fn: str, name: str, t, shape, device) -> int:
+    """A [T][H][D] bf16 tensor whose rows may lie apart (a part of a wider row);
+    -> elements from row to row."""
+    if t.dtype not in _BF16:
+        _bad(fn, E_ARG, f"{name} has type {t.dtype}")
+    if t.shape != shape:
+        _bad(fn, E_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.device != device:
+        _bad(fn, E_ARG, f"{name} is on {t.device}, not {device}")
+    T, H, D = shape
+    row, head, channel = t.stride()
+    if (D > 1 and channel != 1) or (H > 1 and head != D):
+        _bad(fn, E_ARG, f"{name} has gaps within a row")
+    return row if T > 1 else H * D
+
+
+def spear_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
+               y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x [T][H][D] bf16 (rows may lie apart) with every head rotated to its row's
+    position; y may be x itself."""
+    fn = "spear_rope"
+    dev = x.device
+    if x.dim() != 3:
+        _bad(fn, E_SHAPE, f"x has {x.dim()} dimensions, not 3")
+    shape = T, H, D = tuple(int(v) for v in x.shape)
+    xs = _want_rows(fn, "x", x, shape, dev)
+    _want(fn, "positions", positions, _I32, (T,), dev)
+    ys = H * D if y is None else _want_rows(fn, "y", y, shape, dev)
+    if rope.freqs.device != dev:
+        _bad(fn, E_ARG, f"the rotation is on {rope.freqs.device}, not {dev}")
+
+    def call(s):
+        nonlocal y
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=dev)
+        return load().spear_rope(x.data_ptr(), xs, T, H, D, positions.data_ptr(), rope._s,
+                                 y.data_ptr(), ys, s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
+    return y
+
+
+def spear_rope_kv4_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         positions: Optional[torch.Tensor], slots: torch.Tensor,
+                         rope: Optional[Rope], kv: KV4, q_out: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """-> q [T][Hq][D] rotated (q_out may be q itself); k, rotated, and v [T][heads][D]
+    go into their slots of the cache.  q, k and v may be parts of one row; rope
+    None rotates nothing."""
+    fn = "spear_rope_kv4_write"
+    dev = q.device
+    if q.dim() != 3:
+        _bad(fn, E_SHAPE, f"q has {q.dim()} dimensions, not 3")
+    T, Hq = int(q.shape[0]), int(q.shape[1])
+    shape, row = (T, Hq, kv.D), (T, kv.heads, kv.D)
+    qs = _want_rows(fn, "q", q, shape, kv.device)
+    ks = _want_rows(fn, "k", k, row, dev)
+    vs = _want_rows(fn, "v", v, row, dev)
+    _want(fn, "slots", slots, _I64, (T,), dev)
+    if rope is not None:
+        if positions is None:
+            _bad(fn, E_NULL, "positions is missing")
+        _want(fn, "positions", positions, _I32, (T,), dev)
+        if rope.freqs.device != dev:
+            _bad(fn, E_ARG, f"the rotation is on {rope.freqs.device}, not {dev}")
+    ys = Hq * kv.D if q_out is None else _want_rows(fn, "q_out", q_out, shape, dev)
+
+    def call(s):
+        nonlocal q_out
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=q.dtype, device=dev)
+        return load().spear_rope_kv4_write(
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq,
+            None if rope is None else positions.data_ptr(), slots.data_ptr(),
+            None if rope is None else rope._s, kv._s, q_out.data_ptr(), ys, s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
+    return q_out
+
+
+def spear_kv4_read(kv: KV4, slots: torch.Tensor, k: Optional[torch.Tensor] = None,
+                   v: Optional[torch.Tensor] = None, stream=None):
+    """-> (k, v) [T][heads][D] bf16: the cache's rows, exact (zeros for a slot
+    outside the cache)."""
+    fn = "spear_kv4_read"
+    dev = kv.device
+    shape = T, _, _ = (slots.numel(), kv.heads, kv.D)
+    _want(fn, "slots", slots, _I64, (T,), dev)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _want(fn, name, t, _BF16, shape, dev)
+
+    def call(s):
+        nonlocal k, v
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+        return load().spear_kv4_read(kv._s, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), s)
+
+    st = _on(fn, dev, stream, call)
+    if st != SPEAR_OK:
+        _check(fn, st)
+    return k, v
+
+
+def spear_kv4_attention_workspace_size(T: int, B: int, max_fresh: int, Hq: int, heads: int, D: int,
+                                       width: int, P: int) -> int:
+    return int(load().spear_kv4_attention_workspace_size(T, B, max_fresh, Hq, heads, D, width, P))
+
+
+def new_kv4_workspace(T: int, B: int, max_fresh: int, Hq: int, kv: KV4, width: int) -> torch.Tensor:
+    """A workspace for spear_kv4_attention over T rows of B requests, none with more
+    than max_fresh of them, and a table of that width (torch allocation)."""
+    n = spear_kv4_attention_workspace_size(T, B, max_fresh, Hq, kv.heads, kv.D, width, kv.P)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=kv.device)
+
+
+def spear_kv4_attention(q: torch.Tensor, kv: KV4, table: torch.Tensor, q_start: torch.Tensor,
+                        kv_len: torch.Tensor, max_fresh: int, scale: Optional[float] = None,
+                        window: int = 0, y: Optional[torch.Tensor] = None,
+                        lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the step's rows q [T][Hq][D] bf16 over the cache -> y [T][Hq][D]
+    bf16; lse [T][Hq] fp32 is filled if given.  scale None: 1 / sqrt(D).  Rows
+    behind the last request are left as they are."""
+    fn = "spear_kv4_attention"
+    dev, B = kv.device, kv_len.numel()
+    if q.dim() != 3:
+        _bad(fn, E_SHAPE, f"q has {q.dim()} dimensions, not 3")
+    if table.dim() != 2:
+        _bad(fn, E_SHAPE, f"table has {table.dim()} dimensions, not 2")
+    T, Hq, width = int(q.shape[0]), int(q.shape[1]), int(table.shape[1])
+    shape = (T, Hq, kv.D)
+    qs = _want_rows(fn, "q", q, shape, dev)
+    _want(fn, "table", table, _I32, (B, width), dev)
+    _want(fn, "q_start", q_start, _I32, (B + 1,), dev)
+    _want(fn, "kv_len", kv_len, _I32, (B,), dev)
+    if y is not None:
+        _want(fn, "y", y, _BF16, shape, dev)
+    if lse is not None:
+        _want(fn, "lse", lse, _F32, (T, Hq), dev)
+    if workspace is not None:
+        _want_workspace(fn, workspace, dev)
+
+    def call(s):
+        nonlocal y, workspace
+        if y is None:
+            y = torch.empty(shape, dtype=q.dtype, device=dev)
+        if workspace is None:
+            workspace = new_kv4_workspace(T, B, max_fresh, Hq, kv, width)
+        return load().spear_kv4_attention(
+            q.data_ptr(), qs, T, Hq, kv._s, table.data_ptr(), width, q_start.data_ptr(),
+            kv_len.data_ptr(), B, max_fresh, kv.D ** -0.5 if scale is None else scale, window,
+            y.data_ptr(), _at(lse), workspace.data_ptr(), workspace.numel(), s)
 
     st = _on(fn, dev, stream, call)
     if st != SPEAR_OK:

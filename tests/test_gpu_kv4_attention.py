@@ -1,0 +1,176 @@
+"""Attention over the cache of 4 bits against plain fp64."""
+import numpy as np
+import pytest
+import torch
+
+import ref_kv4
+from quantized_gemm_w4a16_amd import spear as sp
+from gpu_util import dev
+from kv4_util import Step, bf16, to64
+
+pytestmark = pytest.mark.gpu
+DIMS = [64, 96, 128, 192, 256]
+
+
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("Hq,heads,P", [(1, 1, 16), (8, 8, 64), (8, 2, 128), (5, 1, 32), (16, 1, 1024), (24, 1, 256)])
+def test_one_token(D, Hq, heads, P):
+    kv = [1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 300]
+    Step(kv, [1] * len(kv), Hq, heads, D, P, seed=D + Hq).check(f"one token D={D} {Hq}/{heads} P={P}")
+
+
+@pytest.mark.parametrize("n", [1, 255, 257, 1000, 2500])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_request(n, D):
+    """A long axis cut into chunks for a single request."""
+    Step([n], [1], 4, 1, D, 16, seed=n).check(f"one request of {n} D={D}")
+
+
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("Hq,heads", [(1, 1), (6, 2), (7, 1)])
+def test_few_and_many_tokens(D, Hq, heads):
+    """Requests of one token, of a few and of whole prompts side by side."""
+    fresh = [1, 2, 3, 17, 40, 5, 70, 1]
+    kv = [90, 2, 64, 17, 101, 128, 70, 1]
+    Step(kv, fresh, Hq, heads, D, 32, seed=D + Hq, pad=5).check(f"mixed D={D} {Hq}/{heads}")
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 100, 1 << 30])
+@pytest.mark.parametrize("D", [64, 128])
+def test_windows(window, D):
+    Step([5, 64, 200, 333, 90, 1], [1, 64, 3, 50, 1, 1], 4, 2, D, 16, seed=window % 97, pad=2).check(
+        f"window {window} D={D}", window=window)
+
+
+@pytest.mark.parametrize("fresh", [[1, 1, 1], [0, 5, 40]])
+def test_rows_that_see_nothing(fresh):
+    """No keys at all, fewer keys than rows, requests without rows."""
+    s = Step([0, 3, 20], fresh, 4, 2, 128, 16, seed=3, pad=3)
+    y = s.check("rows without keys")
+    for b, n in enumerate(s.kv):
+        t0, t1 = s.q_start[b], s.q_start[b + 1]
+        blind = t0 + max(0, (t1 - t0) - n)
+        assert bool((y[t0:blind] == 0).all())
+
+
+def test_no_rows_no_requests():
+    s = Step([5, 9], [0, 0], 2, 2, 64, 16, pad=4)
+    s.check("no rows")
+    kv = s.kv4
+    e = lambda *n: torch.empty(*n, dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert sp.spear_kv4_attention(q, kv, s.dtable, torch.zeros(3, dtype=torch.int32, device="cuda"), s.dkv, 1).shape == (0, 2, 64)
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(q, 7.0)
+    sp.spear_kv4_attention(q, kv, e(0, 4), torch.zeros(1, dtype=torch.int32, device="cuda"), e(0), 1, y=y)
+    assert bool((y == 7.0).all())
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_masked_places_may_hold_anything(window):
+    """NaN in keys and values that some rows see and others do not: only the
+    rows that see them are NaN; pages that were let go are as if masked."""
+    for seed, D in enumerate(DIMS):
+        s = Step([70, 130, 200, 33], [20, 1, 60, 2], 4, 2, D, 16, seed=seed, pad=2)
+        c = s.cache
+        def spoil(b, key, name, head, block):
+            c.scales[name][s.table[b, key // 16], head, block, key % 16] = 255
+        spoil(0, 60, "v", 0, 0)                          # seen by the last ten rows of the request
+        spoil(0, 55, "v", 1, D // 32 - 1)
+        spoil(0, 66, "k", 1, 1)
+        spoil(2, 150, "v", 0, 1)
+        spoil(2, 171, "k", 0, 0)
+        s.table[1, 2] = -1
+        s.table[2, 4] = c.pages
+        s.table[2, 5] = 2 ** 31 - 1
+        s.table[3, 0] = -2 ** 31
+        s.to_device()
+        s.check(f"masked places D={D} window={window}", window=window)
+
+
+def test_every_page_let_go():
+    s = Step([40, 70], [1, 30], 2, 1, 64, 16, seed=1)
+    s.table[:] = -1
+    s.to_device()
+    y = s.check("no pages")
+    assert bool((y == 0).all())
+
+
+def test_lengths_beyond_the_table_are_held():
+    """kv_len past the table's room and q_start past the rows read nothing outside."""
+    s = Step([48, 20], [1, 2], 2, 1, 64, 16, seed=2)
+    want = s.run()
+    s.dkv = dev(np.array([1 << 30, 20], np.int32))
+    s.dstart = dev(np.array([0, 1, 3], np.int32))
+    got = s.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1:], want[1:])
+    s.dstart = dev(np.array([-4, 1, 1 << 20], np.int32))
+    s.dkv = dev(np.array([-3, 20], np.int32))
+    got = s.run()
+    assert torch.equal(got[1:], want[1:]) and bool((got[0] == 0).all())
+
+
+@pytest.mark.parametrize("q_sd,scale", [(40.0, None), (1e-3, None), (1.0, 3.0), (1.0, 1e-20), (1e18, 1e-18)])
+def test_sharp_and_flat_rows(q_sd, scale):
+    Step([200, 90], [1, 33], 4, 2, 128, 32, seed=9, q_sd=q_sd).check(f"q of {q_sd}, scale {scale}", scale=scale)
+
+
+def test_infinite_queries_stay_in_their_rows():
+    s = Step([50, 40], [1, 30], 2, 1, 64, 16, seed=4)
+    want = s.run()
+    s.q[3, 1, 7], s.q[9, 0, 0] = float("inf"), float("nan")
+    got = s.run()
+    spoilt = torch.zeros(s.T, 2, dtype=torch.bool, device="cuda")
+    spoilt[3, 1] = spoilt[9, 0] = True
+    assert bool(got[spoilt].isnan().all()) and torch.equal(got[~spoilt], want[~spoilt])
+
+
+def test_strided_queries_in_place_and_without_lse():
+    s = Step([50, 40, 200], [1, 30, 2], 6, 2, 128, 16, seed=6)
+    want = s.check("whole rows")
+    wide = torch.full((s.T, 10, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:8] = s.q
+    assert torch.equal(s.run(q=wide[:, 2:8]), want)
+    assert torch.equal(s.run(lse=False), want)
+    q = s.q.clone()
+    assert s.run(q=q, y=q) is q and torch.equal(q, want)
+
+
+@pytest.mark.parametrize("most", [0, 1, 3, 30, 1 << 40])
+def test_max_fresh_is_only_a_hint(most):
+    s = Step([50, 40, 200, 64], [1, 30, 2, 7], 6, 2, 128, 16, seed=7)
+    s.check(f"max_fresh {most}", max_fresh=most)
+
+
+@pytest.mark.parametrize("B", [64, 65, 300])
+def test_many_requests(B):
+    rng = np.random.default_rng(B)
+    kv = rng.integers(1, 40, B).tolist()
+    Step(kv, [min(n, int(f)) for n, f in zip(kv, rng.integers(0, 3, B))], 2, 1, 64, 16, seed=B, pad=1).check(f"{B} requests")
+
+
+def test_behind_4_gib():
+    """Codes beyond 2^32 bytes of the cache, scales beyond 2^28."""
+    P, heads, D = 1024, 8, 256
+    pages = (1 << 32) // (heads * P * D // 2) + 2
+    kv = sp.new_kv4(pages, heads, D, P)
+    rng = np.random.default_rng(8)
+    n = 100
+    x, x64 = bf16(rng.normal(0, 1, (n, heads, D)))
+    q, q64 = bf16(rng.normal(0, 1, (1, heads, D)))
+    table = np.array([[pages - 1]], np.int32)
+    slots = (pages - 1) * P + np.arange(n)
+    sp.spear_rope_kv4_write(x, x, x, None, dev(slots), None, kv)
+    small = ref_kv4.Cache(1, heads, D, P, rng)
+    for name in "kv":
+        small.write(name, np.arange(n), x64)
+    y = sp.spear_kv4_attention(q, kv, dev(table), dev(np.array([0, 1], np.int32)), dev(np.array([n], np.int32)), 1)
+    want, err, _, _ = ref_kv4.attention(q64, small, np.zeros((1, 1), np.int32), [0, 1], [n], D ** -0.5)
+    assert (np.abs(to64(y) - want) <= err + ref_kv4.HALF_BF16 * (np.abs(want) + err)).all()
+
+
+def test_repeats_bit_for_bit():
+    s = Step([900, 40, 333], [1, 30, 2], 8, 2, 128, 16, seed=11)
+    want, lse = s.run(), s.lse
+    for _ in range(3):
+        assert torch.equal(s.run(), want) and torch.equal(s.lse, lse)
