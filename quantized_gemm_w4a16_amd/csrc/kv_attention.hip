@@ -19,6 +19,8 @@ constexpr int FEW_ROWS = 16;        // rows of a tile of the kernel for few rows
 constexpr int FEW_WAVES = 4;        // its waves, which take the steps of a chunk in turn
 constexpr int FEW_LEAST = 4;        // steps of a chunk, at least
 constexpr int FEW_ITEMS = 1024;     // items of all key heads that the cut aims at
+constexpr int MANY_LEAST = 4;       // steps of its chunks, at least
+constexpr int MANY_ITEMS = 512;     // items of all key heads that its cut aims at
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 
@@ -29,12 +31,18 @@ struct AttnArgs {
     const int32_t *table, *q_start, *kv_len;
     uint16_t *y;
     float *lse;
-    float *part_o, *part_ml;        // [item][key head][row][D], [item][key head][row][2]
     int64_t T, pages, width;
     int32_t B, heads, G, log_p, window;
-    int32_t target;                 // items of a key head that the cut aims at; 0: no cut
-    int32_t most;                   // items of a key head that there is room for
     float scale;                    // times log2 e
+};
+
+// The requests that a kernel takes and how their keys are cut.
+struct Cut {
+    float *part_o, *part_ml;        // [item][key head][row][D], [item][key head][row][2]
+    int32_t rows0, rows1;           // requests of rows0 < rows <= rows1
+    int32_t target;                 // items of a key head that the cut aims at; 0: no cut
+    int32_t least;                  // steps of a chunk, at least
+    int32_t most;                   // items of a key head that there is room for
 };
 
 // ------------------------------------------------------------------- items
@@ -44,7 +52,7 @@ struct Request {
     int32_t tiles, base, steps;     // row tiles; the first step that a row sees; steps from there
 };
 
-__device__ __forceinline__ Request request_of(const AttnArgs &a, int b, int tile_rows)
+__device__ __forceinline__ Request request_of(const AttnArgs &a, const Cut &c, int b, int tile_rows)
 {
     Request r;
     const int64_t T = a.T;
@@ -57,7 +65,8 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int b, int tile
     r.row0 = q0;
     r.fresh = (int32_t)(q1 - q0);
     r.kv = (int32_t)kv;
-    r.tiles = (int32_t)(((int64_t)r.fresh * a.G + tile_rows - 1) / tile_rows);
+    const int64_t rows = (int64_t)r.fresh * a.G;
+    r.tiles = rows > c.rows0 && rows <= c.rows1 ? (int32_t)((rows + tile_rows - 1) / tile_rows) : 0;
     // the first fresh token stands at kv - fresh
     int32_t lo = a.window ? r.kv - r.fresh - a.window + 1 : 0;
     lo = lo < 0 ? 0 : lo;
@@ -78,29 +87,29 @@ struct Item {
 __device__ __forceinline__ int32_t bcast(int32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // The item (or, by_tile, the tile) number `want`.  Every wave forms the sums over
-// all requests, 64 at a time.  A chunk has as many steps as make about a.target
-// items of a key head; sums are capped at a.most, behind which there is no item.
+// all requests, 64 at a time.  A chunk has as many steps as make about c.target
+// items of a key head; sums are capped at c.most, behind which there is no item.
 template <int ROWS>
-__device__ Item find_item(const AttnArgs &a, int32_t want, bool by_tile)
+__device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by_tile)
 {
     const int lane = threadIdx.x & 63;
     Item it;
     it.found = false;
     it.size = 0x7FFFFFFF;
-    if (a.target) {
+    if (c.target) {
         float work = 0.f;
         for (int b0 = 0; b0 < a.B; b0 += 64) {
             const int b = b0 + lane;
             if (b < a.B) {
-                const Request r = request_of(a, b, ROWS);
+                const Request r = request_of(a, c, b, ROWS);
                 work += (float)r.tiles * (float)r.steps;
             }
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2)
             work += __shfl_xor(work, d);
-        const float s = ceilf(work / (float)a.target);
-        it.size = s < (float)FEW_LEAST ? FEW_LEAST : (s > 1e9f ? 1000000000 : (int32_t)s);
+        const float s = ceilf(work / (float)c.target);
+        it.size = s < (float)c.least ? c.least : (s > 1e9f ? 1000000000 : (int32_t)s);
     }
     int32_t items0 = 0, tiles0 = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -108,11 +117,11 @@ __device__ Item find_item(const AttnArgs &a, int32_t want, bool by_tile)
         int32_t chunks = 0, n = 0, tiles = 0;
         Request r = {};
         if (b < a.B) {
-            r = request_of(a, b, ROWS);
+            r = request_of(a, c, b, ROWS);
             chunks = r.steps <= it.size ? 1 : (r.steps + it.size - 1) / it.size;
-            tiles = r.tiles < a.most ? r.tiles : a.most;
+            tiles = r.tiles < c.most ? r.tiles : c.most;
             const int64_t all = (int64_t)r.tiles * chunks;
-            n = all < a.most ? (int32_t)all : a.most;
+            n = all < c.most ? (int32_t)all : c.most;
         }
         // inclusive sums, held below 2^31 by the cap (64 * most < 2^31)
         int32_t ni = n, ti = tiles;
@@ -143,8 +152,8 @@ __device__ Item find_item(const AttnArgs &a, int32_t want, bool by_tile)
         }
         items0 += bcast(ni, 63);
         tiles0 += bcast(ti, 63);
-        items0 = items0 < a.most ? items0 : a.most;
-        tiles0 = tiles0 < a.most ? tiles0 : a.most;
+        items0 = items0 < c.most ? items0 : c.most;
+        tiles0 = tiles0 < c.most ? tiles0 : c.most;
     }
     return it;
 }
@@ -235,9 +244,11 @@ __device__ __forceinline__ uint2 read_turned(const void *p)
     return __builtin_bit_cast(uint2, v);
 }
 
+// Two fp32 to a pair of bf16 in one instruction.
 __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi)
 {
-    return (uint32_t)f2bf(lo) | ((uint32_t)f2bf(hi) << 16);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // LDS written by this wave is read back by its other lanes: the order of the
@@ -248,6 +259,18 @@ __device__ __forceinline__ void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
+// Four channels from c on of a request's row, and with c == 0 its lse.
+template <int D>
+__device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int head, int row, int c, f32x4 sum, float m, float l)
+{
+    const int64_t hrow = (it.r.row0 + row / a.G) * ((int64_t)a.heads * a.G) + head * a.G + row % a.G;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(a.y + hrow * D + c) =
+        make_uint2(pair_bf16(sum[0] * inv, sum[1] * inv), pair_bf16(sum[2] * inv, sum[3] * inv));
+    if (c == 0 && a.lse)
+        a.lse[hrow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * LN2;
+}
+
 // Matrix instructions, with g the group of a lane and n its place in the group:
 //   S^T [key][row] = K Q^T  lane: row n, keys 16 g + 4 r + i in acc[i][r]
 //   O^T [channel][row] += V^T P^T  lane: row n, channels 16 dt + 4 g + r in o[dt][r]
@@ -256,7 +279,7 @@ __device__ __forceinline__ void wave_order()
 // (g, j) stand for the keys 16 g + 4 (j % 4) + 2 u + j / 4.  V goes through LDS,
 // as bf16, to be read column by column.
 template <int D>
-__global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs a)
+__global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs a, const Cut cut)
 {
     using L = Lay<D>;
     constexpr int DT = D / 16, NS = L::NC * L::W;
@@ -266,7 +289,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs
     __shared__ float s_ml[FEW_WAVES][FEW_ROWS][2];
 
     const int head = blockIdx.x % a.heads;
-    const Item it = find_item<FEW_ROWS>(a, (int32_t)(blockIdx.x / a.heads), false);
+    const Item it = find_item<FEW_ROWS>(a, cut, (int32_t)(blockIdx.x / a.heads), false);
     if (!it.found)
         return;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
@@ -512,64 +535,370 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs
         }
         if (it.chunks > 1) {
             const int64_t p = ((int64_t)(it.item + it.chunk) * a.heads + head) * FEW_ROWS + r;
-            *reinterpret_cast<f32x4 *>(a.part_o + p * D + c) = sum;
+            *reinterpret_cast<f32x4 *>(cut.part_o + p * D + c) = sum;
             if (c == 0) {
-                a.part_ml[2 * p] = mm;
-                a.part_ml[2 * p + 1] = ll;
+                cut.part_ml[2 * p] = mm;
+                cut.part_ml[2 * p + 1] = ll;
             }
-        } else {
-            const int rr = it.tile * FEW_ROWS + r;
-            const int64_t hrow = (it.r.row0 + rr / G) * ((int64_t)a.heads * G) + head * G + rr % G;
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            *reinterpret_cast<uint2 *>(a.y + hrow * D + c) =
-                make_uint2(pair_bf16(sum[0] * inv, sum[1] * inv), pair_bf16(sum[2] * inv, sum[3] * inv));
-            if (c == 0 && a.lse)
-                a.lse[hrow] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * LN2;
+        } else
+            store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
+    }
+}
+
+// -------------------------------------------------------------- many rows
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float max_over_halves(float v)
+{
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+
+// A workgroup's W waves take 32 rows each and share the keys: a step's K and V go
+// to LDS as bf16 once, two steps in turn, while the codes of the one after are on
+// their way.  With h the half of a lane (lane / 32) and n its place in it:
+//   S^T [key][row] = K Q^T          lane: row n, keys 8 (r / 4) + 4 h + r % 4 in s[r]
+//   O^T [channel][row] += V^T P^T   lane: row n, channels 8 (r / 4) + 4 h + r % 4
+// so that P stays where S was, as in the kernel for few rows.  P is one bf16
+// here (2^-9 of its size on average, less than y's own rounding): a second term
+// would make half as many matrix instructions more.
+template <int D, int W>
+struct Tiles {
+    static constexpr int NB = D / 32, KROW = 2 * D + 16, VROW = D == 96 ? 2 * D : 2 * D + 64;
+    static constexpr int UNITS = STEP * NB, U = (UNITS + 64 * W - 1) / (64 * W);
+    static constexpr int BUF = STEP * (KROW + VROW);
+};
+
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : (D > 128 ? 1 : 2)) void many_rows_kernel(const AttnArgs a, const Cut cut)
+{
+    using L = Tiles<D, W>;
+    constexpr int DT = D / 32, KS = D / 16, ROWS = 32 * W;
+    extern __shared__ __attribute__((aligned(16))) uint8_t s_kv[];         // two buffers of K rows, then V rows
+    __shared__ int32_t s_flag[2][2];       // step + 1 whose keys have a lost page; ... a block of NaN in V
+
+    const int head = blockIdx.x % a.heads;
+    const Item it = find_item<ROWS>(a, cut, (int32_t)(blockIdx.x / a.heads), false);
+    if (!it.found)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, n = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = a.G, log_p = a.log_p;
+    const int page_mask = (1 << log_p) - 1;
+    const int pos0 = it.r.kv - it.r.fresh, rows = it.r.fresh * G;
+    const int32_t *table = a.table + (int64_t)it.b * a.width;
+
+    // what the rows from r0 up to r1 see together: [s0, s1), and each of them: [e0, e1]
+    auto range = [&](int r0, int r1, int &s0, int &s1, int &e0, int &e1) {
+        r1 = r1 < rows ? r1 : rows;
+        const int t0 = r0 / G, t1 = (r1 - 1) / G;
+        s0 = a.window && pos0 + t0 - a.window + 1 > 0 ? pos0 + t0 - a.window + 1 : 0;
+        s1 = r0 < r1 ? pos0 + t1 + 1 : 0;
+        e0 = a.window && pos0 + t1 - a.window + 1 > 0 ? pos0 + t1 - a.window + 1 : 0;
+        e1 = pos0 + t0;
+    };
+    int seen0, seen1, x0, x1, mine0, mine1, all0, all1;
+    range(it.tile * ROWS, it.tile * ROWS + ROWS, seen0, seen1, x0, x1);
+    const int row0 = it.tile * ROWS + 32 * wave, row = row0 + n;
+    range(row0, row0 + 32, mine0, mine1, all0, all1);
+
+    int lo = it.r.base + it.chunk * (it.chunks > 1 ? it.size : 0), hi = it.r.base + it.r.steps;
+    if (it.chunks > 1 && lo + it.size < hi)
+        hi = lo + it.size;
+    lo = lo > seen0 / STEP ? lo : seen0 / STEP;
+    const int hi_seen = seen1 > 0 ? (seen1 + STEP - 1) / STEP : 0;
+    hi = hi < hi_seen ? hi : hi_seen;
+
+    u32x4 qf[KS];
+    const int tok = row / G;
+    const int last = row < rows ? pos0 + tok : -1;
+    const int first = a.window && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
+    {
+        const uint16_t *qp = a.q + (it.r.row0 + tok) * a.qs + (int64_t)(head * G + row - tok * G) * D + 8 * h;
+#pragma unroll
+        for (int s = 0; s < KS; s++)
+            qf[s] = row < rows ? ld16(qp + 16 * s) : zero4();
+    }
+    f32x16 o[DT];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int r = 0; r < 16; r++)
+            o[d][r] = 0.f;
+
+    // ---- a step's codes: unit u is a block of 32 channels of a key, of K and of V
+    u32x4 kc[L::U], vc[L::U];
+    uint32_t kb[L::U], vb[L::U], page[L::U];
+    bool gone[L::U];
+    const uint32_t code_page = (uint32_t)a.heads * (D / 2) << log_p, scale_page = (uint32_t)a.heads * L::NB << log_p;
+    const uint32_t last_page = (uint32_t)a.pages - 1;
+    auto unit = [&](int i) { return i * 64 * W + tid; };
+    auto find_pages = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < L::U; i++) {
+            const int key = step * STEP + unit(i) / L::NB;
+            page[i] = step < hi && key < it.r.kv ? (uint32_t)table[key >> log_p] : 0u;
+        }
+    };
+    auto load = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < L::U; i++) {
+            const int blk = unit(i) % L::NB;
+            const uint32_t off = (uint32_t)(step * STEP + unit(i) / L::NB) & page_mask;
+            if (L::UNITS % (64 * W) == 0 || unit(i) < L::UNITS) {
+                gone[i] = page[i] > last_page;
+                const uint32_t p = gone[i] ? 0u : page[i];
+                const uint64_t at = (uint64_t)p * code_page + ((((uint32_t)head << log_p) + off) * (D / 2) + 16 * blk);
+                const uint64_t sat = (uint64_t)p * scale_page + ((((uint32_t)head * L::NB + blk) << log_p) + off);
+                kc[i] = ld16(a.k_codes + at);
+                vc[i] = ld16(a.v_codes + at);
+                kb[i] = a.k_scales[sat];
+                vb[i] = a.v_scales[sat];
+            }
+        }
+    };
+    auto store = [&](int step, int buf) {
+#pragma unroll
+        for (int i = 0; i < L::U; i++) {
+            const int key = unit(i) / L::NB, blk = unit(i) % L::NB;
+            if (L::UNITS % (64 * W) == 0 || unit(i) < L::UNITS) {
+                // keys that no row of the tile sees hold anything: their V is zero.  A
+                // block of NaN in V is put in by hand, for the rows that see it
+                const int at = step * STEP + key;
+                const bool seen = at >= seen0 && at < seen1 && !gone[i];
+                if (gone[i])
+                    s_flag[buf][0] = step + 1;
+                if (seen && vb[i] == 255u)
+                    s_flag[buf][1] = step + 1;
+                const bool clear = !seen || vb[i] == 255u;
+                const float ks = kv4_scale(kb[i]), vs = kv4_scale(clear ? 127u : vb[i]);
+                uint8_t *kp = s_kv + buf * L::BUF + key * L::KROW + 64 * blk;
+                uint8_t *vp = s_kv + buf * L::BUF + STEP * L::KROW + key * L::VROW + 64 * blk;
+#pragma unroll
+                for (int w = 0; w < 4; w++)
+                    *reinterpret_cast<u32x4 *>(kp + 16 * w) = kv4_bf16(kc[i][w], ks);
+                // rows of V that start in the same banks take their words in another order
+                const int turn = key & 1;
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const uint32_t c = turn ? vc[i][w ^ 1] : vc[i][w];
+                    *reinterpret_cast<u32x4 *>(vp + ((16 * w) ^ (16 * turn))) = kv4_bf16(clear ? 0u : c, vs);
+                }
+            }
+        }
+    };
+
+    if (tid < 4)
+        s_flag[tid >> 1][tid & 1] = 0;
+    if (lo < hi) {
+        find_pages(lo);
+        load(lo);
+        find_pages(lo + 1);
+        __syncthreads();
+        store(lo, 0);
+        load(lo + 1);
+        find_pages(lo + 2);
+    }
+    __syncthreads();
+
+    for (int step = lo; step < hi; step++) {
+        const int buf = (step - lo) & 1, key0 = step * STEP;
+        if (step + 1 < hi) {
+            store(step + 1, buf ^ 1);
+            load(step + 2);
+            find_pages(step + 3);
+        }
+        if (key0 < mine1 && key0 + STEP > mine0) {
+            const uint8_t *sk = s_kv + buf * L::BUF, *sv = sk + STEP * L::KROW;
+            uint64_t lost = 0;
+            if (__builtin_amdgcn_readfirstlane(s_flag[buf][0]) == step + 1) {
+                const int key = key0 + lane;
+                lost = __ballot(key < it.r.kv && (uint32_t)table[key >> log_p] > last_page);
+            }
+            f32x16 s[2];
+#pragma unroll
+            for (int kt = 0; kt < 2; kt++) {
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    s[kt][r] = 0.f;
+#pragma unroll
+                for (int c = 0; c < KS; c++)
+                    s[kt] = mfma32(ld16(sk + (32 * kt + n) * L::KROW + 32 * c + 16 * h), qf[c], s[kt]);
+            }
+            if (key0 < all0 || key0 + STEP - 1 > all1 || lost != 0) {
+                const int f = first - key0 - 4 * h, e = last - key0 - 4 * h;
+                const uint64_t gone4 = lost >> (4 * h);
+#pragma unroll
+                for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+                    for (int r = 0; r < 16; r++) {
+                        const int k = 32 * kt + 8 * (r / 4) + r % 4;
+                        s[kt][r] = k >= f && k <= e && !(gone4 >> k & 1) ? s[kt][r] : -INFINITY;
+                    }
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int r = 1; r < 32; r++)
+                top = fmaxf(top, s[r / 16][r % 16]);
+            top = max_over_halves(top) * a.scale;
+            if (__any(top > m)) {
+                const float x = fmaxf(m, top);
+                const float f = m == x ? 1.f : __builtin_amdgcn_exp2f(m - x);
+                m = x;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DT; d++)
+                    o[d] *= f;
+            }
+            const float m0 = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+            for (int kt = 0; kt < 2; kt++) {
+                u32x4 p[2];
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    s[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale, m0));
+                    l += s[kt][r];
+                }
+#pragma unroll
+                for (int r = 0; r < 8; r++)
+                    p[r / 4][r % 4] = pair_bf16(s[kt][2 * r], s[kt][2 * r + 1]);
+#pragma unroll
+                for (int u = 0; u < 2; u++)
+#pragma unroll
+                    for (int d = 0; d < DT; d++) {
+                        const uint8_t *at = sv + (32 * kt + 16 * u + 4 * h + ((lane & 15) >> 2)) * L::VROW + 64 * d +
+                                            32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+                        const uint2 x = read_turned(at), z = read_turned(at + 8 * L::VROW);
+                        o[d] = mfma32(u32x4{x.x, x.y, z.x, z.y}, p[u], o[d]);
+                    }
+            }
+            if (__builtin_amdgcn_readfirstlane(s_flag[buf][1]) == step + 1) {
+                // blocks of NaN in V, for the rows that see their keys
+                const int key = key0 + lane;
+                const uint32_t p = key < it.r.kv ? (uint32_t)table[key >> log_p] : 0xFFFFFFFFu;
+#pragma unroll
+                for (int blk = 0; blk < L::NB; blk++) {
+                    const uint64_t sat = (uint64_t)(p > last_page ? 0u : p) * scale_page +
+                                         ((((uint32_t)head * L::NB + blk) << log_p) + (key & page_mask));
+                    uint64_t who = __ballot(p <= last_page && a.v_scales[sat] == 255);
+                    while (who) {
+                        const int k = key0 + __builtin_ctzll(who);
+                        who &= who - 1;
+                        o[blk] += k >= first && k <= last ? __builtin_nanf("") : 0.f;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    if (row >= rows)
+        return;
+    const int64_t p = ((int64_t)(it.item + it.chunk) * a.heads + head) * ROWS + (row - it.tile * ROWS);
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const f32x4 v = {o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
+            const int c = 32 * d + 8 * r + 4 * h;
+            if (it.chunks > 1)
+                *reinterpret_cast<f32x4 *>(cut.part_o + p * D + c) = v;
+            else
+                store_out<D>(a, it, head, row, c, v, m, l);
+        }
+    if (it.chunks > 1 && h == 0) {
+        cut.part_ml[2 * p] = m;
+        cut.part_ml[2 * p + 1] = l;
+    }
+}
+
+// The chunks of a tile joined, in their order.  A workgroup takes JOIN rows of a
+// tile of a key head; a row's chunks are spread over the threads that share its
+// channels.
+constexpr int JOIN = 4;
+
+template <int D, int ROWS>
+__device__ void join_rows(const AttnArgs &a, const Cut &cut, int tile, int head, int part)
+{
+    constexpr int Q = D / 4, S = 256 / Q;                 // threads of a row's channels; sharers
+    __shared__ f32x4 s_o[S][Q];
+    __shared__ float s_w[256];
+    __shared__ float s_m[4], s_l[4];
+    const Item it = find_item<ROWS>(a, cut, tile, true);
+    if (!it.found || it.chunks < 2)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = tid % Q, sh = tid / Q;
+    const int rows = it.r.fresh * a.G - it.tile * ROWS;
+    const int64_t next = (int64_t)a.heads * ROWS;
+    for (int r = part * JOIN; r < part * JOIN + JOIN && r < ROWS && r < rows; r++) {
+        const int64_t p0 = ((int64_t)it.item * a.heads + head) * ROWS + r;
+        float mm = -INFINITY;
+        for (int i = tid; i < it.chunks; i += 256)
+            mm = fmaxf(mm, cut.part_ml[2 * (p0 + i * next)]);
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2)
+            mm = fmaxf(mm, __shfl_xor(mm, d));
+        __syncthreads();                                  // the row before has been read
+        if (lane == 0)
+            s_m[wave] = mm;
+        __syncthreads();
+        mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int i0 = 0; i0 < it.chunks; i0 += 256) {
+            const int nn = it.chunks - i0 < 256 ? it.chunks - i0 : 256;
+            if (i0)
+                __syncthreads();
+            float w = 0.f;
+            if (tid < nn) {
+                const int64_t p = p0 + (i0 + tid) * next;
+                w = __builtin_amdgcn_exp2f(cut.part_ml[2 * p] - ref);
+                ll += w * cut.part_ml[2 * p + 1];
+            }
+            s_w[tid] = w;
+            __syncthreads();
+            if (sh < S) {
+#pragma unroll 4
+                for (int i = sh; i < nn; i += S)
+                    sum += s_w[i] * *reinterpret_cast<const f32x4 *>(cut.part_o + (p0 + (i0 + i) * next) * D + 4 * q);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2)
+            ll += __shfl_xor(ll, d);
+        if (lane == 0)
+            s_l[wave] = ll;
+        if (sh < S)
+            s_o[sh][q] = sum;
+        __syncthreads();
+        if (tid < Q) {
+            for (int i = 1; i < S; i++)
+                sum += s_o[i][q];
+            store_out<D>(a, it, head, it.tile * ROWS + r, 4 * q, sum, mm, s_l[0] + s_l[1] + s_l[2] + s_l[3]);
         }
     }
 }
 
-// The chunks of a tile joined, in their order; a workgroup takes a tile of a key head.
 template <int D, int ROWS>
-__global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a)
+__global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, const Cut cut)
 {
-    const int head = blockIdx.x % a.heads;
-    const Item it = find_item<ROWS>(a, (int32_t)(blockIdx.x / a.heads), true);
-    if (!it.found || it.chunks < 2)
-        return;
-    const int G = a.G, rows = it.r.fresh * G - it.tile * ROWS;
-    const int64_t p0 = ((int64_t)it.item * a.heads + head) * ROWS, next = (int64_t)a.heads * ROWS;
-    for (int x = threadIdx.x; x < ROWS * (D / 4); x += 256) {
-        const int r = x / (D / 4), c = 4 * (x % (D / 4));
-        if (r >= rows)
-            break;
-        float mm = -INFINITY;
-        for (int i = 0; i < it.chunks; i++)
-            mm = fmaxf(mm, a.part_ml[2 * (p0 + i * next + r)]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < it.chunks; i++) {
-            const int64_t p = p0 + i * next + r;
-            const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ref);
-            ll += f * a.part_ml[2 * p + 1];
-            sum += f * *reinterpret_cast<const f32x4 *>(a.part_o + p * D + c);
-        }
-        const int rr = it.tile * ROWS + r;
-        const int64_t hrow = (it.r.row0 + rr / G) * ((int64_t)a.heads * G) + head * G + rr % G;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        *reinterpret_cast<uint2 *>(a.y + hrow * D + c) =
-            make_uint2(pair_bf16(sum[0] * inv, sum[1] * inv), pair_bf16(sum[2] * inv, sum[3] * inv));
-        if (c == 0 && a.lse)
-            a.lse[hrow] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * LN2;
-    }
+    join_rows<D, ROWS>(a, cut, (int)(blockIdx.x / a.heads), blockIdx.x % a.heads, blockIdx.y);
 }
 
 // ------------------------------------------------------------------- host
 struct AttnLayout {
-    int64_t tiles, items;           // of a key head, at most
-    int32_t target;                 // 0: no cut
-    size_t part_o, part_ml, total;
+    int64_t tiles[2], items[2];     // of a key head, at most: kernel for few rows, for many
+    int32_t target[2];              // 0: no cut; -1: no launch
+    int32_t limit;                  // rows of a request up to which the kernel for few takes it
+    int32_t wide;                   // eight waves a workgroup
+    size_t part_o[2], part_ml[2], total;
 };
 
 bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
@@ -582,39 +911,86 @@ bool attention_sizes(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_
            width >= 1 && width <= SPEAR_MAX_CONTEXT / P && T * Hq <= (int64_t)1 << 27;
 }
 
+constexpr int FEW_LIMIT = 32;       // rows of a request up to which the kernel for few takes it
+
 AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_t heads, int32_t D)
 {
     AttnLayout L;
-    const int64_t G = Hq / heads, rows = T * G;
-    // tiles of a key head: at most one more a request than its rows fill, and no
-    // fewer than all rows fill and requests of max_fresh rows make
-    const int64_t more = T < B ? T : B;
-    L.tiles = rows / FEW_ROWS + more;
-    int64_t least = (rows + FEW_ROWS - 1) / FEW_ROWS;
-    const int64_t each = max_fresh > 0 ? (T + max_fresh - 1) / max_fresh : 0;
-    least = least > each ? least : each;
-    const int64_t cut = (FEW_ITEMS + heads - 1) / heads;
-    L.target = least * heads >= FEW_ITEMS ? 0 : (int32_t)cut;
-    L.items = L.tiles + (L.target ? cut + 16 : 0);
-    // The room of the parts does not depend on max_fresh and grows with T and B, so
-    // that a workspace of the largest step serves every other: with a cut, least is
-    // below cut and L.tiles below cut + more.
-    const int64_t room = (L.tiles < cut + more ? L.tiles : cut + more) + cut + 16;
-    L.part_o = 0;
-    L.part_ml = (size_t)(room * heads * FEW_ROWS * D) * sizeof(float);
-    L.total = L.part_ml + (size_t)(room * heads * FEW_ROWS * 2) * sizeof(float);
+    const int64_t G = Hq / heads, rows = T * G, more = T < B ? T : B;
+    // Requests of more rows than the limit take the other kernel, if there may be any.
+    const bool both = T > 0 && max_fresh * G > FEW_LIMIT;
+    L.limit = both ? FEW_LIMIT : 0x7FFFFFFF;
+    L.wide = D <= 192 && rows * heads >= (int64_t)256 * 512;
+    const int many = 32 * (L.wide ? 8 : 4);
+    size_t off = 0;
+    for (int k = 0; k < 2; k++) {
+        const int tile = k ? many : FEW_ROWS, goal = k ? MANY_ITEMS : FEW_ITEMS;
+        const int64_t cut = (goal + heads - 1) / heads;
+        // tiles of a key head: at most one more a request than its rows fill (few
+        // rows: at most what a request may have), and no fewer than all rows fill
+        // and requests of max_fresh rows make
+        int64_t tiles = rows / tile + more, least = (rows + tile - 1) / tile;
+        const int64_t each = max_fresh > 0 ? (T + max_fresh - 1) / max_fresh : 0;
+        least = least > each ? least : each;
+        if (!k && both) {
+            const int64_t few = more * (FEW_LIMIT / FEW_ROWS);
+            tiles = tiles < few ? tiles : few;
+            least = 0;
+        }
+        L.target[k] = k && !both ? -1 : (least * heads >= goal ? 0 : (int32_t)cut);
+        L.tiles[k] = tiles;
+        L.items[k] = tiles + (L.target[k] ? cut + 16 : 0);
+        // The room of the parts does not depend on max_fresh and grows with T and B,
+        // so that a workspace of the largest step serves every other: ...
+        const int64_t fewest = k ? rows / 128 : rows / FEW_ROWS;
+        const int64_t room = (fewest < cut ? fewest : cut) + more + cut + 16;
+        const int64_t room_rows = room * heads * (k ? 256 : FEW_ROWS);
+        L.part_o[k] = off;
+        off += (size_t)(room_rows * D) * sizeof(float);
+        L.part_ml[k] = off;
+        off += (size_t)(room_rows * 2) * sizeof(float);
+    }
+    L.total = off;
     return L;
 }
 
-template <int D>
-hipError_t launch_attention(const AttnArgs &a, const AttnLayout &L, hipStream_t s)
+template <int D, int W>
+hipError_t launch_many(const AttnArgs &a, const Cut &c, const AttnLayout &L, hipStream_t s)
 {
-    hipLaunchKernelGGL((few_rows_kernel<D>), dim3((unsigned)(L.items * a.heads)), dim3(64 * FEW_WAVES), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.target)
+    constexpr int ROWS = 32 * W;
+    const size_t lds = 2 * Tiles<D, W>::BUF;
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&many_rows_kernel<D, W>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (attr != hipSuccess)
+        return attr;
+    hipLaunchKernelGGL((many_rows_kernel<D, W>), dim3((unsigned)(L.items[1] * a.heads)), dim3(64 * W), lds, s, a, c);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !c.target)
         return e;
-    hipLaunchKernelGGL((join_chunks_kernel<D, FEW_ROWS>), dim3((unsigned)(L.tiles * a.heads)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((join_chunks_kernel<D, ROWS>), dim3((unsigned)(L.tiles[1] * a.heads), ROWS / JOIN), dim3(256), 0, s, a, c);
     return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_attention(const AttnArgs &a, const AttnLayout &L, uint8_t *ws, hipStream_t s)
+{
+    Cut c[2];
+    for (int k = 0; k < 2; k++)
+        c[k] = {reinterpret_cast<float *>(ws + L.part_o[k]), reinterpret_cast<float *>(ws + L.part_ml[k]), k ? L.limit : 0,
+                k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST, (int32_t)L.items[k]};
+    hipLaunchKernelGGL((few_rows_kernel<D>), dim3((unsigned)(L.items[0] * a.heads)), dim3(64 * FEW_WAVES), 0, s, a, c[0]);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && c[0].target) {
+        hipLaunchKernelGGL((join_chunks_kernel<D, FEW_ROWS>), dim3((unsigned)(L.tiles[0] * a.heads), FEW_ROWS / JOIN), dim3(256), 0, s,
+                           a, c[0]);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess || L.target[1] < 0)
+        return e;
+    if constexpr (D <= 192)
+        if (L.wide)
+            return launch_many<D, 8>(a, c[1], L, s);
+    return launch_many<D, 4>(a, c[1], L, s);
 }
 
 } // namespace
@@ -657,17 +1033,15 @@ spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t 
         return st;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     const AttnArgs a = {q, q_stride, kv->k_codes, kv->k_scales, kv->v_codes, kv->v_scales, table, q_start, kv_len, y, lse,
-                        reinterpret_cast<float *>(ws + L.part_o), reinterpret_cast<float *>(ws + L.part_ml), T, kv->pages,
-                        width, B, kv->heads, Hq / kv->heads, __builtin_ctz(kv->P), window, L.target, (int32_t)L.items,
-                        scale * LOG2E};
+                        T, kv->pages, width, B, kv->heads, Hq / kv->heads, __builtin_ctz(kv->P), window, scale * LOG2E};
     const hipStream_t s = (hipStream_t)stream;
     hipError_t e = hipSuccess;
     switch (kv->D) {
-    case 64: e = launch_attention<64>(a, L, s); break;
-    case 96: e = launch_attention<96>(a, L, s); break;
-    case 128: e = launch_attention<128>(a, L, s); break;
-    case 192: e = launch_attention<192>(a, L, s); break;
-    default: e = launch_attention<256>(a, L, s); break;
+    case 64: e = launch_attention<64>(a, L, ws, s); break;
+    case 96: e = launch_attention<96>(a, L, ws, s); break;
+    case 128: e = launch_attention<128>(a, L, ws, s); break;
+    case 192: e = launch_attention<192>(a, L, ws, s); break;
+    default: e = launch_attention<256>(a, L, ws, s); break;
     }
     return e == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
 }
