@@ -549,9 +549,10 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *     knows; it chooses kernels and their tiles, the result is right without it).
  *   scale > 0, finite; window 0 (none) .. 2^30.
  *   workspace device scratch of spear_kv4_attention_workspace_size bytes (0 for
- *     sizes out of range), 256-byte aligned; needs no zeroing and holds nothing
- *     between calls.  The size grows with T and B and hangs on neither max_fresh
- *     nor width, so one for the largest step serves the others.
+ *     sizes out of range), 256-byte aligned, zeroed once (spear_workspace_init):
+ *     its counters are zero again when a call's work has ended.  The size grows
+ *     with T and B and hangs on neither max_fresh nor width, so one for the
+ *     largest step serves the others, also between calls of other sizes.
  */
 size_t spear_kv4_attention_workspace_size(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
                                           int32_t heads, int32_t D, int64_t width, int32_t P);

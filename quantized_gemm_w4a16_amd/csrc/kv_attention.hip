@@ -6,7 +6,8 @@
 // The keys that a tile sees are cut into chunks of whole 64-token steps; a
 // (tile, chunk, key head) is a workgroup's item.  One pass over the keys holds a
 // row's maximum m, sum l and output o; an item that has its tile's keys to itself
-// writes y, the others leave (m, l, o) in the workspace for a second launch.
+// writes y, the others leave (m, l, o) in the workspace, to be joined in the
+// chunks' order: by the last of them to finish (few rows), or by a second launch.
 #include <math.h>
 
 #include "kv4.hpp"
@@ -18,7 +19,8 @@ constexpr int STEP = 64;            // keys of a step
 constexpr int FEW_ROWS = 16;        // rows of a tile of the kernel for few rows
 constexpr int FEW_WAVES = 4;        // its waves, which take the steps of a chunk in turn
 constexpr int FEW_LEAST = 4;        // steps of a chunk, at least
-constexpr int FEW_ITEMS = 1024;     // items of all key heads that the cut aims at
+constexpr int FEW_ITEMS = 768;      // items of all key heads that the cut aims at: three a CU
+constexpr int JB = 8;               // chunks whose parts are on their way at once in the join
 constexpr int MANY_LEAST = 4;       // steps of its chunks, at least
 constexpr int MANY_ITEMS = 512;     // items of all key heads that its cut aims at
 constexpr float LOG2E = 1.44269504088896340736f;
@@ -43,7 +45,9 @@ struct Cut {
     int32_t target;                 // items of a key head that the cut aims at; 0: no cut
     int32_t least;                  // steps of a chunk, at least
     int32_t most;                   // items of a key head that there is room for
+    uint32_t *count;                // [tile][key head] chunks that are done; 0 between calls
 };
+constexpr int64_t COUNTS = 8192;    // of those: a cut has no more tiles of all key heads
 
 // ------------------------------------------------------------------- items
 struct Request {
@@ -81,14 +85,43 @@ struct Item {
     int32_t tile, chunk, chunks;    // of its request
     int32_t size;                   // steps of a chunk
     int32_t item;                   // first item of the tile
+    int32_t number;                 // of the tile, of all requests
     bool found;
 };
 
 __device__ __forceinline__ int32_t bcast(int32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
+// Sums over the lanes up to this one (16 lanes, then the rows of 16 before).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t from_lane(int32_t v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int32_t scan64(int32_t v)
+{
+    v += from_lane<0x111, 0xF>(v);
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);
+    return v + from_lane<0x143, 0xC>(v);
+}
+__device__ __forceinline__ float total64(float v)
+{
+    v += __int_as_float(from_lane<0x111, 0xF>(__float_as_int(v)));
+    v += __int_as_float(from_lane<0x112, 0xF>(__float_as_int(v)));
+    v += __int_as_float(from_lane<0x114, 0xF>(__float_as_int(v)));
+    v += __int_as_float(from_lane<0x118, 0xF>(__float_as_int(v)));
+    v += __int_as_float(from_lane<0x142, 0xA>(__float_as_int(v)));
+    v += __int_as_float(from_lane<0x143, 0xC>(__float_as_int(v)));
+    return __int_as_float(bcast(__float_as_int(v), 63));
+}
+
 // The item (or, by_tile, the tile) number `want`.  Every wave forms the sums over
 // all requests, 64 at a time.  A chunk has as many steps as make about c.target
 // items of a key head; sums are capped at c.most, behind which there is no item.
+// A tile whose items do not all lie below c.most (rows that q_start gives to more
+// than one request) has none, so that its count of chunks ends where it began.
 template <int ROWS>
 __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by_tile)
 {
@@ -105,10 +138,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
                 work += (float)r.tiles * (float)r.steps;
             }
         }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2)
-            work += __shfl_xor(work, d);
-        const float s = ceilf(work / (float)c.target);
+        const float s = ceilf(total64(work) / (float)c.target);
         it.size = s < (float)c.least ? c.least : (s > 1e9f ? 1000000000 : (int32_t)s);
     }
     int32_t items0 = 0, tiles0 = 0;
@@ -123,19 +153,13 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             const int64_t all = (int64_t)r.tiles * chunks;
             n = all < c.most ? (int32_t)all : c.most;
         }
-        // inclusive sums, held below 2^31 by the cap (64 * most < 2^31)
-        int32_t ni = n, ti = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int32_t x = __shfl_up(ni, d), y = __shfl_up(ti, d);
-            ni += lane >= d ? x : 0;
-            ti += lane >= d ? y : 0;
-        }
+        // held below 2^31 by the cap (64 * most < 2^31)
+        const int32_t ni = scan64(n), ti = scan64(tiles);
         const int32_t end = by_tile ? tiles0 + ti : items0 + ni, len = by_tile ? tiles : n;
         const uint64_t hit = __ballot(end > want && end - len <= want);
         if (hit) {
             const int src = __builtin_ctzll(hit);
-            const int32_t first_item = bcast(items0 + ni - n, src), first = bcast(end - len, src);
+            const int32_t first_item = bcast(items0 + ni - n, src), first_tile = bcast(tiles0 + ti - tiles, src);
             it.r.row0 = (int64_t)(uint32_t)bcast((int32_t)r.row0, src);
             it.r.fresh = bcast(r.fresh, src);
             it.r.kv = bcast(r.kv, src);
@@ -143,11 +167,12 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             it.r.base = bcast(r.base, src);
             it.r.steps = bcast(r.steps, src);
             it.chunks = bcast(chunks, src);
-            it.tile = by_tile ? want - first : (want - first) / it.chunks;
-            it.chunk = by_tile ? 0 : (want - first) % it.chunks;
+            it.tile = by_tile ? want - first_tile : (want - first_item) / it.chunks;
+            it.chunk = by_tile ? 0 : (want - first_item) % it.chunks;
             it.item = first_item + it.tile * it.chunks;
+            it.number = first_tile + it.tile;
             it.b = b0 + src;
-            it.found = true;
+            it.found = it.chunks < 2 || (it.item <= c.most - it.chunks && (int64_t)(it.number + 1) * a.heads <= COUNTS);
             return it;
         }
         items0 += bcast(ni, 63);
@@ -259,6 +284,23 @@ __device__ __forceinline__ void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
+// Partial results pass from workgroup to workgroup within a launch: they are
+// written through to where every XCD reads, and a workgroup counts itself as done
+// only when its stores have returned.  (An agent-scope release would write back
+// the whole L2 of the XCD for each.)
+__device__ __forceinline__ void store_far(float *p, float x, float y)
+{
+    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_far(const float *p)
+{
+    const uint64_t v = __hip_atomic_load(reinterpret_cast<uint64_t *>(const_cast<float *>(p)), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // Four channels from c on of a request's row, and with c == 0 its lse.
 template <int D>
 __device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int head, int row, int c, f32x4 sum, float m, float l)
@@ -279,7 +321,7 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int
 // (g, j) stand for the keys 16 g + 4 (j % 4) + 2 u + j / 4.  V goes through LDS,
 // as bf16, to be read column by column.
 template <int D>
-__global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs a, const Cut cut)
+__global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_kernel(const AttnArgs a, const Cut cut)
 {
     using L = Lay<D>;
     constexpr int DT = D / 16, NS = L::NC * L::W;
@@ -287,6 +329,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs
     static_assert(V_BYTES >= 16 * D * 4, "the waves' outputs are joined in the same LDS");
     __shared__ __attribute__((aligned(16))) uint8_t s_v[FEW_WAVES][V_BYTES];
     __shared__ float s_ml[FEW_WAVES][FEW_ROWS][2];
+    __shared__ bool s_last;
 
     const int head = blockIdx.x % a.heads;
     const Item it = find_item<FEW_ROWS>(a, cut, (int32_t)(blockIdx.x / a.heads), false);
@@ -535,12 +578,87 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(const AttnArgs
         }
         if (it.chunks > 1) {
             const int64_t p = ((int64_t)(it.item + it.chunk) * a.heads + head) * FEW_ROWS + r;
-            *reinterpret_cast<f32x4 *>(cut.part_o + p * D + c) = sum;
-            if (c == 0) {
-                cut.part_ml[2 * p] = mm;
-                cut.part_ml[2 * p + 1] = ll;
-            }
+            store_far(cut.part_o + p * D + c, sum[0], sum[1]);
+            store_far(cut.part_o + p * D + c + 2, sum[2], sum[3]);
+            if (c == 0)
+                store_far(cut.part_ml + 2 * p, mm, ll);
         } else
+            store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
+    }
+    if (it.chunks < 2)
+        return;
+
+    // ---- the last workgroup of the tile joins its chunks
+    uint32_t *count = cut.count + (int64_t)it.number * a.heads + head;
+    stores_done();
+    __syncthreads();
+    if (tid == 0)
+        s_last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)it.chunks - 1;
+    __syncthreads();
+    if (!s_last)
+        return;
+    if (tid == 0)
+        __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // sh threads share a row's four channels, a chunk each in turn
+    const int real_rows = rows < FEW_ROWS ? rows : FEW_ROWS, work = real_rows * (D / 4);
+    int sharers = 1;
+    while (2 * sharers * work <= 64 * FEW_WAVES)
+        sharers *= 2;
+    const int64_t p0 = ((int64_t)it.item * a.heads + head) * FEW_ROWS, next = (int64_t)a.heads * FEW_ROWS;
+    float *s_part = reinterpret_cast<float *>(s_v);                        // [thread][6]
+    for (int x0 = 0; x0 < work; x0 += 64 * FEW_WAVES) {
+        const int x = x0 + tid % (sharers > 1 ? 64 * FEW_WAVES / sharers : 64 * FEW_WAVES);
+        const int sh = sharers > 1 ? tid / (64 * FEW_WAVES / sharers) : 0;
+        const bool in = x < work;
+        const int r = in ? x / (D / 4) : 0, c = in ? 4 * (x % (D / 4)) : 0;
+        float mm = -INFINITY, ll = 0.f;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int i0 = sh; i0 < it.chunks; i0 += JB * sharers) {
+            float2 ml[JB], lo2[JB], hi2[JB];
+#pragma unroll
+            for (int j = 0; j < JB; j++) {
+                const int i = i0 + j * sharers < it.chunks ? i0 + j * sharers : i0;
+                const int64_t p = p0 + i * next + r;
+                ml[j] = load_far(cut.part_ml + 2 * p);
+                lo2[j] = load_far(cut.part_o + p * D + c);
+                hi2[j] = load_far(cut.part_o + p * D + c + 2);
+            }
+            float up = mm;
+#pragma unroll
+            for (int j = 0; j < JB; j++)
+                up = fmaxf(up, ml[j].x);
+            const float ref = up == -INFINITY ? 0.f : up, f = __builtin_amdgcn_exp2f(mm - ref);
+            ll *= f;
+            sum *= f;
+            mm = up;
+#pragma unroll
+            for (int j = 0; j < JB; j++) {
+                const float w = i0 + j * sharers < it.chunks ? __builtin_amdgcn_exp2f(ml[j].x - ref) : 0.f;
+                if (w != 0.f) {
+                    ll += w * ml[j].y;
+                    sum += w * f32x4{lo2[j].x, lo2[j].y, hi2[j].x, hi2[j].y};
+                }
+            }
+        }
+        if (sharers > 1) {
+            __syncthreads();
+            s_part[tid * 6] = mm;
+            s_part[tid * 6 + 1] = ll;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                s_part[tid * 6 + 2 + e] = sum[e];
+            __syncthreads();
+            if (sh == 0)
+                for (int j = 1; j < sharers; j++) {
+                    const float *o2 = s_part + (tid + j * (64 * FEW_WAVES / sharers)) * 6;
+                    const float up = fmaxf(mm, o2[0]), ref = up == -INFINITY ? 0.f : up;
+                    const float f = __builtin_amdgcn_exp2f(mm - ref), w = __builtin_amdgcn_exp2f(o2[0] - ref);
+                    mm = up;
+                    ll = f * ll + w * o2[1];
+                    sum = f * sum + w * f32x4{o2[2], o2[3], o2[4], o2[5]};
+                }
+        }
+        if (in && sh == 0)
             store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
     }
 }
@@ -568,17 +686,23 @@ __device__ __forceinline__ float max_over_halves(float v)
 template <int D, int W>
 struct Tiles {
     static constexpr int NB = D / 32, KROW = 2 * D + 16, VROW = D == 96 ? 2 * D : 2 * D + 64;
-    static constexpr int UNITS = STEP * NB, U = (UNITS + 64 * W - 1) / (64 * W);
-    static constexpr int BUF = STEP * (KROW + VROW);
+    // Keys of a step: heads of more than 128 channels take half as many, so that two
+    // workgroups fit a CU.
+    static constexpr int KT = D <= 128 ? 2 : 1, SK = 32 * KT;
+    static constexpr int UNITS = SK * NB, U = (2 * UNITS + 64 * W - 1) / (64 * W);
+    static constexpr int BUF = SK * (KROW + VROW);
 };
 
 template <int D, int W>
-__global__ __launch_bounds__(64 * W, W == 8 ? 2 : (D > 128 ? 1 : 2)) void many_rows_kernel(const AttnArgs a, const Cut cut)
+__global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(const AttnArgs a, const Cut cut)
 {
     using L = Tiles<D, W>;
-    constexpr int DT = D / 32, KS = D / 16, ROWS = 32 * W;
+    constexpr int DT = D / 32, KS = D / 16, ROWS = 32 * W, KT = L::KT, SK = L::SK;
+    // The scores of a step are formed one step ahead, beside the exponentials of the
+    // step before, where there are registers for two steps' scores.
+    constexpr int AHEAD = D <= 128 ? 1 : 0;
     extern __shared__ __attribute__((aligned(16))) uint8_t s_kv[];         // two buffers of K rows, then V rows
-    __shared__ int32_t s_flag[2][2];       // step + 1 whose keys have a lost page; ... a block of NaN in V
+    __shared__ int32_t s_flag[5][2];       // step + 1 if a page of its keys is gone; ... if its V has a block of NaN
 
     const int head = blockIdx.x % a.heads;
     const Item it = find_item<ROWS>(a, cut, (int32_t)(blockIdx.x / a.heads), false);
@@ -608,8 +732,11 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : (D > 128 ? 1 : 2)) void many_r
     int lo = it.r.base + it.chunk * (it.chunks > 1 ? it.size : 0), hi = it.r.base + it.r.steps;
     if (it.chunks > 1 && lo + it.size < hi)
         hi = lo + it.size;
-    lo = lo > seen0 / STEP ? lo : seen0 / STEP;
-    const int hi_seen = seen1 > 0 ? (seen1 + STEP - 1) / STEP : 0;
+    // from here on in steps of SK keys
+    lo *= STEP / SK;
+    hi *= STEP / SK;
+    lo = lo > seen0 / SK ? lo : seen0 / SK;
+    const int hi_seen = seen1 > 0 ? (seen1 + SK - 1) / SK : 0;
     hi = hi < hi_seen ? hi : hi_seen;
 
     u32x4 qf[KS];
@@ -630,170 +757,189 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : (D > 128 ? 1 : 2)) void many_r
         for (int r = 0; r < 16; r++)
             o[d][r] = 0.f;
 
-    // ---- a step's codes: unit u is a block of 32 channels of a key, of K and of V
-    u32x4 kc[L::U], vc[L::U];
-    uint32_t kb[L::U], vb[L::U], page[L::U];
+    // ---- codes on their way: unit u is a block of 32 channels of a key, of K (of step
+    // `ahead`) below UNITS and of V (of step ahead - AHEAD) from there on, a wave all
+    // of the one or the other
+    u32x4 code[L::U];
+    uint32_t byte[L::U], page[L::U];
     bool gone[L::U];
     const uint32_t code_page = (uint32_t)a.heads * (D / 2) << log_p, scale_page = (uint32_t)a.heads * L::NB << log_p;
     const uint32_t last_page = (uint32_t)a.pages - 1;
-    auto unit = [&](int i) { return i * 64 * W + tid; };
-    auto find_pages = [&](int step) {
+    auto is_v = [&](int i) { return i * 64 * W + 64 * wave >= L::UNITS; };
+    auto is_unit = [&](int i) { return 2 * L::UNITS % (64 * W) == 0 || i * 64 * W + 64 * wave < 2 * L::UNITS; };
+    auto unit = [&](int i) { return i * 64 * W + tid - (is_v(i) ? L::UNITS : 0); };
+    auto find_pages = [&](int ahead) {
 #pragma unroll
         for (int i = 0; i < L::U; i++) {
-            const int key = step * STEP + unit(i) / L::NB;
-            page[i] = step < hi && key < it.r.kv ? (uint32_t)table[key >> log_p] : 0u;
+            const int step = ahead - AHEAD * is_v(i), key = step * SK + unit(i) / L::NB;
+            const bool in = (step >= lo) & (step < hi) & (key < it.r.kv);
+            const uint32_t p = (uint32_t)table[in ? key >> log_p : 0];
+            page[i] = in ? p : 0u;
         }
     };
-    auto load = [&](int step) {
+    auto load = [&](int ahead) {
 #pragma unroll
-        for (int i = 0; i < L::U; i++) {
-            const int blk = unit(i) % L::NB;
-            const uint32_t off = (uint32_t)(step * STEP + unit(i) / L::NB) & page_mask;
-            if (L::UNITS % (64 * W) == 0 || unit(i) < L::UNITS) {
+        for (int i = 0; i < L::U; i++)
+            if (is_unit(i)) {
+                const int blk = unit(i) % L::NB;
+                const uint32_t off = (uint32_t)((ahead - AHEAD * is_v(i)) * SK + unit(i) / L::NB) & page_mask;
                 gone[i] = page[i] > last_page;
                 const uint32_t p = gone[i] ? 0u : page[i];
-                const uint64_t at = (uint64_t)p * code_page + ((((uint32_t)head << log_p) + off) * (D / 2) + 16 * blk);
-                const uint64_t sat = (uint64_t)p * scale_page + ((((uint32_t)head * L::NB + blk) << log_p) + off);
-                kc[i] = ld16(a.k_codes + at);
-                vc[i] = ld16(a.v_codes + at);
-                kb[i] = a.k_scales[sat];
-                vb[i] = a.v_scales[sat];
+                code[i] = ld16((is_v(i) ? a.v_codes : a.k_codes) + ((uint64_t)p * code_page +
+                               ((((uint32_t)head << log_p) + off) * (D / 2) + 16 * blk)));
+                byte[i] = (is_v(i) ? a.v_scales : a.k_scales)[(uint64_t)p * scale_page +
+                                                              ((((uint32_t)head * L::NB + blk) << log_p) + off)];
             }
-        }
     };
-    auto store = [&](int step, int buf) {
+    // No branch: the stores are spread between matrix instructions.
+    auto store = [&](int ahead) {
 #pragma unroll
-        for (int i = 0; i < L::U; i++) {
-            const int key = unit(i) / L::NB, blk = unit(i) % L::NB;
-            if (L::UNITS % (64 * W) == 0 || unit(i) < L::UNITS) {
+        for (int i = 0; i < L::U; i++)
+            if (is_unit(i)) {
+                const int key = unit(i) / L::NB, blk = unit(i) % L::NB, step = ahead - AHEAD * is_v(i), at = step * SK + key;
                 // keys that no row of the tile sees hold anything: their V is zero.  A
                 // block of NaN in V is put in by hand, for the rows that see it
-                const int at = step * STEP + key;
-                const bool seen = at >= seen0 && at < seen1 && !gone[i];
-                if (gone[i])
-                    s_flag[buf][0] = step + 1;
-                if (seen && vb[i] == 255u)
-                    s_flag[buf][1] = step + 1;
-                const bool clear = !seen || vb[i] == 255u;
-                const float ks = kv4_scale(kb[i]), vs = kv4_scale(clear ? 127u : vb[i]);
-                uint8_t *kp = s_kv + buf * L::BUF + key * L::KROW + 64 * blk;
-                uint8_t *vp = s_kv + buf * L::BUF + STEP * L::KROW + key * L::VROW + 64 * blk;
-#pragma unroll
-                for (int w = 0; w < 4; w++)
-                    *reinterpret_cast<u32x4 *>(kp + 16 * w) = kv4_bf16(kc[i][w], ks);
+                const bool seen = (at >= seen0) & (at < seen1) & !gone[i], nan = seen & (byte[i] == 255u);
+                const bool clear = is_v(i) & (!seen | nan), note = is_v(i) ? nan : gone[i];
+                s_flag[note ? step & 3 : 4][is_v(i)] = step + 1;
+                const float sc = kv4_scale(clear ? 127u : byte[i]);
                 // rows of V that start in the same banks take their words in another order
-                const int turn = key & 1;
+                const int turn = is_v(i) ? key & 1 : 0;
+                uint8_t *p = s_kv + (step & 1) * L::BUF + (is_v(i) ? SK * L::KROW + key * L::VROW : key * L::KROW) + 64 * blk;
 #pragma unroll
                 for (int w = 0; w < 4; w++) {
-                    const uint32_t c = turn ? vc[i][w ^ 1] : vc[i][w];
-                    *reinterpret_cast<u32x4 *>(vp + ((16 * w) ^ (16 * turn))) = kv4_bf16(clear ? 0u : c, vs);
+                    const uint32_t c = turn ? code[i][w ^ 1] : code[i][w];
+                    *reinterpret_cast<u32x4 *>(p + ((16 * w) ^ (16 * turn))) = kv4_bf16(clear ? 0u : c, sc);
                 }
             }
+    };
+    f32x16 s[KT];
+    auto scores = [&](int step, f32x16 (&z)[KT]) {
+        const uint8_t *sk = s_kv + (step & 1) * L::BUF + n * L::KROW + 16 * h;
+#pragma unroll
+        for (int kt = 0; kt < KT; kt++) {
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                z[kt][r] = 0.f;
+#pragma unroll
+            for (int c = 0; c < KS; c++)
+                z[kt] = mfma32(ld16(sk + 32 * kt * L::KROW + 32 * c), qf[c], z[kt]);
         }
     };
 
-    if (tid < 4)
+    if (tid < 8)
         s_flag[tid >> 1][tid & 1] = 0;
     if (lo < hi) {
         find_pages(lo);
         load(lo);
         find_pages(lo + 1);
         __syncthreads();
-        store(lo, 0);
+        store(lo);
         load(lo + 1);
         find_pages(lo + 2);
-    }
-    __syncthreads();
-
-    for (int step = lo; step < hi; step++) {
-        const int buf = (step - lo) & 1, key0 = step * STEP;
-        if (step + 1 < hi) {
-            store(step + 1, buf ^ 1);
-            load(step + 2);
-            find_pages(step + 3);
+        if constexpr (AHEAD) {
+            store(lo + 1);
+            load(lo + 2);
+            find_pages(lo + 3);
+            __syncthreads();
+            scores(lo, s);
         }
-        if (key0 < mine1 && key0 + STEP > mine0) {
-            const uint8_t *sk = s_kv + buf * L::BUF, *sv = sk + STEP * L::KROW;
-            uint64_t lost = 0;
-            if (__builtin_amdgcn_readfirstlane(s_flag[buf][0]) == step + 1) {
-                const int key = key0 + lane;
-                lost = __ballot(key < it.r.kv && (uint32_t)table[key >> log_p] > last_page);
-            }
-            f32x16 s[2];
+        __syncthreads();                                  // before K of the step after next takes its place
+    }
+
+    // Step: the scores of the next step are formed, and its V and the K of the one
+    // behind it (AHEAD = 0: its own scores, the next step's K and V) go to LDS, while
+    // this step's probabilities are formed and used.
+    auto body = [&](int step, f32x16 (&s)[KT], f32x16 (&z)[KT]) {
+        const int key0 = step * SK;
+        if constexpr (!AHEAD)
+            scores(step, s);
+        uint64_t lost = 0;
+        if (__builtin_amdgcn_readfirstlane(s_flag[step & 3][0]) == step + 1) {
+            const int key = key0 + lane;
+            lost = __ballot(lane < SK && key < it.r.kv && (uint32_t)table[key >> log_p] > last_page);
+        }
+        if (key0 < all0 || key0 + SK - 1 > all1 || lost != 0) {
+            const int f = first - key0 - 4 * h, e = last - key0 - 4 * h;
+            const uint64_t gone4 = lost >> (4 * h);
 #pragma unroll
-            for (int kt = 0; kt < 2; kt++) {
-#pragma unroll
-                for (int r = 0; r < 16; r++)
-                    s[kt][r] = 0.f;
-#pragma unroll
-                for (int c = 0; c < KS; c++)
-                    s[kt] = mfma32(ld16(sk + (32 * kt + n) * L::KROW + 32 * c + 16 * h), qf[c], s[kt]);
-            }
-            if (key0 < all0 || key0 + STEP - 1 > all1 || lost != 0) {
-                const int f = first - key0 - 4 * h, e = last - key0 - 4 * h;
-                const uint64_t gone4 = lost >> (4 * h);
-#pragma unroll
-                for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-                    for (int r = 0; r < 16; r++) {
-                        const int k = 32 * kt + 8 * (r / 4) + r % 4;
-                        s[kt][r] = k >= f && k <= e && !(gone4 >> k & 1) ? s[kt][r] : -INFINITY;
-                    }
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int r = 1; r < 32; r++)
-                top = fmaxf(top, s[r / 16][r % 16]);
-            top = max_over_halves(top) * a.scale;
-            if (__any(top > m)) {
-                const float x = fmaxf(m, top);
-                const float f = m == x ? 1.f : __builtin_amdgcn_exp2f(m - x);
-                m = x;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DT; d++)
-                    o[d] *= f;
-            }
-            const float m0 = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-            for (int kt = 0; kt < 2; kt++) {
-                u32x4 p[2];
+            for (int kt = 0; kt < KT; kt++)
 #pragma unroll
                 for (int r = 0; r < 16; r++) {
-                    s[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale, m0));
-                    l += s[kt][r];
+                    const int k = 32 * kt + 8 * (r / 4) + r % 4;
+                    s[kt][r] = k >= f && k <= e && !(gone4 >> k & 1) ? s[kt][r] : -INFINITY;
                 }
+        }
+        float top = s[0][0];
 #pragma unroll
-                for (int r = 0; r < 8; r++)
-                    p[r / 4][r % 4] = pair_bf16(s[kt][2 * r], s[kt][2 * r + 1]);
+        for (int r = 1; r < 16 * KT; r++)
+            top = fmaxf(top, s[r / 16][r % 16]);
+        top = max_over_halves(top) * a.scale;
+        if (__any(top > m)) {
+            const float x = fmaxf(m, top);
+            const float f = m == x ? 1.f : __builtin_amdgcn_exp2f(m - x);
+            m = x;
+            l *= f;
 #pragma unroll
-                for (int u = 0; u < 2; u++)
+            for (int d = 0; d < DT; d++)
+                o[d] *= f;
+        }
+        const float m0 = m == -INFINITY ? 0.f : -m;
+        if constexpr (AHEAD)
+            scores(step + 1, z);
+        u32x4 p[KT][2];
 #pragma unroll
-                    for (int d = 0; d < DT; d++) {
-                        const uint8_t *at = sv + (32 * kt + 16 * u + 4 * h + ((lane & 15) >> 2)) * L::VROW + 64 * d +
-                                            32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-                        const uint2 x = read_turned(at), z = read_turned(at + 8 * L::VROW);
-                        o[d] = mfma32(u32x4{x.x, x.y, z.x, z.y}, p[u], o[d]);
-                    }
+        for (int kt = 0; kt < KT; kt++) {
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                s[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale, m0));
+                l += s[kt][r];
             }
-            if (__builtin_amdgcn_readfirstlane(s_flag[buf][1]) == step + 1) {
-                // blocks of NaN in V, for the rows that see their keys
-                const int key = key0 + lane;
-                const uint32_t p = key < it.r.kv ? (uint32_t)table[key >> log_p] : 0xFFFFFFFFu;
 #pragma unroll
-                for (int blk = 0; blk < L::NB; blk++) {
-                    const uint64_t sat = (uint64_t)(p > last_page ? 0u : p) * scale_page +
-                                         ((((uint32_t)head * L::NB + blk) << log_p) + (key & page_mask));
-                    uint64_t who = __ballot(p <= last_page && a.v_scales[sat] == 255);
-                    while (who) {
-                        const int k = key0 + __builtin_ctzll(who);
-                        who &= who - 1;
-                        o[blk] += k >= first && k <= last ? __builtin_nanf("") : 0.f;
-                    }
+            for (int r = 0; r < 8; r++)
+                p[kt][r / 4][r % 4] = pair_bf16(s[kt][2 * r], s[kt][2 * r + 1]);
+        }
+        store(step + 1 + AHEAD);
+        load(step + 2 + AHEAD);
+        find_pages(step + 3 + AHEAD);
+        const uint8_t *sv = s_kv + (step & 1) * L::BUF + SK * L::KROW + (4 * h + ((lane & 15) >> 2)) * L::VROW +
+                            32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+#pragma unroll
+        for (int u = 0; u < 2 * KT; u++)
+#pragma unroll
+            for (int d = 0; d < DT; d++) {
+                const uint8_t *at = sv + 16 * u * L::VROW + 64 * d;
+                const uint2 x = read_turned(at), y = read_turned(at + 8 * L::VROW);
+                o[d] = mfma32(u32x4{x.x, x.y, y.x, y.y}, p[u / 2][u % 2], o[d]);
+            }
+        const int32_t nan = __builtin_amdgcn_readfirstlane(s_flag[step & 3][1]);
+        if (nan == step + 1) {
+            // blocks of NaN in V, for the rows that see their keys
+            const int key = key0 + lane;
+            const uint32_t p = lane < SK && key < it.r.kv ? (uint32_t)table[key >> log_p] : 0xFFFFFFFFu;
+#pragma unroll
+            for (int blk = 0; blk < L::NB; blk++) {
+                const uint64_t sat = (uint64_t)(p > last_page ? 0u : p) * scale_page +
+                                     ((((uint32_t)head * L::NB + blk) << log_p) + (key & page_mask));
+                uint64_t who = __ballot(p <= last_page && a.v_scales[sat] == 255);
+                while (who) {
+                    const int k = key0 + __builtin_ctzll(who);
+                    who &= who - 1;
+                    o[blk] += k >= first && k <= last ? __builtin_nanf("") : 0.f;
                 }
             }
         }
         __syncthreads();
+    };
+    f32x16 z[KT];
+    for (int step = lo; step < hi; step += 2) {
+        body(step, s, z);
+        if (step + 1 < hi) {
+            if constexpr (AHEAD)
+                body(step + 1, z, s);
+            else
+                body(step + 1, s, z);
+        }
     }
 
     auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
@@ -818,78 +964,76 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : (D > 128 ? 1 : 2)) void many_r
     }
 }
 
-// The chunks of a tile joined, in their order.  A workgroup takes JOIN rows of a
-// tile of a key head; a row's chunks are spread over the threads that share its
-// channels.
+// The chunks of a tile of many rows joined, in their order: a wave takes JOIN rows,
+// whose channels it splits by four; the lanes left over share the chunks.
 constexpr int JOIN = 4;
-
-template <int D, int ROWS>
-__device__ void join_rows(const AttnArgs &a, const Cut &cut, int tile, int head, int part)
-{
-    constexpr int Q = D / 4, S = 256 / Q;                 // threads of a row's channels; sharers
-    __shared__ f32x4 s_o[S][Q];
-    __shared__ float s_w[256];
-    __shared__ float s_m[4], s_l[4];
-    const Item it = find_item<ROWS>(a, cut, tile, true);
-    if (!it.found || it.chunks < 2)
-        return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = tid % Q, sh = tid / Q;
-    const int rows = it.r.fresh * a.G - it.tile * ROWS;
-    const int64_t next = (int64_t)a.heads * ROWS;
-    for (int r = part * JOIN; r < part * JOIN + JOIN && r < ROWS && r < rows; r++) {
-        const int64_t p0 = ((int64_t)it.item * a.heads + head) * ROWS + r;
-        float mm = -INFINITY;
-        for (int i = tid; i < it.chunks; i += 256)
-            mm = fmaxf(mm, cut.part_ml[2 * (p0 + i * next)]);
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2)
-            mm = fmaxf(mm, __shfl_xor(mm, d));
-        __syncthreads();                                  // the row before has been read
-        if (lane == 0)
-            s_m[wave] = mm;
-        __syncthreads();
-        mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-        const float ref = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int i0 = 0; i0 < it.chunks; i0 += 256) {
-            const int nn = it.chunks - i0 < 256 ? it.chunks - i0 : 256;
-            if (i0)
-                __syncthreads();
-            float w = 0.f;
-            if (tid < nn) {
-                const int64_t p = p0 + (i0 + tid) * next;
-                w = __builtin_amdgcn_exp2f(cut.part_ml[2 * p] - ref);
-                ll += w * cut.part_ml[2 * p + 1];
-            }
-            s_w[tid] = w;
-            __syncthreads();
-            if (sh < S) {
-#pragma unroll 4
-                for (int i = sh; i < nn; i += S)
-                    sum += s_w[i] * *reinterpret_cast<const f32x4 *>(cut.part_o + (p0 + (i0 + i) * next) * D + 4 * q);
-            }
-        }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2)
-            ll += __shfl_xor(ll, d);
-        if (lane == 0)
-            s_l[wave] = ll;
-        if (sh < S)
-            s_o[sh][q] = sum;
-        __syncthreads();
-        if (tid < Q) {
-            for (int i = 1; i < S; i++)
-                sum += s_o[i][q];
-            store_out<D>(a, it, head, it.tile * ROWS + r, 4 * q, sum, mm, s_l[0] + s_l[1] + s_l[2] + s_l[3]);
-        }
-    }
-}
 
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, const Cut cut)
 {
-    join_rows<D, ROWS>(a, cut, (int)(blockIdx.x / a.heads), blockIdx.x % a.heads, blockIdx.y);
+    constexpr int Q = D / 4, S = Q <= 32 ? (Q <= 16 ? 4 : 2) : 1;
+    const int head = blockIdx.x % a.heads;
+    const Item it = find_item<ROWS>(a, cut, (int32_t)(blockIdx.x / a.heads), true);
+    if (!it.found || it.chunks < 2)
+        return;
+    const int lane = threadIdx.x & 63, q = lane % (64 / S), sh = lane / (64 / S);
+    const int r0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * JOIN, rows = it.r.fresh * a.G - it.tile * ROWS;
+    const int64_t p0 = ((int64_t)it.item * a.heads + head) * ROWS, next = (int64_t)a.heads * ROWS;
+    if (r0 >= rows)
+        return;
+    const int c = 4 * (q < Q ? q : 0);
+    float mm[JOIN], ll[JOIN];
+    f32x4 sum[JOIN];
+#pragma unroll
+    for (int r = 0; r < JOIN; r++) {
+        mm[r] = -INFINITY;
+        ll[r] = 0.f;
+        sum[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int i0 = sh; i0 < it.chunks; i0 += 4 * S) {
+        float2 ml[4][JOIN];
+        f32x4 v[4][JOIN];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int r = 0; r < JOIN; r++) {
+                const int i = i0 + j * S < it.chunks ? i0 + j * S : i0;
+                const int64_t p = p0 + i * next + (r0 + r < rows ? r0 + r : r0);
+                ml[j][r] = *reinterpret_cast<const float2 *>(cut.part_ml + 2 * p);
+                v[j][r] = *reinterpret_cast<const f32x4 *>(cut.part_o + p * D + c);
+            }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (i0 + j * S < it.chunks)
+#pragma unroll
+                for (int r = 0; r < JOIN; r++) {
+                    const float up = fmaxf(mm[r], ml[j][r].x), ref = up == -INFINITY ? 0.f : up;
+                    const float f = __builtin_amdgcn_exp2f(mm[r] - ref), w = __builtin_amdgcn_exp2f(ml[j][r].x - ref);
+                    mm[r] = up;
+                    ll[r] = f * ll[r] + w * ml[j][r].y;
+                    sum[r] = f * sum[r] + w * v[j][r];
+                }
+    }
+#pragma unroll
+    for (int d = 64 / S; d < 64; d *= 2)
+#pragma unroll
+        for (int r = 0; r < JOIN; r++) {
+            const float m2 = __shfl_xor(mm[r], d), l2 = __shfl_xor(ll[r], d);
+            const float up = fmaxf(mm[r], m2), ref = up == -INFINITY ? 0.f : up;
+            const float f = __builtin_amdgcn_exp2f(mm[r] - ref), w = __builtin_amdgcn_exp2f(m2 - ref);
+            mm[r] = up;
+            // the same order in both lanes
+            const float x = f * ll[r], y = w * l2;
+            ll[r] = x + y;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                sum[r][e] = f * sum[r][e] + w * __shfl_xor(sum[r][e], d);
+        }
+    if (sh == 0 && q < Q)
+#pragma unroll
+        for (int r = 0; r < JOIN; r++)
+            if (r0 + r < rows && r0 + r < ROWS)
+                store_out<D>(a, it, head, it.tile * ROWS + r0 + r, c, sum[r], mm[r], ll[r]);
 }
 
 // ------------------------------------------------------------------- host
@@ -920,9 +1064,9 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
     // Requests of more rows than the limit take the other kernel, if there may be any.
     const bool both = T > 0 && max_fresh * G > FEW_LIMIT;
     L.limit = both ? FEW_LIMIT : 0x7FFFFFFF;
-    L.wide = D <= 192 && rows * heads >= (int64_t)256 * 512;
+    L.wide = D <= 128 && rows * heads >= (int64_t)256 * 512;
     const int many = 32 * (L.wide ? 8 : 4);
-    size_t off = 0;
+    size_t off = COUNTS * sizeof(uint32_t);           // first, whatever the sizes: calls of all sizes share it
     for (int k = 0; k < 2; k++) {
         const int tile = k ? many : FEW_ROWS, goal = k ? MANY_ITEMS : FEW_ITEMS;
         const int64_t cut = (goal + heads - 1) / heads;
@@ -937,7 +1081,7 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
             tiles = tiles < few ? tiles : few;
             least = 0;
         }
-        L.target[k] = k && !both ? -1 : (least * heads >= goal ? 0 : (int32_t)cut);
+        L.target[k] = k && !both ? -1 : (least * heads >= goal || tiles * heads > COUNTS ? 0 : (int32_t)cut);
         L.tiles[k] = tiles;
         L.items[k] = tiles + (L.target[k] ? cut + 16 : 0);
         // The room of the parts does not depend on max_fresh and grows with T and B,
@@ -967,7 +1111,7 @@ hipError_t launch_many(const AttnArgs &a, const Cut &c, const AttnLayout &L, hip
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !c.target)
         return e;
-    hipLaunchKernelGGL((join_chunks_kernel<D, ROWS>), dim3((unsigned)(L.tiles[1] * a.heads), ROWS / JOIN), dim3(256), 0, s, a, c);
+    hipLaunchKernelGGL((join_chunks_kernel<D, ROWS>), dim3((unsigned)(L.tiles[1] * a.heads), ROWS / (4 * JOIN)), dim3(256), 0, s, a, c);
     return hipGetLastError();
 }
 
@@ -977,17 +1121,13 @@ hipError_t launch_attention(const AttnArgs &a, const AttnLayout &L, uint8_t *ws,
     Cut c[2];
     for (int k = 0; k < 2; k++)
         c[k] = {reinterpret_cast<float *>(ws + L.part_o[k]), reinterpret_cast<float *>(ws + L.part_ml[k]), k ? L.limit : 0,
-                k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST, (int32_t)L.items[k]};
+                k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST, (int32_t)L.items[k],
+                reinterpret_cast<uint32_t *>(ws)};
     hipLaunchKernelGGL((few_rows_kernel<D>), dim3((unsigned)(L.items[0] * a.heads)), dim3(64 * FEW_WAVES), 0, s, a, c[0]);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && c[0].target) {
-        hipLaunchKernelGGL((join_chunks_kernel<D, FEW_ROWS>), dim3((unsigned)(L.tiles[0] * a.heads), FEW_ROWS / JOIN), dim3(256), 0, s,
-                           a, c[0]);
-        e = hipGetLastError();
-    }
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || L.target[1] < 0)
         return e;
-    if constexpr (D <= 192)
+    if constexpr (D <= 128)
         if (L.wide)
             return launch_many<D, 8>(a, c[1], L, s);
     return launch_many<D, 4>(a, c[1], L, s);

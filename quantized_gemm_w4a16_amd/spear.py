@@ -914,10 +914,11 @@ def spear_kv4_attention_workspace_size(T: int, B: int, max_fresh: int, Hq: int, 
 
 
 def new_kv4_workspace(T: int, B: int, max_fresh: int, Hq: int, kv: KV4, width: int) -> torch.Tensor:
-    """A workspace for spear_kv4_attention over T rows of B requests, none with more
-    than max_fresh of them, and a table of that width (torch allocation)."""
+    """A zero-filled workspace for spear_kv4_attention over T rows of B requests,
+    none with more than max_fresh of them, and a table of that width (torch
+    allocation)."""
     n = spear_kv4_attention_workspace_size(T, B, max_fresh, Hq, kv.heads, kv.D, width, kv.P)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=kv.device)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=kv.device)
 
 
 def spear_kv4_attention(q: torch.Tensor, kv: KV4, table: torch.Tensor, q_start: torch.Tensor,
