@@ -41,13 +41,16 @@ struct AttnArgs {
 // The requests that a kernel takes and how their keys are cut.
 struct Cut {
     float *part_o, *part_ml;        // [item][key head][row][D], [item][key head][row][2]
+    float *group_ml;                // as part_ml, of groups of chunks
     int32_t rows0, rows1;           // requests of rows0 < rows <= rows1
     int32_t target;                 // items of a key head that the cut aims at; 0: no cut
     int32_t least;                  // steps of a chunk, at least
     int32_t most;                   // items of a key head that there is room for
-    uint32_t *count;                // [tile][key head] chunks that are done; 0 between calls
+    uint32_t *count;                // [tile][key head] parts that are done; then [item][key head] chunks of a
+                                    // group; all 0 between calls
 };
-constexpr int64_t COUNTS = 8192;    // of those: a cut has no more tiles of all key heads
+constexpr int64_t COUNTS = 8192;            // tiles of all key heads that a cut may have
+constexpr int64_t GROUP_COUNTS = 32768;     // items
 
 // ------------------------------------------------------------------- items
 struct Request {
@@ -173,6 +176,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             it.number = first_tile + it.tile;
             it.b = b0 + src;
             it.found = it.chunks < 2 || (it.item <= c.most - it.chunks && (int64_t)(it.number + 1) * a.heads <= COUNTS);
+            static_assert(COUNTS + FEW_ITEMS + 17 * SPEAR_MAX_HEADS <= GROUP_COUNTS, "c.most items of all key heads");
             return it;
         }
         items0 += bcast(ni, 63);
@@ -381,18 +385,29 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
     Part<D> kp, vp;
     const int32_t *table = a.table + (int64_t)b * a.width;
     // Page and place of this lane's four tokens of a step.  Steps behind the last
-    // read the first page of the cache, and nothing of it is used.
-    auto page_of = [&](int step) {
-        const int t0 = step * STEP + 4 * n;
-        return step < hi && t0 < it.r.kv ? table[t0 >> log_p] : 0;
+    // read the first page of the cache, and nothing of it is used.  What is loaded is
+    // first touched a step later: a use of it here would wait for it.
+    auto in_step = [&](int step) { return (step < hi) & (step * STEP + 4 * n < it.r.kv); };
+    auto page_of = [&](int step) { return (uint32_t)table[in_step(step) ? (step * STEP + 4 * n) >> log_p : 0]; };
+    const uint32_t last_page = (uint32_t)a.pages - 1;
+    bool lost;
+    int64_t ph;
+    int32_t off;
+    auto place = [&](int step, uint32_t page) {
+        const bool in = in_step(step);
+        lost = in & (page > last_page);
+        ph = (int64_t)(in & !lost ? page : 0u) * a.heads + head;
+        off = (int32_t)((step * STEP + 4 * n) & page_mask);
     };
-    int page = page_of(lo + wave);
-    bool lost = page < 0 || page >= a.pages;
-    int64_t ph = (int64_t)(lost ? 0 : page) * a.heads + head;
-    int32_t off = (int32_t)(((lo + wave) * STEP + 4 * n) & page_mask);
+    // Loads return in the order they are issued, and the waits in the loop are for the
+    // order there: page, K, V.
+    place(lo + wave, page_of(lo + wave));
+    uint32_t page_next = page_of(lo + wave + FEW_WAVES);
+    __builtin_amdgcn_sched_barrier(0);
     load_part<D>(kp, a.k_codes, a.k_scales, ph, off, log_p, g);
+    __builtin_amdgcn_sched_barrier(0);
     load_part<D>(vp, a.v_codes, a.v_scales, ph, off, log_p, g);
-    int page_next = page_of(lo + wave + FEW_WAVES);
+    __builtin_amdgcn_sched_barrier(0);
 
     for (int step = lo + wave; step < hi; step += FEW_WAVES) {
         const int key0 = step * STEP;
@@ -411,12 +426,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
         }
         // the next step's keys
         const bool lost_now = lost;
-        page = page_next;
-        lost = page < 0 || page >= a.pages;
-        ph = (int64_t)(lost ? 0 : page) * a.heads + head;
-        off = (int32_t)((key0 + FEW_WAVES * STEP + 4 * n) & page_mask);
-        load_part<D>(kp, a.k_codes, a.k_scales, ph, off, log_p, g);
+        place(step + FEW_WAVES, page_next);
         page_next = page_of(step + 2 * FEW_WAVES);
+        __builtin_amdgcn_sched_barrier(0);
+        load_part<D>(kp, a.k_codes, a.k_scales, ph, off, log_p, g);
+        __builtin_amdgcn_sched_barrier(0);
 
         const bool edge = key0 < all0 || key0 + STEP - 1 > all1 || lost16 != 0;
         float top = -INFINITY;
@@ -543,7 +557,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                 o[d] = mfma16(vt, p_lo, o[d]);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         load_part<D>(vp, a.v_codes, a.v_scales, ph, off, log_p, g);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     // ---- the four waves' parts of the chunk
@@ -588,79 +604,106 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
     if (it.chunks < 2)
         return;
 
-    // ---- the last workgroup of the tile joins its chunks
-    uint32_t *count = cut.count + (int64_t)it.number * a.heads + head;
-    stores_done();
-    __syncthreads();
-    if (tid == 0)
-        s_last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)it.chunks - 1;
-    __syncthreads();
-    if (!s_last)
-        return;
-    if (tid == 0)
-        __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // sh threads share a row's four channels, a chunk each in turn
+    // ---- the last workgroup to finish joins the chunks, in their order.  A CU takes
+    // in some 40 GB/s of them, so many are joined in two steps, by groups of about as
+    // many as there are groups (92 chunks: 15 -> 6 us behind the last).
     const int real_rows = rows < FEW_ROWS ? rows : FEW_ROWS, work = real_rows * (D / 4);
-    int sharers = 1;
+    int sharers = 1;                                      // threads that share a row's four channels, a chunk each in turn
     while (2 * sharers * work <= 64 * FEW_WAVES)
         sharers *= 2;
-    const int64_t p0 = ((int64_t)it.item * a.heads + head) * FEW_ROWS, next = (int64_t)a.heads * FEW_ROWS;
+    const int64_t next = (int64_t)a.heads * FEW_ROWS;
     float *s_part = reinterpret_cast<float *>(s_v);                        // [thread][6]
-    for (int x0 = 0; x0 < work; x0 += 64 * FEW_WAVES) {
-        const int x = x0 + tid % (sharers > 1 ? 64 * FEW_WAVES / sharers : 64 * FEW_WAVES);
-        const int sh = sharers > 1 ? tid / (64 * FEW_WAVES / sharers) : 0;
-        const bool in = x < work;
-        const int r = in ? x / (D / 4) : 0, c = in ? 4 * (x % (D / 4)) : 0;
-        float mm = -INFINITY, ll = 0.f;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int i0 = sh; i0 < it.chunks; i0 += JB * sharers) {
-            float2 ml[JB], lo2[JB], hi2[JB];
+    auto is_last = [&](uint32_t *count, int n) {
+        stores_done();
+        __syncthreads();
+        if (tid == 0) {
+            s_last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)n - 1;
+            if (s_last)
+                __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        return s_last;
+    };
+    // n parts, the first of `item`, `by` items apart; into the first of them, or y
+    auto join = [&](int item, int by, int n, const float *part_ml, bool to_y) {
+        const int64_t p0 = ((int64_t)item * a.heads + head) * FEW_ROWS;
+        for (int x0 = 0; x0 < work; x0 += 64 * FEW_WAVES) {
+            const int x = x0 + tid % (64 * FEW_WAVES / sharers), sh = tid / (64 * FEW_WAVES / sharers);
+            const bool in = x < work;
+            const int r = in ? x / (D / 4) : 0, c = in ? 4 * (x % (D / 4)) : 0;
+            float mm = -INFINITY, ll = 0.f;
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+            for (int i0 = sh; i0 < n; i0 += JB * sharers) {
+                float2 ml[JB], lo2[JB], hi2[JB];
 #pragma unroll
-            for (int j = 0; j < JB; j++) {
-                const int i = i0 + j * sharers < it.chunks ? i0 + j * sharers : i0;
-                const int64_t p = p0 + i * next + r;
-                ml[j] = load_far(cut.part_ml + 2 * p);
-                lo2[j] = load_far(cut.part_o + p * D + c);
-                hi2[j] = load_far(cut.part_o + p * D + c + 2);
+                for (int j = 0; j < JB; j++) {
+                    const int i = i0 + j * sharers < n ? i0 + j * sharers : i0;
+                    const int64_t p = p0 + (int64_t)i * by * next + r;
+                    ml[j] = load_far(part_ml + 2 * p);
+                    lo2[j] = load_far(cut.part_o + p * D + c);
+                    hi2[j] = load_far(cut.part_o + p * D + c + 2);
+                }
+                float up = mm;
+#pragma unroll
+                for (int j = 0; j < JB; j++)
+                    up = fmaxf(up, ml[j].x);
+                const float ref = up == -INFINITY ? 0.f : up, f = __builtin_amdgcn_exp2f(mm - ref);
+                ll *= f;
+                sum *= f;
+                mm = up;
+#pragma unroll
+                for (int j = 0; j < JB; j++) {
+                    const float w = i0 + j * sharers < n ? __builtin_amdgcn_exp2f(ml[j].x - ref) : 0.f;
+                    if (w != 0.f) {
+                        ll += w * ml[j].y;
+                        sum += w * f32x4{lo2[j].x, lo2[j].y, hi2[j].x, hi2[j].y};
+                    }
+                }
             }
-            float up = mm;
+            if (sharers > 1) {
+                __syncthreads();
+                s_part[tid * 6] = mm;
+                s_part[tid * 6 + 1] = ll;
 #pragma unroll
-            for (int j = 0; j < JB; j++)
-                up = fmaxf(up, ml[j].x);
-            const float ref = up == -INFINITY ? 0.f : up, f = __builtin_amdgcn_exp2f(mm - ref);
-            ll *= f;
-            sum *= f;
-            mm = up;
-#pragma unroll
-            for (int j = 0; j < JB; j++) {
-                const float w = i0 + j * sharers < it.chunks ? __builtin_amdgcn_exp2f(ml[j].x - ref) : 0.f;
-                if (w != 0.f) {
-                    ll += w * ml[j].y;
-                    sum += w * f32x4{lo2[j].x, lo2[j].y, hi2[j].x, hi2[j].y};
+                for (int e = 0; e < 4; e++)
+                    s_part[tid * 6 + 2 + e] = sum[e];
+                __syncthreads();
+                if (sh == 0)
+                    for (int j = 1; j < sharers; j++) {
+                        const float *o2 = s_part + (tid + j * (64 * FEW_WAVES / sharers)) * 6;
+                        const float up = fmaxf(mm, o2[0]), ref = up == -INFINITY ? 0.f : up;
+                        const float f = __builtin_amdgcn_exp2f(mm - ref), w = __builtin_amdgcn_exp2f(o2[0] - ref);
+                        mm = up;
+                        ll = f * ll + w * o2[1];
+                        sum = f * sum + w * f32x4{o2[2], o2[3], o2[4], o2[5]};
+                    }
+            }
+            if (in && sh == 0) {
+                if (to_y)
+                    store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
+                else {
+                    // a row's m and l, which its other threads may still read, to a place of
+                    // their own
+                    store_far(cut.part_o + (p0 + r) * D + c, sum[0], sum[1]);
+                    store_far(cut.part_o + (p0 + r) * D + c + 2, sum[2], sum[3]);
+                    if (c == 0)
+                        store_far(cut.group_ml + 2 * (p0 + r), mm, ll);
                 }
             }
         }
-        if (sharers > 1) {
-            __syncthreads();
-            s_part[tid * 6] = mm;
-            s_part[tid * 6 + 1] = ll;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                s_part[tid * 6 + 2 + e] = sum[e];
-            __syncthreads();
-            if (sh == 0)
-                for (int j = 1; j < sharers; j++) {
-                    const float *o2 = s_part + (tid + j * (64 * FEW_WAVES / sharers)) * 6;
-                    const float up = fmaxf(mm, o2[0]), ref = up == -INFINITY ? 0.f : up;
-                    const float f = __builtin_amdgcn_exp2f(mm - ref), w = __builtin_amdgcn_exp2f(o2[0] - ref);
-                    mm = up;
-                    ll = f * ll + w * o2[1];
-                    sum = f * sum + w * f32x4{o2[2], o2[3], o2[4], o2[5]};
-                }
-        }
-        if (in && sh == 0)
-            store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
+    };
+    int size = it.chunks, groups = 1;
+    if (it.chunks > 2 * JB) {
+        size = (int)ceilf(__builtin_sqrtf((float)it.chunks));
+        groups = (it.chunks + size - 1) / size;
+        const int first_chunk = it.chunk / size * size, n = it.chunks - first_chunk < size ? it.chunks - first_chunk : size;
+        const int item = it.item + first_chunk;
+        if (!is_last(cut.count + COUNTS + (int64_t)item * a.heads + head, n))
+            return;
+        join(item, 1, n, cut.part_ml, false);
     }
+    if (is_last(cut.count + (int64_t)it.number * a.heads + head, groups > 1 ? groups : it.chunks))
+        join(it.item, groups > 1 ? size : 1, groups > 1 ? groups : it.chunks, groups > 1 ? cut.group_ml : cut.part_ml, true);
 }
 
 // -------------------------------------------------------------- many rows
@@ -761,21 +804,22 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
     // `ahead`) below UNITS and of V (of step ahead - AHEAD) from there on, a wave all
     // of the one or the other
     u32x4 code[L::U];
-    uint32_t byte[L::U], page[L::U];
+    uint32_t scales[L::U], page[L::U];
     bool gone[L::U];
     const uint32_t code_page = (uint32_t)a.heads * (D / 2) << log_p, scale_page = (uint32_t)a.heads * L::NB << log_p;
     const uint32_t last_page = (uint32_t)a.pages - 1;
     auto is_v = [&](int i) { return i * 64 * W + 64 * wave >= L::UNITS; };
     auto is_unit = [&](int i) { return 2 * L::UNITS % (64 * W) == 0 || i * 64 * W + 64 * wave < 2 * L::UNITS; };
     auto unit = [&](int i) { return i * 64 * W + tid - (is_v(i) ? L::UNITS : 0); };
+    // What is loaded is first touched a step later: a use of it here would wait for it.
+    auto real_key = [&](int ahead, int i) {
+        const int step = ahead - AHEAD * is_v(i);
+        return (step >= lo) & (step < hi) & (step * SK + unit(i) / L::NB < it.r.kv);
+    };
     auto find_pages = [&](int ahead) {
 #pragma unroll
-        for (int i = 0; i < L::U; i++) {
-            const int step = ahead - AHEAD * is_v(i), key = step * SK + unit(i) / L::NB;
-            const bool in = (step >= lo) & (step < hi) & (key < it.r.kv);
-            const uint32_t p = (uint32_t)table[in ? key >> log_p : 0];
-            page[i] = in ? p : 0u;
-        }
+        for (int i = 0; i < L::U; i++)
+            page[i] = (uint32_t)table[real_key(ahead, i) ? ((ahead - AHEAD * is_v(i)) * SK + unit(i) / L::NB) >> log_p : 0];
     };
     auto load = [&](int ahead) {
 #pragma unroll
@@ -783,12 +827,14 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             if (is_unit(i)) {
                 const int blk = unit(i) % L::NB;
                 const uint32_t off = (uint32_t)((ahead - AHEAD * is_v(i)) * SK + unit(i) / L::NB) & page_mask;
-                gone[i] = page[i] > last_page;
-                const uint32_t p = gone[i] ? 0u : page[i];
+                const bool in = real_key(ahead, i);
+                gone[i] = in & (page[i] > last_page);
+                const uint32_t p = in & !gone[i] ? page[i] : 0u;
                 code[i] = ld16((is_v(i) ? a.v_codes : a.k_codes) + ((uint64_t)p * code_page +
                                ((((uint32_t)head << log_p) + off) * (D / 2) + 16 * blk)));
-                byte[i] = (is_v(i) ? a.v_scales : a.k_scales)[(uint64_t)p * scale_page +
-                                                              ((((uint32_t)head * L::NB + blk) << log_p) + off)];
+                // the scales of four tokens, of which key % 4 is this unit's
+                scales[i] = *reinterpret_cast<const uint32_t *>((is_v(i) ? a.v_scales : a.k_scales) +
+                                (uint64_t)p * scale_page + ((((uint32_t)head * L::NB + blk) << log_p) + (off & ~3u)));
             }
     };
     // No branch: the stores are spread between matrix instructions.
@@ -797,12 +843,13 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
         for (int i = 0; i < L::U; i++)
             if (is_unit(i)) {
                 const int key = unit(i) / L::NB, blk = unit(i) % L::NB, step = ahead - AHEAD * is_v(i), at = step * SK + key;
+                const uint32_t byte = (scales[i] >> (8 * (key & 3))) & 255u;
                 // keys that no row of the tile sees hold anything: their V is zero.  A
                 // block of NaN in V is put in by hand, for the rows that see it
-                const bool seen = (at >= seen0) & (at < seen1) & !gone[i], nan = seen & (byte[i] == 255u);
+                const bool seen = (at >= seen0) & (at < seen1) & !gone[i], nan = seen & (byte == 255u);
                 const bool clear = is_v(i) & (!seen | nan), note = is_v(i) ? nan : gone[i];
                 s_flag[note ? step & 3 : 4][is_v(i)] = step + 1;
-                const float sc = kv4_scale(clear ? 127u : byte[i]);
+                const float sc = kv4_scale(clear ? 127u : byte);
                 // rows of V that start in the same banks take their words in another order
                 const int turn = is_v(i) ? key & 1 : 0;
                 uint8_t *p = s_kv + (step & 1) * L::BUF + (is_v(i) ? SK * L::KROW + key * L::VROW : key * L::KROW) + 64 * blk;
@@ -1042,7 +1089,7 @@ struct AttnLayout {
     int32_t target[2];              // 0: no cut; -1: no launch
     int32_t limit;                  // rows of a request up to which the kernel for few takes it
     int32_t wide;                   // eight waves a workgroup
-    size_t part_o[2], part_ml[2], total;
+    size_t part_o[2], part_ml[2], group_ml, total;
 };
 
 bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
@@ -1066,7 +1113,7 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
     L.limit = both ? FEW_LIMIT : 0x7FFFFFFF;
     L.wide = D <= 128 && rows * heads >= (int64_t)256 * 512;
     const int many = 32 * (L.wide ? 8 : 4);
-    size_t off = COUNTS * sizeof(uint32_t);           // first, whatever the sizes: calls of all sizes share it
+    size_t off = (COUNTS + GROUP_COUNTS) * sizeof(uint32_t);           // first, whatever the sizes: calls of all sizes share it
     for (int k = 0; k < 2; k++) {
         const int tile = k ? many : FEW_ROWS, goal = k ? MANY_ITEMS : FEW_ITEMS;
         const int64_t cut = (goal + heads - 1) / heads;
@@ -1093,6 +1140,10 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         off += (size_t)(room_rows * D) * sizeof(float);
         L.part_ml[k] = off;
         off += (size_t)(room_rows * 2) * sizeof(float);
+        if (!k) {
+            L.group_ml = off;
+            off += (size_t)(room_rows * 2) * sizeof(float);
+        }
     }
     L.total = off;
     return L;
@@ -1120,8 +1171,8 @@ hipError_t launch_attention(const AttnArgs &a, const AttnLayout &L, uint8_t *ws,
 {
     Cut c[2];
     for (int k = 0; k < 2; k++)
-        c[k] = {reinterpret_cast<float *>(ws + L.part_o[k]), reinterpret_cast<float *>(ws + L.part_ml[k]), k ? L.limit : 0,
-                k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST, (int32_t)L.items[k],
+        c[k] = {reinterpret_cast<float *>(ws + L.part_o[k]), reinterpret_cast<float *>(ws + L.part_ml[k]),
+                reinterpret_cast<float *>(ws + L.group_ml), k ? L.limit : 0, k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST, (int32_t)L.items[k],
                 reinterpret_cast<uint32_t *>(ws)};
     hipLaunchKernelGGL((few_rows_kernel<D>), dim3((unsigned)(L.items[0] * a.heads)), dim3(64 * FEW_WAVES), 0, s, a, c[0]);
     const hipError_t e = hipGetLastError();

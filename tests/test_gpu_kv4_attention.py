@@ -174,3 +174,81 @@ def test_repeats_bit_for_bit():
     want, lse = s.run(), s.lse
     for _ in range(3):
         assert torch.equal(s.run(), want) and torch.equal(s.lse, lse)
+
+
+@pytest.mark.parametrize("D,Hq,heads,n", [(64, 1, 1, 6000), (128, 8, 1, 20000), (96, 16, 1, 12000), (128, 2, 2, 33000), (256, 5, 1, 9000)])
+def test_many_chunks(D, Hq, heads, n):
+    """Chunks joined by groups, and groups joined."""
+    Step([n, 40], [1, 1], Hq, heads, D, 64, seed=n).check(f"{n} keys of D={D}, {Hq}/{heads}")
+
+
+def test_chunks_of_many_rows():
+    """A few dozen rows over a long context: cut, and joined by a second launch."""
+    Step([9000, 700], [40, 9], 4, 1, 64, 64, seed=12).check("40 rows on 9000 keys")
+    Step([5000], [70], 2, 1, 256, 16, seed=13).check("70 rows on 5000 keys, D=256")
+
+
+def test_one_workspace_for_calls_of_all_sizes():
+    """Calls of other sizes in between leave the counters as they found them."""
+    big = Step([6000, 300, 1, 900], [1, 60, 1, 2], 8, 2, 128, 16, seed=14)
+    small = Step([2500], [1], 8, 2, 128, 16, seed=15)
+    wide = Step([4000, 17], [1, 9], 16, 1, 256, 16, seed=16)
+    ws = max((sp.new_kv4_workspace(s.T, len(s.kv), max(s.fresh), s.Hq, s.kv4, s.width) for s in (big, small, wide)), key=len)
+    want = [s.run() for s in (big, small, wide)]
+    for _ in range(3):
+        for s, w in zip((big, small, wide), want):
+            assert torch.equal(s.run(workspace=ws), w)
+
+
+def test_in_a_graph():
+    """Captured once for the largest step and replayed on others: lengths, pages and
+    rows change, the launches do not."""
+    B, T, Hq, heads, D, P, width = 6, 40, 8, 2, 128, 16, 120
+    steps = [Step(kv, fresh, Hq, heads, D, P, seed=20 + i, pad=T - sum(fresh), width=width - max([1] + [-(-n // P) for n in kv]))
+             for i, (kv, fresh) in enumerate([([1900, 30, 1, 400, 64, 17], [1, 1, 1, 1, 1, 1]), ([50, 60, 20, 16, 0, 5], [30, 1, 3, 0, 0, 5]),
+                                              ([1, 1900, 1900, 3, 3, 3], [1, 1, 1, 1, 1, 1]), ([0] * 6, [0] * 6)])]
+    pages = max(s.cache.pages for s in steps)
+    kv = sp.new_kv4(pages, heads, D, P)
+    e = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")
+    q, table, start, n = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda"), e(B, width), e(B + 1), e(B)
+    y, lse = torch.empty_like(q), torch.empty(T, Hq, device="cuda")
+    ws = sp.new_kv4_workspace(T, B, 30, Hq, kv, width)
+    call = lambda y, lse, ws: sp.spear_kv4_attention(q, kv, table, start, n, 30, y=y, lse=lse, workspace=ws)
+
+    def put(s):
+        for mine, theirs in ((kv.k_codes, s.kv4.k_codes), (kv.k_scales, s.kv4.k_scales), (kv.v_codes, s.kv4.v_codes), (kv.v_scales, s.kv4.v_scales)):
+            mine[: theirs.shape[0]].copy_(theirs)
+        q.copy_(s.q), table.copy_(s.dtable), start.copy_(s.dstart), n.copy_(s.dkv)
+
+    put(steps[0])
+    call(y, lse, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(y, lse, ws)
+    for s in steps + steps[:2]:
+        put(s)
+        y.fill_(7.0), lse.fill_(7.0)
+        g.replay()
+        y2, lse2 = torch.full_like(y, 7.0), torch.full_like(lse, 7.0)
+        call(y2, lse2, None)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(lse, lse2)
+        s.lse = lse
+        s.check("replayed", y=y)
+
+
+def test_two_streams_at_once():
+    steps = [Step([3000, 70], [1, 40], 8, 2, 128, 16, seed=31), Step([40, 2500, 9], [9, 1, 1], 4, 4, 64, 32, seed=32)]
+    want = [s.run() for s in steps]
+    ws = [sp.new_kv4_workspace(s.T, len(s.kv), max(s.fresh), s.Hq, s.kv4, s.width) for s in steps]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(6):
+        for i, s in enumerate(steps):
+            got[i] = sp.spear_kv4_attention(s.q, s.kv4, s.dtable, s.dstart, s.dkv, max(s.fresh), y=got[i], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for s, g, w in zip(steps, got, want):
+        n = int(s.q_start[-1])
+        assert torch.equal(g[:n], w[:n])
