@@ -488,7 +488,8 @@ spear_status spear_rope_frequencies(int32_t rot, double base, int32_t kind, doub
  * spear_rope -- y = x with every head rotated to its row's position:
  *   y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t),
  *   t = position * freqs[i], (a, b) the i-th pair, m = scale
- * computed in fp64 and rounded once to bf16, so that far positions lose nothing.
+ * with angles, cosines and sines in fp64 (far positions lose nothing) and y off by
+ * 2^-23 |y| + 2^-38 |x| before it is rounded to bf16.
  *   x [T][H][D] bf16, x_stride elements from a row to the next (a multiple of 8,
  *     at least H D); y likewise with y_stride; x and y 16-byte aligned.  y may be
  *     x itself (then with its stride); it overlaps no other input.

@@ -23,6 +23,13 @@ __device__ __forceinline__ u32x4 kv4_bf16(uint32_t codes, float scale)
 // The scale byte as the power of two.
 __device__ __forceinline__ float kv4_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// Two fp32 to a pair of bf16 in one instruction.
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // Host: SPEAR_OK if the cache's pointers and sizes are as spear.h has them.
 spear_status check_kv4(const spear_kv4 *kv);
 

@@ -273,13 +273,6 @@ __device__ __forceinline__ uint2 read_turned(const void *p)
     return __builtin_bit_cast(uint2, v);
 }
 
-// Two fp32 to a pair of bf16 in one instruction.
-__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi)
-{
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
 // LDS written by this wave is read back by its other lanes: the order of the
 // wave's own accesses suffices, the compiler only has to keep it.
 __device__ __forceinline__ void wave_order()

@@ -169,7 +169,7 @@ struct RopeArgs {
     const double *freqs;             // NULL: nothing is rotated
     double scale;
     uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
-    int64_t places;                  // pages * P
+    int64_t places, T;               // pages * P; rows
     int32_t Hq, Hkv, D, rot, layout, log_p;
 };
 
@@ -189,9 +189,34 @@ __device__ __forceinline__ uint32_t quad(uint32_t v)
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
 
-// Eight channels of a block of 32 whose other channels the lane's quad holds ->
-// the eight codes; *byte the block's scale.
-__device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
+// The largest of the quad's lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v)
+{
+    uint32_t o = quad<0xB1>(v);                          // lanes 1 0 3 2
+    v = o > v ? o : v;
+    o = quad<0x4E>(v);                                   // lanes 2 3 0 1
+    return o > v ? o : v;
+}
+
+// The exponent of a block whose largest magnitude has the bits `top`, plus 127: a
+// mantissa of 1.75 or more carries into it.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t top)
+{
+    const int e = (int)((top + 0x200000u) >> 23) - 2;
+    return e < 2 ? 2u : (e > 252 ? 252u : (uint32_t)e);
+}
+
+__device__ __forceinline__ uint32_t codes8(const float (&f)[8], uint32_t e)
+{
+    const float s = kv4_scale(e);
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[0], f[1], s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[2], f[3], s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[4], f[5], s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[6], f[7], s, 3);
+}
+
+__device__ __forceinline__ uint32_t top8(const float (&f)[8])
 {
     uint32_t top = 0;
 #pragma unroll
@@ -199,30 +224,33 @@ __device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
         const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
         top = b > top ? b : top;
     }
-    uint32_t o = quad<0xB1>(top);                        // lanes 1 0 3 2 of the quad
-    top = o > top ? o : top;
-    o = quad<0x4E>(top);                                 // lanes 2 3 0 1
-    top = o > top ? o : top;
-    // a mantissa of 1.75 or more carries into the exponent
-    int e = (int)((top + 0x200000u) >> 23) - 2;
-    e = e < 2 ? 2 : (e > 252 ? 252 : e);
-    const float s = kv4_scale((uint32_t)e);
-    uint32_t r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[0], f[1], s, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[2], f[3], s, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[4], f[5], s, 2);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[6], f[7], s, 3);
-    *byte = top >= 0x7F800000u ? 255u : (uint32_t)e;     // a NaN or an infinity
-    return r;
+    return quad_max(top);
 }
 
-// A workgroup takes one row and up to N * (256 / (D / 8)) of its heads, a thread
-// eight channels (16 bytes) of up to N heads, always the same channels, so that
-// their cosines stay in registers.  The row is staged in LDS, where a channel
-// finds its partner whatever rot is; all reads of a head come before its writes
-// (a row may be rotated in place).  Angles, rotation and rounding are in fp64: at
-// position 2^20 an fp32 angle is off by 2^-5, and a value next to a border of
-// e2m1 would fall on the other side.
+// Eight channels of a block of 32 whose other channels the lane's quad holds ->
+// the eight codes; *byte the block's scale.
+__device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
+{
+    const uint32_t top = top8(f), e = block_exponent(top);
+    *byte = top >= 0x7F800000u ? 255u : e;               // a NaN or an infinity
+    return codes8(f, e);
+}
+
+// A workgroup takes up to N * (256 / (D / 8)) heads of a row; without the cache,
+// then of the row gridDim.x further on, whose channels are on their way while it
+// works on this one (6000 rows of 24 heads of 256: 28.7 -> 25.2 us, what a copy
+// takes; with the cache the loop's registers halve the workgroups of a CU, and
+// 8192 rows of 32 + 8 + 8 heads of 128 take 68 us for 50).  A thread has eight channels (16 bytes) of up to N heads, always the same
+// channels.  The row is staged in LDS, where a channel finds its partner whatever
+// rot is; all reads of a head come before its writes (a row may be rotated in
+// place).
+//
+// Angles, cosines and sines are fp64: at position 2^20 an fp32 angle is off by
+// 2^-5.  q is rotated in fp32 with the factors in two terms, of which the first
+// has 16 bits, so that its products with bf16 are exact: x c0 + p s0 is rounded
+// once, and r = (x c0 + p s0) + (x c1 + p s1) is off by 2^-23 |r| + 2^-38 |x, p|
+// before its rounding to bf16.  k, whose values next to a border of e2m1 would
+// fall on the other side, is rotated in fp64.
 template <int N, bool KV>
 __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
 {
@@ -231,103 +259,146 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
     const int tid = threadIdx.x, D = a.D, cph = D / 8, hpi = 256 / cph;
     const int hl = tid / cph, c = tid - hl * cph;
     const int heads = a.Hq + (KV ? 2 * a.Hkv : 0), h0 = blockIdx.y * (hpi * N) + hl;
-    const int64_t t = blockIdx.x;
     const int n = a.rot / 2;
+    const bool pairs = a.layout == SPEAR_ROPE_PAIRS, turn = a.freqs && 8 * c < a.rot;
     u32x4 x[N];
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int h = h0 + i * hpi;
-        x[i] = zero4();
-        if (hl < hpi && h < heads) {
-            const uint16_t *p = h < a.Hq ? a.q + t * a.qs + (int64_t)h * D
-                                : h < a.Hq + a.Hkv ? a.k + t * a.ks + (int64_t)(h - a.Hq) * D
-                                                   : a.v + t * a.vs + (int64_t)(h - a.Hq - a.Hkv) * D;
-            x[i] = ld16(p + 8 * c);
-        }
-    }
     int64_t slot = -1;
-    if (KV)
-        slot = a.slots[t];
-    if (a.freqs && tid < n) {
-        double s, co;
-        sincos((double)a.pos[t] * a.freqs[tid], &s, &co);
-        s_cs[tid] = make_double2(co * a.scale, s * a.scale);
-    }
+    int32_t pos = 0;
+    const double freq = a.freqs && tid < n ? a.freqs[tid] : 0.0;
+    auto load = [&](int64_t t) {
 #pragma unroll
-    for (int i = 0; i < N; i++)
-        s_x[i][tid] = x[i];
-    __syncthreads();
-    if (hl >= hpi)
-        return;
-
-    // y_j = x_j co_j + x_partner si_j for the channels below rot
-    const bool turn = a.freqs && 8 * c < a.rot;
-    double co[8], si[8];
-    int at[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int e = 8 * c + j;
-        co[j] = 1.0;
-        si[j] = 0.0;
-        at[j] = e;
-        if (a.freqs && e < a.rot) {
-            const bool second = a.layout == SPEAR_ROPE_PAIRS ? (e & 1) : e >= n;
-            const int i = a.layout == SPEAR_ROPE_PAIRS ? e >> 1 : (second ? e - n : e);
-            const double2 cs = s_cs[i];
-            co[j] = cs.x;
-            si[j] = second ? cs.y : -cs.y;
-            at[j] = a.layout == SPEAR_ROPE_PAIRS ? e ^ 1 : (second ? e - n : e + n);
+        for (int i = 0; i < N; i++) {
+            const int h = h0 + i * hpi;
+            if (hl < hpi && h < heads) {
+                const uint16_t *p = h < a.Hq ? a.q + t * a.qs + (int64_t)h * D
+                                    : h < a.Hq + a.Hkv ? a.k + t * a.ks + (int64_t)(h - a.Hq) * D
+                                                       : a.v + t * a.vs + (int64_t)(h - a.Hq - a.Hkv) * D;
+                x[i] = ld16(p + 8 * c);
+            }
         }
-    }
-    const bool there = KV && slot >= 0 && slot < a.places;
-    const int64_t page = slot >> a.log_p, off = slot & ((1 << a.log_p) - 1);
+        if (KV)
+            slot = a.slots[t];
+        if (a.freqs && tid < n)
+            pos = a.pos[t];
+    };
+    load(blockIdx.x);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        if (a.freqs && tid < n) {
+            double s, co;
+            sincos((double)pos * freq, &s, &co);
+            s_cs[tid] = make_double2(co * a.scale, s * a.scale);
+        }
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int h = h0 + i * hpi;
-        if (h >= heads)
-            continue;
-        const bool is_q = h < a.Hq, is_v = KV && h >= a.Hq + a.Hkv;
-        float f[8];
-        if (turn && !is_v) {
-            const uint16_t *row = reinterpret_cast<const uint16_t *>(&s_x[i][hl * cph]);
+        for (int i = 0; i < N; i++)
+            s_x[i][tid] = x[i];
+        const bool there = KV && slot >= 0 && slot < a.places;
+        const int64_t page = slot >> a.log_p, off = slot & ((1 << a.log_p) - 1);
+        __syncthreads();
+        if (!KV && t + gridDim.x < a.T)
+            load(t + gridDim.x);
+
+        // y_j = x_j c_j + x_partner s_j for the channels below rot (the others: c 1, s 0)
+        float c0[8], c1[8], s0[8], s1[8];
+        int at = 8 * c;                                   // (half) the first partner
+        if (turn) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const float own = bf16f((uint16_t)(x[i][j >> 1] >> (16 * (j & 1))));
-                const double r = (double)own * co[j] + (double)bf16f(row[at[j]]) * si[j];
-                f[j] = 8 * c + j < a.rot ? keep_odd(r) : own;
+                const int e = 8 * c + j;
+                const bool second = pairs ? (e & 1) : e >= n, in = e < a.rot;
+                const double2 cs = in ? s_cs[pairs ? e >> 1 : (second ? e - n : e)] : make_double2(1.0, 0.0);
+                const double sn = second ? cs.y : -cs.y;
+                c0[j] = __uint_as_float(__float_as_uint((float)cs.x) & 0xFFFFFF00u);
+                c1[j] = (float)(cs.x - (double)c0[j]);
+                s0[j] = __uint_as_float(__float_as_uint((float)sn) & 0xFFFFFF00u);
+                s1[j] = (float)(sn - (double)s0[j]);
             }
-        } else {
+            at += 8 * c >= n ? -n : n;
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int h = h0 + i * hpi;
+            if (hl >= hpi || h >= heads)
+                continue;
+            const bool is_q = h < a.Hq, is_v = KV && h >= a.Hq + a.Hkv;
+            const u32x4 own = s_x[i][tid];
+            float f[8];
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                f[j] = bf16f((uint16_t)(x[i][j >> 1] >> (16 * (j & 1))));
-        }
-        if (is_q) {
-            u32x4 o;
+                f[j] = bf16f((uint16_t)(own[j >> 1] >> (16 * (j & 1))));
+            if (turn && !is_v) {
+                const uint16_t *row = reinterpret_cast<const uint16_t *>(&s_x[i][hl * cph]);
+                float p[8];
+                if (pairs) {
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                o[j] = (uint32_t)f2bf(f[2 * j]) | ((uint32_t)f2bf(f[2 * j + 1]) << 16);
-            *reinterpret_cast<u32x4 *>(a.y + t * a.ys + (int64_t)h * D + 8 * c) = o;
-        } else if (KV && there) {
-            uint32_t byte;
-            const uint32_t codes = hold8(f, &byte);
-            const int64_t ph = page * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0));
-            uint8_t *cp = is_v ? a.v_codes : a.k_codes, *sp = is_v ? a.v_scales : a.k_scales;
-            *reinterpret_cast<uint32_t *>(cp + (((ph << a.log_p) + off) * (D / 2) + 4 * c)) = codes;
-            if ((c & 3) == 0)
-                sp[((ph * (D / 32) + (c >> 2)) << a.log_p) + off] = (uint8_t)byte;
+                    for (int j = 0; j < 8; j++)
+                        p[j] = f[j ^ 1];
+                } else if (n % 8 == 0) {                  // the partners lie in one chunk, as the channels do
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + at);
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        p[j] = bf16f((uint16_t)(v[j >> 1] >> (16 * (j & 1))));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const int e = 8 * c + j;
+                        p[j] = bf16f(row[e < n ? e + n : (e < a.rot ? e - n : e)]);
+                    }
+                }
+                if (is_q) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float r = __builtin_fmaf(f[j], c0[j], p[j] * s0[j]) + __builtin_fmaf(f[j], c1[j], p[j] * s1[j]);
+                        f[j] = 8 * c + j < a.rot ? r : f[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const int e = 8 * c + j;
+                        const bool second = pairs ? (e & 1) : e >= n;
+                        const double2 cs = s_cs[e < a.rot ? (pairs ? e >> 1 : (second ? e - n : e)) : 0];
+                        const double r = (double)f[j] * cs.x + (double)p[j] * (second ? cs.y : -cs.y);
+                        f[j] = e < a.rot ? keep_odd(r) : f[j];
+                    }
+                }
+            }
+            if (is_q) {
+                u32x4 o;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    o[j] = pair_bf16(f[2 * j], f[2 * j + 1]);
+                *reinterpret_cast<u32x4 *>(a.y + t * a.ys + (int64_t)h * D + 8 * c) = o;
+            } else if (KV && there) {
+                uint32_t byte;
+                const uint32_t codes = hold8(f, &byte);
+                const int64_t ph = page * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0));
+                uint8_t *cp = is_v ? a.v_codes : a.k_codes, *sp = is_v ? a.v_scales : a.k_scales;
+                *reinterpret_cast<uint32_t *>(cp + (((ph << a.log_p) + off) * (D / 2) + 4 * c)) = codes;
+                if ((c & 3) == 0)
+                    sp[((ph * (D / 32) + (c >> 2)) << a.log_p) + off] = (uint8_t)byte;
+            }
         }
+        if (KV)
+            return;
+        __syncthreads();                                  // the row has been read: the next one takes its place
     }
 }
+
+constexpr int64_t ROPE_BLOCKS = 1280;  // workgroups that run at once
 
 template <bool KV>
 hipError_t launch_rope(const RopeArgs &a, int64_t T, hipStream_t s)
 {
     const int heads = a.Hq + (KV ? 2 * a.Hkv : 0), hpi = 256 / (a.D / 8);
-    // few rows: more workgroups, a head a thread
-    if (T * heads <= (int64_t)hpi * 2048)
-        hipLaunchKernelGGL((rope_kernel<1, KV>), dim3((unsigned)T, (unsigned)((heads + hpi - 1) / hpi)), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((rope_kernel<4, KV>), dim3((unsigned)T, (unsigned)((heads + 4 * hpi - 1) / (4 * hpi))), dim3(256), 0, s, a);
+    // few rows: more workgroups, a head a thread; else as many as a row has, up to four
+    const int n = T * heads <= (int64_t)hpi * 2048 ? 1 : (heads + hpi - 1) / hpi;
+    const int64_t parts = (heads + hpi * (n < 4 ? n : 4) - 1) / (hpi * (n < 4 ? n : 4)), most = ROPE_BLOCKS / parts;
+    const dim3 grid((unsigned)(!KV && most < T ? (most < 1 ? 1 : most) : T), (unsigned)parts);
+    switch (n) {
+    case 1: hipLaunchKernelGGL((rope_kernel<1, KV>), grid, dim3(256), 0, s, a); break;
+    case 2: hipLaunchKernelGGL((rope_kernel<2, KV>), grid, dim3(256), 0, s, a); break;
+    case 3: hipLaunchKernelGGL((rope_kernel<3, KV>), grid, dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL((rope_kernel<4, KV>), grid, dim3(256), 0, s, a); break;
+    }
     return hipGetLastError();
 }
 
@@ -472,6 +543,7 @@ spear_status spear_rope(const spear_bf16 *x, int64_t x_stride, int64_t T, int32_
     a.layout = rope->layout;
     a.Hq = H;
     a.D = D;
+    a.T = T;
     return launch_rope<false>(a, T, (hipStream_t)stream) == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
 }
 
@@ -503,7 +575,7 @@ spear_status spear_rope_kv4_write(const spear_bf16 *q, int64_t q_stride, const s
     if (st != SPEAR_OK || T == 0)
         return st;
     RopeArgs a = {q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, positions, slots, rope ? rope->freqs : nullptr,
-                  rope ? rope->scale : 1.0, kv->k_codes, kv->k_scales, kv->v_codes, kv->v_scales, kv->pages * kv->P, Hq,
+                  rope ? rope->scale : 1.0, kv->k_codes, kv->k_scales, kv->v_codes, kv->v_scales, kv->pages * kv->P, T, Hq,
                   kv->heads, kv->D, rope ? rope->rot : 0, rope ? rope->layout : 0, __builtin_ctz(kv->P)};
     return launch_rope<true>(a, T, (hipStream_t)stream) == hipSuccess ? SPEAR_OK : SPEAR_E_HIP;
 }

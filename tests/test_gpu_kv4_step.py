@@ -89,10 +89,14 @@ def test_plan_in_a_graph():
 
 # ------------------------------------------------------------------------ rope
 def same_bf16(got, want64):
-    """got is the bf16 nearest to want64 (its angles are good to 2^-50 of a turn)."""
+    """got is want64 rounded to bf16, from a value that is off by 2^-23 |y| + 2^-38 |x|:
+    the factors are held as c0 + c1 with c1 2^-16 of c0 and rounded (2^-41); x c0 +
+    p s0 is rounded once (2^-24 of its size), so are the small terms' product and sum
+    (2^-40 each) and the last sum (2^-24)."""
     w = torch.from_numpy(want64)
     err = (got.double().cpu() - w).abs().numpy()
-    assert (err <= ref_kv4.HALF_BF16 * np.abs(want64) * (1 + 1e-9) + 1e-300 + 1e-9 * np.abs(want64).max() * 2.0 ** -10).all()
+    before = 2.0 ** -23 * np.abs(want64) + 2.0 ** -38 * np.abs(want64).max() * 4
+    assert (err <= ref_kv4.HALF_BF16 * (np.abs(want64) + before) + before).all()
 
 
 @pytest.mark.parametrize("layout", [sp.ROPE_HALF, sp.ROPE_PAIRS])
@@ -207,3 +211,24 @@ def test_write_behind_4_gib():
     want = ref_kv4.value(*ref_kv4.hold(x64))
     want[3] = 0.0
     assert np.array_equal(to64(k), want) and np.array_equal(to64(v), want)
+
+
+@pytest.mark.parametrize("layout", [sp.ROPE_HALF, sp.ROPE_PAIRS])
+def test_rotated_keys_next_to_the_borders(layout):
+    """Keys made so that many rotated channels lie within a few fp32 steps of a tie or
+    of the exponent's step: the codes are those of the exact rotation."""
+    rng = np.random.default_rng(3)
+    T, D, heads, P = 400, 128, 2, 64
+    f = sp.spear_rope_frequencies(D)
+    pos = rng.integers(0, 1 << 20, T).astype(np.int32)
+    target = rng.choice(np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0, 0.0]), (T, heads, D)) * rng.choice([-1.0, 1.0], (T, heads, D))
+    k, k64 = bf16(ref_kv4.rotate(target, -pos.astype(np.int64), f.numpy(), layout) * np.exp2(rng.integers(-8, 8, (T, heads, 1))))
+    small = rng.random((T, heads, 1)) < 0.2              # and pairs of very different size
+    k = torch.where(torch.from_numpy(small).cuda() & (torch.arange(D, device="cuda") % 7 == 0), k * 2.0 ** -20, k)
+    k64 = to64(k)
+    slots = np.arange(T, dtype=np.int64)
+    kv, cache = sp.new_kv4(-(-T // P), heads, D, P), ref_kv4.Cache(-(-T // P), heads, D, P, rng)
+    sp.spear_rope_kv4_write(k, k, k, dev(pos), dev(slots), sp.Rope(f.cuda(), layout), kv)
+    cache.write("k", slots, ref_kv4.rotate(k64, pos, f.numpy(), layout))
+    got, _ = sp.spear_kv4_read(kv, dev(slots))
+    assert np.array_equal(to64(got), cache.read("k", slots))
