@@ -478,10 +478,11 @@ class _On:
 def _on(fn: str, device, stream, call):
     """call(stream handle) with the device and stream current.  Small layers take
     10 us on the GPU, so nothing is switched that already is as it should be."""
+    index = device.index                                  # None on the CPU
+    if stream is None and index is not None and index == _current_device():
+        return call(_current_stream(index))
     if device.type != "cuda":
         _bad(fn, E_ARG, f"tensors are on {device}, not on a GPU")
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(_current_stream(device.index))
     with _On(device, stream):
         return call(_current_stream(device.index))
 
@@ -490,8 +491,9 @@ def _public_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# torch's own raw query, where it has one (0.1 us for 1.2)
+# torch's own raw queries, where it has them (0.1 us for 1.2, 0.05 for 0.25)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 # The C structs as packed bytes, a fifth of the time of filling ctypes
 # structures field by field.
@@ -803,17 +805,18 @@ class Rope:
 def _want_rows(fn: str, name: str, t, shape, device) -> int:
     """A [T][H][D] bf16 tensor whose rows may lie apart (a part of a wider row);
     -> elements from row to row."""
+    T, H, D = shape
+    if t.shape == shape and t.dtype in _BF16 and t.device == device:
+        row, head, channel = t.stride()
+        if channel == 1 and (head == D or H == 1):
+            return row if T > 1 else H * D
     if t.dtype not in _BF16:
         _bad(fn, E_ARG, f"{name} has type {t.dtype}")
     if t.shape != shape:
         _bad(fn, E_SHAPE, f"{name} has shape {tuple(t.shape)}, not {shape}")
     if t.device != device:
         _bad(fn, E_ARG, f"{name} is on {t.device}, not {device}")
-    T, H, D = shape
-    row, head, channel = t.stride()
-    if (D > 1 and channel != 1) or (H > 1 and head != D):
-        _bad(fn, E_ARG, f"{name} has gaps within a row")
-    return row if T > 1 else H * D
+    _bad(fn, E_ARG, f"{name} has gaps within a row")
 
 
 def spear_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
@@ -822,9 +825,10 @@ def spear_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
     position; y may be x itself."""
     fn = "spear_rope"
     dev = x.device
-    if x.dim() != 3:
-        _bad(fn, E_SHAPE, f"x has {x.dim()} dimensions, not 3")
-    shape = T, H, D = tuple(int(v) for v in x.shape)
+    shape = x.shape
+    if len(shape) != 3:
+        _bad(fn, E_SHAPE, f"x has {len(shape)} dimensions, not 3")
+    T, H, D = shape
     xs = _want_rows(fn, "x", x, shape, dev)
     _want(fn, "positions", positions, _I32, (T,), dev)
     ys = H * D if y is None else _want_rows(fn, "y", y, shape, dev)
