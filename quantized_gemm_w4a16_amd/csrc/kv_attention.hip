@@ -18,11 +18,13 @@ namespace {
 constexpr int STEP = 64;            // keys of a step
 constexpr int FEW_ROWS = 16;        // rows of a tile of the kernel for few rows
 constexpr int FEW_WAVES = 4;        // its waves, which take the steps of a chunk in turn
-constexpr int FEW_LEAST = 4;        // steps of a chunk, at least
-constexpr int FEW_ITEMS = 768;      // items of all key heads that the cut aims at: three a CU
+constexpr int FEW_ITEMS = 768;      // items of all key heads that the cut aims at: three a CU (wide heads two)
+// Steps of a chunk, at least: a join costs as much as some steps, and pays where
+// there are CUs without work.  us with 4 / 16: one request of 1021 keys and 8 heads 9.4
+// / 11.4, 300 tiles of up to 5 steps 16.5 / 10.7, 450 tiles of up to 25 53 / 43.
+constexpr int FEW_LEAST = 4, FEW_LEAST_FULL = 16;
 constexpr int JB = 8;               // chunks whose parts are on their way at once in the join
 constexpr int MANY_LEAST = 4;       // steps of its chunks, at least
-constexpr int MANY_ITEMS = 512;     // items of all key heads that its cut aims at
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 
@@ -44,7 +46,7 @@ struct Cut {
     float *group_ml;                // as part_ml, of groups of chunks
     int32_t rows0, rows1;           // requests of rows0 < rows <= rows1
     int32_t target;                 // items of a key head that the cut aims at; 0: no cut
-    int32_t least;                  // steps of a chunk, at least
+    int32_t least, least_full;      // steps of a chunk, at least: with few tiles, with a tile a CU
     int32_t most;                   // items of a key head that there is room for
     uint32_t *count;                // [tile][key head] parts that are done; then [item][key head] chunks of a
                                     // group; all 0 between calls
@@ -132,17 +134,22 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
     Item it;
     it.found = false;
     it.size = 0x7FFFFFFF;
+    int32_t uncut = 0;                                    // steps below which a tile stays whole
     if (c.target) {
-        float work = 0.f;
+        float work = 0.f, tiles = 0.f;
         for (int b0 = 0; b0 < a.B; b0 += 64) {
             const int b = b0 + lane;
             if (b < a.B) {
                 const Request r = request_of(a, c, b, ROWS);
                 work += (float)r.tiles * (float)r.steps;
+                tiles += (float)r.tiles;
             }
         }
         const float s = ceilf(total64(work) / (float)c.target);
-        it.size = s < (float)c.least ? c.least : (s > 1e9f ? 1000000000 : (int32_t)s);
+        const float fill = total64(tiles) * (float)a.heads * (float)c.least_full * (1.f / 256.f);
+        const int32_t least = fill > (float)c.least_full ? c.least_full : (fill < (float)c.least ? c.least : (int32_t)fill);
+        it.size = s < (float)least ? least : (s > 1e9f ? 1000000000 : (int32_t)s);
+        uncut = 2 * least;
     }
     int32_t items0 = 0, tiles0 = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -151,7 +158,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
         Request r = {};
         if (b < a.B) {
             r = request_of(a, c, b, ROWS);
-            chunks = r.steps <= it.size ? 1 : (r.steps + it.size - 1) / it.size;
+            chunks = r.steps <= it.size || r.steps < uncut ? 1 : (r.steps + it.size - 1) / it.size;
             tiles = r.tiles < c.most ? r.tiles : c.most;
             const int64_t all = (int64_t)r.tiles * chunks;
             n = all < c.most ? (int32_t)all : c.most;
@@ -170,6 +177,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             it.r.base = bcast(r.base, src);
             it.r.steps = bcast(r.steps, src);
             it.chunks = bcast(chunks, src);
+            it.size = (it.r.steps + it.chunks - 1) / it.chunks;
             it.tile = by_tile ? want - first_tile : (want - first_item) / it.chunks;
             it.chunk = by_tile ? 0 : (want - first_item) % it.chunks;
             it.item = first_item + it.tile * it.chunks;
@@ -734,9 +742,6 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
 {
     using L = Tiles<D, W>;
     constexpr int DT = D / 32, KS = D / 16, ROWS = 32 * W, KT = L::KT, SK = L::SK;
-    // The scores of a step are formed one step ahead, beside the exponentials of the
-    // step before, where there are registers for two steps' scores.
-    constexpr int AHEAD = D <= 128 ? 1 : 0;
     extern __shared__ __attribute__((aligned(16))) uint8_t s_kv[];         // two buffers of K rows, then V rows
     __shared__ int32_t s_flag[5][2];       // step + 1 if a page of its keys is gone; ... if its V has a block of NaN
 
@@ -793,9 +798,8 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
         for (int r = 0; r < 16; r++)
             o[d][r] = 0.f;
 
-    // ---- codes on their way: unit u is a block of 32 channels of a key, of K (of step
-    // `ahead`) below UNITS and of V (of step ahead - AHEAD) from there on, a wave all
-    // of the one or the other
+    // ---- codes on their way: unit u is a block of 32 channels of a key, of K below
+    // UNITS and of V from there on, a wave all of the one or the other
     u32x4 code[L::U];
     uint32_t scales[L::U], page[L::U];
     bool gone[L::U];
@@ -805,22 +809,19 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
     auto is_unit = [&](int i) { return 2 * L::UNITS % (64 * W) == 0 || i * 64 * W + 64 * wave < 2 * L::UNITS; };
     auto unit = [&](int i) { return i * 64 * W + tid - (is_v(i) ? L::UNITS : 0); };
     // What is loaded is first touched a step later: a use of it here would wait for it.
-    auto real_key = [&](int ahead, int i) {
-        const int step = ahead - AHEAD * is_v(i);
-        return (step >= lo) & (step < hi) & (step * SK + unit(i) / L::NB < it.r.kv);
-    };
-    auto find_pages = [&](int ahead) {
+    auto real_key = [&](int step, int i) { return (step < hi) & (step * SK + unit(i) / L::NB < it.r.kv); };
+    auto find_pages = [&](int step) {
 #pragma unroll
         for (int i = 0; i < L::U; i++)
-            page[i] = (uint32_t)table[real_key(ahead, i) ? ((ahead - AHEAD * is_v(i)) * SK + unit(i) / L::NB) >> log_p : 0];
+            page[i] = (uint32_t)table[real_key(step, i) ? (step * SK + unit(i) / L::NB) >> log_p : 0];
     };
-    auto load = [&](int ahead) {
+    auto load = [&](int step) {
 #pragma unroll
         for (int i = 0; i < L::U; i++)
             if (is_unit(i)) {
                 const int blk = unit(i) % L::NB;
-                const uint32_t off = (uint32_t)((ahead - AHEAD * is_v(i)) * SK + unit(i) / L::NB) & page_mask;
-                const bool in = real_key(ahead, i);
+                const uint32_t off = (uint32_t)(step * SK + unit(i) / L::NB) & page_mask;
+                const bool in = real_key(step, i);
                 gone[i] = in & (page[i] > last_page);
                 const uint32_t p = in & !gone[i] ? page[i] : 0u;
                 code[i] = ld16((is_v(i) ? a.v_codes : a.k_codes) + ((uint64_t)p * code_page +
@@ -831,11 +832,11 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             }
     };
     // No branch: the stores are spread between matrix instructions.
-    auto store = [&](int ahead) {
+    auto store = [&](int step) {
 #pragma unroll
         for (int i = 0; i < L::U; i++)
             if (is_unit(i)) {
-                const int key = unit(i) / L::NB, blk = unit(i) % L::NB, step = ahead - AHEAD * is_v(i), at = step * SK + key;
+                const int key = unit(i) / L::NB, blk = unit(i) % L::NB, at = step * SK + key;
                 const uint32_t byte = (scales[i] >> (8 * (key & 3))) & 255u;
                 // keys that no row of the tile sees hold anything: their V is zero.  A
                 // block of NaN in V is put in by hand, for the rows that see it
@@ -853,7 +854,6 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
                 }
             }
     };
-    f32x16 s[KT];
     auto scores = [&](int step, f32x16 (&z)[KT]) {
         const uint8_t *sk = s_kv + (step & 1) * L::BUF + n * L::KROW + 16 * h;
 #pragma unroll
@@ -877,23 +877,15 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
         store(lo);
         load(lo + 1);
         find_pages(lo + 2);
-        if constexpr (AHEAD) {
-            store(lo + 1);
-            load(lo + 2);
-            find_pages(lo + 3);
-            __syncthreads();
-            scores(lo, s);
-        }
-        __syncthreads();                                  // before K of the step after next takes its place
+        __syncthreads();
     }
 
-    // Step: the scores of the next step are formed, and its V and the K of the one
-    // behind it (AHEAD = 0: its own scores, the next step's K and V) go to LDS, while
-    // this step's probabilities are formed and used.
-    auto body = [&](int step, f32x16 (&s)[KT], f32x16 (&z)[KT]) {
+    // The next step's K and V go to LDS while this one's probabilities are formed and
+    // used: the compiler spreads them between the matrix instructions.
+    for (int step = lo; step < hi; step++) {
         const int key0 = step * SK;
-        if constexpr (!AHEAD)
-            scores(step, s);
+        f32x16 s[KT];
+        scores(step, s);
         uint64_t lost = 0;
         if (__builtin_amdgcn_readfirstlane(s_flag[step & 3][0]) == step + 1) {
             const int key = key0 + lane;
@@ -925,8 +917,6 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
                 o[d] *= f;
         }
         const float m0 = m == -INFINITY ? 0.f : -m;
-        if constexpr (AHEAD)
-            scores(step + 1, z);
         u32x4 p[KT][2];
 #pragma unroll
         for (int kt = 0; kt < KT; kt++) {
@@ -939,9 +929,9 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             for (int r = 0; r < 8; r++)
                 p[kt][r / 4][r % 4] = pair_bf16(s[kt][2 * r], s[kt][2 * r + 1]);
         }
-        store(step + 1 + AHEAD);
-        load(step + 2 + AHEAD);
-        find_pages(step + 3 + AHEAD);
+        store(step + 1);
+        load(step + 2);
+        find_pages(step + 3);
         const uint8_t *sv = s_kv + (step & 1) * L::BUF + SK * L::KROW + (4 * h + ((lane & 15) >> 2)) * L::VROW +
                             32 * ((lane >> 4) & 1) + 8 * (lane & 3);
 #pragma unroll
@@ -970,16 +960,6 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             }
         }
         __syncthreads();
-    };
-    f32x16 z[KT];
-    for (int step = lo; step < hi; step += 2) {
-        body(step, s, z);
-        if (step + 1 < hi) {
-            if constexpr (AHEAD)
-                body(step + 1, z, s);
-            else
-                body(step + 1, s, z);
-        }
     }
 
     auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
@@ -1095,21 +1075,33 @@ bool attention_sizes(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_
            width >= 1 && width <= SPEAR_MAX_CONTEXT / P && T * Hq <= (int64_t)1 << 27;
 }
 
-constexpr int FEW_LIMIT = 32;       // rows of a request up to which the kernel for few takes it
+// Requests of up to FEW_LIMIT rows take the kernel for few rows, and so do all of a
+// step of few rows and keys (all heads), which that one spreads over more
+// workgroups and without a second launch.  us, few / both: 300 rows of a prompt, 16
+// heads over 8, 17 / 26; 1000 rows 24 / 38; 64 rows on 8192 keys, 32 over 8, 34 / 40
+// (2^24 rows x keys); 16 requests of 20 rows on up to 3000, 73 / 52 (2^25); 256 rows
+// on 8192 107 / 62.  The keys are what the table has room for; an entry wider than
+// the lengths takes both.
+constexpr int FEW_LIMIT = 32;
+constexpr int64_t FEW_WORK = (int64_t)1 << 24;
+// Eight waves a workgroup, which share the staging of a step's keys, if requests fill
+// them (1024 rows a key head on 8192 keys 187 -> 166 us; 80 rows 52 -> 70).
+constexpr int WIDE_ROWS = 256;
 
-AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_t heads, int32_t D)
+AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_t heads, int32_t D, int64_t keys)
 {
     AttnLayout L;
     const int64_t G = Hq / heads, rows = T * G, more = T < B ? T : B;
-    // Requests of more rows than the limit take the other kernel, if there may be any.
-    const bool both = T > 0 && max_fresh * G > FEW_LIMIT;
-    L.limit = both ? FEW_LIMIT : 0x7FFFFFFF;
-    L.wide = D <= 128 && rows * heads >= (int64_t)256 * 512;
+    max_fresh = max_fresh < T ? max_fresh : T;
+    const bool both = T > 0 && max_fresh * G > FEW_LIMIT && rows * heads > FEW_WORK / (keys < 1 ? 1 : keys);
+    L.limit = both ? FEW_LIMIT : 0x7FFFFFFF;              // (one kernel alone takes all)
+    L.wide = D <= 128 && max_fresh * G >= WIDE_ROWS;
     const int many = 32 * (L.wide ? 8 : 4);
+    const int resident = L.wide || D > 192 ? 256 : 512;   // workgroups of the kernel for many rows
     size_t off = (COUNTS + GROUP_COUNTS) * sizeof(uint32_t);           // first, whatever the sizes: calls of all sizes share it
     for (int k = 0; k < 2; k++) {
-        const int tile = k ? many : FEW_ROWS, goal = k ? MANY_ITEMS : FEW_ITEMS;
-        const int64_t cut = (goal + heads - 1) / heads;
+        const int tile = k ? many : FEW_ROWS, goal = k ? resident : (D > 128 ? 512 : FEW_ITEMS);
+        const int64_t cut = (goal + heads - 1) / heads, most_cut = ((k ? 512 : FEW_ITEMS) + heads - 1) / heads;
         // tiles of a key head: at most one more a request than its rows fill (few
         // rows: at most what a request may have), and no fewer than all rows fill
         // and requests of max_fresh rows make
@@ -1127,7 +1119,7 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         // The room of the parts does not depend on max_fresh and grows with T and B,
         // so that a workspace of the largest step serves every other: ...
         const int64_t fewest = k ? rows / 128 : rows / FEW_ROWS;
-        const int64_t room = (fewest < cut ? fewest : cut) + more + cut + 16;
+        const int64_t room = (fewest < most_cut ? fewest : most_cut) + more + most_cut + 16;
         const int64_t room_rows = room * heads * (k ? 256 : FEW_ROWS);
         L.part_o[k] = off;
         off += (size_t)(room_rows * D) * sizeof(float);
@@ -1165,7 +1157,8 @@ hipError_t launch_attention(const AttnArgs &a, const AttnLayout &L, uint8_t *ws,
     Cut c[2];
     for (int k = 0; k < 2; k++)
         c[k] = {reinterpret_cast<float *>(ws + L.part_o[k]), reinterpret_cast<float *>(ws + L.part_ml[k]),
-                reinterpret_cast<float *>(ws + L.group_ml), k ? L.limit : 0, k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST, (int32_t)L.items[k],
+                reinterpret_cast<float *>(ws + L.group_ml), k ? L.limit : 0, k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST,
+                k ? MANY_LEAST : FEW_LEAST_FULL, (int32_t)L.items[k],
                 reinterpret_cast<uint32_t *>(ws)};
     hipLaunchKernelGGL((few_rows_kernel<D>), dim3((unsigned)(L.items[0] * a.heads)), dim3(64 * FEW_WAVES), 0, s, a, c[0]);
     const hipError_t e = hipGetLastError();
@@ -1187,7 +1180,7 @@ extern "C" {
 size_t spear_kv4_attention_workspace_size(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
                                           int32_t heads, int32_t D, int64_t width, int32_t P)
 {
-    return attention_sizes(T, B, max_fresh, Hq, heads, D, width, P) ? attention_layout(T, B, max_fresh, Hq, heads, D).total : 0;
+    return attention_sizes(T, B, max_fresh, Hq, heads, D, width, P) ? attention_layout(T, B, max_fresh, Hq, heads, D, width * P).total : 0;
 }
 
 spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t T, int32_t Hq,
@@ -1209,7 +1202,8 @@ spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t 
         return SPEAR_E_ARG;
     if (!al(q, 16) || !al(y, 16) || !al(table, 4) || !al(q_start, 4) || !al(kv_len, 4) || !al(lse, 4) || !al(workspace, 256))
         return SPEAR_E_ALIGN;
-    const AttnLayout L = attention_layout(T, B, max_fresh, Hq, kv->heads, kv->D);
+    const AttnLayout L = attention_layout(T, B, max_fresh, Hq, kv->heads, kv->D,
+                                          window && window + max_fresh < width * kv->P ? window + max_fresh : width * kv->P);
     if (ws_bytes < L.total)
         return SPEAR_E_WORKSPACE;
     st = check_device();

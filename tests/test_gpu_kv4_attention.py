@@ -12,6 +12,13 @@ pytestmark = pytest.mark.gpu
 DIMS = [64, 96, 128, 192, 256]
 
 
+def room(P, many):
+    """Table columns behind the pages.  A step of few rows and keys takes the kernel
+    for few rows alone, and the keys are what the table has room for: with room for
+    2^24, requests of more than 32 rows take the kernel for many."""
+    return (1 << 24) // P if many else 0
+
+
 @pytest.mark.parametrize("D", DIMS)
 @pytest.mark.parametrize("Hq,heads,P", [(1, 1, 16), (8, 8, 64), (8, 2, 128), (5, 1, 32), (16, 1, 1024), (24, 1, 256)])
 def test_one_token(D, Hq, heads, P):
@@ -28,24 +35,42 @@ def test_one_request(n, D):
 
 @pytest.mark.parametrize("D", DIMS)
 @pytest.mark.parametrize("Hq,heads", [(1, 1), (6, 2), (7, 1)])
-def test_few_and_many_tokens(D, Hq, heads):
+@pytest.mark.parametrize("many", [False, True])
+def test_few_and_many_tokens(D, Hq, heads, many):
     """Requests of one token, of a few and of whole prompts side by side."""
     fresh = [1, 2, 3, 17, 40, 5, 70, 1]
     kv = [90, 2, 64, 17, 101, 128, 70, 1]
-    Step(kv, fresh, Hq, heads, D, 32, seed=D + Hq, pad=5).check(f"mixed D={D} {Hq}/{heads}")
+    Step(kv, fresh, Hq, heads, D, 32, seed=D + Hq, pad=5, width=room(32, many)).check(f"mixed D={D} {Hq}/{heads} many={many}")
+
+
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("fresh,G", [(33, 1), (64, 2), (65, 4), (130, 2), (257, 1), (300, 3)])
+def test_chunks_of_a_prompt(D, fresh, G):
+    """Rows that end inside a tile of 128 or 256, on keys that end inside a step."""
+    Step([fresh + 3, fresh, fresh + 200], [fresh, fresh, 1], G, 1, D, 16, seed=fresh, pad=1, width=room(16, True)).check(
+        f"{fresh} rows x {G}, D={D}")
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 100, 1 << 30])
-@pytest.mark.parametrize("D", [64, 128])
-def test_windows(window, D):
-    Step([5, 64, 200, 333, 90, 1], [1, 64, 3, 50, 1, 1], 4, 2, D, 16, seed=window % 97, pad=2).check(
-        f"window {window} D={D}", window=window)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("pad", [2, 1 << 18])
+def test_windows(window, D, pad):
+    """(with many padded rows, requests of more than 32 take the kernel for many)"""
+    s = Step([5, 64, 200, 333, 90, 1], [1, 64, 3, 50, 1, 1], 4, 2, D, 16, seed=window % 97, pad=2)
+    s.check(f"window {window} D={D}", window=window)
+    if pad > 2:
+        q = torch.zeros(pad, 4, D, dtype=torch.bfloat16, device="cuda")
+        q[: s.T] = s.q
+        y = sp.spear_kv4_attention(q, s.kv4, s.dtable, s.dstart, s.dkv, 64, window=window, y=torch.full_like(q, 7.0))
+        s.check(f"window {window} D={D} of {pad} rows", y=y[: s.T], window=window)
+        assert bool((y[s.T:] == 7.0).all())
 
 
 @pytest.mark.parametrize("fresh", [[1, 1, 1], [0, 5, 40]])
-def test_rows_that_see_nothing(fresh):
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_that_see_nothing(fresh, many):
     """No keys at all, fewer keys than rows, requests without rows."""
-    s = Step([0, 3, 20], fresh, 4, 2, 128, 16, seed=3, pad=3)
+    s = Step([0, 3, 20], fresh, 4, 2, 128, 16, seed=3, pad=3, width=room(16, many))
     y = s.check("rows without keys")
     for b, n in enumerate(s.kv):
         t0, t1 = s.q_start[b], s.q_start[b + 1]
@@ -66,12 +91,12 @@ def test_no_rows_no_requests():
     assert bool((y == 7.0).all())
 
 
-@pytest.mark.parametrize("window", [0, 40])
-def test_masked_places_may_hold_anything(window):
+@pytest.mark.parametrize("window,many", [(0, False), (0, True), (40, False)])
+def test_masked_places_may_hold_anything(window, many):
     """NaN in keys and values that some rows see and others do not: only the
     rows that see them are NaN; pages that were let go are as if masked."""
     for seed, D in enumerate(DIMS):
-        s = Step([70, 130, 200, 33], [20, 1, 60, 2], 4, 2, D, 16, seed=seed, pad=2)
+        s = Step([70, 130, 200, 33], [20, 1, 60, 2], 4, 2, D, 16, seed=seed, pad=2, width=room(16, many))
         c = s.cache
         def spoil(b, key, name, head, block):
             c.scales[name][s.table[b, key // 16], head, block, key % 16] = 255
@@ -85,11 +110,12 @@ def test_masked_places_may_hold_anything(window):
         s.table[2, 5] = 2 ** 31 - 1
         s.table[3, 0] = -2 ** 31
         s.to_device()
-        s.check(f"masked places D={D} window={window}", window=window)
+        s.check(f"masked places D={D} window={window} many={many}", window=window)
 
 
-def test_every_page_let_go():
-    s = Step([40, 70], [1, 30], 2, 1, 64, 16, seed=1)
+@pytest.mark.parametrize("many", [False, True])
+def test_every_page_let_go(many):
+    s = Step([40, 70], [1, 30], 2, 1, 64, 16, seed=1, width=room(16, many))
     s.table[:] = -1
     s.to_device()
     y = s.check("no pages")
@@ -111,12 +137,14 @@ def test_lengths_beyond_the_table_are_held():
 
 
 @pytest.mark.parametrize("q_sd,scale", [(40.0, None), (1e-3, None), (1.0, 3.0), (1.0, 1e-20), (1e18, 1e-18)])
-def test_sharp_and_flat_rows(q_sd, scale):
-    Step([200, 90], [1, 33], 4, 2, 128, 32, seed=9, q_sd=q_sd).check(f"q of {q_sd}, scale {scale}", scale=scale)
+@pytest.mark.parametrize("many", [False, True])
+def test_sharp_and_flat_rows(q_sd, scale, many):
+    Step([200, 90], [1, 33], 4, 2, 128, 32, seed=9, q_sd=q_sd, width=room(32, many)).check(f"q of {q_sd}, scale {scale}", scale=scale)
 
 
-def test_infinite_queries_stay_in_their_rows():
-    s = Step([50, 40], [1, 30], 2, 1, 64, 16, seed=4)
+@pytest.mark.parametrize("many", [False, True])
+def test_infinite_queries_stay_in_their_rows(many):
+    s = Step([50, 40], [1, 30], 2, 1, 64, 16, seed=4, width=room(16, many))
     want = s.run()
     s.q[3, 1, 7], s.q[9, 0, 0] = float("inf"), float("nan")
     got = s.run()
@@ -125,8 +153,9 @@ def test_infinite_queries_stay_in_their_rows():
     assert bool(got[spoilt].isnan().all()) and torch.equal(got[~spoilt], want[~spoilt])
 
 
-def test_strided_queries_in_place_and_without_lse():
-    s = Step([50, 40, 200], [1, 30, 2], 6, 2, 128, 16, seed=6)
+@pytest.mark.parametrize("many", [False, True])
+def test_strided_queries_in_place_and_without_lse(many):
+    s = Step([50, 40, 200], [1, 30, 2], 6, 2, 128, 16, seed=6, width=room(16, many))
     want = s.check("whole rows")
     wide = torch.full((s.T, 10, 128), 3.0, dtype=torch.bfloat16, device="cuda")
     wide[:, 2:8] = s.q
@@ -138,6 +167,7 @@ def test_strided_queries_in_place_and_without_lse():
 
 @pytest.mark.parametrize("most", [0, 1, 3, 30, 1 << 40])
 def test_max_fresh_is_only_a_hint(most):
+    Step([50, 40, 200, 64], [1, 30, 2, 7], 6, 2, 128, 16, seed=7, width=room(16, True)).check(f"max_fresh {most}, wide", max_fresh=most)
     s = Step([50, 40, 200, 64], [1, 30, 2, 7], 6, 2, 128, 16, seed=7)
     s.check(f"max_fresh {most}", max_fresh=most)
 
@@ -170,7 +200,7 @@ def test_behind_4_gib():
 
 
 def test_repeats_bit_for_bit():
-    s = Step([900, 40, 333], [1, 30, 2], 8, 2, 128, 16, seed=11)
+    s = Step([900, 2000, 333], [1, 70, 2], 8, 2, 128, 16, seed=11, width=room(16, True))
     want, lse = s.run(), s.lse
     for _ in range(3):
         assert torch.equal(s.run(), want) and torch.equal(s.lse, lse)
@@ -184,13 +214,14 @@ def test_many_chunks(D, Hq, heads, n):
 
 def test_chunks_of_many_rows():
     """A few dozen rows over a long context: cut, and joined by a second launch."""
-    Step([9000, 700], [40, 9], 4, 1, 64, 64, seed=12).check("40 rows on 9000 keys")
-    Step([5000], [70], 2, 1, 256, 16, seed=13).check("70 rows on 5000 keys, D=256")
+    Step([9000, 700], [40, 9], 4, 1, 64, 64, seed=12, width=room(64, True)).check("40 rows on 9000 keys")
+    Step([5000], [70], 2, 1, 256, 16, seed=13, width=room(16, True)).check("70 rows on 5000 keys, D=256")
+    Step([4000, 300], [130, 20], 2, 1, 128, 16, seed=14, width=room(16, True)).check("130 rows on 4000 keys, eight waves")
 
 
 def test_one_workspace_for_calls_of_all_sizes():
     """Calls of other sizes in between leave the counters as they found them."""
-    big = Step([6000, 300, 1, 900], [1, 60, 1, 2], 8, 2, 128, 16, seed=14)
+    big = Step([6000, 300, 1, 900], [1, 60, 1, 2], 8, 2, 128, 16, seed=14, width=room(16, True))
     small = Step([2500], [1], 8, 2, 128, 16, seed=15)
     wide = Step([4000, 17], [1, 9], 16, 1, 256, 16, seed=16)
     ws = max((sp.new_kv4_workspace(s.T, len(s.kv), max(s.fresh), s.Hq, s.kv4, s.width) for s in (big, small, wide)), key=len)
@@ -200,10 +231,11 @@ def test_one_workspace_for_calls_of_all_sizes():
             assert torch.equal(s.run(workspace=ws), w)
 
 
-def test_in_a_graph():
+@pytest.mark.parametrize("width", [120, 1 << 20])
+def test_in_a_graph(width):
     """Captured once for the largest step and replayed on others: lengths, pages and
     rows change, the launches do not."""
-    B, T, Hq, heads, D, P, width = 6, 40, 8, 2, 128, 16, 120
+    B, T, Hq, heads, D, P = 6, 40, 8, 2, 128, 16
     steps = [Step(kv, fresh, Hq, heads, D, P, seed=20 + i, pad=T - sum(fresh), width=width - max([1] + [-(-n // P) for n in kv]))
              for i, (kv, fresh) in enumerate([([1900, 30, 1, 400, 64, 17], [1, 1, 1, 1, 1, 1]), ([50, 60, 20, 16, 0, 5], [30, 1, 3, 0, 0, 5]),
                                               ([1, 1900, 1900, 3, 3, 3], [1, 1, 1, 1, 1, 1]), ([0] * 6, [0] * 6)])]
@@ -239,7 +271,7 @@ def test_in_a_graph():
 
 
 def test_two_streams_at_once():
-    steps = [Step([3000, 70], [1, 40], 8, 2, 128, 16, seed=31), Step([40, 2500, 9], [9, 1, 1], 4, 4, 64, 32, seed=32)]
+    steps = [Step([3000, 70], [1, 40], 8, 2, 128, 16, seed=31, width=room(16, True)), Step([40, 2500, 9], [9, 1, 1], 4, 4, 64, 32, seed=32)]
     want = [s.run() for s in steps]
     ws = [sp.new_kv4_workspace(s.T, len(s.kv), max(s.fresh), s.Hq, s.kv4, s.width) for s in steps]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
