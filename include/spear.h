@@ -508,7 +508,8 @@ spear_status spear_rope(const spear_bf16 *x, int64_t x_stride, int64_t T, int32_
  * rotates nothing (positions is then unused).
  *   q [T][Hq][D], k and v [T][heads][D] bf16, each with a stride from row to row
  *     (a multiple of 8, at least its row); 16-byte aligned.  They may be parts of
- *     one row, and q_out may be q itself (with its stride).
+ *     one row, and q_out may be q itself (with its stride); otherwise it overlaps
+ *     no input.
  *   slots [T]: page * P + place; a row whose slot lies outside the cache is
  *     not written to it (its q is rotated all the same).  No slot may occur twice.
  */
@@ -548,7 +549,7 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *   table [B][width], q_start [B + 1], kv_len [B] as spear_kv4_plan leaves them.
  *   max_fresh: no request has more rows than that (an upper bound that the host
  *     knows; it chooses kernels and their tiles, the result is right without it).
- *   scale > 0, finite; window 0 (none) .. 2^30.
+ *   scale > 0, finite (times log2 e too); window 0 (none) .. 2^30.
  *   workspace device scratch of spear_kv4_attention_workspace_size bytes (0 for
  *     sizes out of range), 256-byte aligned, zeroed once (spear_workspace_init):
  *     its counters are zero again when a call's work has ended.  The size grows

@@ -135,12 +135,15 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
     it.found = false;
     it.size = 0x7FFFFFFF;
     int32_t uncut = 0;                                    // steps below which a tile stays whole
+    Request mine = {};
+    if (lane < a.B)
+        mine = request_of(a, c, lane, ROWS);
     if (c.target) {
         float work = 0.f, tiles = 0.f;
         for (int b0 = 0; b0 < a.B; b0 += 64) {
             const int b = b0 + lane;
             if (b < a.B) {
-                const Request r = request_of(a, c, b, ROWS);
+                const Request r = b0 ? request_of(a, c, b, ROWS) : mine;
                 work += (float)r.tiles * (float)r.steps;
                 tiles += (float)r.tiles;
             }
@@ -157,7 +160,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
         int32_t chunks = 0, n = 0, tiles = 0;
         Request r = {};
         if (b < a.B) {
-            r = request_of(a, c, b, ROWS);
+            r = b0 ? request_of(a, c, b, ROWS) : mine;
             chunks = r.steps <= it.size || r.steps < uncut ? 1 : (r.steps + it.size - 1) / it.size;
             tiles = r.tiles < c.most ? r.tiles : c.most;
             const int64_t all = (int64_t)r.tiles * chunks;
@@ -742,7 +745,7 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
 {
     using L = Tiles<D, W>;
     constexpr int DT = D / 32, KS = D / 16, ROWS = 32 * W, KT = L::KT, SK = L::SK;
-    extern __shared__ __attribute__((aligned(16))) uint8_t s_kv[];         // two buffers of K rows, then V rows
+    __shared__ __attribute__((aligned(16))) uint8_t s_kv[2 * L::BUF];      // two buffers of K rows, then V rows
     __shared__ int32_t s_flag[5][2];       // step + 1 if a page of its keys is gone; ... if its V has a block of NaN
 
     const int head = blockIdx.x % a.heads;
@@ -1138,12 +1141,7 @@ template <int D, int W>
 hipError_t launch_many(const AttnArgs &a, const Cut &c, const AttnLayout &L, hipStream_t s)
 {
     constexpr int ROWS = 32 * W;
-    const size_t lds = 2 * Tiles<D, W>::BUF;
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(&many_rows_kernel<D, W>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (attr != hipSuccess)
-        return attr;
-    hipLaunchKernelGGL((many_rows_kernel<D, W>), dim3((unsigned)(L.items[1] * a.heads)), dim3(64 * W), lds, s, a, c);
+    hipLaunchKernelGGL((many_rows_kernel<D, W>), dim3((unsigned)(L.items[1] * a.heads)), dim3(64 * W), 0, s, a, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !c.target)
         return e;
@@ -1198,7 +1196,7 @@ spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t 
         window > SPEAR_MAX_CONTEXT || q_stride < (int64_t)Hq * kv->D || q_stride % 8 != 0 ||
         q_stride > ((int64_t)1 << 36) || (q == y && q_stride != (int64_t)Hq * kv->D))
         return SPEAR_E_SHAPE;
-    if (!(scale > 0.f) || !isfinite(scale))
+    if (!(scale > 0.f) || !isfinite(scale * LOG2E))
         return SPEAR_E_ARG;
     if (!al(q, 16) || !al(y, 16) || !al(table, 4) || !al(q_start, 4) || !al(kv_len, 4) || !al(lse, 4) || !al(workspace, 256))
         return SPEAR_E_ALIGN;

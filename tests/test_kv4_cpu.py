@@ -136,7 +136,7 @@ def test_attention_refusals():
     assert f(T=-1) == f(B=-1) == f(B=4097) == f(Hq=3) == f(Hq=0) == f(Hq=256, qs=1 << 16) == f(width=0) == f(most=-1) == E_SHAPE
     assert f(qs=504) == f(qs=516) == f(window=-1) == f(width=1 << 30) == f(T=1 << 23, Hq=32, qs=4096) == E_SHAPE
     assert f(q=A, y=A, qs=1024) == E_SHAPE
-    for s in (0.0, -1.0, float("nan"), float("inf")):
+    for s in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert f(scale=s) == E_ARG
     assert f(q=A + 8) == f(y=A + 8) == f(lse=A + 2) == f(ws=A + 64) == f(kv_len=A + 2) == E_ALIGN
     need = sp.spear_kv4_attention_workspace_size(4, 2, 2, 4, 2, 128, 4, 16)
