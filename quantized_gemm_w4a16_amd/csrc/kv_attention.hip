@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
     auto place = [&](int step, uint32_t page) {
         const bool in = in_step(step);
         lost = in & (page > last_page);
-        ph = (int64_t)(in & !lost ? page : 0u) * a.heads + head;
+        ph = (int64_t)((in & !lost) ? page : 0u) * a.heads + head;
         off = (int32_t)((step * STEP + 4 * n) & page_mask);
     };
     // Loads return in the order they are issued, and the waits in the loop are for the
@@ -826,7 +826,7 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
                 const uint32_t off = (uint32_t)(step * SK + unit(i) / L::NB) & page_mask;
                 const bool in = real_key(step, i);
                 gone[i] = in & (page[i] > last_page);
-                const uint32_t p = in & !gone[i] ? page[i] : 0u;
+                const uint32_t p = (in & !gone[i]) ? page[i] : 0u;
                 code[i] = ld16((is_v(i) ? a.v_codes : a.k_codes) + ((uint64_t)p * code_page +
                                ((((uint32_t)head << log_p) + off) * (D / 2) + 16 * blk)));
                 // the scales of four tokens, of which key % 4 is this unit's
@@ -1200,6 +1200,7 @@ spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t 
         return SPEAR_E_ARG;
     if (!al(q, 16) || !al(y, 16) || !al(table, 4) || !al(q_start, 4) || !al(kv_len, 4) || !al(lse, 4) || !al(workspace, 256))
         return SPEAR_E_ALIGN;
+    max_fresh = max_fresh < T ? max_fresh : T;
     const AttnLayout L = attention_layout(T, B, max_fresh, Hq, kv->heads, kv->D,
                                           window && window + max_fresh < width * kv->P ? window + max_fresh : width * kv->P);
     if (ws_bytes < L.total)
