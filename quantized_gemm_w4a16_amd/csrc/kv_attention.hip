@@ -657,8 +657,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                 mm = up;
 #pragma unroll
                 for (int j = 0; j < JB; j++) {
-                    const float w = i0 + j * sharers < n ? __builtin_amdgcn_exp2f(ml[j].x - ref) : 0.f;
-                    if (w != 0.f) {
+                    // (a part whose weight is 0 counts too: it may hold a NaN)
+                    const float w = __builtin_amdgcn_exp2f(ml[j].x - ref);
+                    if (i0 + j * sharers < n) {
                         ll += w * ml[j].y;
                         sum += w * f32x4{lo2[j].x, lo2[j].y, hi2[j].x, hi2[j].y};
                     }

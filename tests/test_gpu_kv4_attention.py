@@ -113,6 +113,26 @@ def test_masked_places_may_hold_anything(window, many):
         s.check(f"masked places D={D} window={window} many={many}", window=window)
 
 
+@pytest.mark.parametrize("n", [700, 6000])
+@pytest.mark.parametrize("D,Hq,heads", [(64, 2, 1), (128, 8, 1), (256, 3, 3)])
+def test_nan_among_keys_that_count_for_nothing(n, D, Hq, heads):
+    """A long axis in chunks: a NaN that a row sees makes it NaN, from a chunk whose
+    other scores lie far below the rest as well."""
+    for where in ("q", "k", "v"):
+        s = Step([n], [1], Hq, heads, D, 16, seed=n + D)
+        if where == "q":
+            s.q[0, 0, 5] = float("nan")
+            s.q64[0, 0, 5] = np.nan
+        else:
+            s.cache.scales[where][s.table[0, n // 2 // 16], 0, 1, n // 2 % 16] = 255
+        s.to_device()
+        want, _, _, _ = ref_kv4.attention(s.q64, s.cache, s.table, s.q_start, s.kv, 40.0)
+        assert np.isnan(want).any() and (heads == 1 or not np.isnan(want).all())
+        # scores of some hundreds: outside the chunk of the largest, probabilities are 0
+        got = to64(s.run(scale=40.0))
+        assert (np.isnan(got) == np.isnan(want)).all(), where
+
+
 @pytest.mark.parametrize("many", [False, True])
 def test_every_page_let_go(many):
     s = Step([40, 70], [1, 30], 2, 1, 64, 16, seed=1, width=room(16, many))
