@@ -717,6 +717,12 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// A matrix instruction of 32 x 32 needs 12 wait states before a vector instruction
+// reads its result.  Where branches lie between, the compiler has counted the longer
+// path only (9 states at D = 192), so they are spent here.
+__device__ __forceinline__ void results_there(f32x16 (&z)[1]) { asm volatile("s_nop 11" : "+v"(z[0])); }
+__device__ __forceinline__ void results_there(f32x16 (&z)[2]) { asm volatile("s_nop 11" : "+v"(z[0]), "+v"(z[1])); }
+
 __device__ __forceinline__ float max_over_halves(float v)
 {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -869,6 +875,7 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             for (int c = 0; c < KS; c++)
                 z[kt] = mfma32(ld16(sk + 32 * kt * L::KROW + 32 * c), qf[c], z[kt]);
         }
+        results_there(z);
     };
 
     if (tid < 8)
