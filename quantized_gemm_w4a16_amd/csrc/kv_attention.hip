@@ -202,12 +202,16 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
 // How the D channels of a token's head lie in the operands of the matrix
 // instructions: NC chunks of CW channels, of which lane group g (16 lanes) holds
 // CW / 4 consecutive ones, eight to a depth step of the instruction.  A group's
-// codes are one load of W words, and all of them belong to one block.
+// codes are one load of W words, and all of them belong to one block; at D = 96 (12
+// bytes, not three loads of 4 from chunks of 32: 48 requests of up to 16000, 32 heads over 8: 99 -> 40 us)
+// to the blocks of the group's first and last word.
 template <int D>
 struct Lay {
-    static constexpr int CW = D % 128 == 0 ? 128 : (D % 64 == 0 ? 64 : 32);
+    static constexpr int CW = D % 128 == 0 ? 128 : (D % 64 == 0 ? 64 : 96);
     static constexpr int NC = D / CW;
     static constexpr int W = CW / 32;
+    static constexpr int NS = W == 3 ? 2 : NC;   // blocks of a group
+    static __device__ __forceinline__ int block(int s, int g) { return W == 3 ? (24 * g + 16 * s) / 32 : (s * CW + g * (CW / 4)) / 32; }
     static constexpr int ROW = 2 * D + 32;   // bytes of a V row in LDS: 8 rows start in 8 different 32-byte banks
 };
 
@@ -229,7 +233,9 @@ __device__ __forceinline__ Words<W> load_words(const uint8_t *p)
         r.w[0] = v.x;
         r.w[1 % W] = v.y;
     } else
-        r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+        for (int w = 0; w < W; w++)
+            r.w[w] = reinterpret_cast<const uint32_t *>(p)[w];
     return r;
 }
 
@@ -239,7 +245,22 @@ __device__ __forceinline__ Words<W> load_words(const uint8_t *p)
 template <int D>
 struct Part {
     Words<Lay<D>::W> c[Lay<D>::NC][4];
-    uint32_t s[Lay<D>::NC];
+    uint32_t s[Lay<D>::NS];
+
+    // the four scales of word w of chunk n
+    __device__ __forceinline__ uint32_t scales(int n, int w, int g) const
+    {
+        if (Lay<D>::W != 3)
+            return s[n];
+        return w == 0 ? s[0] : (w == 2 || g == 1 ? s[Lay<D>::NS - 1] : s[0]);
+    }
+    // token i's values are finite: its scales are 1
+    __device__ __forceinline__ void tame(int i)
+    {
+#pragma unroll
+        for (int n = 0; n < Lay<D>::NS; n++)
+            s[n] = (s[n] & ~(255u << (8 * i))) | (127u << (8 * i));
+    }
 };
 
 template <int D>
@@ -249,13 +270,13 @@ __device__ __forceinline__ void load_part(Part<D> &p, const uint8_t *codes, cons
     using L = Lay<D>;
     const uint8_t *c = codes + ((ph << log_p) + off) * (D / 2) + g * (L::CW / 8);
 #pragma unroll
-    for (int n = 0; n < L::NC; n++) {
+    for (int n = 0; n < L::NC; n++)
 #pragma unroll
         for (int i = 0; i < 4; i++)
             p.c[n][i] = load_words<L::W>(c + i * (D / 2) + n * (L::CW / 2));
-        const int block = (n * L::CW + g * (L::CW / 4)) / 32;
-        p.s[n] = *reinterpret_cast<const uint32_t *>(scales + ((ph * (D / 32) + block) << log_p) + off);
-    }
+#pragma unroll
+    for (int n = 0; n < L::NS; n++)
+        p.s[n] = *reinterpret_cast<const uint32_t *>(scales + ((ph * (D / 32) + L::block(n, g)) << log_p) + off);
 }
 
 __device__ __forceinline__ float scale_of(uint32_t word, int i) { return kv4_scale((word >> (8 * i)) & 255u); }
@@ -421,12 +442,10 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
         for (int i = 0; i < 4; i++) {
             acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < L::NC; c++) {
-                const float s = scale_of(kp.s[c], i);
+            for (int c = 0; c < L::NC; c++)
 #pragma unroll
                 for (int w = 0; w < L::W; w++)
-                    acc[i] = mfma16(kv4_bf16(kp.c[c][i].w[w], s), qf[c * L::W + w], acc[i]);
-            }
+                    acc[i] = mfma16(kv4_bf16(kp.c[c][i].w[w], scale_of(kp.scales(c, w, g), i)), qf[c * L::W + w], acc[i]);
         }
         // the next step's keys
         const bool lost_now = lost;
@@ -445,19 +464,17 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                 for (int r = 0; r < 4; r++) {
                     const int key = key0 + 16 * g + 4 * r + i;
                     const bool sees = key >= first && key <= last && !(lost16 >> (4 * g + r) & 1);
-                    acc[i][r] = sees ? acc[i][r] * a.scale : -INFINITY;
+                    acc[i][r] = sees ? acc[i][r] : -INFINITY;
                     top = fmaxf(top, acc[i][r]);
                 }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    acc[i][r] *= a.scale;
+                for (int r = 0; r < 4; r++)
                     top = fmaxf(top, acc[i][r]);
-                }
         }
-        top = max_over_groups(top);
+        top = max_over_groups(top) * a.scale;
         if (__any(top > m)) {
             const float up = fmaxf(m, top);
             const float f = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up);
@@ -467,42 +484,36 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
             for (int d = 0; d < DT; d++)
                 o[d] *= f;
         }
-        const float m0 = m == -INFINITY ? 0.f : m;
+        const float m0 = m == -INFINITY ? 0.f : -m;
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int r = 0; r < 4; r++) {
-                acc[i][r] = __builtin_amdgcn_exp2f(acc[i][r] - m0);
+                acc[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][r], a.scale, m0));
                 l += acc[i][r];
             }
 
-        // keys that no row of the tile sees hold anything: their V is zero
+        // keys that no row of the tile sees hold anything: their V is made finite, which
+        // probabilities of 0 leave out
         if (key0 < seen0 || key0 + STEP > seen1 || lost16 != 0) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int key = key0 + 4 * n + i;
-                if (lost_now || key < seen0 || key >= seen1) {
-#pragma unroll
-                    for (int c = 0; c < L::NC; c++) {
-#pragma unroll
-                        for (int w = 0; w < L::W; w++)
-                            vp.c[c][i].w[w] = 0;
-                        vp.s[c] = (vp.s[c] & ~(255u << (8 * i))) | (127u << (8 * i));
-                    }
-                }
+                if (lost_now || key < seen0 || key >= seen1)
+                    vp.tame(i);
             }
         }
         // A block of NaN counts for the rows that see its key only; a zero
         // probability would carry it to the others.
         bool nan_here = false;
 #pragma unroll
-        for (int c = 0; c < L::NC; c++) {
+        for (int c = 0; c < L::NS; c++) {
             const uint32_t x = ~vp.s[c];
             nan_here |= ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
         }
         if (__any(nan_here)) {
 #pragma unroll
-            for (int c = 0; c < L::NC; c++)
+            for (int c = 0; c < L::NS; c++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const bool mine = ((vp.s[c] >> (8 * i)) & 255u) == 255u;
@@ -510,19 +521,15 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                     while (who) {
                         const int src = __builtin_ctzll(who);
                         who &= who - 1;
-                        const int key = key0 + 4 * (src & 15) + i, block = (c * L::CW + (src >> 4) * (L::CW / 4)) / 32;
+                        const int key = key0 + 4 * (src & 15) + i, block = L::block(c, src >> 4);
                         const float add = key >= first && key <= last ? __builtin_nanf("") : 0.f;
 #pragma unroll
                         for (int d = 0; d < DT; d++)
                             if (d / 2 == block)
                                 o[d] += add;
                     }
-                    if (mine) {
-#pragma unroll
-                        for (int w = 0; w < L::W; w++)
-                            vp.c[c][i].w[w] = 0;
+                    if (mine)
                         vp.s[c] = (vp.s[c] & ~(255u << (8 * i))) | (127u << (8 * i));
-                    }
                 }
         }
 
@@ -533,13 +540,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
 #pragma unroll
             for (int e = 0; e < 2; e++)
 #pragma unroll
-                for (int c = 0; c < L::NC; c++) {
-                    const float s = scale_of(vp.s[c], 2 * u + e);
+                for (int c = 0; c < L::NC; c++)
 #pragma unroll
                     for (int w = 0; w < L::W; w++)
                         *reinterpret_cast<u32x4 *>(sv + (e * 16 + n) * L::ROW + 2 * (c * L::CW + g * (L::CW / 4)) + 16 * w) =
-                            kv4_bf16(vp.c[c][2 * u + e].w[w], s);
-                }
+                            kv4_bf16(vp.c[c][2 * u + e].w[w], scale_of(vp.scales(c, w, g), 2 * u + e));
             wave_order();
             // P as a sum of two bf16: V is read once for both, and P's rounding is gone (2^-17)
             u32x4 p_hi, p_lo;
@@ -848,8 +853,9 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             if (is_unit(i)) {
                 const int key = unit(i) / L::NB, blk = unit(i) % L::NB, at = step * SK + key;
                 const uint32_t byte = (scales[i] >> (8 * (key & 3))) & 255u;
-                // keys that no row of the tile sees hold anything: their V is zero.  A
-                // block of NaN in V is put in by hand, for the rows that see it
+                // keys that no row of the tile sees hold anything: their V is made finite,
+                // which probabilities of 0 leave out.  A block of NaN in V is put in by
+                // hand, for the rows that see it
                 const bool seen = (at >= seen0) & (at < seen1) & !gone[i], nan = seen & (byte == 255u);
                 const bool clear = is_v(i) & (!seen | nan), note = is_v(i) ? nan : gone[i];
                 s_flag[note ? step & 3 : 4][is_v(i)] = step + 1;
@@ -860,7 +866,7 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
 #pragma unroll
                 for (int w = 0; w < 4; w++) {
                     const uint32_t c = turn ? code[i][w ^ 1] : code[i][w];
-                    *reinterpret_cast<u32x4 *>(p + ((16 * w) ^ (16 * turn))) = kv4_bf16(clear ? 0u : c, sc);
+                    *reinterpret_cast<u32x4 *>(p + ((16 * w) ^ (16 * turn))) = kv4_bf16(c, sc);
                 }
             }
     };
