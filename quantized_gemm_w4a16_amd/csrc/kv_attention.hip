@@ -202,16 +202,18 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
 // How the D channels of a token's head lie in the operands of the matrix
 // instructions: NC chunks of CW channels, of which lane group g (16 lanes) holds
 // CW / 4 consecutive ones, eight to a depth step of the instruction.  A group's
-// codes are one load of W words, and all of them belong to one block; at D = 96 (12
-// bytes, not three loads of 4 from chunks of 32: 48 requests of up to 16000, 32 heads over 8: 99 -> 40 us)
-// to the blocks of the group's first and last word.
+// codes are W words side by side, and all of them belong to one block; at D = 96
+// and 192, to the blocks of the group's first and last word.  (There, three chunks
+// of 32 or 64 would have a block each, but loads of 4 or 8 bytes: 48 requests of up
+// to 16000 tokens, 32 heads over 8, 99 -> 40 and 111 -> 86 us.)
 template <int D>
 struct Lay {
-    static constexpr int CW = D % 128 == 0 ? 128 : (D % 64 == 0 ? 64 : 96);
+    static constexpr int CW = D % 128 == 0 ? 128 : D;
     static constexpr int NC = D / CW;
     static constexpr int W = CW / 32;
-    static constexpr int NS = W == 3 ? 2 : NC;   // blocks of a group
-    static __device__ __forceinline__ int block(int s, int g) { return W == 3 ? (24 * g + 16 * s) / 32 : (s * CW + g * (CW / 4)) / 32; }
+    static constexpr bool TWO = W % 3 == 0;
+    static constexpr int NS = TWO ? 2 : NC;  // blocks of a group
+    static __device__ __forceinline__ int block(int s, int g) { return (g * (CW / 4) + s * (TWO ? CW / 4 - 8 : CW)) / 32; }
     static constexpr int ROW = 2 * D + 32;   // bytes of a V row in LDS: 8 rows start in 8 different 32-byte banks
 };
 
@@ -250,9 +252,10 @@ struct Part {
     // the four scales of word w of chunk n
     __device__ __forceinline__ uint32_t scales(int n, int w, int g) const
     {
-        if (Lay<D>::W != 3)
+        if (!Lay<D>::TWO)
             return s[n];
-        return w == 0 ? s[0] : (w == 2 || g == 1 ? s[Lay<D>::NS - 1] : s[0]);
+        const int third = 3 * w / Lay<D>::W;
+        return third == 0 ? s[0] : (third == 2 || g % 2 ? s[Lay<D>::NS - 1] : s[0]);
     }
     // token i's values are finite: its scales are 1
     __device__ __forceinline__ void tame(int i)
@@ -269,6 +272,19 @@ __device__ __forceinline__ void load_part(Part<D> &p, const uint8_t *codes, cons
 {
     using L = Lay<D>;
     const uint8_t *c = codes + ((ph << log_p) + off) * (D / 2) + g * (L::CW / 8);
+    if (D == 64) {
+        // a group has a token's 32 bytes at first (turn_part): four loads of 8 bytes a lane
+        // take 39 us where these take 32 (48 requests of up to 16000 tokens, 32 heads over 8)
+        c = codes + ((ph << log_p) + off + g) * 32;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const u32x4 v = ld16(c + 8 * i);
+            p.c[0][i].w[0] = v[0];
+            p.c[0][i].w[1 % L::W] = v[1];
+            p.c[0][i + 1].w[0] = v[2];
+            p.c[0][i + 1].w[1 % L::W] = v[3];
+        }
+    } else
 #pragma unroll
     for (int n = 0; n < L::NC; n++)
 #pragma unroll
@@ -277,6 +293,34 @@ __device__ __forceinline__ void load_part(Part<D> &p, const uint8_t *codes, cons
 #pragma unroll
     for (int n = 0; n < L::NS; n++)
         p.s[n] = *reinterpret_cast<const uint32_t *>(scales + ((ph * (D / 32) + L::block(n, g)) << log_p) + off);
+}
+
+// D = 64: from group g's token 4R + g, pieces c[0][0 .. 3] of its channels, to the
+// tokens 4R .. 4R + 3, channels 16 g .. 16 g + 15 of each.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b)
+{
+    auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap_rows(uint32_t &a, uint32_t &b)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+template <int D>
+__device__ __forceinline__ void turn_part(Part<D> &p)
+{
+    if (D != 64)
+        return;
+#pragma unroll
+    for (int w = 0; w < Lay<D>::W; w++) {
+        swap_halves(p.c[0][0].w[w], p.c[0][2].w[w]);
+        swap_halves(p.c[0][1].w[w], p.c[0][3].w[w]);
+        swap_rows(p.c[0][0].w[w], p.c[0][1].w[w]);
+        swap_rows(p.c[0][2].w[w], p.c[0][3].w[w]);
+    }
 }
 
 __device__ __forceinline__ float scale_of(uint32_t word, int i) { return kv4_scale((word >> (8 * i)) & 255u); }
@@ -438,6 +482,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
         const int key0 = step * STEP;
         const uint32_t lost16 = (uint32_t)(__ballot(lost) & 0xFFFF);       // bit R: the keys 4R .. 4R + 3
         f32x4 acc[4];
+        turn_part<D>(kp);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -534,6 +579,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
         }
 
         uint8_t *sv = s_v[wave];
+        turn_part<D>(vp);
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             wave_order();
