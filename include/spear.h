@@ -539,8 +539,8 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *   lse[t][h] = log sum_j exp(scale q . k)       (natural; optional)
  * Sums and softmax are in fp32, y is rounded once to bf16.  Requests of one
  * token, of a few and of long chunks may stand side by side.  A row that sees
- * nothing gets zeros and lse -inf; rows behind the last request are left as they
- * were.  A table entry outside [0, pages) (a page that was let go) is as if its
+ * nothing, or scores of -inf only, gets zeros and lse -inf; one that sees a NaN is
+ * NaN; rows behind the last request are left as they were.  A table entry outside [0, pages) (a page that was let go) is as if its
  * tokens were masked; what masked places hold, NaN and infinities among it, does
  * not count.  kv_len is held within [0, width P] and q_start within [0, T].
  *   q [T][Hq][D] bf16 with q_stride elements from row to row (a multiple of 8);
@@ -552,7 +552,8 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *   scale > 0, finite (times log2 e too); window 0 (none) .. 2^30.
  *   workspace device scratch of spear_kv4_attention_workspace_size bytes (0 for
  *     sizes out of range), 256-byte aligned, zeroed once (spear_workspace_init):
- *     its counters are zero again when a call's work has ended.  The size grows
+ *     its counters are zero again when a call's work has ended.  It is not
+ *     one that other entry points have written to.  The size grows
  *     with T and B and hangs on neither max_fresh nor width, so one for the
  *     largest step serves the others, also between calls of other sizes.
  */

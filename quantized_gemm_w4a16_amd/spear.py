@@ -755,6 +755,7 @@ def spear_kv4_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tenso
     dev, B = cached.device, cached.numel()
     if table.dim() != 2:
         _bad(fn, E_SHAPE, f"table has {table.dim()} dimensions, not 2")
+    _want_int32(fn, "P", P)
     width = int(table.shape[1])
     _want(fn, "cached", cached, _I32, (B,), dev)
     _want(fn, "fresh", fresh, _I32, (B,), dev)
@@ -785,6 +786,7 @@ def spear_rope_frequencies(rot: int, base: float = 10000.0, kind: int = ROPE_PLA
                            high: float = 32.0) -> torch.Tensor:
     """The rot / 2 frequencies of a rotation, fp64 on the host; kind (ROPE_PLAIN,
     _LINEAR, _BASE, _PARTS) says how positions are stretched by factor."""
+    _want_int32("spear_rope_frequencies", "rot", rot)
     f = torch.empty(max(rot // 2, 1), dtype=torch.float64)
     _check("spear_rope_frequencies",
            load().spear_rope_frequencies(rot, base, kind, factor, original, low, high, _ptr(f)))
@@ -800,6 +802,12 @@ class Rope:
         _want("Rope", "freqs", freqs, (torch.float64,), (freqs.numel(),), freqs.device)
         self.freqs, self.layout, self.scale, self.rot = freqs, int(layout), float(scale), 2 * freqs.numel()
         self._s = bytes(_Rotation(_ptr(freqs), self.scale, self.rot, self.layout))
+
+
+def _want_int32(fn: str, name: str, n: int):
+    """ctypes cuts a larger number to 32 bits."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        _bad(fn, E_SHAPE, f"{name} is {n}")
 
 
 def _want_rows(fn: str, name: str, t, shape, device) -> int:
@@ -939,6 +947,7 @@ def spear_kv4_attention(q: torch.Tensor, kv: KV4, table: torch.Tensor, q_start: 
         _bad(fn, E_SHAPE, f"q has {q.dim()} dimensions, not 3")
     if table.dim() != 2:
         _bad(fn, E_SHAPE, f"table has {table.dim()} dimensions, not 2")
+    _want_int32(fn, "window", window)
     T, Hq, width = int(q.shape[0]), int(q.shape[1]), int(table.shape[1])
     shape = (T, Hq, kv.D)
     qs = _want_rows(fn, "q", q, shape, dev)

@@ -196,3 +196,12 @@ def test_binding_checks_its_tensors():
     refused(E_SHAPE, sp.spear_kv4_plan, n, n[:1], table, free, nf, 4, 16)
     refused(E_SHAPE, sp.spear_kv4_plan, n, n, table, free, nf, 4, 16, plan=sp.new_kv4_plan(2, 5, device="cpu"))
     refused(E_ARG, sp.spear_kv4_plan, n, n.long(), table, free, nf, 4, 16)
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    i32 = torch.int32
+    kv, x = sp.new_kv4(4, 2, 64, 16, device="cpu"), torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    table, start, n, one = torch.zeros(2, 3, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32)
+    refused(E_SHAPE, sp.spear_kv4_attention, x, kv, table, start, n, 2, window=(1 << 32) + 5)
+    refused(E_SHAPE, sp.spear_kv4_plan, n, n, table, one, one, 4, (1 << 32) + 16)
+    refused(E_SHAPE, sp.spear_rope_frequencies, (1 << 32) + 64)
