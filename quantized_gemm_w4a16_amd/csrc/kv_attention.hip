@@ -48,6 +48,7 @@ struct Cut {
     int32_t target;                 // items of a key head that the cut aims at; 0: no cut
     int32_t least, least_full;      // steps of a chunk, at least: with few tiles, with a tile a CU
     int32_t most;                   // items of a key head that there is room for
+    int32_t fit;                    // chunks are made to fit c.target, or twice that
     uint32_t *count;                // [tile][key head] parts that are done; then [item][key head] chunks of a
                                     // group; all 0 between calls
 };
@@ -123,8 +124,8 @@ __device__ __forceinline__ float total64(float v)
 }
 
 // The item (or, by_tile, the tile) number `want`.  Every wave forms the sums over
-// all requests, 64 at a time.  A chunk has as many steps as make about c.target
-// items of a key head; sums are capped at c.most, behind which there is no item.
+// all requests, 64 at a time.  A chunk has as many steps as make c.target
+// items of a key head, or twice as many; sums are capped at c.most, behind which there is no item.
 // A tile whose items do not all lie below c.most (rows that q_start gives to more
 // than one request) has none, so that its count of chunks ends where it began.
 template <int ROWS>
@@ -148,11 +149,39 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
                 tiles += (float)r.tiles;
             }
         }
-        const float s = ceilf(total64(work) / (float)c.target);
+        float s = ceilf(total64(work) / (float)c.target);
         const float fill = total64(tiles) * (float)a.heads * (float)c.least_full * (1.f / 256.f);
         const int32_t least = fill > (float)c.least_full ? c.least_full : (fill < (float)c.least ? c.least : (int32_t)fill);
-        it.size = s < (float)least ? least : (s > 1e9f ? 1000000000 : (int32_t)s);
         uncut = 2 * least;
+        s = s < (float)least ? (float)least : s;
+        // A tile has whole chunks, so there are more of them than work / s, and the few
+        // behind c.target start when the first have ended.  Somewhat longer ones fit, or
+        // there are twice as many (48 requests of 300 to 16000 tokens, 32 heads over 8, 128
+        // channels 56.8 -> 52.3 us by the former, 256 channels 103 -> 98 by the latter).
+        // Not before the kernel for many rows, where it finds little to do (80 rows of 8
+        // requests each 67 -> 69 us).
+        const float s0 = s, most = ceilf(1.4f * s0);
+        for (int k = 0; c.fit; k++) {
+            float n = 0.f;
+            for (int b0 = 0; b0 < a.B; b0 += 64) {
+                const int b = b0 + lane;
+                if (b < a.B) {
+                    const Request r = b0 ? request_of(a, c, b, ROWS) : mine;
+                    n += (float)r.tiles * ((float)r.steps <= s || r.steps < uncut ? 1.f : ceilf((float)r.steps / s));
+                }
+            }
+            n = total64(n);
+            if (n <= (float)c.target)
+                break;
+            if (s >= most || k == 7) {
+                s = ceilf(0.5f * s0);
+                s = s < (float)least ? (float)least : s;
+                break;
+            }
+            s = ceilf(s * n / (float)c.target);
+            s = s > most ? most : s;
+        }
+        it.size = s > 1e9f ? 1000000000 : (int32_t)s;
     }
     int32_t items0 = 0, tiles0 = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -187,7 +216,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             it.number = first_tile + it.tile;
             it.b = b0 + src;
             it.found = it.chunks < 2 || (it.item <= c.most - it.chunks && (int64_t)(it.number + 1) * a.heads <= COUNTS);
-            static_assert(COUNTS + FEW_ITEMS + 17 * SPEAR_MAX_HEADS <= GROUP_COUNTS, "c.most items of all key heads");
+            static_assert(COUNTS + 2 * FEW_ITEMS + 18 * SPEAR_MAX_HEADS <= GROUP_COUNTS, "c.most items of all key heads");
             return it;
         }
         items0 += bcast(ni, 63);
@@ -1200,11 +1229,11 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         }
         L.target[k] = k && !both ? -1 : (least * heads >= goal || tiles * heads > COUNTS ? 0 : (int32_t)cut);
         L.tiles[k] = tiles;
-        L.items[k] = tiles + (L.target[k] ? cut + 16 : 0);
+        L.items[k] = tiles + (L.target[k] ? (k || both ? cut : 2 * cut) + 16 : 0);
         // The room of the parts does not depend on max_fresh and grows with T and B,
         // so that a workspace of the largest step serves every other.
         const int64_t fewest = k ? rows / 128 : rows / FEW_ROWS;
-        const int64_t room = (fewest < most_cut ? fewest : most_cut) + more + most_cut + 16;
+        const int64_t room = (fewest < most_cut ? fewest : most_cut) + more + (k ? most_cut : 2 * most_cut) + 16;
         const int64_t room_rows = room * heads * (k ? 256 : FEW_ROWS);
         L.part_o[k] = off;
         off += (size_t)(room_rows * D) * sizeof(float);
@@ -1238,7 +1267,7 @@ hipError_t launch_attention(const AttnArgs &a, const AttnLayout &L, uint8_t *ws,
     for (int k = 0; k < 2; k++)
         c[k] = {reinterpret_cast<float *>(ws + L.part_o[k]), reinterpret_cast<float *>(ws + L.part_ml[k]),
                 reinterpret_cast<float *>(ws + L.group_ml), k ? L.limit : 0, k ? 0x7FFFFFFF : L.limit, L.target[k], k ? MANY_LEAST : FEW_LEAST,
-                k ? MANY_LEAST : FEW_LEAST_FULL, (int32_t)L.items[k],
+                k ? MANY_LEAST : FEW_LEAST_FULL, (int32_t)L.items[k], L.target[1] < 0,
                 reinterpret_cast<uint32_t *>(ws)};
     hipLaunchKernelGGL((few_rows_kernel<D>), dim3((unsigned)(L.items[0] * a.heads)), dim3(64 * FEW_WAVES), 0, s, a, c[0]);
     const hipError_t e = hipGetLastError();
