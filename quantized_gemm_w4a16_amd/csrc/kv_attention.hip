@@ -57,7 +57,7 @@ constexpr int64_t GROUP_COUNTS = 32768;     // items
 
 // ------------------------------------------------------------------- items
 struct Request {
-    int64_t row0;                   // its first row of q
+    int32_t row0;                   // its first row of q
     int32_t fresh, kv;              // its rows and keys
     int32_t tiles, base, steps;     // row tiles; the first step that a row sees; steps from there
 };
@@ -65,18 +65,16 @@ struct Request {
 __device__ __forceinline__ Request request_of(const AttnArgs &a, const Cut &c, int b, int tile_rows)
 {
     Request r;
-    const int64_t T = a.T;
-    int64_t q0 = a.q_start[b], q1 = a.q_start[b + 1];
+    const int32_t T = (int32_t)a.T, room = (int32_t)(a.width << a.log_p);
+    int32_t q0 = a.q_start[b], q1 = a.q_start[b + 1];
     q0 = q0 < 0 ? 0 : (q0 > T ? T : q0);
     q1 = q1 < q0 ? q0 : (q1 > T ? T : q1);
-    const int64_t room = a.width << a.log_p;
-    int64_t kv = a.kv_len[b];
-    kv = kv < 0 ? 0 : (kv > room ? room : kv);
+    const int32_t kv = a.kv_len[b];
+    r.kv = kv < 0 ? 0 : (kv > room ? room : kv);
     r.row0 = q0;
-    r.fresh = (int32_t)(q1 - q0);
-    r.kv = (int32_t)kv;
-    const int64_t rows = (int64_t)r.fresh * a.G;
-    r.tiles = rows > c.rows0 && rows <= c.rows1 ? (int32_t)((rows + tile_rows - 1) / tile_rows) : 0;
+    r.fresh = q1 - q0;
+    const int32_t rows = r.fresh * a.G;
+    r.tiles = rows > c.rows0 && rows <= c.rows1 ? (rows + tile_rows - 1) / tile_rows : 0;
     // the first fresh token stands at kv - fresh
     int32_t lo = a.window ? r.kv - r.fresh - a.window + 1 : 0;
     lo = lo < 0 ? 0 : lo;
@@ -122,6 +120,27 @@ __device__ __forceinline__ float total64(float v)
     v += __int_as_float(from_lane<0x143, 0xC>(__float_as_int(v)));
     return __int_as_float(bcast(__float_as_int(v), 63));
 }
+
+// a / b where it is at most 2^22, and a and b less than 2^25: a reciprocal's product is
+// off by less than one.
+__device__ __forceinline__ int32_t quotient(int32_t a, int32_t b)
+{
+    const int32_t q = (int32_t)((float)a * __builtin_amdgcn_rcpf((float)b)), r = a - q * b;
+    return q + (r >= b) - (r < 0);
+}
+
+// Token and query head of the rows of a tile, from a multiplication: with the tile's
+// first row `rem` rows into token `tok`, (rem + i) / G for rem + i < 320 and G <= 64 by
+// 2^16 / G, cut, plus one (all of them tried).
+struct TileRows {
+    int32_t tok, rem, by, G;
+    __device__ __forceinline__ TileRows(int32_t first, int32_t G)
+        : tok(first / G), rem(first - tok * G), by((int32_t)(65536.f * __builtin_amdgcn_rcpf((float)G)) + 1), G(G)
+    {
+    }
+    __device__ __forceinline__ int32_t token(int32_t i) const { return tok + ((rem + i) * by >> 16); }
+    __device__ __forceinline__ int32_t head(int32_t i, int32_t token) const { return rem + i - (token - tok) * G; }
+};
 
 // The item (or, by_tile, the tile) number `want`.  Every wave forms the sums over
 // all requests, 64 at a time.  A chunk has as many steps as make c.target
@@ -190,7 +209,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
         Request r = {};
         if (b < a.B) {
             r = b0 ? request_of(a, c, b, ROWS) : mine;
-            chunks = r.steps <= it.size || r.steps < uncut ? 1 : (r.steps + it.size - 1) / it.size;
+            chunks = r.steps <= it.size || r.steps < uncut ? 1 : quotient(r.steps + it.size - 1, it.size);
             tiles = r.tiles < c.most ? r.tiles : c.most;
             const int64_t all = (int64_t)r.tiles * chunks;
             n = all < c.most ? (int32_t)all : c.most;
@@ -202,7 +221,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
         if (hit) {
             const int src = __builtin_ctzll(hit);
             const int32_t first_item = bcast(items0 + ni - n, src), first_tile = bcast(tiles0 + ti - tiles, src);
-            it.r.row0 = (int64_t)(uint32_t)bcast((int32_t)r.row0, src);
+            it.r.row0 = bcast(r.row0, src);
             it.r.fresh = bcast(r.fresh, src);
             it.r.kv = bcast(r.kv, src);
             it.r.tiles = bcast(r.tiles, src);
@@ -210,8 +229,8 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             it.r.steps = bcast(r.steps, src);
             it.chunks = bcast(chunks, src);
             it.size = (it.r.steps + it.chunks - 1) / it.chunks;
-            it.tile = by_tile ? want - first_tile : (want - first_item) / it.chunks;
-            it.chunk = by_tile ? 0 : (want - first_item) % it.chunks;
+            it.tile = by_tile ? want - first_tile : (it.chunks < 2 ? want - first_item : quotient(want - first_item, it.chunks));
+            it.chunk = by_tile ? 0 : want - first_item - it.tile * it.chunks;
             it.item = first_item + it.tile * it.chunks;
             it.number = first_tile + it.tile;
             it.b = b0 + src;
@@ -403,11 +422,13 @@ __device__ __forceinline__ float2 load_far(const float *p)
 }
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Four channels from c on of a request's row, and with c == 0 its lse.
+// Four channels from c on of row i of a tile, and with c == 0 its lse.
 template <int D>
-__device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int head, int row, int c, f32x4 sum, float m, float l)
+__device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int head, const TileRows &rows, int i, int c, f32x4 sum,
+                                          float m, float l)
 {
-    const int64_t hrow = (it.r.row0 + row / a.G) * ((int64_t)a.heads * a.G) + head * a.G + row % a.G;
+    const int32_t tok = rows.token(i);
+    const int64_t hrow = (it.r.row0 + tok) * ((int64_t)a.heads * a.G) + head * a.G + rows.head(i, tok);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     *reinterpret_cast<uint2 *>(a.y + hrow * D + c) =
         make_uint2(pair_bf16(sum[0] * inv, sum[1] * inv), pair_bf16(sum[2] * inv, sum[3] * inv));
@@ -459,15 +480,15 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
     const int64_t page_mask = (1 << log_p) - 1;
 
     // this lane's row and the positions it sees, [first, last]
-    const int row = it.tile * FEW_ROWS + n;
-    const int tok = row / G, qh = row - tok * G;
+    const TileRows tile_rows(it.tile * FEW_ROWS, G);
+    const int tok = tile_rows.token(n), qh = tile_rows.head(n, tok);
     const bool real = tok < it.r.fresh;
     const int pos0 = it.r.kv - it.r.fresh;
     const int last = real ? pos0 + tok : -1;
     const int first = a.window && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
     // ... and what the tile's rows see together
-    const int tok0 = it.tile * FEW_ROWS / G;
-    int tok1 = (it.tile * FEW_ROWS + FEW_ROWS - 1) / G;
+    const int tok0 = tile_rows.tok;
+    int tok1 = tile_rows.token(FEW_ROWS - 1);
     tok1 = tok1 < it.r.fresh ? tok1 : it.r.fresh - 1;
     const int seen1 = pos0 + tok1 + 1;                                     // one past the last
     const int seen0 = a.window && pos0 + tok0 - a.window + 1 > 0 ? pos0 + tok0 - a.window + 1 : 0;
@@ -483,7 +504,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
 
     u32x4 qf[NS];
     {
-        const uint16_t *qp = a.q + (it.r.row0 + tok) * a.qs + (int64_t)(head * G + qh) * D;
+        const uint16_t *qp = a.q + (int64_t)(it.r.row0 + tok) * a.qs + (int64_t)(head * G + qh) * D;
 #pragma unroll
         for (int c = 0; c < L::NC; c++)
 #pragma unroll
@@ -699,7 +720,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
             if (c == 0)
                 store_far(cut.part_ml + 2 * p, mm, ll);
         } else
-            store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
+            store_out<D>(a, it, head, tile_rows, r, c, sum, mm, ll);
     }
     if (it.chunks < 2)
         return;
@@ -781,7 +802,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
             }
             if (in && sh == 0) {
                 if (to_y)
-                    store_out<D>(a, it, head, it.tile * FEW_ROWS + r, c, sum, mm, ll);
+                    store_out<D>(a, it, head, tile_rows, r, c, sum, mm, ll);
                 else {
                     // a row's m and l, which its other threads may still read, to a place of
                     // their own
@@ -866,11 +887,13 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
     const int page_mask = (1 << log_p) - 1;
     const int pos0 = it.r.kv - it.r.fresh, rows = it.r.fresh * G;
     const int32_t *table = a.table + (int64_t)it.b * a.width;
+    const int first_row = it.tile * ROWS;
+    const TileRows tile_rows(first_row, G);
 
     // what the rows from r0 up to r1 see together: [s0, s1), and each of them: [e0, e1]
     auto range = [&](int r0, int r1, int &s0, int &s1, int &e0, int &e1) {
         r1 = r1 < rows ? r1 : rows;
-        const int t0 = r0 / G, t1 = (r1 - 1) / G;
+        const int t0 = tile_rows.token(r0 - first_row), t1 = tile_rows.token(r1 - 1 - first_row);
         s0 = a.window && pos0 + t0 - a.window + 1 > 0 ? pos0 + t0 - a.window + 1 : 0;
         s1 = r0 < r1 ? pos0 + t1 + 1 : 0;
         e0 = a.window && pos0 + t1 - a.window + 1 > 0 ? pos0 + t1 - a.window + 1 : 0;
@@ -892,11 +915,11 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
     hi = hi < hi_seen ? hi : hi_seen;
 
     u32x4 qf[KS];
-    const int tok = row / G;
+    const int tok = tile_rows.token(row - first_row);
     const int last = row < rows ? pos0 + tok : -1;
     const int first = a.window && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
     {
-        const uint16_t *qp = a.q + (it.r.row0 + tok) * a.qs + (int64_t)(head * G + row - tok * G) * D + 8 * h;
+        const uint16_t *qp = a.q + (int64_t)(it.r.row0 + tok) * a.qs + (int64_t)(head * G + tile_rows.head(row - first_row, tok)) * D + 8 * h;
 #pragma unroll
         for (int s = 0; s < KS; s++)
             qf[s] = row < rows ? ld16(qp + 16 * s) : zero4();
@@ -1089,7 +1112,7 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             if (it.chunks > 1)
                 *reinterpret_cast<f32x4 *>(cut.part_o + p * D + c) = v;
             else
-                store_out<D>(a, it, head, row, c, v, m, l);
+                store_out<D>(a, it, head, tile_rows, row - first_row, c, v, m, l);
         }
     if (it.chunks > 1 && h == 0) {
         cut.part_ml[2 * p] = m;
@@ -1116,6 +1139,7 @@ __global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, cons
     if (r0 >= rows)
         return;
     const int c = 4 * (q < Q ? q : 0);
+    const TileRows tile_rows(it.tile * ROWS, a.G);
     float mm[JOIN], ll[JOIN];
     f32x4 sum[JOIN];
 #pragma unroll
@@ -1167,7 +1191,7 @@ __global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, cons
 #pragma unroll
         for (int r = 0; r < JOIN; r++)
             if (r0 + r < rows && r0 + r < ROWS)
-                store_out<D>(a, it, head, it.tile * ROWS + r0 + r, c, sum[r], mm[r], ll[r]);
+                store_out<D>(a, it, head, tile_rows, r0 + r, c, sum[r], mm[r], ll[r]);
 }
 
 // ------------------------------------------------------------------- host
