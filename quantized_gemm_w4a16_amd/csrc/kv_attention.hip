@@ -444,7 +444,7 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int
 // the first product's operand where they were loaded, V's pass through LDS of the
 // wave's own, so that no wave waits for another inside the loop.  Requests of one
 // token are bound by the cache's bytes (48 requests of up to 16000 tokens, 32 heads
-// of 128 over 8: 207 MB in 48 us, 4.3 TB/s; without the products as fast), long ones
+// of 128 over 8: 207 MB in 44 us, 4.7 TB/s), long ones
 // cut over the whole chip also by what comes before and after (two of 131000 tokens
 // 136 MB in 38 us, of which the plan, the first page and the first keys take 5 and the
 // join 8).  Tiles of many rows on few keys are bound by the instructions of a wave: it

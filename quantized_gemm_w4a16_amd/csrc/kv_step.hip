@@ -17,8 +17,8 @@ bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 // thread) and takes its share of the new pages and of the rows; the first writes
 // what there is one of.  Nothing that a workgroup reads is written by another:
 // a row whose page is new computes the page from the free list.  Bound by round trips
-// (lengths, then the table or the free list): one request 3.9 us, 256 requests of
-// up to 700 tokens 5.2 us, in one launch.
+// (lengths, then the table or the free list): one request 3.8 us, 256 requests of
+// up to 700 tokens 5.1 us, in one launch.
 constexpr int PL_THREADS = 512;
 constexpr int PL_MOST = SPEAR_MAX_REQUESTS / PL_THREADS;
 
