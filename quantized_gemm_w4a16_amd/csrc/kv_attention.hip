@@ -169,7 +169,8 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
             }
         }
         float s = ceilf(total64(work) / (float)c.target);
-        const float fill = total64(tiles) * (float)a.heads * (float)c.least_full * (1.f / 256.f);
+        tiles = total64(tiles);
+        const float fill = tiles * (float)a.heads * (float)c.least_full * (1.f / 256.f);
         const int32_t least = fill > (float)c.least_full ? c.least_full : (fill < (float)c.least ? c.least : (int32_t)fill);
         uncut = 2 * least;
         s = s < (float)least ? (float)least : s;
@@ -180,7 +181,7 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
         // Not before the kernel for many rows, where it finds little to do (80 rows of 8
         // requests each 67 -> 69 us).
         const float s0 = s, most = ceilf(1.4f * s0);
-        for (int k = 0; c.fit; k++) {
+        for (int k = tiles > 0.6f * (float)c.target ? 7 : 0; c.fit; k++) {       // (so many hardly fit)
             float n = 0.f;
             for (int b0 = 0; b0 < a.B; b0 += 64) {
                 const int b = b0 + lane;
