@@ -187,6 +187,9 @@ __device__ __forceinline__ float keep_odd(double x)
     return (float)__longlong_as_double((b & 0xFFFFFFFF00000000ull) | kept);
 }
 
+// The first 16 bits of x, rounded towards 0, of which its product with a bf16 is exact.
+__device__ __forceinline__ float high_term(double x) { return __uint_as_float(__float_as_uint((float)x) & 0xFFFFFF00u); }
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t quad(uint32_t v)
 {
@@ -242,12 +245,14 @@ __device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
 
 // A workgroup takes up to N * (256 / (D / 8)) heads of a row; without the cache,
 // then of the row gridDim.x further on, whose channels are on their way while it
-// works on this one (6000 rows of 24 heads of 256: 28.7 -> 25.2 us, what a copy
-// takes; with the cache the loop's registers halve the workgroups of a CU, and
-// 8192 rows of 32 + 8 + 8 heads of 128 take 68 us, without it 40).  A thread has
-// eight channels (16 bytes) of up to N heads, always the same channels.  The row is
-// staged in LDS, where a channel finds its partner whatever rot is; all reads of a
-// head come before its writes (a row may be rotated in place).
+// works on this one (6000 rows of 24 heads of 256: 28.7 -> 25.2 us; with the cache
+// the loop's registers halve the workgroups of a CU, and 8192 rows of 32 + 8 + 8 heads
+// of 128 take 68 us, without it 40).  Bound by bytes (24.1 us, 147 MB) and, with the
+// cache, as much by vector instructions (37 us, 177 MB): the terms of a factor are
+// formed once a row, not by every thread (25.5 and 41 us).  A thread has eight
+// channels (16 bytes) of up to N heads, always the same channels.  The row is staged
+// in LDS, where a channel finds its partner whatever rot is; all reads of a head come
+// before its writes (a row may be rotated in place).
 //
 // Angles, cosines and sines are fp64: at position 2^20 an fp32 angle is off by
 // 2^-5.  q is rotated in fp32 with the factors in two terms, of which the first
@@ -259,12 +264,15 @@ template <int N, bool KV>
 __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
 {
     __shared__ u32x4 s_x[N][256];
-    __shared__ double2 s_cs[128];
+    __shared__ double2 s_cs[KV ? 128 : 1];
+    __shared__ f32x4 s_cf[128];                           // cosine and sine in two terms each
     const int tid = threadIdx.x, D = a.D, cph = D / 8, hpi = 256 / cph;
     const int hl = tid / cph, c = tid - hl * cph;
     const int heads = a.Hq + (KV ? 2 * a.Hkv : 0), h0 = blockIdx.y * (hpi * N) + hl;
     const int n = a.rot / 2;
     const bool pairs = a.layout == SPEAR_ROPE_PAIRS, turn = a.freqs && 8 * c < a.rot;
+    // (half) the frequency of a channel; of none behind rot
+    auto place = [&](int e) { return e < n ? e : (e < a.rot ? e - n : 0); };
     u32x4 x[N];
     int64_t slot = -1;
     int32_t pos = 0;
@@ -290,7 +298,12 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
         if (a.freqs && tid < n) {
             double s, co;
             sincos((double)pos * freq, &s, &co);
-            s_cs[tid] = make_double2(co * a.scale, s * a.scale);
+            co *= a.scale;
+            s *= a.scale;
+            const float c0 = high_term(co), s0 = high_term(s);
+            s_cf[tid] = f32x4{c0, (float)(co - (double)c0), s0, (float)(s - (double)s0)};
+            if (KV)
+                s_cs[tid] = make_double2(co, s);
         }
 #pragma unroll
         for (int i = 0; i < N; i++)
@@ -301,21 +314,19 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
         if (!KV && t + gridDim.x < a.T)
             load(t + gridDim.x);
 
-        // y_j = x_j c_j + x_partner s_j for the channels below rot (the others: c 1, s 0)
-        float c0[8], c1[8], s0[8], s1[8];
+        // y_j = x_j c_j + p_j s_j for the channels below rot, p_j the partner, negative for
+        // the first of a pair
+        f32x4 cs[8];
         int at = 8 * c;                                   // (half) the first partner
         if (turn) {
+            if (pairs) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int e = 8 * c + j;
-                const bool second = pairs ? (e & 1) : e >= n, in = e < a.rot;
-                const double2 cs = in ? s_cs[pairs ? e >> 1 : (second ? e - n : e)] : make_double2(1.0, 0.0);
-                const double sn = second ? cs.y : -cs.y;
-                c0[j] = __uint_as_float(__float_as_uint((float)cs.x) & 0xFFFFFF00u);
-                c1[j] = (float)(cs.x - (double)c0[j]);
-                s0[j] = __uint_as_float(__float_as_uint((float)sn) & 0xFFFFFF00u);
-                s1[j] = (float)(sn - (double)s0[j]);
-            }
+                for (int j = 0; j < 8; j += 2)
+                    cs[j] = cs[j + 1] = s_cf[4 * c + j / 2 < n ? 4 * c + j / 2 : 0];
+            } else
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    cs[j] = s_cf[place(8 * c + j)];
             at += 8 * c >= n ? -n : n;
         }
 #pragma unroll
@@ -335,32 +346,33 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
                 if (pairs) {
 #pragma unroll
                     for (int j = 0; j < 8; j++)
-                        p[j] = f[j ^ 1];
+                        p[j] = j & 1 ? f[j ^ 1] : -f[j ^ 1];
                 } else if (n % 8 == 0) {                  // the partners lie in one chunk, as the channels do
                     const u32x4 v = *reinterpret_cast<const u32x4 *>(row + at);
+                    const uint32_t sign = at > 8 * c ? 0x80008000u : 0u;
 #pragma unroll
                     for (int j = 0; j < 8; j++)
-                        p[j] = bf16f((uint16_t)(v[j >> 1] >> (16 * (j & 1))));
+                        p[j] = bf16f((uint16_t)((v[j >> 1] ^ sign) >> (16 * (j & 1))));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
                         const int e = 8 * c + j;
-                        p[j] = bf16f(row[e < n ? e + n : (e < a.rot ? e - n : e)]);
+                        const float v = bf16f(row[e < n ? e + n : (e < a.rot ? e - n : e)]);
+                        p[j] = e < n ? -v : v;
                     }
                 }
                 if (is_q) {
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        const float r = __builtin_fmaf(f[j], c0[j], p[j] * s0[j]) + __builtin_fmaf(f[j], c1[j], p[j] * s1[j]);
+                        const float r = __builtin_fmaf(f[j], cs[j][0], p[j] * cs[j][2]) + __builtin_fmaf(f[j], cs[j][1], p[j] * cs[j][3]);
                         f[j] = 8 * c + j < a.rot ? r : f[j];
                     }
-                } else {
+                } else if (KV) {
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
                         const int e = 8 * c + j;
-                        const bool second = pairs ? (e & 1) : e >= n;
-                        const double2 cs = s_cs[e < a.rot ? (pairs ? e >> 1 : (second ? e - n : e)) : 0];
-                        const double r = (double)f[j] * cs.x + (double)p[j] * (second ? cs.y : -cs.y);
+                        const double2 d = s_cs[pairs ? (e < a.rot ? e >> 1 : 0) : place(e)];
+                        const double r = (double)f[j] * d.x + (double)p[j] * d.y;
                         f[j] = e < a.rot ? keep_odd(r) : f[j];
                     }
                 }
