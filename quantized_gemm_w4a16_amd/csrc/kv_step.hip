@@ -399,7 +399,11 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
     }
 }
 
-constexpr int64_t ROPE_BLOCKS = 1280;  // workgroups that run at once
+// Workgroups that run at once, of up to two heads a thread and of more (us from cold
+// memory with 1280 / 1024 / 768 of them: 8192 rows of 32 heads of 128 31.9 / 26.2 / 26.7,
+// 3500 of 16 heads of 192 12.2 / 10.6 / 11.5; three heads a thread, 6000 rows of 24 heads
+// of 256, 29.7 / 31.1 / 29.0).
+constexpr int64_t ROPE_BLOCKS_2 = 1024, ROPE_BLOCKS_4 = 768;
 
 template <bool KV>
 hipError_t launch_rope(const RopeArgs &a, int64_t T, hipStream_t s)
@@ -407,7 +411,7 @@ hipError_t launch_rope(const RopeArgs &a, int64_t T, hipStream_t s)
     const int heads = a.Hq + (KV ? 2 * a.Hkv : 0), hpi = 256 / (a.D / 8);
     // few rows: more workgroups, a head a thread; else as many as a row has, up to four
     const int n = T * heads <= (int64_t)hpi * 2048 ? 1 : (heads + hpi - 1) / hpi;
-    const int64_t parts = (heads + hpi * (n < 4 ? n : 4) - 1) / (hpi * (n < 4 ? n : 4)), most = ROPE_BLOCKS / parts;
+    const int64_t parts = (heads + hpi * (n < 4 ? n : 4) - 1) / (hpi * (n < 4 ? n : 4)), most = (n <= 2 ? ROPE_BLOCKS_2 : ROPE_BLOCKS_4) / parts;
     const dim3 grid((unsigned)(!KV && most < T ? (most < 1 ? 1 : most) : T), (unsigned)parts);
     switch (n) {
     case 1: hipLaunchKernelGGL((rope_kernel<1, KV>), grid, dim3(256), 0, s, a); break;
