@@ -1256,10 +1256,13 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         L.tiles[k] = tiles;
         L.items[k] = tiles + (L.target[k] ? (k || both ? cut : 2 * cut) + 16 : 0);
         // The room of the parts does not depend on max_fresh and grows with T and B,
-        // so that a workspace of the largest step serves every other.
-        const int64_t fewest = k ? rows / 128 : rows / FEW_ROWS;
-        const int64_t room = (fewest < most_cut ? fewest : most_cut) + more + (k ? most_cut : 2 * most_cut) + 16;
-        const int64_t room_rows = room * heads * (k ? 256 : FEW_ROWS);
+        // so that a workspace of the largest step serves every other.  Where there are
+        // parts, tiles * heads <= COUNTS, and rows fill up to most_cut tiles, or (few rows,
+        // before the other kernel) two a request.
+        const int64_t fill = k ? rows / 128 : rows / FEW_ROWS, full = !k && more > most_cut ? more : most_cut;
+        const int64_t extra = (k ? most_cut : 2 * most_cut) + 16;
+        const int64_t parts = ((fill < full ? fill : full) + more + extra) * heads, most_parts = COUNTS + extra * heads;
+        const int64_t room_rows = (parts < most_parts ? parts : most_parts) * (k ? 256 : FEW_ROWS);
         L.part_o[k] = off;
         off += (size_t)(room_rows * D) * sizeof(float);
         L.part_ml[k] = off;

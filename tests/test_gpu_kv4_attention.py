@@ -304,3 +304,38 @@ def test_two_streams_at_once():
     for s, g, w in zip(steps, got, want):
         n = int(s.q_start[-1])
         assert torch.equal(g[:n], w[:n])
+
+
+def test_many_short_requests_around_a_long_one():
+    """Parts of a request cut into chunks behind a thousand whole tiles: each request's
+    rows are those of a call of its own."""
+    heads, D, P, fresh, n_long = 8, 64, 64, 17, 40000
+    kv_len = np.full(512, 30, np.int32)
+    kv_len[[3, 509]] = n_long
+    counts = np.full(512, fresh, np.int32)
+    counts[100] = 40
+    kv_len[100] = 64
+    pages = -(-kv_len // P)
+    width = int(pages.max()) + room(P, True)
+    table = torch.full((512, width), -1, dtype=torch.int32, device="cuda")
+    first = np.concatenate(([0], np.cumsum(pages)))
+    for b in (3, 509, 100):
+        table[b, : pages[b]] = torch.arange(first[b], first[b + 1], dtype=torch.int32, device="cuda")
+    one = pages == 1
+    table[torch.from_numpy(np.flatnonzero(one)).cuda(), 0] = dev(first[:-1][one].astype(np.int32))
+    kv = sp.new_kv4(int(first[-1]), heads, D, P)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    places = int(first[-1]) * P
+    k, v = (torch.randn(places, heads, D, device="cuda", generator=g, dtype=torch.float32).bfloat16() for _ in "kv")
+    sp.spear_rope_kv4_write(k, k, v, None, torch.arange(places, device="cuda"), None, kv)
+    start = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
+    q = torch.randn(int(start[-1]), heads, D, device="cuda", generator=g, dtype=torch.float32).bfloat16()
+    y = sp.spear_kv4_attention(q, kv, table, dev(start), dev(kv_len), 40)
+    for b in (0, 3, 100, 300, 508, 509, 510, 511):
+        t0, t1 = int(start[b]), int(start[b + 1])
+        alone = sp.spear_kv4_attention(q[t0:t1].contiguous(), kv, table[b : b + 1, : pages[b]].contiguous(),
+                                       dev(np.array([0, t1 - t0], np.int32)), dev(kv_len[b : b + 1]), t1 - t0)
+        # two roundings to bf16, and in the kernel for many rows P's, with |v| <= 6
+        off = (y[t0:t1].double() - alone.double()).abs()
+        bound = 2.1 * ref_kv4.HALF_BF16 * alone.double().abs() + (6 * ref_kv4.HALF_BF16 if b == 100 else 2 ** -14)
+        assert bool((off <= bound).all()), (b, float(off.max()))

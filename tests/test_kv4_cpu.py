@@ -205,3 +205,12 @@ def test_numbers_beyond_32_bits_are_refused():
     refused(E_SHAPE, sp.spear_kv4_attention, x, kv, table, start, n, 2, window=(1 << 32) + 5)
     refused(E_SHAPE, sp.spear_kv4_plan, n, n, table, one, one, 4, (1 << 32) + 16)
     refused(E_SHAPE, sp.spear_rope_frequencies, (1 << 32) + 64)
+
+
+def test_attention_workspace_is_bounded():
+    """Parts are of 8192 tiles and two rounds of chunks at most, however many requests."""
+    f = sp.spear_kv4_attention_workspace_size
+    for B, heads, D in ((4096, 8, 128), (4096, 64, 256), (300, 1, 64)):
+        n = f(1 << 15, B, 1 << 15, heads, heads, D, 1000, 64)
+        few, many = 8192 + (2 * (768 + heads) + 16 * heads), 8192 + (512 + heads) + 16 * heads
+        assert 0 < n <= 4 * (few * 16 * (D + 4) + many * 256 * (D + 2) + 8192 + 32768)
