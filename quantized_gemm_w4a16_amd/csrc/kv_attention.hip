@@ -1262,7 +1262,8 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         const int64_t fill = k ? rows / 128 : rows / FEW_ROWS, full = !k && more > most_cut ? more : most_cut;
         const int64_t extra = (k ? most_cut : 2 * most_cut) + 16;
         const int64_t parts = ((fill < full ? fill : full) + more + extra) * heads, most_parts = COUNTS + extra * heads;
-        const int64_t room_rows = (parts < most_parts ? parts : most_parts) * (k ? 256 : FEW_ROWS);
+        // (so few rows have no request for the kernel for many)
+        const int64_t room_rows = k && rows <= FEW_LIMIT ? 0 : (parts < most_parts ? parts : most_parts) * (k ? 256 : FEW_ROWS);
         L.part_o[k] = off;
         off += (size_t)(room_rows * D) * sizeof(float);
         L.part_ml[k] = off;
