@@ -489,7 +489,9 @@ spear_status spear_rope_frequencies(int32_t rot, double base, int32_t kind, doub
  *   y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t),
  *   t = position * freqs[i], (a, b) the i-th pair, m = scale
  * with angles, cosines and sines in fp64 (far positions lose nothing) and y off by
- * 2^-23 |y| + 2^-38 |x| before it is rounded to bf16.
+ * 2^-23 |y| + 2^-38 |x| before it is rounded to bf16.  Infinities and NaN give what
+ * the formula gives for them (at position 0 an infinite x_a: y_a infinite, y_b NaN),
+ * and no product on the way is cut at fp32's range.
  *   x [T][H][D] bf16, x_stride elements from a row to the next (a multiple of 8,
  *     at least H D); y likewise with y_stride; x and y 16-byte aligned.  y may be
  *     x itself (then with its stride); it overlaps no other input.

@@ -259,9 +259,11 @@ __device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
 // has 16 bits, so that its products with bf16 are exact: x c0 + p s0 is rounded
 // once, and r = (x c0 + p s0) + (x c1 + p s1) is off by 2^-23 |r| + 2^-38 |x, p|
 // before its rounding to bf16.  k, whose values next to a border of e2m1 would
-// fall on the other side, is rotated in fp64.
+// fall on the other side, is rotated in fp64.  (Two heads a thread without the cache:
+// four waves a SIMD, as launch_rope counts on, are 128 registers; left to itself the
+// compiler takes 131.)
 template <int N, bool KV>
-__global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
+__global__ __launch_bounds__(256, N == 2 && !KV ? 4 : 1) void rope_kernel(const RopeArgs a)
 {
     __shared__ u32x4 s_x[N][256];
     __shared__ double2 s_cs[KV ? 128 : 1];
@@ -362,10 +364,30 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a)
                     }
                 }
                 if (is_q) {
+                    float top = 0.f;
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
                         const float r = __builtin_fmaf(f[j], cs[j][0], p[j] * cs[j][2]) + __builtin_fmaf(f[j], cs[j][1], p[j] * cs[j][3]);
+                        top = __builtin_elementwise_maximum(top, __builtin_fabsf(r));       // (a NaN stays)
                         f[j] = 8 * c + j < a.rot ? r : f[j];
+                    }
+                    // An infinity times a second term of 0 or of the other sign is a NaN that the
+                    // formula has not, and a product beyond fp32 may be on its way to less: such
+                    // channels are formed anew, in fp64, from what LDS holds.
+                    if (!(top < INFINITY)) {
+                        int e0 = 8 * c;
+                        asm volatile("" : "+v"(e0));      // (no register holds these addresses all along)
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const int e = e0 + j;
+                            if (e < a.rot) {
+                                const bool second = pairs ? e & 1 : e >= n;
+                                const int step = pairs ? 1 : n;
+                                const f32x4 w = s_cf[pairs ? e >> 1 : place(e)];
+                                const double other = (double)bf16f(row[second ? e - step : e + step]) * ((double)w[2] + (double)w[3]);
+                                f[j] = (float)((double)bf16f(row[e]) * ((double)w[0] + (double)w[1]) + (second ? other : -other));
+                            }
+                        }
                     }
                 } else if (KV) {
 #pragma unroll
