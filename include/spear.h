@@ -392,6 +392,7 @@ spear_status spear_w4_experts(const spear_bf16 *x, int64_t M, const spear_expert
  *   e = f - 2, or f - 1 where a / 2^f >= 1.75 (a rounded to two significant bits
  *       has the next exponent), held within [-125, 125]; a = 0 gives -125
  *   code = x / 2^e rounded to the nearest level, ties to the even code, at most 6
+ *       (a rotated key may lie beyond fp32's range, and is finite all the same)
  *   scale byte = e + 127;  a block with a NaN or an infinity: 255, and reads NaN
  * so that a value that is read back is exact in bf16.  Pages of P tokens, a
  * head's tokens side by side (device pointers, each 16-byte aligned):

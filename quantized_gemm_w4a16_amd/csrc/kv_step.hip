@@ -1,6 +1,7 @@
 // kv_step.hip -- the plan of a serving step, rotary positions, and the cache of
 // 4 bits written and read (spear_kv4_plan, spear_rope, spear_rope_kv4_write,
 // spear_kv4_read, spear_rope_frequencies) for gfx950.
+#include <float.h>
 #include <math.h>
 
 #include "kv4.hpp"
@@ -223,6 +224,8 @@ __device__ __forceinline__ uint32_t codes8(const float (&f)[8], uint32_t e)
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[6], f[7], s, 3);
 }
 
+// The largest magnitude's bits among eight channels and those that the quad's other
+// lanes hold of their block.
 __device__ __forceinline__ uint32_t top8(const float (&f)[8])
 {
     uint32_t top = 0;
@@ -234,11 +237,11 @@ __device__ __forceinline__ uint32_t top8(const float (&f)[8])
     return quad_max(top);
 }
 
-// Eight channels of a block of 32 whose other channels the lane's quad holds ->
-// the eight codes; *byte the block's scale.
-__device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t *byte)
+// Eight channels of a block of 32 whose largest magnitude has the bits `top` -> the
+// eight codes; *byte the block's scale.
+__device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t top, uint32_t *byte)
 {
-    const uint32_t top = top8(f), e = block_exponent(top);
+    const uint32_t e = block_exponent(top);
     *byte = top >= 0x7F800000u ? 255u : e;               // a NaN or an infinity
     return codes8(f, e);
 }
@@ -342,8 +345,25 @@ __global__ __launch_bounds__(256, N == 2 && !KV ? 4 : 1) void rope_kernel(const 
 #pragma unroll
             for (int j = 0; j < 8; j++)
                 f[j] = bf16f((uint16_t)(own[j >> 1] >> (16 * (j & 1))));
+            const uint16_t *row = reinterpret_cast<const uint16_t *>(&s_x[i][hl * cph]);
+            // the rotated channels in fp64, from what LDS holds (e0 is opaque: no
+            // register is to hold these addresses all along)
+            auto anew = [&](auto factors, auto rounded) {
+                int e0 = 8 * c;
+                asm volatile("" : "+v"(e0));
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int e = e0 + j;
+                    if (e < a.rot) {
+                        const bool second = pairs ? e & 1 : e >= n;
+                        const int step = pairs ? 1 : n;
+                        const double2 d = factors(pairs ? e >> 1 : place(e));
+                        const double other = (double)bf16f(row[second ? e - step : e + step]) * d.y;
+                        f[j] = rounded((double)bf16f(row[e]) * d.x + (second ? other : -other));
+                    }
+                }
+            };
             if (turn && !is_v) {
-                const uint16_t *row = reinterpret_cast<const uint16_t *>(&s_x[i][hl * cph]);
                 float p[8];
                 if (pairs) {
 #pragma unroll
@@ -373,22 +393,12 @@ __global__ __launch_bounds__(256, N == 2 && !KV ? 4 : 1) void rope_kernel(const 
                     }
                     // An infinity times a second term of 0 or of the other sign is a NaN that the
                     // formula has not, and a product beyond fp32 may be on its way to less: such
-                    // channels are formed anew, in fp64, from what LDS holds.
-                    if (!(top < INFINITY)) {
-                        int e0 = 8 * c;
-                        asm volatile("" : "+v"(e0));      // (no register holds these addresses all along)
-#pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            const int e = e0 + j;
-                            if (e < a.rot) {
-                                const bool second = pairs ? e & 1 : e >= n;
-                                const int step = pairs ? 1 : n;
-                                const f32x4 w = s_cf[pairs ? e >> 1 : place(e)];
-                                const double other = (double)bf16f(row[second ? e - step : e + step]) * ((double)w[2] + (double)w[3]);
-                                f[j] = (float)((double)bf16f(row[e]) * ((double)w[0] + (double)w[1]) + (second ? other : -other));
-                            }
-                        }
-                    }
+                    // channels are formed anew in fp64.
+                    if (!(top < INFINITY))
+                        anew([&](int at_cs) {
+                            const f32x4 w = s_cf[at_cs];
+                            return make_double2((double)w[0] + (double)w[1], (double)w[2] + (double)w[3]);
+                        }, [](double r) { return (float)r; });
                 } else if (KV) {
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
@@ -406,8 +416,17 @@ __global__ __launch_bounds__(256, N == 2 && !KV ? 4 : 1) void rope_kernel(const 
                     o[j] = pair_bf16(f[2 * j], f[2 * j + 1]);
                 *reinterpret_cast<u32x4 *>(a.y + t * a.ys + (int64_t)h * D + 8 * c) = o;
             } else if (KV && there) {
+                uint32_t top = top8(f);
+                if (top == 0x7F800000u && !is_v) {        // (of the quad) a key beyond fp32 is held as the largest
+                    if (turn)
+                        anew([&](int at_cs) { return s_cs[at_cs]; }, [](double r) {
+                            const float k = keep_odd(r);
+                            return __builtin_fabsf(k) == INFINITY && __builtin_fabs(r) < INFINITY ? __builtin_copysignf(FLT_MAX, k) : k;
+                        });
+                    top = top8(f);
+                }
                 uint32_t byte;
-                const uint32_t codes = hold8(f, &byte);
+                const uint32_t codes = hold8(f, top, &byte);
                 const int64_t ph = page * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0));
                 uint8_t *cp = is_v ? a.v_codes : a.k_codes, *sp = is_v ? a.v_scales : a.k_scales;
                 *reinterpret_cast<uint32_t *>(cp + (((ph << a.log_p) + off) * (D / 2) + 4 * c)) = codes;
