@@ -461,7 +461,7 @@ spear_status spear_kv4_plan(const int32_t *cached, const int32_t *fresh, int32_t
 /* Rotary positions: the first rot channels of every head, the others as they are. */
 typedef struct spear_rotation {
     const double *freqs; /* device [rot / 2]: angle of one position, radians; 8-byte aligned */
-    double scale;        /* factor of the rotated channels (1: none); finite                  */
+    double scale;        /* factor m of the rotated channels (1: none); 0 or 2^-100 <= |m| <= 2^100 */
     int32_t rot;         /* even, 2 .. D                                                       */
     int32_t layout;      /* SPEAR_ROPE_HALF or SPEAR_ROPE_PAIRS                               */
 } spear_rotation;
@@ -489,10 +489,10 @@ spear_status spear_rope_frequencies(int32_t rot, double base, int32_t kind, doub
  * spear_rope -- y = x with every head rotated to its row's position:
  *   y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t),
  *   t = position * freqs[i], (a, b) the i-th pair, m = scale
- * with angles, cosines and sines in fp64 (far positions lose nothing) and y off by
- * 2^-23 |y| + 2^-38 |x| before it is rounded to bf16.  Infinities and NaN give what
- * the formula gives for them (at position 0 an infinite x_a: y_a infinite, y_b NaN),
- * and no product on the way is cut at fp32's range.
+ * with angles, cosines and sines in fp64 (far positions lose nothing) and y off from
+ * these by 2^-23 |y| + 2^-37 |m| (|x_a| + |x_b|) + 2^-147 before it is rounded to bf16.
+ * Infinities and NaN give what the formula gives for them (at position 0 an infinite
+ * x_a: y_a infinite, y_b NaN), and no product on the way is cut at fp32's range.
  *   x [T][H][D] bf16, x_stride elements from a row to the next (a multiple of 8,
  *     at least H D); y likewise with y_stride; x and y 16-byte aligned.  y may be
  *     x itself (then with its stride); it overlaps no other input.

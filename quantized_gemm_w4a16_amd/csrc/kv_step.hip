@@ -260,8 +260,9 @@ __device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t top, uin
 // Angles, cosines and sines are fp64: at position 2^20 an fp32 angle is off by
 // 2^-5.  q is rotated in fp32 with the factors in two terms, of which the first
 // has 16 bits, so that its products with bf16 are exact: x c0 + p s0 is rounded
-// once, and r = (x c0 + p s0) + (x c1 + p s1) is off by 2^-23 |r| + 2^-38 |x, p|
-// before its rounding to bf16.  k, whose values next to a border of e2m1 would
+// once.  The second terms, 2^-15 of the first at most, are rounded to 2^-40, and the
+// product, the sum and the join of theirs to 2^-39: r = (x c0 + p s0) + (x c1 + p s1) is
+// off by 2^-23 |r| + 2^-37 |m| (|x| + |p|) before its rounding to bf16.  k, whose values next to a border of e2m1 would
 // fall on the other side, is rotated in fp64.  (Two heads a thread without the cache:
 // four waves a SIMD, as launch_rope counts on, are 128 registers; left to itself the
 // compiler takes 131.)
@@ -505,7 +506,9 @@ spear_status check_rotation(const spear_rotation *r, int32_t D)
         return SPEAR_E_NULL;
     if (r->rot < 2 || r->rot > D || r->rot % 2 != 0)
         return SPEAR_E_SHAPE;
-    if ((r->layout != SPEAR_ROPE_HALF && r->layout != SPEAR_ROPE_PAIRS) || !isfinite(r->scale))
+    // within fp32's range with room for the second terms (2^-40 of the first) and for sums
+    const double m = fabs(r->scale);
+    if ((r->layout != SPEAR_ROPE_HALF && r->layout != SPEAR_ROPE_PAIRS) || !(m == 0.0 || (m >= 0x1p-100 && m <= 0x1p100)))
         return SPEAR_E_ARG;
     return al(r->freqs, 8) ? SPEAR_OK : SPEAR_E_ALIGN;
 }
