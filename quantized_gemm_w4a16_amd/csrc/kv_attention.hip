@@ -423,6 +423,79 @@ __device__ __forceinline__ float2 load_far(const float *p)
 }
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// A row's maximum m is that of its products z = q . k.  Its probabilities are held as
+//   2^(scale z - e), e = scale m rounded, by one fma each (scale with log2 e in it),
+// and from |e| = FAR on, where e has no bits behind the point (and may lie beyond fp32),
+//   2^(scale (z - m)).
+constexpr float FAR = 0x1p24f;
+
+// Rounded by itself: never the product of an fma.
+__device__ __forceinline__ float scaled(float m, float scale)
+{
+#pragma clang fp contract(off)
+    return m * scale;
+}
+__device__ __forceinline__ bool is_far(float m, float e) { return (__builtin_fabsf(e) >= FAR) & (__builtin_fabsf(m) < INFINITY); }
+
+// What probabilities held for the maximum m weigh where up >= m is the maximum: where
+// neither is far, and where one may be.
+__device__ __forceinline__ float part_weight(float m, float up, float scale)
+{
+    return __builtin_amdgcn_exp2f(scaled(m, scale) - scaled(up, scale));
+}
+__device__ __forceinline__ float far_weight(float m, float up, float scale)
+{
+    const float e = scaled(m, scale), e_up = scaled(up, scale);
+    const float d = (e - e_up) + ((is_far(m, e) ? __builtin_fmaf(m, scale, -e) : 0.f) -
+                                  (is_far(up, e_up) ? __builtin_fmaf(up, scale, -e_up) : 0.f));
+    return __builtin_amdgcn_exp2f(d > -INFINITY ? d : (m - up) * scale);
+}
+// The sum of a part whose maximum is far has its sign set.
+__device__ __forceinline__ float marked(float l, float m, float scale) { return is_far(m, scaled(m, scale)) ? -l : l; }
+
+// The part (m2, l2, v) joined to (m, l, sum) where a maximum may be far.
+__device__ __forceinline__ void join_far(float &m, float &l, f32x4 &sum, float m2, float l2, f32x4 v, float scale)
+{
+    const float up = fmaxf(m, m2), ref = up == -INFINITY ? 0.f : up;
+    const float f = far_weight(m, ref, scale), w = far_weight(m2, ref, scale);
+    l = marked(f * __builtin_fabsf(l) + w * __builtin_fabsf(l2), up, scale);
+    sum = f * sum + w * v;
+    m = up;
+}
+
+// A row's maximum as it goes over the keys (of the lane's row, in all lanes that share it).
+struct RowMax {
+    float m = -INFINITY;
+    float least = -INFINITY;        // m; -INFINITY where it is far: products then lose m first
+    float add = 0.f;                // of the fma that makes products exponents
+
+    __device__ __forceinline__ bool takes(float top) const { return __any(top > least); }
+    // Products z of which `top` is the row's largest: what was held so far is to be
+    // multiplied by the result.
+    template <class V, int N>
+    __device__ __forceinline__ float take(float top, float scale, V (&z)[N])
+    {
+        const float up = fmaxf(m, top), e = scaled(up, scale);
+        float f = part_weight(m, up, scale);
+        const bool now = is_far(up, e), was = least < m;
+        add = up == -INFINITY ? 0.f : -e;
+        least = up;
+        if (__builtin_expect(__any(now | was), 0)) {
+            f = far_weight(m, up, scale);
+            add = now ? 0.f : add;
+            least = now ? -INFINITY : up;
+            const float off = now ? up : 0.f;
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                z[i] -= off;
+        }
+        f = m == up ? 1.f : f;
+        m = up;
+        return f;
+    }
+    __device__ __forceinline__ float marked_sum(float l) const { return least < m ? -l : l; }
+};
+
 // Four channels from c on of row i of a tile, and with c == 0 its lse.
 template <int D>
 __device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int head, const TileRows &rows, int i, int c, f32x4 sum,
@@ -433,8 +506,10 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, const Item &it, int
     const float inv = l == 0.f ? 0.f : 1.f / l;
     *reinterpret_cast<uint2 *>(a.y + hrow * D + c) =
         make_uint2(pair_bf16(sum[0] * inv, sum[1] * inv), pair_bf16(sum[2] * inv, sum[3] * inv));
-    if (c == 0 && a.lse)
-        a.lse[hrow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * LN2;
+    if (c == 0 && a.lse) {
+        const float e = scaled(m, a.scale), log2_l = __log2f(l);       // (e beyond fp32: without log2 e)
+        a.lse[hrow] = l == 0.f ? -INFINITY : (__builtin_fabsf(e) < INFINITY ? (e + log2_l) * LN2 : m * (a.scale * LN2) + log2_l * LN2);
+    }
 }
 
 // One tile of 16 rows and a chunk of its keys:
@@ -516,7 +591,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
 #pragma unroll
     for (int d = 0; d < DT; d++)
         o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    RowMax best;
+    float l = 0.f;
 
     Part<D> kp, vp;
     const int32_t *table = a.table + (int64_t)b * a.width;
@@ -586,22 +662,19 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                 for (int r = 0; r < 4; r++)
                     top = fmaxf(top, acc[i][r]);
         }
-        top = max_over_groups(top) * a.scale;
-        if (__any(top > m)) {
-            const float up = fmaxf(m, top);
-            const float f = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up);
-            m = up;
+        top = max_over_groups(top);
+        if (best.takes(top)) {
+            const float f = best.take(top, a.scale, acc);
             l *= f;
 #pragma unroll
             for (int d = 0; d < DT; d++)
                 o[d] *= f;
         }
-        const float m0 = m == -INFINITY ? 0.f : -m;
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int r = 0; r < 4; r++) {
-                acc[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][r], a.scale, m0));
+                acc[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][r], a.scale, best.add));
                 l += acc[i][r];
             }
 
@@ -692,8 +765,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
     for (int d = 0; d < DT; d++)
         *reinterpret_cast<f32x4 *>(so + n * D + 16 * d + 4 * g) = o[d];
     if (g == 0) {
-        s_ml[wave][n][0] = m;
-        s_ml[wave][n][1] = l;
+        s_ml[wave][n][0] = best.m;
+        s_ml[wave][n][1] = best.marked_sum(l);
     }
     __syncthreads();
     const int rows = it.r.fresh * G - it.tile * FEW_ROWS;                  // real rows of the tile
@@ -706,13 +779,25 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
         for (int w = 0; w < FEW_WAVES; w++)
             mm = fmaxf(mm, s_ml[w][r][0]);
         const float ref = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
+        float ll = 0.f, least = 0.f;
         f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
+        for (int w = 0; w < FEW_WAVES; w++)
+            least = fminf(least, s_ml[w][r][1]);
+#pragma unroll
         for (int w = 0; w < FEW_WAVES; w++) {
-            const float f = __builtin_amdgcn_exp2f(s_ml[w][r][0] - ref);
+            const float f = part_weight(s_ml[w][r][0], ref, a.scale);
             ll += f * s_ml[w][r][1];
             sum += f * *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(s_v[w]) + r * D + c);
+        }
+        if (__builtin_expect(least < 0.f, 0)) {
+            mm = -INFINITY;
+            ll = 0.f;
+            sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma nounroll
+            for (int w = 0; w < FEW_WAVES; w++)
+                join_far(mm, ll, sum, s_ml[w][r][0], s_ml[w][r][1],
+                         *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(s_v[w]) + r * D + c), a.scale);
         }
         if (it.chunks > 1) {
             const int64_t p = ((int64_t)(it.item + it.chunk) * a.heads + head) * FEW_ROWS + r;
@@ -721,7 +806,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
             if (c == 0)
                 store_far(cut.part_ml + 2 * p, mm, ll);
         } else
-            store_out<D>(a, it, head, tile_rows, r, c, sum, mm, ll);
+            store_out<D>(a, it, head, tile_rows, r, c, sum, mm, __builtin_fabsf(ll));
     }
     if (it.chunks < 2)
         return;
@@ -755,6 +840,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
             const int r = in ? x / (D / 4) : 0, c = in ? 4 * (x % (D / 4)) : 0;
             float mm = -INFINITY, ll = 0.f;
             f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+            float least = 0.f;
             for (int i0 = sh; i0 < n; i0 += JB * sharers) {
                 float2 ml[JB], lo2[JB], hi2[JB];
 #pragma unroll
@@ -767,20 +853,33 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                 }
                 float up = mm;
 #pragma unroll
-                for (int j = 0; j < JB; j++)
+                for (int j = 0; j < JB; j++) {
                     up = fmaxf(up, ml[j].x);
-                const float ref = up == -INFINITY ? 0.f : up, f = __builtin_amdgcn_exp2f(mm - ref);
+                    least = fminf(least, ml[j].y);
+                }
+                const float ref = up == -INFINITY ? 0.f : up, f = part_weight(mm, ref, a.scale);
                 ll *= f;
                 sum *= f;
                 mm = up;
 #pragma unroll
                 for (int j = 0; j < JB; j++) {
                     // (a part whose weight is 0 counts too: it may hold a NaN)
-                    const float w = __builtin_amdgcn_exp2f(ml[j].x - ref);
+                    const float w = part_weight(ml[j].x, ref, a.scale);
                     if (i0 + j * sharers < n) {
                         ll += w * ml[j].y;
                         sum += w * f32x4{lo2[j].x, lo2[j].y, hi2[j].x, hi2[j].y};
                     }
+                }
+            }
+            if (__builtin_expect(least < 0.f, 0)) {
+                mm = -INFINITY;
+                ll = 0.f;
+                sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma nounroll
+                for (int i = sh; i < n; i += sharers) {
+                    const int64_t p = p0 + (int64_t)i * by * next + r;
+                    const float2 ml = load_far(part_ml + 2 * p), lo2 = load_far(cut.part_o + p * D + c), hi2 = load_far(cut.part_o + p * D + c + 2);
+                    join_far(mm, ll, sum, ml.x, ml.y, f32x4{lo2.x, lo2.y, hi2.x, hi2.y}, a.scale);
                 }
             }
             if (sharers > 1) {
@@ -795,7 +894,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
                     for (int j = 1; j < sharers; j++) {
                         const float *o2 = s_part + (tid + j * (64 * FEW_WAVES / sharers)) * 6;
                         const float up = fmaxf(mm, o2[0]), ref = up == -INFINITY ? 0.f : up;
-                        const float f = __builtin_amdgcn_exp2f(mm - ref), w = __builtin_amdgcn_exp2f(o2[0] - ref);
+                        if (__builtin_expect(fminf(ll, o2[1]) < 0.f, 0)) {
+                            join_far(mm, ll, sum, o2[0], o2[1], f32x4{o2[2], o2[3], o2[4], o2[5]}, a.scale);
+                            continue;
+                        }
+                        const float f = part_weight(mm, ref, a.scale), w = part_weight(o2[0], ref, a.scale);
                         mm = up;
                         ll = f * ll + w * o2[1];
                         sum = f * sum + w * f32x4{o2[2], o2[3], o2[4], o2[5]};
@@ -803,7 +906,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, D <= 128 ? 3 : 2) void few_rows_ker
             }
             if (in && sh == 0) {
                 if (to_y)
-                    store_out<D>(a, it, head, tile_rows, r, c, sum, mm, ll);
+                    store_out<D>(a, it, head, tile_rows, r, c, sum, mm, __builtin_fabsf(ll));
                 else {
                     // a row's m and l, which its other threads may still read, to a place of
                     // their own
@@ -926,7 +1029,8 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             qf[s] = row < rows ? ld16(qp + 16 * s) : zero4();
     }
     f32x16 o[DT];
-    float m = -INFINITY, l = 0.f;
+    RowMax best;
+    float l = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; d++)
 #pragma unroll
@@ -1043,23 +1147,20 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
 #pragma unroll
         for (int r = 1; r < 16 * KT; r++)
             top = fmaxf(top, s[r / 16][r % 16]);
-        top = max_over_halves(top) * a.scale;
-        if (__any(top > m)) {
-            const float x = fmaxf(m, top);
-            const float f = m == x ? 1.f : __builtin_amdgcn_exp2f(m - x);
-            m = x;
+        top = max_over_halves(top);
+        if (best.takes(top)) {
+            const float f = best.take(top, a.scale, s);
             l *= f;
 #pragma unroll
             for (int d = 0; d < DT; d++)
                 o[d] *= f;
         }
-        const float m0 = m == -INFINITY ? 0.f : -m;
         u32x4 p[KT][2];
 #pragma unroll
         for (int kt = 0; kt < KT; kt++) {
 #pragma unroll
             for (int r = 0; r < 16; r++) {
-                s[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale, m0));
+                s[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale, best.add));
                 l += s[kt][r];
             }
 #pragma unroll
@@ -1113,11 +1214,11 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
             if (it.chunks > 1)
                 *reinterpret_cast<f32x4 *>(cut.part_o + p * D + c) = v;
             else
-                store_out<D>(a, it, head, tile_rows, row - first_row, c, v, m, l);
+                store_out<D>(a, it, head, tile_rows, row - first_row, c, v, best.m, l);
         }
     if (it.chunks > 1 && h == 0) {
-        cut.part_ml[2 * p] = m;
-        cut.part_ml[2 * p + 1] = l;
+        cut.part_ml[2 * p] = best.m;
+        cut.part_ml[2 * p + 1] = best.marked_sum(l);
     }
 }
 
@@ -1127,7 +1228,7 @@ __global__ __launch_bounds__(64 * W, D > 192 ? 1 : 2) void many_rows_kernel(cons
 constexpr int JOIN = 4;
 
 template <int D, int ROWS>
-__global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, const Cut cut)
+__global__ __launch_bounds__(256, 3) void join_chunks_kernel(const AttnArgs a, const Cut cut)
 {
     constexpr int Q = D / 4, S = Q <= 32 ? (Q <= 16 ? 4 : 2) : 1;
     const int head = blockIdx.x % a.heads;
@@ -1143,6 +1244,7 @@ __global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, cons
     const TileRows tile_rows(it.tile * ROWS, a.G);
     float mm[JOIN], ll[JOIN];
     f32x4 sum[JOIN];
+    float least = 0.f;
 #pragma unroll
     for (int r = 0; r < JOIN; r++) {
         mm[r] = -INFINITY;
@@ -1167,32 +1269,59 @@ __global__ __launch_bounds__(256) void join_chunks_kernel(const AttnArgs a, cons
 #pragma unroll
                 for (int r = 0; r < JOIN; r++) {
                     const float up = fmaxf(mm[r], ml[j][r].x), ref = up == -INFINITY ? 0.f : up;
-                    const float f = __builtin_amdgcn_exp2f(mm[r] - ref), w = __builtin_amdgcn_exp2f(ml[j][r].x - ref);
+                    const float f = part_weight(mm[r], ref, a.scale), w = part_weight(ml[j][r].x, ref, a.scale);
+                    least = fminf(least, ml[j][r].y);
                     mm[r] = up;
                     ll[r] = f * ll[r] + w * ml[j][r].y;
                     sum[r] = f * sum[r] + w * v[j][r];
                 }
     }
-#pragma unroll
-    for (int d = 64 / S; d < 64; d *= 2)
+    const bool far = __any(least < 0.f);
+    if (__builtin_expect(far, 0))
 #pragma unroll
         for (int r = 0; r < JOIN; r++) {
-            const float m2 = __shfl_xor(mm[r], d), l2 = __shfl_xor(ll[r], d);
-            const float up = fmaxf(mm[r], m2), ref = up == -INFINITY ? 0.f : up;
-            const float f = __builtin_amdgcn_exp2f(mm[r] - ref), w = __builtin_amdgcn_exp2f(m2 - ref);
-            mm[r] = up;
-            // the same order in both lanes
-            const float x = f * ll[r], y = w * l2;
-            ll[r] = x + y;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                sum[r][e] = f * sum[r][e] + w * __shfl_xor(sum[r][e], d);
+            float m = -INFINITY, l = 0.f;
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+            least = 0.f;
+#pragma nounroll
+            for (int i = sh; i < it.chunks; i += S) {
+                const int64_t p = p0 + i * next + (r0 + r < rows ? r0 + r : r0);
+                const float2 ml = *reinterpret_cast<const float2 *>(cut.part_ml + 2 * p);
+                least = fminf(least, ml.y);
+                join_far(m, l, o, ml.x, ml.y, *reinterpret_cast<const f32x4 *>(cut.part_o + p * D + c), a.scale);
+            }
+            if (least < 0.f) {                            // (the other rows keep their bits)
+                mm[r] = m;
+                ll[r] = l;
+                sum[r] = o;
+            }
         }
+    auto across = [&](auto weight) {
+#pragma unroll
+        for (int d = 64 / S; d < 64; d *= 2)
+#pragma unroll
+            for (int r = 0; r < JOIN; r++) {
+                const float m2 = __shfl_xor(mm[r], d), l2 = __shfl_xor(ll[r], d);
+                const float up = fmaxf(mm[r], m2), ref = up == -INFINITY ? 0.f : up;
+                const float f = weight(mm[r], ref, a.scale), w = weight(m2, ref, a.scale);
+                mm[r] = up;
+                // the same order in both lanes
+                const float x = f * __builtin_fabsf(ll[r]), y = w * __builtin_fabsf(l2);
+                ll[r] = x + y;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    sum[r][e] = f * sum[r][e] + w * __shfl_xor(sum[r][e], d);
+            }
+    };
+    if (__builtin_expect(far, 0))
+        across(far_weight);
+    else
+        across(part_weight);
     if (sh == 0 && q < Q)
 #pragma unroll
         for (int r = 0; r < JOIN; r++)
             if (r0 + r < rows && r0 + r < ROWS)
-                store_out<D>(a, it, head, tile_rows, r0 + r, c, sum[r], mm[r], ll[r]);
+                store_out<D>(a, it, head, tile_rows, r0 + r, c, sum[r], mm[r], __builtin_fabsf(ll[r]));
 }
 
 // ------------------------------------------------------------------- host
