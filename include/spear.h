@@ -540,14 +540,16 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *     p - window only
  *   y[t][h] = sum_j softmax_j(scale q[t][h] . k[j][h / G]) v[j][h / G],  G = Hq / heads
  *   lse[t][h] = log sum_j exp(scale q . k)       (natural; optional)
- * Sums and softmax are in fp32, y is rounded once to bf16.  Products q . k that pass
- * fp32's range only when they are scaled count by their differences (lse is rounded to
- * fp32, an infinity where it lies beyond).  Requests of one token, of a few and of long
- * chunks may stand side by side.  A row that sees nothing, or scores of -inf only, gets
- * zeros and lse -inf; one that sees a NaN is NaN; rows behind the last request are left
- * as they were.  A table entry outside [0, pages) (a page that was let go) is as if its
- * tokens were masked; what masked places hold, NaN and infinities among it, does not
- * count.  kv_len is held within [0, width P] and q_start within [0, T].
+ * Sums and softmax are in fp32, y is rounded once to bf16.  Probabilities meet v as
+ * two bf16 (off by 2^-17 of their size at most), in requests of many rows as one
+ * (2^-8).  Products q .  k that pass fp32's range only when they are scaled count by
+ * their differences (lse is rounded to fp32, an infinity where it lies beyond).
+ * Requests of one token, of a few and of long chunks may stand side by side.  A row
+ * that sees nothing, or scores of -inf only, gets zeros and lse -inf; one that sees a
+ * NaN is NaN; rows behind the last request are left as they were.  A table entry
+ * outside [0, pages) (a page that was let go) is as if its tokens were masked; what
+ * masked places hold, NaN and infinities among it, does not count.  kv_len is held
+ * within [0, width P] and q_start within [0, T].
  *   q [T][Hq][D] bf16 with q_stride elements from row to row (a multiple of 8);
  *     y [T][Hq][D] bf16 without gaps; both 16-byte aligned; y may be q itself if
  *     q has no gaps.  Hq a multiple of heads, G <= 64, T Hq <= 2^27.
