@@ -542,7 +542,7 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *   lse[t][h] = log sum_j exp(scale q . k)       (natural; optional)
  * Sums and softmax are in fp32, y is rounded once to bf16.  Probabilities meet v as
  * two bf16 (off by 2^-17 of their size at most), in requests of many rows as one
- * (2^-8).  Products q .  k that pass fp32's range only when they are scaled count by
+ * (2^-8).  Products q . k that pass fp32's range only when they are scaled count by
  * their differences (lse is rounded to fp32, an infinity where it lies beyond).
  * Requests of one token, of a few and of long chunks may stand side by side.  A row
  * that sees nothing, or scores of -inf only, gets zeros and lse -inf; one that sees a
