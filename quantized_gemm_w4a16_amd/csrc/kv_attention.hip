@@ -1343,13 +1343,17 @@ bool attention_sizes(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_
            width >= 1 && width <= SPEAR_MAX_CONTEXT / P && T * Hq <= (int64_t)1 << 27;
 }
 
-// Requests of up to FEW_LIMIT rows take the kernel for few rows, and so do all of a
-// step of few rows and keys (all heads), which that one spreads over more
-// workgroups and without a second launch.  us, few / both: 300 rows of a prompt, 16
-// heads over 8, 17 / 26; 1000 rows 24 / 38; 64 rows on 8192 keys, 32 over 8, 34 / 40
-// (2^24 rows x keys); 16 requests of 20 rows on up to 3000, 73 / 52 (2^25); 256 rows
-// on 8192 107 / 62.  The keys are what the table has room for; an entry wider than
-// the lengths takes both.
+// Steps whose requests have up to FEW_ROWS_ALL rows take the kernel for few rows, which
+// spreads them over more workgroups without a second launch, and so do steps of few rows
+// and keys (all heads).  us, few / both: 48 requests on up to 8000 keys, one token of a
+// group of 64 of 128 channels 34 / 48, of 256 54 / 127; 64 rows, 8 heads of 256 199 / 577,
+// 4 of 128 62 / 77, of 64 52 / 46 (the one size that it does not pay for); 128 rows, 4 of
+// 128 107 / 88.  300 rows of a prompt, 16 heads over 8, 17 / 26; 1000 rows 24 / 38; 64 rows
+// on 8192 keys, 32 over 8, 34 / 40 (2^24 rows x keys); 256 rows on 8192 107 / 62.  The
+// keys are what the table has room for; an entry wider than the lengths takes both.
+// Where a step takes both, requests of up to FEW_LIMIT rows take the one for few, and
+// those of one token, whose G rows are up to 64.
+constexpr int FEW_ROWS_ALL = 64;
 constexpr int FEW_LIMIT = 32;
 constexpr int64_t FEW_WORK = (int64_t)1 << 24;
 // Eight waves a workgroup, which share the staging of a step's keys, if requests fill
@@ -1361,8 +1365,9 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
     AttnLayout L;
     const int64_t G = Hq / heads, rows = T * G, more = T < B ? T : B;
     max_fresh = max_fresh < T ? max_fresh : T;
-    const bool both = T > 0 && max_fresh * G > FEW_LIMIT && rows * heads > FEW_WORK / (keys < 1 ? 1 : keys);
-    L.limit = both ? FEW_LIMIT : 0x7FFFFFFF;              // (one kernel alone takes all)
+    const bool both = T > 0 && max_fresh * G > FEW_ROWS_ALL && rows * heads > FEW_WORK / (keys < 1 ? 1 : keys);
+    const int64_t limit = G > FEW_LIMIT ? G : FEW_LIMIT, of_few = (limit + FEW_ROWS - 1) / FEW_ROWS;     // tiles of a request
+    L.limit = both ? (int32_t)limit : 0x7FFFFFFF;         // (one kernel alone takes all)
     L.wide = D <= 128 && max_fresh * G >= WIDE_ROWS;
     const int many = 32 * (L.wide ? 8 : 4);
     const int resident = L.wide || D > 192 ? 256 : 512;   // workgroups of the kernel for many rows
@@ -1377,7 +1382,7 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         const int64_t each = max_fresh > 0 ? (T + max_fresh - 1) / max_fresh : 0;
         least = least > each ? least : each;
         if (!k && both) {
-            const int64_t few = more * (FEW_LIMIT / FEW_ROWS);
+            const int64_t few = more * of_few;
             tiles = tiles < few ? tiles : few;
             least = 0;
         }
@@ -1387,12 +1392,13 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         // The room of the parts does not depend on max_fresh and grows with T and B,
         // so that a workspace of the largest step serves every other.  Where there are
         // parts, tiles * heads <= COUNTS, and rows fill up to most_cut tiles, or (few rows,
-        // before the other kernel) two a request.
-        const int64_t fill = k ? rows / 128 : rows / FEW_ROWS, full = !k && more > most_cut ? more : most_cut;
+        // before the other kernel) of_few a request, one of which `more` counts.
+        const int64_t fill = k ? rows / 128 : rows / FEW_ROWS, behind = more * (of_few - 1);
+        const int64_t full = !k && behind > most_cut ? behind : most_cut;
         const int64_t extra = (k ? most_cut : 2 * most_cut) + 16;
         const int64_t parts = ((fill < full ? fill : full) + more + extra) * heads, most_parts = COUNTS + extra * heads;
         // (so few rows have no request for the kernel for many)
-        const int64_t room_rows = k && rows <= FEW_LIMIT ? 0 : (parts < most_parts ? parts : most_parts) * (k ? 256 : FEW_ROWS);
+        const int64_t room_rows = k && rows <= FEW_ROWS_ALL ? 0 : (parts < most_parts ? parts : most_parts) * (k ? 256 : FEW_ROWS);
         L.part_o[k] = off;
         off += (size_t)(room_rows * D) * sizeof(float);
         L.part_ml[k] = off;
