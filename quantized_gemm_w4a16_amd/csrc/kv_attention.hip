@@ -1363,7 +1363,7 @@ constexpr int WIDE_ROWS = 256;
 AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_t heads, int32_t D, int64_t keys)
 {
     AttnLayout L;
-    const int64_t G = Hq / heads, rows = T * G, more = T < B ? T : B;
+    const int64_t G = Hq / heads, rows = T * G, requests = T < B ? T : B;
     max_fresh = max_fresh < T ? max_fresh : T;
     const bool both = T > 0 && max_fresh * G > FEW_ROWS_ALL && rows * heads > FEW_WORK / (keys < 1 ? 1 : keys);
     const int64_t limit = G > FEW_LIMIT ? G : FEW_LIMIT, of_few = (limit + FEW_ROWS - 1) / FEW_ROWS;     // tiles of a request
@@ -1376,8 +1376,10 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
         const int tile = k ? many : FEW_ROWS, goal = k ? resident : (D > 128 ? 512 : FEW_ITEMS);
         const int64_t cut = (goal + heads - 1) / heads, most_cut = ((k ? 512 : FEW_ITEMS) + heads - 1) / heads;
         // tiles of a key head: at most one more a request than its rows fill (few
-        // rows: at most what a request may have), and no fewer than all rows fill
-        // and requests of max_fresh rows make
+        // rows: at most what a request may have; many: of the requests that can have
+        // more than limit rows), and no fewer than all rows fill and requests of
+        // max_fresh rows make
+        const int64_t longer = rows / (limit + 1), more = k && longer < requests ? longer : requests;
         int64_t tiles = rows / tile + more, least = (rows + tile - 1) / tile;
         const int64_t each = max_fresh > 0 ? (T + max_fresh - 1) / max_fresh : 0;
         least = least > each ? least : each;
