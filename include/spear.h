@@ -558,12 +558,13 @@ spear_status spear_kv4_read(const spear_kv4 *kv, const int64_t *slots, int64_t T
  *     knows; it chooses kernels and their tiles, the result is right without it).
  *   scale > 0, finite (times log2 e too); window 0 (none) .. 2^30.
  *   workspace device scratch of spear_kv4_attention_workspace_size bytes (0 for
- *     sizes out of range), 256-byte aligned, zeroed once (spear_workspace_init):
- *     its counters are zero again when a call's work has ended.  It is not
- *     one that other entry points have written to.  The size grows
+ *     sizes out of range), 256-byte aligned, its first SPEAR_KV4_COUNTER_BYTES zeroed
+ *     once (spear_workspace_init): its counters are zero again when a call's work has
+ *     ended.  It is not one that other entry points have written to.  The size grows
  *     with T and B and hangs on neither max_fresh nor width, so one for the
  *     largest step serves the others, also between calls of other sizes.
  */
+#define SPEAR_KV4_COUNTER_BYTES ((size_t)163840)
 size_t spear_kv4_attention_workspace_size(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
                                           int32_t heads, int32_t D, int64_t width, int32_t P);
 spear_status spear_kv4_attention(const spear_bf16 *q, int64_t q_stride, int64_t T, int32_t Hq,

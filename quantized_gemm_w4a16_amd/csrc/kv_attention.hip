@@ -54,6 +54,7 @@ struct Cut {
 };
 constexpr int64_t COUNTS = 8192;            // tiles of all key heads that a cut may have
 constexpr int64_t GROUP_COUNTS = 32768;     // items
+static_assert((COUNTS + GROUP_COUNTS) * sizeof(uint32_t) == SPEAR_KV4_COUNTER_BYTES, "the part that a caller zeroes");
 
 // ------------------------------------------------------------------- items
 struct Request {
@@ -1371,7 +1372,7 @@ AttnLayout attention_layout(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq,
     L.wide = D <= 128 && max_fresh * G >= WIDE_ROWS;
     const int many = 32 * (L.wide ? 8 : 4);
     const int resident = L.wide || D > 192 ? 256 : 512;   // workgroups of the kernel for many rows
-    size_t off = (COUNTS + GROUP_COUNTS) * sizeof(uint32_t);           // first, whatever the sizes: calls of all sizes share it
+    size_t off = SPEAR_KV4_COUNTER_BYTES;                 // first, whatever the sizes: calls of all sizes share it
     for (int k = 0; k < 2; k++) {
         const int tile = k ? many : FEW_ROWS, goal = k ? resident : (D > 128 ? 512 : FEW_ITEMS);
         const int64_t cut = (goal + heads - 1) / heads, most_cut = ((k ? 512 : FEW_ITEMS) + heads - 1) / heads;

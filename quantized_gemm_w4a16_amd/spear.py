@@ -41,6 +41,7 @@ SCORE_SIGMOID = 1
 MAX_EXPERTS = 512
 MAX_TOPK = 32
 MAX_GROUPS = 64
+KV4_COUNTER_BYTES = 163840
 ROPE_HALF = 0
 ROPE_PAIRS = 1
 ROPE_PLAIN = 0
@@ -926,11 +927,13 @@ def spear_kv4_attention_workspace_size(T: int, B: int, max_fresh: int, Hq: int, 
 
 
 def new_kv4_workspace(T: int, B: int, max_fresh: int, Hq: int, kv: KV4, width: int) -> torch.Tensor:
-    """A zero-filled workspace for spear_kv4_attention over T rows of B requests,
-    none with more than max_fresh of them, and a table of that width (torch
+    """A workspace for spear_kv4_attention over T rows of B requests, none with more
+    than max_fresh of them, and a table of that width, its counters zeroed (torch
     allocation)."""
     n = spear_kv4_attention_workspace_size(T, B, max_fresh, Hq, kv.heads, kv.D, width, kv.P)
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=kv.device)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=kv.device)
+    ws[:KV4_COUNTER_BYTES].zero_()
+    return ws
 
 
 def spear_kv4_attention(q: torch.Tensor, kv: KV4, table: torch.Tensor, q_start: torch.Tensor,

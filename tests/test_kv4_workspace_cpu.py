@@ -1,10 +1,15 @@
 """What the attention's workspace takes: as much as its parts need, growing with the
 rows and requests of a step alone."""
 import itertools
+import os
+import re
+
+import torch
 
 from quantized_gemm_w4a16_amd import spear as sp
 
 size = sp.spear_kv4_attention_workspace_size
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "spear.h")
 
 
 def test_decode_steps_hold_no_room_for_prompts_of_each_request():
@@ -24,3 +29,13 @@ def test_one_for_the_largest_step_serves_the_others():
                 assert 0 < n[t, b] <= n[t2, b2], (t, b, t2, b2)
         for (t, b), most in itertools.product(steps, (0, 7, 1 << 40)):
             assert size(t, b, most, Hq, heads, D, 1, 16) == n[t, b]
+
+
+def test_only_the_counters_are_zeroed(monkeypatch):
+    """A call without a workspace clears 160 KB, not all of it."""
+    assert int(re.search(r"SPEAR_KV4_COUNTER_BYTES \(\(size_t\)(\d+)\)", open(HEADER).read()).group(1)) == sp.KV4_COUNTER_BYTES
+    monkeypatch.setattr(torch, "empty", lambda *n, **kw: torch.full(n, 255, **kw))
+    kv = sp.KV4(*(torch.full(s, 0, dtype=torch.uint8) for s in ((4, 2, 16, 32), (4, 2, 2, 16)) * 2))
+    ws = sp.new_kv4_workspace(3, 2, 2, 4, kv, 5)
+    assert ws.numel() == size(3, 2, 2, 4, 2, 64, 5, 16)
+    assert not ws[: sp.KV4_COUNTER_BYTES].any() and bool((ws[sp.KV4_COUNTER_BYTES:] == 255).all())
