@@ -898,11 +898,14 @@ def spear_rope_kv4_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 
 def spear_kv4_read(kv: KV4, slots: torch.Tensor, k: Optional[torch.Tensor] = None,
-                   v: Optional[torch.Tensor] = None, stream=None):
+                   v: Optional[torch.Tensor] = None, stream=None, parts: str = "kv"):
     """-> (k, v) [T][heads][D] bf16: the cache's rows, exact (zeros for a slot
-    outside the cache)."""
+    outside the cache); parts "k" or "v" reads that one alone and gives None for
+    the other."""
     fn = "spear_kv4_read"
     dev = kv.device
+    if parts not in ("kv", "k", "v") or (k is not None and "k" not in parts) or (v is not None and "v" not in parts):
+        _bad(fn, E_ARG, f"parts is {parts!r}")
     shape = T, _, _ = (slots.numel(), kv.heads, kv.D)
     _want(fn, "slots", slots, _I64, (T,), dev)
     for name, t in (("k", k), ("v", v)):
@@ -911,9 +914,11 @@ def spear_kv4_read(kv: KV4, slots: torch.Tensor, k: Optional[torch.Tensor] = Non
 
     def call(s):
         nonlocal k, v
-        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-        return load().spear_kv4_read(kv._s, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), s)
+        if k is None and "k" in parts:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if v is None and "v" in parts:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        return load().spear_kv4_read(kv._s, slots.data_ptr(), T, _at(k), _at(v), s)
 
     st = _on(fn, dev, stream, call)
     if st != SPEAR_OK:
