@@ -23,6 +23,7 @@ constexpr int FEW_ITEMS = 768;      // items of all key heads that the cut aims 
 // there are CUs without work.  us with 4 / 16: one request of 1021 keys and 8 heads 9.4
 // / 11.4, 300 tiles of up to 5 steps 16.5 / 10.7, 450 tiles of up to 25 53 / 43.
 constexpr int FEW_LEAST = 4, FEW_LEAST_FULL = 16;
+constexpr int FIT_REQUESTS = 256;   // requests of a step whose chunks are made to fit
 constexpr int JB = 8;               // chunks whose parts are on their way at once in the join
 constexpr int MANY_LEAST = 4;       // steps of its chunks, at least
 constexpr float LOG2E = 1.44269504088896340736f;
@@ -180,9 +181,15 @@ __device__ Item find_item(const AttnArgs &a, const Cut &c, int32_t want, bool by
         // there are twice as many (48 requests of 300 to 16000 tokens, 32 heads over 8, 128
         // channels 56.8 -> 52.3 us by the former, 256 channels 103 -> 98 by the latter).
         // Not before the kernel for many rows, where it finds little to do (80 rows of 8
-        // requests each 67 -> 69 us).
+        // requests each 67 -> 69 us), and not for many requests, whose walks cost more than
+        // it gives (one key head of 128 channels, requests of 300 to 6000 tokens: 307 of them
+        // 35 us with and 31 without, 537 62 and 52; of 256 channels 256 of them 48 and 54,
+        // 358 70 and 66).
+        // So many tiles as 0.6 of what is aimed at hardly fit, and are cut in half at once
+        // (us, counted first / at once: 134 requests of 300 to 16000 tokens, 4 heads of 64
+        // 50 / 46, of 128 74 / 70; 67 of 2000 to 6000, 8 heads of 128 56 / 61, 81 78 / 75).
         const float s0 = s, most = ceilf(1.4f * s0);
-        for (int k = tiles > 0.6f * (float)c.target ? 7 : 0; c.fit; k++) {       // (so many hardly fit)
+        for (int k = tiles > 0.6f * (float)c.target ? 7 : 0; c.fit && a.B <= FIT_REQUESTS; k++) {
             float n = 0.f;
             for (int b0 = 0; b0 < a.B; b0 += 64) {
                 const int b = b0 + lane;
