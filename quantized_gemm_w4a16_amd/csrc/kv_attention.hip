@@ -966,8 +966,8 @@ __device__ __forceinline__ float max_over_halves(float v)
 // so that P stays where S was, as in the kernel for few rows.  P is one bf16
 // here (off by 2^-8 of its size at most, as y is by its own rounding, and the sum goes over
 // many of them): a second term would make half as many matrix instructions more.
-// 8192 tokens of a prompt on 16384 keys, 32 heads of 128 over 8: 1.65 TFLOP in 1.73 ms,
-// 950 TFLOP/s.  The waves meet at each step, so its matrix instructions (two fifths of
+// 8192 tokens of a prompt on 16384 keys, 32 heads of 128 over 8: 1.65 TFLOP in 1.75 ms,
+// 941 TFLOP/s.  The waves meet at each step, so its matrix instructions (two fifths of
 // the time), exponentials and LDS reads hardly overlap; probabilities without
 // exponentials take 8 % less, steps without reads of K 13 %, of V 10 %, without the
 // staging 25 %.

@@ -18,8 +18,8 @@ bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 // thread) and takes its share of the new pages and of the rows; the first writes
 // what there is one of.  Nothing that a workgroup reads is written by another:
 // a row whose page is new computes the page from the free list.  Bound by round trips
-// (lengths, then the table or the free list): one request 3.8 us, 256 requests of
-// up to 700 tokens 5.1 us, in one launch.
+// (lengths, then the table or the free list): one request 4.1 us, 256 requests of
+// up to 535 tokens 5.4 us, in one launch.
 constexpr int PL_THREADS = 512;
 constexpr int PL_MOST = SPEAR_MAX_REQUESTS / PL_THREADS;
 
@@ -251,7 +251,7 @@ __device__ __forceinline__ uint32_t hold8(const float (&f)[8], uint32_t top, uin
 // works on this one (6000 rows of 24 heads of 256: 28.7 -> 25.2 us; with the cache
 // the loop's registers halve the workgroups of a CU, and 8192 rows of 32 + 8 + 8 heads
 // of 128 take 68 us, without it 40).  Bound by bytes (24.1 us, 147 MB) and, with the
-// cache, as much by vector instructions (37 us, 177 MB): the terms of a factor are
+// cache, as much by vector instructions (38 us, 177 MB): the terms of a factor are
 // formed once a row, not by every thread (25.5 and 41 us).  A thread has eight
 // channels (16 bytes) of up to N heads, always the same channels.  The row is staged
 // in LDS, where a channel finds its partner whatever rot is; all reads of a head come
