@@ -1354,13 +1354,14 @@ bool attention_sizes(int64_t T, int32_t B, int64_t max_fresh, int32_t Hq, int32_
 // Steps whose requests have up to FEW_ROWS_ALL rows take the kernel for few rows, which
 // spreads them over more workgroups without a second launch, and so do steps of few rows
 // and keys (all heads).  us, few / both: 48 requests on up to 8000 keys, one token of a
-// group of 64 of 128 channels 34 / 48, of 256 54 / 127; 64 rows, 8 heads of 256 199 / 577,
-// 4 of 128 62 / 77; 128 rows, 4 of 128 107 / 88.  It does not pay for 64 rows, 4 heads of
-// 64, 52 / 46, and, since every workgroup walks the requests, for a thousand of them with
-// 64 rows each on up to 400 keys, 8 heads of 128, 549 / 498 (40 rows 396 / 467, heads of
-// 256 1015 / 1213, 300 requests on up to 1000 keys 146 / 167).  300 rows of a prompt, 16 heads over 8, 17 / 26; 1000 rows 24 / 38; 64 rows
-// on 8192 keys, 32 over 8, 34 / 40 (2^24 rows x keys); 256 rows on 8192 107 / 62.  The
-// keys are what the table has room for; an entry wider than the lengths takes both.
+// group of 64 of 128 channels 34 / 48, of 256 54 / 127; 64 rows, 8 heads of 256 199 /
+// 577, 4 of 128 62 / 77; 128 rows, 4 of 128 107 / 88.  It does not pay for 64 rows, 4
+// heads of 64, 52 / 46, and, since every workgroup walks the requests, for a thousand of
+// them with 64 rows each on up to 400 keys, 8 heads of 128, 549 / 498 (40 rows 396 / 467,
+// heads of 256 1015 / 1213, 300 requests on up to 1000 keys 146 / 167).  300 rows of a
+// prompt, 16 heads over 8, 17 / 26; 1000 rows 24 / 38; 64 rows on 8192 keys, 32 over 8,
+// 34 / 40 (2^24 rows x keys); 256 rows on 8192 107 / 62.  The keys are what the table has
+// room for; an entry wider than the lengths takes both.
 // Where a step takes both, requests of up to FEW_LIMIT rows take the one for few, and
 // those of one token, whose G rows are up to 64.
 constexpr int FEW_ROWS_ALL = 64;
